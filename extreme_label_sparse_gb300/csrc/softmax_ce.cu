@@ -1,0 +1,1024 @@
+// Softmax cross entropy over a large label set (definitions in include/sg.h):
+//   z = h W^T,  lse_t = log sum_v exp z_tv,
+//   loss_t = lse_t - (1 - e) z_t,y - e mean_v z_t,
+//   g_tv = dloss_t (exp(z_tv - lse_t) - (1 - e) [v = y_t] - e / V),
+//   dh = g W,  dW = g^T h.
+// The logits never reach memory.  Forward: one matrix product whose epilogue
+// reduces each tile of logits to a running maximum and sum per row; a small
+// kernel joins them.  Backward, over pieces of the vocabulary: the product
+// again, its epilogue turning logits into g (16 bits, one piece of it held at
+// a time), then one launch with the tiles of both gradient products.
+//
+// All three products share one kernel: a persistent CTA, or a pair of CTAs on
+// one 256 x 256 tile where there are more than 128 rows, walks a list of
+// tiles.  A producer warp streams 128-byte wide K blocks of A and B through a
+// ring of shared-memory stages (TMA, 128-byte swizzle), one thread issues
+// tcgen05.mma into one of two TMEM accumulators, and eight warps work on the
+// other one.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "sg_internal.cuh"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+
+using namespace tc;
+
+namespace {
+
+#define CE_FAIL(code, ...)         \
+    do {                           \
+        sg_set_error(__VA_ARGS__); \
+        return code;               \
+    } while (0)
+#define CE_TRY(expr)            \
+    do {                        \
+        sg_status rc_ = (expr); \
+        if (rc_ != SG_OK)       \
+            return rc_;         \
+    } while (0)
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kSMs = 152;
+constexpr int kEpiWarps = 8;
+constexpr int kCeThreads = 32 * (kEpiWarps + 2);
+constexpr int kBN = 256;                 // tile columns
+constexpr uint32_t kBox = 8192;          // one TMA box: 64 rows of 128 bytes
+constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's output box: 32 rows of 128 bytes
+constexpr int kBand = 16;                // row tiles that walk the vocabulary together
+
+template <int CG>
+struct Cfg {
+    static constexpr int BM = 128 * CG;            // tile rows
+    static constexpr int BRows = kBN / CG;         // rows of B in one CTA
+    static constexpr uint32_t kA = 2 * kBox;       // bytes of A's and B's part of a stage
+    static constexpr uint32_t kB = (BRows / 64) * kBox;
+    static constexpr uint32_t kStage = kA + kB;
+    static constexpr int NS = CG == 2 ? 6 : 4;
+    static constexpr uint32_t kSmem = NS * kStage + kEpiWarps * kStgWarp + 1024;
+    static constexpr int C = kSMs / CG;            // clusters
+};
+
+enum Mode { kLse = 0, kProb = 1, kGrad = 2 };
+
+struct CeCtl {
+    uint64_t full[6], empty[6], tfull[2], tempty[2];
+    uint32_t tmem;
+    int abort_flag;
+};
+
+struct CeArgs {
+    int32_t T, V, H;      // rows, vocabulary, features
+    int32_t v0;           // first vocabulary row of the piece
+    int32_t nm, nn, nk;   // tiles of the logits (rows, columns of the piece), K blocks
+    int32_t f16;          // 16-bit operands are fp16, not bf16
+    // kLse
+    const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
+    const int32_t *targets;
+    float2 *part;         // [slot][Tp] running maximum (of z log2 e) and sum
+    float *zsum;          // [slot][Tp] sum of z, or NULL
+    float *ztgt;          // [T] the target's logit
+    int32_t Tp, ignore;
+    // kProb
+    const float *lse, *dloss, *gscale;  // gscale: factor of g (NULL: 1)
+    float smooth;
+    // kGrad: dh units first (rows x features x pieces of K), then dW tiles
+    int32_t dh_tiles, dh_nn, dh_split, dh_kb;  // tiles, tiles along H, pieces, K blocks in all
+    int32_t dw_tiles, dw_nn, dw_hi, dw_lo, dw_nk;
+    int32_t first;        // the piece is the first: dh sums start from zero
+    float *acc;           // dh sums, [unit][CTA][column / 4][128 rows][4]
+    const float *ginv;    // 1 / gscale (NULL: 1)
+    uint16_t *dW;         // where dW's rows do not suit TMA, else NULL
+    int64_t lddW;
+    int32_t *status;
+};
+
+struct Tile {
+    int kind;  // 0: logits, 1: dh, 2: dW
+    int m0, n0, k0, nk, unit;
+};
+
+// tile i of cluster c
+template <int CG, int MODE>
+__device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
+{
+    constexpr int C = Cfg<CG>::C, BM = Cfg<CG>::BM;
+    if constexpr (MODE != kGrad) {
+        // bands of kBand row tiles; inside a band the row tile runs fastest,
+        // so W is read from memory once for a band
+        const int64_t l = (int64_t)i * C + c;
+        if (l >= (int64_t)a.nm * a.nn)
+            return false;
+        const int64_t per = (int64_t)kBand * a.nn;
+        const int b = (int)(l / per), r = (int)(l - b * per);
+        const int mc = min(kBand, a.nm - b * kBand);
+        const int n = r / mc;
+        t.kind = 0;
+        t.m0 = (b * kBand + (r - n * mc)) * BM;
+        t.n0 = n * kBN;
+        t.k0 = 0;
+        t.nk = a.nk;
+        t.unit = n;
+        return true;
+    } else {
+        const int units = a.dh_tiles * a.dh_split;
+        const int hi = units % C;  // clusters below `hi` have one dh unit more
+        const int mine = units / C + (c < hi ? 1 : 0);
+        if (i < mine) {
+            const int u = i * C + c, s = u / a.dh_tiles, x = u - s * a.dh_tiles;
+            t.kind = 1;
+            t.m0 = x / a.dh_nn * BM;
+            t.n0 = x % a.dh_nn * kBN;
+            t.k0 = (int)((int64_t)s * a.dh_kb / a.dh_split);
+            t.nk = (int)((int64_t)(s + 1) * a.dh_kb / a.dh_split) - t.k0;
+            t.unit = u;
+            return true;
+        }
+        i -= mine;
+        // dW tiles in turn over the clusters; those with one dh unit more take
+        // only the first dw_hi turns
+        int64_t l;
+        if (i < a.dw_hi)
+            l = (int64_t)i * C + c;
+        else if (i < a.dw_lo && c >= hi)
+            l = (int64_t)a.dw_hi * C + (int64_t)(i - a.dw_hi) * (C - hi) + (c - hi);
+        else
+            return false;
+        if (l >= a.dw_tiles)
+            return false;
+        t.kind = 2;
+        t.m0 = (int)(l / a.dw_nn) * BM;
+        t.n0 = (int)(l % a.dw_nn) * kBN;
+        t.k0 = 0;
+        t.nk = a.dw_nk;
+        t.unit = 0;
+        return true;
+    }
+}
+
+// K-major: rows of 128 bytes of K, 8 rows to a swizzle atom.  MN-major: boxes
+// of 64 rows (128 bytes) by 64 K, kBox apart.
+__device__ __forceinline__ uint64_t op_desc(uint32_t tile, bool mn, int ks)
+{
+    return mn ? sdesc(tile + (uint32_t)ks * 2048, kBox, 1024, kLayoutSW128)
+              : sdesc(tile + (uint32_t)ks * 32, 16, 1024, kLayoutSW128);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16)
+{
+    return f16 ? pack2_f16(a, b) : pack2(a, b);
+}
+
+// 64 columns (32 packed words) of this warp's 32 rows into its swizzled box
+__device__ __forceinline__ void stage_words(uint8_t *stg, int lane, int word0, const uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(stg + lane * 128 + ((((word0 >> 2) + i) ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// maps: kLse, kProb: A = h, B = W, out = g (kProb); kGrad: g, W, h, out = dW
+template <int CG, int MODE, bool F8>
+__global__ void __launch_bounds__(kCeThreads, 1)
+    k_ce(const __grid_constant__ CUtensorMap m_h, const __grid_constant__ CUtensorMap m_W,
+         const __grid_constant__ CUtensorMap m_g, const __grid_constant__ CUtensorMap m_dW, const CeArgs a)
+{
+    using K = Cfg<CG>;
+    constexpr int NS = K::NS;
+    constexpr int KE = F8 ? 128 : 64;  // elements of a K block
+    __shared__ CeCtl c;
+    extern __shared__ uint8_t dsm[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)cluster_rank() : 0;
+    const int cl = (int)blockIdx.x / CG;
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        c.abort_flag = 0;
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&c.full[s]), 1);
+            mbar_init(smem_u32(&c.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c.tfull[b]), 1);
+            mbar_init(smem_u32(&c.tempty[b]), CG * kEpiWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kEpiWarps + 1) {
+        tmem_alloc_cg<CG>(smem_u32(&c.tmem), 512);
+        tmem_relinquish_cg<CG>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();
+    tc_fence_after();
+    const uint32_t tbase = c.tmem;
+    volatile int *abort_flag = &c.abort_flag;
+    Tile t;
+
+    if (warp == kEpiWarps) {
+        // ---------------------------------------------------------- producer
+        if (lane == 0) {
+            Ring r;
+            bool ok = true;
+            for (int i = 0; ok && tile_at<CG, MODE>(a, cl, i, t); ++i) {
+                const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
+                const CUtensorMap *ma = t.kind ? &m_g : &m_h, *mb = t.kind == 2 ? &m_h : &m_W;
+                const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
+                const int b_row = t.kind == 2 ? 0 : a.v0;  // rows of W start at the piece
+                for (int kb = 0; kb < t.nk; ++kb) {
+                    if (!mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = base + (uint32_t)r.i * K::kStage;
+                    uint32_t bar = smem_u32(&c.full[r.i]);
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(bar, CG * K::kStage);
+                    if constexpr (CG == 2)
+                        bar = mapa(bar, 0);
+                    const int k = (t.k0 + kb) * KE;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_2d_cg<CG>(st + j * kBox, ma, a_mn ? am + 64 * j : k, a_mn ? k : am + 64 * j, bar);
+#pragma unroll
+                    for (int j = 0; j < K::BRows / 64; ++j)
+                        tma_load_2d_cg<CG>(st + K::kA + j * kBox, mb, b_mn ? bn + 64 * j : k,
+                                           b_mn ? b_row + k : b_row + bn + 64 * j, bar);
+                    r.next(NS);
+                }
+            }
+            if (!ok) {
+                // gave up: copies may still be on their way into this CTA (and
+                // signal the pair's first CTA); they land long before this
+                const uint64_t t0 = global_ns();
+                while (global_ns() - t0 < 1000000u) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kEpiWarps + 1) {
+        // ---------------------------------------------------------- MMA
+        if (rank == 0) {
+            Ring r;
+            int it = 0;
+            bool ok = true;
+            for (int i = 0; ok && tile_at<CG, MODE>(a, cl, i, t); ++i) {
+                if (t.nk == 0)
+                    continue;
+                const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
+                const uint32_t idesc = (F8 || a.f16 ? idesc_f16(K::BM, kBN, a_mn, b_mn)
+                                                    : idesc_bf16(K::BM, kBN, a_mn, b_mn));
+                const int buf = it & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tempty[buf]),
+                                                               ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.status));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                for (int kb = 0; kb < t.nk; ++kb) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_cluster(smem_u32(&c.full[r.i]), r.ph, abort_flag, a.status));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t st = base + (uint32_t)r.i * K::kStage;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_cg<CG, F8>(tbase + buf * kBN, op_desc(st, a_mn, ks), op_desc(st + K::kA, b_mn, ks),
+                                           idesc, (kb > 0 || ks > 0) ? 1u : 0u);
+                        mma_commit_cg<CG>(smem_u32(&c.empty[r.i]));
+                    }
+                    __syncwarp();
+                    r.next(NS);
+                }
+                if (ok && lane == 0)
+                    mma_commit_cg<CG>(smem_u32(&c.tfull[buf]));
+                __syncwarp();
+                ++it;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue
+        // a warp reads its quarter of the TMEM lanes (tile rows) and one half
+        // of the tile's columns; a thread has one row
+        const int q = warp & 3, half = warp >> 2;
+        const int row_in = rank * 128 + q * 32 + lane;
+        uint8_t *stg = dsm + (base - smem_u32(dsm)) + NS * K::kStage + warp * kStgWarp;
+        const uint32_t stg_s = smem_u32(stg);
+        float m2 = -INFINITY, s = 0.f, zs = 0.f;
+        int it = 0;
+        for (int i = 0; tile_at<CG, MODE>(a, cl, i, t); ++i) {
+            if (t.nk == 0)
+                continue;
+            const int buf = it & 1;
+            const int row = t.m0 + row_in;              // row of the tile's A operand
+            const int col0 = t.n0 + half * (kBN / 2);   // first column of this warp
+            const uint32_t tm = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kBN + half * (kBN / 2));
+            // what the row needs, before the wait
+            int tgt = -1;
+            [[maybe_unused]] float cf = 0.f, l2 = 0.f, hs = 1.f;
+            if constexpr (MODE != kGrad) {
+                if (row < a.T) {
+                    const int y = a.targets[row];
+                    const bool live = y != a.ignore && y >= 0 && y < a.V;
+                    if (live)
+                        tgt = y - a.v0 - col0;  // this warp's column of the target, if it has it
+                    if constexpr (MODE == kProb) {
+                        l2 = a.lse[row] * kLog2e;
+                        if (live)
+                            cf = a.dloss[row] * (a.gscale ? a.gscale[0] : 1.f);
+                        else
+                            l2 = INFINITY;
+                    } else if constexpr (F8) {
+                        hs = a.h_scale ? a.h_scale[row] : 1.f;
+                    }
+                }
+            }
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait_cluster(smem_u32(&c.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, a.status)))
+                break;
+            tc_fence_after();
+            if constexpr (MODE == kLse) {
+                const int left = a.V - a.v0 - col0;  // columns of the vocabulary from col0 on
+#pragma unroll 1
+                for (int cc = 0; cc < kBN / 2; cc += 32) {
+                    float v[32];
+                    tmem_ld_chunk<32>(tm + cc, v);
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[x] *= hs * (a.W_scale && cc + x < left ? __ldg(a.W_scale + col0 + cc + x) : 1.f);
+                    }
+                    if (tgt >= cc && tgt < cc + 32) {
+                        float z = 0.f;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            z += x == tgt - cc ? v[x] : 0.f;
+                        a.ztgt[row] = z;
+                    }
+                    if (a.zsum) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            zs += cc + x < left ? v[x] : 0.f;
+                    }
+                    if (cc + 32 > left) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (cc + x >= left)
+                                v[x] = -INFINITY;
+                    }
+                    float top = v[0];
+#pragma unroll
+                    for (int x = 1; x < 32; ++x)
+                        top = fmaxf(top, v[x]);
+                    const float m = fmaxf(m2, top * kLog2e);
+                    const float mm = m == -INFINITY ? 0.f : m;
+                    float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        p[x & 3] += ex2(fmaf(v[x], kLog2e, -mm));
+                    s = fmaf(s, ex2(m2 - mm), (p[0] + p[1]) + (p[2] + p[3]));
+                    m2 = m;
+                }
+                // one row tile: the running values cover all tiles of this
+                // CTA; else they are written out for every tile
+                if (a.nm > 1) {
+                    const int64_t at = (int64_t)(t.unit * 2 + half) * a.Tp + row;
+                    a.part[at] = make_float2(m2, s);
+                    if (a.zsum)
+                        a.zsum[at] = zs;
+                    m2 = -INFINITY;
+                    s = zs = 0.f;
+                }
+            } else if constexpr (MODE == kProb) {
+                const int left = a.V - a.v0 - col0;
+                const float off = cf * (a.smooth / (float)a.V), hit = cf * (1.f - a.smooth);
+#pragma unroll 1
+                for (int cc = 0; cc < kBN / 2; cc += 32) {
+                    float v[32];
+                    tmem_ld_chunk<32>(tm + cc, v);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        v[x] = cf == 0.f ? 0.f : fmaf(ex2(fmaf(v[x], kLog2e, -l2)), cf, -off);
+                    if (tgt >= cc && tgt < cc + 32) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[x] -= x == tgt - cc ? hit : 0.f;
+                    }
+                    if (cc + 32 > left) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (cc + x >= left)
+                                v[x] = 0.f;
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        w[x] = pack16(v[2 * x], v[2 * x + 1], a.f16);
+                    if ((cc & 32) == 0) {
+                        if (lane == 0)
+                            bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    stage_words(stg, lane, (cc & 32) / 2, w);
+                    if (cc & 32) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0 && row < a.T) {  // lane 0 has the warp's first row
+                            tma_store_2d(&m_g, col0 + cc - 32, row, stg_s);
+                            bulk_commit();
+                        }
+                    }
+                }
+            } else {
+                if (t.kind == 1) {
+                    float4 *acc = reinterpret_cast<float4 *>(a.acc) +
+                                  ((int64_t)(t.unit * CG + rank) * (kBN / 4) + half * (kBN / 8)) * 128 + q * 32 + lane;
+#pragma unroll 1
+                    for (int cc = 0; cc < kBN / 2; cc += 32) {
+                        float v[32];
+                        tmem_ld_chunk<32>(tm + cc, v);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            float4 *p = acc + (cc / 4 + x) * 128;
+                            float4 o = a.first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+                            o.x += v[4 * x];
+                            o.y += v[4 * x + 1];
+                            o.z += v[4 * x + 2];
+                            o.w += v[4 * x + 3];
+                            *p = o;
+                        }
+                    }
+                } else {
+                    const float inv = a.ginv ? a.ginv[0] : 1.f;
+                    const int64_t row0 = (int64_t)a.v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
+#pragma unroll 1
+                    for (int cc = 0; cc < kBN / 2; cc += 32) {
+                        float v[32];
+                        tmem_ld_chunk<32>(tm + cc, v);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = pack16(v[2 * x] * inv, v[2 * x + 1] * inv, a.f16);
+                        if ((cc & 32) == 0) {
+                            if (lane == 0)
+                                bulk_wait_read<0>();
+                            __syncwarp();
+                        }
+                        stage_words(stg, lane, (cc & 32) / 2, w);
+                        if ((cc & 32) == 0)
+                            continue;
+                        const int x0 = col0 + cc - 32;
+                        if (!a.dW) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0 && row0 < a.V && x0 < a.H) {
+                                tma_store_2d(&m_dW, x0, (int)row0, stg_s);
+                                bulk_commit();
+                            }
+                        } else {
+                            __syncwarp();
+                            for (int r = 0; r < 32 && row0 + r < a.V; ++r)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int e = lane + 32 * j;
+                                    if (x0 + e < a.H)
+                                        a.dW[(row0 + r) * a.lddW + x0 + e] = *reinterpret_cast<const uint16_t *>(
+                                            stg + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+                                }
+                            __syncwarp();
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&c.tempty[buf]);
+                if constexpr (CG == 2)
+                    mbar_arrive_remote(mapa(bar, 0));
+                else
+                    mbar_arrive(bar);
+            }
+            ++it;
+        }
+        if constexpr (MODE == kLse) {
+            if (a.nm == 1) {
+                const int64_t at = (int64_t)(cl * 2 + half) * a.Tp + row_in;
+                a.part[at] = make_float2(m2, s);
+                if (a.zsum)
+                    a.zsum[at] = zs;
+            }
+        }
+        if (lane == 0)
+            bulk_wait<0>();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();
+    if (warp == kEpiWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc_cg<CG>(tbase, 512);
+    }
+}
+
+// ---------------------------------------------------------------- small kernels
+// lse and loss of 32 rows from their partial maxima and sums
+__global__ void __launch_bounds__(1024)
+    k_ce_join(const float2 *__restrict__ part, const float *__restrict__ zsum, const float *__restrict__ ztgt,
+              int slots, int Tp, int T, int V, const int32_t *__restrict__ targets, int ignore, float smooth,
+              float *__restrict__ loss, float *__restrict__ lse, int32_t *status)
+{
+    __shared__ float2 sm[32][33];
+    __shared__ float sz[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int t = blockIdx.x * 32 + lane;  // below Tp, a multiple of 128
+    float m = -INFINITY, s = 0.f, zs = 0.f;
+    for (int i = warp; i < slots; i += 32) {
+        const float2 p = part[(int64_t)i * Tp + t];
+        const float mn = fmaxf(m, p.x), ms = mn == -INFINITY ? 0.f : mn;
+        s = s * exp2f(m - ms) + p.y * exp2f(p.x - ms);
+        m = mn;
+        if (zsum)
+            zs += zsum[(int64_t)i * Tp + t];
+    }
+    sm[warp][lane] = make_float2(m, s);
+    sz[warp][lane] = zs;
+    __syncthreads();
+    if (warp != 0 || t >= T)
+        return;
+    for (int w = 1; w < 32; ++w) {
+        const float2 p = sm[w][lane];
+        const float mn = fmaxf(m, p.x), ms = mn == -INFINITY ? 0.f : mn;
+        s = s * exp2f(m - ms) + p.y * exp2f(p.x - ms);
+        m = mn;
+        zs += sz[w][lane];
+    }
+    const float l = (m + log2f(s)) * kLn2;
+    lse[t] = l;
+    const int y = targets[t];
+    float out = 0.f;
+    if (y >= 0 && y < V && y != ignore) {
+        out = l - (1.f - smooth) * ztgt[t];
+        if (zsum)
+            out -= smooth * (zs / (float)V);
+    } else if (y != ignore && status) {
+        sg_flag(status, SG_ERR_DATA);
+    }
+    loss[t] = out;
+}
+
+// fp16 gradients of the logits: dloss is often 1 / T, and softmax times it
+// falls below fp16's range.  A power of two brings the largest |dloss| to
+// 2^14 .. 2^15 (|g| <= |dloss|); the products' epilogues take it out again.
+__global__ void __launch_bounds__(1024) k_ce_gscale(const float *__restrict__ dloss, int T, float *__restrict__ out)
+{
+    __shared__ float sm[32];
+    float top = 0.f;
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const float v = fabsf(dloss[t]);
+        if (v < INFINITY)
+            top = fmaxf(top, v);
+    }
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0)
+        sm[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 32; ++w)
+            top = fmaxf(top, sm[w]);
+        int e = top > 0.f ? 14 - ilogbf(top) : 0;
+        e = max(-100, min(100, e));
+        out[0] = ldexpf(1.f, e);
+        out[1] = ldexpf(1.f, -e);
+    }
+}
+
+// dh = the sum of its pieces, 32 rows x 64 columns to a CTA
+template <int CG>
+__global__ void __launch_bounds__(256)
+    k_ce_dh(const float4 *__restrict__ acc, int tiles, int nn, int split, int T, int H, const float *ginv, int f16,
+            uint16_t *__restrict__ dh, int64_t lddh)
+{
+    __shared__ uint16_t sm[32][66];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int x = blockIdx.x / (CG * 4), rq = blockIdx.x % (CG * 4);  // tile, 32-row quarter of it
+    const int row0 = x / nn * Cfg<CG>::BM + rq * 32, col0 = x % nn * kBN + blockIdx.y * 64;
+    if (row0 >= T || col0 >= H)
+        return;
+    const float inv = ginv ? ginv[0] : 1.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int c4 = warp * 2 + j;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < split; ++s) {
+            const int64_t u = (int64_t)s * tiles + x;
+            const float4 o =
+                acc[((u * CG + rq / 4) * (kBN / 4) + blockIdx.y * 16 + c4) * 128 + (rq & 3) * 32 + lane];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+        }
+        *reinterpret_cast<uint32_t *>(&sm[lane][c4 * 4]) = pack16(v.x * inv, v.y * inv, f16);
+        *reinterpret_cast<uint32_t *>(&sm[lane][c4 * 4 + 2]) = pack16(v.z * inv, v.w * inv, f16);
+    }
+    __syncthreads();
+    for (int r = warp; r < 32 && row0 + r < T; r += 8)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (col0 + lane + 32 * j < H)
+                dh[(int64_t)(row0 + r) * lddh + col0 + lane + 32 * j] = sm[r][lane + 32 * j];
+}
+
+// rows that do not start on 16 bytes, copied to a stride that does
+template <typename E>
+__global__ void __launch_bounds__(256)
+    k_ce_pack(const E *__restrict__ src, int64_t ld, int64_t rows, int cols, E *__restrict__ dst, int64_t ldd)
+{
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int c = threadIdx.x; c < cols; c += 256)
+            dst[r * ldd + c] = src[r * ld + c];
+}
+
+// ---------------------------------------------------------------- host
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode_ce{nullptr};
+
+// row-major matrix in boxes of 64 rows x 128 bytes (or box_rows), 128-byte
+// swizzle
+sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int elem,
+                 uint32_t box_rows, const char *what)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = g_encode_ce.load(std::memory_order_acquire);
+    if (!enc) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn) {
+            cudaGetLastError();
+            CE_FAIL(SG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+        }
+        enc = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+        g_encode_ce.store(enc, std::memory_order_release);
+    }
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
+    cuuint32_t box[2] = {128u / (uint32_t)elem, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                           const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        CE_FAIL(SG_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
+    return SG_OK;
+}
+
+template <int CG, int MODE, bool F8>
+sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CUtensorMap &dW,
+                    const CeArgs &a, cudaStream_t st)
+{
+    // once for each device (one bit of the mask)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    SG_TRY_CUDA(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        SG_TRY_CUDA(cudaFuncSetAttribute(k_ce<CG, MODE, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Cfg<CG>::kSmem));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(Cfg<CG>::C * CG);
+    cfg.blockDim = dim3(kCeThreads);
+    cfg.dynamicSmemBytes = Cfg<CG>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    SG_TRY_CUDA(cudaLaunchKernelEx(&cfg, k_ce<CG, MODE, F8>, h, W, g, dW, a));
+    return SG_OK;
+}
+
+// One call's tiles and the places of its work memory
+struct Plan {
+    int es = 2, CG = 1, BM = 128, C = kSMs;
+    bool pack_h = false, pack_W = false;
+    int64_t ldp = 0;             // row stride of the packed copies
+    int64_t nm = 0, Tp = 0;
+    // forward
+    int64_t slots = 0;
+    // backward
+    int64_t Vc = 0, nn = 0;      // vocabulary of a piece, its tiles
+    int64_t dh_nn = 0, dh_tiles = 0, split = 1;
+    // byte offsets
+    int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
+};
+
+bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
+
+// K blocks that a tile's epilogue costs where its own product is shorter
+int64_t tile_cost(int64_t nk) { return (nk > 6 ? nk : 6) + 1; }
+
+void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
+               int32_t dtype, bool backward, Plan *p)
+{
+    p->es = dtype == SG_E4M3 ? 1 : 2;
+    p->CG = T > 128 ? 2 : 1;
+    p->BM = 128 * p->CG;
+    p->C = kSMs / p->CG;
+    p->pack_h = !tma_ok(h, ldh, p->es);
+    p->pack_W = !tma_ok(W, ldw, p->es);
+    p->ldp = ceil_div(H * p->es, 16) * 16 / p->es;
+    p->nm = ceil_div(T, p->BM);
+    p->Tp = p->nm * p->BM;
+    auto take = [&](int64_t n) {
+        const int64_t at = p->bytes;
+        p->bytes += ceil_div(n, 256) * 256;
+        return at;
+    };
+    if (p->pack_h)
+        p->o_h = take(T * p->ldp * p->es);
+    if (p->pack_W)
+        p->o_W = take(V * p->ldp * p->es);
+    if (!backward) {
+        p->slots = 2 * (p->nm == 1 ? (int64_t)p->C : ceil_div(V, kBN));
+        p->o_part = take(p->slots * p->Tp * 8);
+        p->o_zsum = take(p->slots * p->Tp * 4);
+        p->o_ztgt = take(T * 4);
+        return;
+    }
+    // a piece of g holds at most 256 MB
+    int64_t Vc = (256ll << 20) / 2 / T / kBN * kBN;
+    if (Vc < kBN)
+        Vc = kBN;
+    if (Vc > ceil_div(V, kBN) * kBN)
+        Vc = ceil_div(V, kBN) * kBN;
+    p->Vc = Vc;
+    p->nn = Vc / kBN;
+    p->dh_nn = ceil_div(H, kBN);
+    p->dh_tiles = p->nm * p->dh_nn;
+    // split K of dh until its units and the dW tiles fill the clusters evenly
+    const int64_t kb = ceil_div(V < Vc ? V : Vc, 64), dw = ceil_div(Vc, p->BM) * p->dh_nn * tile_cost(ceil_div(T, 64));
+    double best = 0;
+    for (int64_t n = 1; n <= kb && n <= 64; ++n) {
+        const int64_t units = p->dh_tiles * n, cost = tile_cost(ceil_div(kb, n)) + 2;
+        const double even = (double)(units * cost + dw) / p->C;
+        const double last = (double)(ceil_div(units, p->C) * cost);
+        const double span = (even > last ? even : last) * (1.0 + 0.002 * (double)n);
+        if (n == 1 || span < best) {
+            best = span;
+            p->split = n;
+        }
+    }
+    p->o_gs = take(8);
+    p->o_g = take(T * Vc * 2);
+    p->o_acc = take(p->dh_tiles * p->split * p->BM * kBN * 4);
+}
+
+sg_status check_ce(const char *fn, const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
+                   int64_t V, int32_t dtype, bool backward)
+{
+    if (dtype != SG_BF16 && dtype != SG_F16 && (dtype != SG_E4M3 || backward))
+        CE_FAIL(SG_ERR_INVALID, "%s: dtype %d is not SG_BF16 or SG_F16%s", fn, dtype,
+                backward ? "" : " or SG_E4M3");
+    if (T < 0 || H < 1 || V < 1)
+        CE_FAIL(SG_ERR_INVALID, "%s: need T >= 0, H >= 1 and V >= 1 (T=%lld H=%lld V=%lld)", fn, (long long)T,
+                (long long)H, (long long)V);
+    if (T > (1 << 24) || H > (1 << 20) || V > (1ll << 30))
+        CE_FAIL(SG_ERR_UNSUPPORTED, "%s: T=%lld, H=%lld or V=%lld is above 2^24, 2^20 or 2^30", fn, (long long)T,
+                (long long)H, (long long)V);
+    if (ldh < H || ldw < H)
+        CE_FAIL(SG_ERR_INVALID, "%s: a row stride (%lld, %lld) is below H=%lld", fn, (long long)ldh, (long long)ldw,
+                (long long)H);
+    const int64_t es = dtype == SG_E4M3 ? 1 : 2;
+    if ((uintptr_t)h % es != 0 || (uintptr_t)W % es != 0)
+        CE_FAIL(SG_ERR_INVALID, "%s: h or W is not aligned to its elements", fn);
+    return SG_OK;
+}
+
+template <typename E>
+void pack(const void *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t ldd, cudaStream_t st)
+{
+    const int64_t grid = rows < 152 * 8 ? rows : 152 * 8;
+    k_ce_pack<E><<<(unsigned)grid, 256, 0, st>>>(static_cast<const E *>(src), ld, rows, (int)cols,
+                                                 static_cast<E *>(dst), ldd);
+}
+
+// maps of h and W, packed first where their rows need it
+sg_status operand_maps(const Plan &p, const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
+                       int64_t V, uint8_t *work, CUtensorMap *mh, CUtensorMap *mW, cudaStream_t st)
+{
+    auto packed = [&](const void *&src, int64_t &ld, int64_t rows, int64_t at) {
+        if (p.es == 1)
+            pack<uint8_t>(src, ld, rows, H, work + at, p.ldp, st);
+        else
+            pack<uint16_t>(src, ld, rows, H, work + at, p.ldp, st);
+        src = work + at;
+        ld = p.ldp;
+    };
+    if (p.pack_h)
+        packed(h, ldh, T, p.o_h);
+    if (p.pack_W)
+        packed(W, ldw, V, p.o_W);
+    SG_TRY_CUDA(cudaGetLastError());
+    CE_TRY(map_of(mh, h, H, T, ldh, p.es, 64, "h"));
+    return map_of(mW, W, H, V, ldw, p.es, 64, "W");
+}
+
+}  // namespace
+
+extern "C" {
+
+sg_status sg_softmax_ce_work(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
+                             int32_t dtype, int32_t backward, int64_t *bytes)
+{
+    const char *fn = "sg_softmax_ce_work";
+    if (!bytes)
+        CE_FAIL(SG_ERR_INVALID, "%s: bytes is NULL", fn);
+    CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, backward != 0));
+    Plan p;
+    if (T > 0)
+        make_plan(h, ldh, T, H, W, ldw, V, dtype, backward != 0, &p);
+    *bytes = p.bytes;
+    return SG_OK;
+}
+
+sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, int64_t T, int64_t H, const void *W,
+                            int64_t ldw, const float *W_scale, int64_t V, int32_t dtype, const int32_t *targets,
+                            int32_t ignore_index, double smoothing, float *loss, float *lse, void *work,
+                            int64_t work_bytes, int32_t *status, void *stream)
+{
+    const char *fn = "sg_softmax_ce_fwd";
+    NvtxRange nvtx_(fn);
+    CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, false));
+    if (!W || (T && (!h || !targets || !loss || !lse)))
+        CE_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
+    if ((h_scale || W_scale) && dtype != SG_E4M3)
+        CE_FAIL(SG_ERR_INVALID, "%s: scales go with SG_E4M3 rows only", fn);
+    if (!(smoothing >= 0.0 && smoothing <= 1.0))
+        CE_FAIL(SG_ERR_INVALID, "%s: smoothing=%g is outside [0, 1]", fn, smoothing);
+    if (T == 0)
+        return SG_OK;
+    Plan p;
+    make_plan(h, ldh, T, H, W, ldw, V, dtype, false, &p);
+    if (!work || work_bytes < p.bytes || ((uintptr_t)work & 255) != 0)
+        CE_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_softmax_ce_work), aligned to 256", fn,
+                (long long)p.bytes);
+    cudaStream_t st = (cudaStream_t)stream;
+    uint8_t *w8 = static_cast<uint8_t *>(work);
+    CUtensorMap mh, mW;
+    CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, st));
+    CeArgs a = {};
+    a.T = (int32_t)T;
+    a.V = (int32_t)V;
+    a.H = (int32_t)H;
+    a.nm = (int32_t)p.nm;
+    a.nn = (int32_t)ceil_div(V, kBN);
+    a.nk = (int32_t)ceil_div(H * p.es, 128);
+    a.f16 = dtype == SG_F16;
+    a.h_scale = h_scale;
+    a.W_scale = W_scale;
+    a.targets = targets;
+    a.ignore = ignore_index;
+    a.part = reinterpret_cast<float2 *>(w8 + p.o_part);
+    a.zsum = smoothing > 0 ? reinterpret_cast<float *>(w8 + p.o_zsum) : nullptr;
+    a.ztgt = reinterpret_cast<float *>(w8 + p.o_ztgt);
+    a.Tp = (int32_t)p.Tp;
+    a.status = status;
+    if (dtype == SG_E4M3)
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, a, st))
+                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, a, st)));
+    else
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, a, st))
+                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, a, st)));
+    k_ce_join<<<(unsigned)ceil_div(T, 32), 1024, 0, st>>>(a.part, a.zsum, a.ztgt, (int)p.slots, (int)p.Tp, (int)T,
+                                                          (int)V, targets, ignore_index, (float)smoothing, loss, lse,
+                                                          status);
+    SG_TRY_CUDA(cudaGetLastError());
+    return SG_OK;
+}
+
+sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
+                            int32_t dtype, const int32_t *targets, int32_t ignore_index, double smoothing,
+                            const float *lse, const float *dloss, void *dh, int64_t lddh, void *dW, int64_t lddw,
+                            void *work, int64_t work_bytes, int32_t *status, void *stream)
+{
+    const char *fn = "sg_softmax_ce_bwd";
+    NvtxRange nvtx_(fn);
+    CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, true));
+    if (!W || (T && (!h || !targets || !lse || !dloss)) || (!dh && !dW))
+        CE_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
+    if (!(smoothing >= 0.0 && smoothing <= 1.0))
+        CE_FAIL(SG_ERR_INVALID, "%s: smoothing=%g is outside [0, 1]", fn, smoothing);
+    if ((dh && (lddh < H || (uintptr_t)dh % 2 != 0)) || (dW && (lddw < H || (uintptr_t)dW % 2 != 0)))
+        CE_FAIL(SG_ERR_INVALID, "%s: dh or dW has a row stride below H or is not aligned to its elements", fn);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {
+        if (dW)
+            SG_TRY_CUDA(cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)H * 2, (size_t)V, st));
+        return SG_OK;
+    }
+    Plan p;
+    make_plan(h, ldh, T, H, W, ldw, V, dtype, true, &p);
+    if (!work || work_bytes < p.bytes || ((uintptr_t)work & 255) != 0)
+        CE_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_softmax_ce_work), aligned to 256", fn,
+                (long long)p.bytes);
+    uint8_t *w8 = static_cast<uint8_t *>(work);
+    CUtensorMap mh, mW, mg, mgs, mdW;
+    CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, st));
+    // g: [T][Vc], loaded in boxes of 64 rows, stored in boxes of 32
+    CE_TRY(map_of(&mg, w8 + p.o_g, p.Vc, T, p.Vc, 2, 64, "g"));
+    CE_TRY(map_of(&mgs, w8 + p.o_g, p.Vc, T, p.Vc, 2, 32, "g"));
+    // a TMA store ends on a multiple of 16 bytes: with other widths it would
+    // write past a row's end
+    const bool dw_tma = dW && tma_ok(dW, lddw, 2) && H % 8 == 0;
+    if (dw_tma)
+        CE_TRY(map_of(&mdW, dW, H, V, lddw, 2, 32, "dW"));
+    else
+        mdW = mgs;
+    CeArgs a = {};
+    a.T = (int32_t)T;
+    a.V = (int32_t)V;
+    a.H = (int32_t)H;
+    a.nm = (int32_t)p.nm;
+    a.nk = (int32_t)ceil_div(H, 64);
+    a.f16 = dtype == SG_F16;
+    a.targets = targets;
+    a.ignore = ignore_index;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.smooth = (float)smoothing;
+    a.dh_nn = a.dw_nn = (int32_t)p.dh_nn;
+    a.dh_split = (int32_t)p.split;
+    a.dh_tiles = dh ? (int32_t)p.dh_tiles : 0;
+    a.dw_nk = (int32_t)ceil_div(T, 64);
+    a.acc = reinterpret_cast<float *>(w8 + p.o_acc);
+    a.dW = dW && !dw_tma ? static_cast<uint16_t *>(dW) : nullptr;
+    a.lddW = lddw;
+    a.status = status;
+    if (dtype == SG_F16) {
+        float *gs = reinterpret_cast<float *>(w8 + p.o_gs);
+        k_ce_gscale<<<1, 1024, 0, st>>>(dloss, (int)T, gs);
+        SG_TRY_CUDA(cudaGetLastError());
+        a.gscale = gs;
+        a.ginv = gs + 1;
+    }
+    for (int64_t v0 = 0; v0 < V; v0 += p.Vc) {
+        const int64_t vc = V - v0 < p.Vc ? V - v0 : p.Vc;
+        a.v0 = (int32_t)v0;
+        a.first = v0 == 0;
+        a.nn = (int32_t)ceil_div(vc, kBN);
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kProb, false>(mh, mW, mgs, mdW, a, st))
+                         : (launch_ce<2, kProb, false>(mh, mW, mgs, mdW, a, st)));
+        a.dh_kb = (int32_t)ceil_div(vc, 64);
+        a.dw_tiles = dW ? (int32_t)(ceil_div(vc, p.BM) * p.dh_nn) : 0;
+        // turns of dW tiles so that all clusters end at about the same time
+        const int64_t units = (int64_t)a.dh_tiles * p.split, hi = units % p.C;
+        const int64_t less = dh ? ceil_div(tile_cost(ceil_div(a.dh_kb, p.split)) + 2, tile_cost(a.dw_nk)) : 0;
+        int64_t q_hi = hi ? (a.dw_tiles - less * (p.C - hi)) / p.C : 0;
+        if (q_hi < 0)
+            q_hi = 0;
+        a.dw_hi = (int32_t)q_hi;
+        a.dw_lo = (int32_t)(q_hi + ceil_div(a.dw_tiles - q_hi * p.C > 0 ? a.dw_tiles - q_hi * p.C : 0, p.C - hi));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mh, mW, mg, mdW, a, st))
+                         : (launch_ce<2, kGrad, false>(mh, mW, mg, mdW, a, st)));
+    }
+    if (dh) {
+        const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), kBN / 64);
+        const float4 *acc = reinterpret_cast<const float4 *>(a.acc);
+        if (p.CG == 1)
+            k_ce_dh<1><<<grid, 256, 0, st>>>(acc, (int)p.dh_tiles, (int)p.dh_nn, (int)p.split, (int)T, (int)H, a.ginv,
+                                             a.f16, static_cast<uint16_t *>(dh), lddh);
+        else
+            k_ce_dh<2><<<grid, 256, 0, st>>>(acc, (int)p.dh_tiles, (int)p.dh_nn, (int)p.split, (int)T, (int)H, a.ginv,
+                                             a.f16, static_cast<uint16_t *>(dh), lddh);
+        SG_TRY_CUDA(cudaGetLastError());
+    }
+    return SG_OK;
+}
+
+}  // extern "C"

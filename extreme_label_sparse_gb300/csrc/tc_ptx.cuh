@@ -452,6 +452,103 @@ __device__ __forceinline__ void red_add_v4(float *dst, float a, float b, float c
                  : "memory");
 }
 
+// ------------------------------------------------------------------ CTA pairs
+// tcgen05 operations of one CTA (CG = 1) or of the pair of a 2-CTA cluster
+// (CG = 2).  A pair's MMA is issued by one thread of the rank-0 CTA; its A and
+// B tiles lie half in each CTA's shared memory (at the same addresses) and
+// each CTA's TMEM gets its own 128 rows of D.
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t holder_smem, uint32_t ncols)
+{
+    if constexpr (CG == 1)
+        tmem_alloc(holder_smem, ncols);
+    else
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(holder_smem),
+                     "r"(ncols)
+                     : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_relinquish_cg()
+{
+    if constexpr (CG == 1)
+        tmem_relinquish();
+    else
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols)
+{
+    if constexpr (CG == 1)
+        tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// 16-bit operands (kind::f16, K = 16) or 8-bit floats (kind::f8f6f4, K = 32),
+// fp32 accumulation
+template <int CG, bool F8>
+__device__ __forceinline__ void mma_cg(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+#define SG_MMA_CG(group, kind)                                                                             \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                                  \
+                 "setp.ne.b32 p, %4, 0;\n\t"                                                               \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                                     \
+                 : "memory")
+    if constexpr (CG == 1 && !F8)
+        SG_MMA_CG("1", "f16");
+    else if constexpr (CG == 1)
+        SG_MMA_CG("1", "f8f6f4");
+    else if constexpr (!F8)
+        SG_MMA_CG("2", "f16");
+    else
+        SG_MMA_CG("2", "f8f6f4");
+#undef SG_MMA_CG
+}
+
+// arrive once on `bar` (of both CTAs of a pair, at the same address) when
+// every MMA this thread issued so far has completed
+template <int CG>
+__device__ __forceinline__ void mma_commit_cg(uint32_t bar)
+{
+    if constexpr (CG == 1)
+        mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+// TMA tile load into this CTA's shared memory; with CG = 2 `bar` is the
+// cluster address of a barrier of either CTA of the pair
+template <int CG>
+__device__ __forceinline__ void tma_load_2d_cg(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    if constexpr (CG == 1)
+        tma_load_2d(dst, map, x, y, bar);
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+
+// tile of shared memory -> global memory (parts outside the map are left
+// out), tracked by this thread's bulk groups; x and y are not negative
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     (uint64_t)map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ descriptors
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading
 // and stride byte offsets (16-byte units), version 1, swizzle layout.

@@ -21,6 +21,7 @@ _lib = None
 SG_OK, SG_ERR_INVALID, SG_ERR_UNSUPPORTED, SG_ERR_CUDA = 0, -1, -2, -3
 SG_ERR_OOM, SG_ERR_TIMEOUT, SG_ERR_DATA = -4, -5, -6
 SG_ENGINE_AUTO, SG_ENGINE_SIMT, SG_ENGINE_TC, SG_ENGINE_FUSED = 0, 1, 2, 3
+SG_BF16, SG_F16, SG_F32, SG_E4M3 = 0, 1, 2, 3
 KIND_NAMES = ("prep", "fwd", "bce", "dW", "dh", "step")
 
 
@@ -45,6 +46,7 @@ def load():
                                "extreme_label_sparse_gb300.build() first")
         lib = C.CDLL(str(_LIB_PATH))
         P, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
+        u64, f64 = C.c_uint64, C.c_double
         sig = {
             "sg_layout_build": ([P, i64, i32, P, i32, i32, i32, i64, P, C.POINTER(P)], C.c_int),
             "sg_layout_export": ([P, P, P, P, P], C.c_int),
@@ -81,6 +83,17 @@ def load():
             "sg_proj_bwd": ([P, i32, i32, P, i32, P, P, P, P, i32, P], C.c_int),
             "sg_headtail_step": ([P, P, P, i32, i32, P, P, P, P, P, i64, P, P, P, i64, P, P, P, P, P, P, P],
                                  C.c_int),
+            "sg_dropout": ([P, i64, i64, i64, i32, f64, u64, u64, P, i64, P], C.c_int),
+            "sg_add_rmsnorm_fwd": ([P, i64, P, i64, i64, i64, i32, P, f64, f64, u64, u64, P, i64, P, P, i64, P, i64,
+                                    P, P], C.c_int),
+            "sg_add_rmsnorm_bwd_work": ([i64, i64, C.POINTER(i64)], C.c_int),
+            "sg_add_rmsnorm_bwd": ([P, i64, P, i64, P, i64, i64, i64, i32, P, P, f64, u64, u64, P, i64, P, i64, P, P,
+                                    i64, P], C.c_int),
+            "sg_softmax_ce_work": ([P, i64, i64, i64, P, i64, i64, i32, i32, C.POINTER(i64)], C.c_int),
+            "sg_softmax_ce_fwd": ([P, i64, P, i64, i64, P, i64, P, i64, i32, P, i32, f64, P, P, P, i64, P, P],
+                                  C.c_int),
+            "sg_softmax_ce_bwd": ([P, i64, i64, i64, P, i64, i64, i32, P, i32, f64, P, P, P, i64, P, i64, P, i64, P,
+                                   P], C.c_int),
             "sg_timing_start": ([P, i32], C.c_int),
             "sg_timing_stop": ([P, P, P], C.c_int),
             "sg_last_error": ([], C.c_char_p),
@@ -482,3 +495,169 @@ def sg_rewire(layout: Layout, h, dZ, W, n_drop: int, idx_out, W_out):
                             _dev(W, "W", _BF16, layout.L * layout.F), int(n_drop),
                             _dev(idx_out, "idx_out", _I32, layout.K * layout.F),
                             _dev(W_out, "W_out", _BF16, layout.L * layout.F), _stream(h.device)))
+
+
+# ---------------------------------------------------------------- around the layer
+_DTYPE = {torch.bfloat16: SG_BF16, torch.float16: SG_F16, torch.float32: SG_F32, torch.float8_e4m3fn: SG_E4M3}
+_F32 = (torch.float32,)
+
+
+def _mat(t, name: str, shape, dtypes, device):
+    """(pointer, row stride) of a [rows, cols] matrix on `device` whose rows
+    are contiguous; (NULL, cols) for None."""
+    if t is None:
+        return None, shape[1]
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rs, cs = t.stride()
+    if cs != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rs < shape[1]:
+        if shape[0] > 1:
+            raise ValueError(f"the rows of {name} overlap")
+        rs = shape[1]
+    return t.data_ptr(), rs
+
+
+def _vec(t, name: str, n: int, dtypes, device):
+    """Pointer of a contiguous vector of n elements on `device` (None: NULL)."""
+    if t is None:
+        return None
+    p = _dev(t, name, dtypes, n)
+    if t.device != device:
+        raise ValueError(f"{name} must be on the device of the others")
+    return p
+
+
+def _rows_of(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return tuple(t.shape), t.device, (t.dtype,)
+
+
+def _call(fn, device, *args):
+    """One library call on the current stream of `device`, which is made the
+    current device for it."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)))
+
+
+def sg_dropout(x: torch.Tensor, p: float, seed: int, offset: int, y: torch.Tensor):
+    """y = dropout(x) with the mask of (seed, offset) (see sg.h); the backward
+    pass is the same call on the gradient.  y may be x."""
+    shape, dev, dt = _rows_of(x, "x")
+    xp, ldx = _mat(x, "x", shape, tuple(_DTYPE), dev)
+    yp, ldy = _mat(y, "y", shape, dt, dev)
+    _call(load().sg_dropout, dev, xp, ldx, shape[0], shape[1], _DTYPE[dt[0]], p, seed, offset, yp, ldy)
+
+
+def sg_add_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None, u=None, rstd=None, y=None,
+                       y8=None, y8_scale=None, drop_p: float = 0.0, seed: int = 0, offset: int = 0):
+    """u = residual + dropout(x), y = u / rms(u) * weight; y8 with y8_scale
+    hold y in 8 bits with a scale for each row.  Outputs that are None are not
+    written (see sg.h)."""
+    shape, dev, dt = _rows_of(x, "x")
+    xp, ldx = _mat(x, "x", shape, tuple(_DTYPE), dev)
+    rp, ldr = _mat(residual, "residual", shape, dt, dev)
+    up, ldu = _mat(u, "u", shape, dt, dev)
+    yp, ldy = _mat(y, "y", shape, dt, dev)
+    qp, ldq = _mat(y8, "y8", shape, (torch.float8_e4m3fn,), dev)
+    _call(load().sg_add_rmsnorm_fwd, dev, xp, ldx, rp, ldr, shape[0], shape[1], _DTYPE[dt[0]],
+          _vec(weight, "weight", shape[1], dt, dev), eps, drop_p, seed, offset, up, ldu,
+          _vec(rstd, "rstd", shape[0], _F32, dev), yp, ldy, qp, ldq, _vec(y8_scale, "y8_scale", shape[0], _F32, dev))
+
+
+def sg_add_rmsnorm_bwd(dy: torch.Tensor, u: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, du, dweight=None,
+                       du_in=None, dx=None, drop_p: float = 0.0, seed: int = 0, offset: int = 0, work=None):
+    """Gradient of sg_add_rmsnorm_fwd (see sg.h).  work: a uint8 tensor of
+    sg_add_rmsnorm_bwd_work bytes; one is taken from torch's allocator if it is
+    None."""
+    shape, dev, dt = _rows_of(dy, "dy")
+    gp, ldg = _mat(dy, "dy", shape, tuple(_DTYPE), dev)
+    up, ldu = _mat(u, "u", shape, dt, dev)
+    ip, ldi = _mat(du_in, "du_in", shape, dt, dev)
+    op, ldo = _mat(du, "du", shape, dt, dev)
+    xp, ldx = _mat(dx, "dx", shape, dt, dev)
+    if dweight is not None and work is None:
+        work = torch.empty(sg_add_rmsnorm_bwd_work(*shape), dtype=torch.uint8, device=dev)
+    _call(load().sg_add_rmsnorm_bwd, dev, gp, ldg, up, ldu, ip, ldi, shape[0], shape[1], _DTYPE[dt[0]],
+          _vec(weight, "weight", shape[1], dt, dev), _vec(rstd, "rstd", shape[0], _F32, dev), drop_p, seed, offset,
+          op, ldo, xp, ldx, _vec(dweight, "dweight", shape[1], _F32, dev),
+          _vec(work, "work", None, (torch.uint8,), dev), 0 if work is None else work.numel())
+
+
+def sg_add_rmsnorm_bwd_work(rows: int, cols: int) -> int:
+    """Bytes of work memory that sg_add_rmsnorm_bwd needs for dweight."""
+    n = C.c_int64(0)
+    _check(load().sg_add_rmsnorm_bwd_work(rows, cols, C.byref(n)))
+    return int(n.value)
+
+
+_16BIT = (torch.bfloat16, torch.float16)
+
+
+def _head(h, W, dtypes):
+    """(h pointer, ldh, T, H, W pointer, ldw, V, dtype) of a dense head."""
+    (T, H), dev, dt = _rows_of(h, "h")
+    (V, _), _, _ = _rows_of(W, "W")
+    hp, ldh = _mat(h, "h", (T, H), dtypes, dev)
+    wp, ldw = _mat(W, "W", (V, H), dt, dev)
+    return hp, ldh, T, H, wp, ldw, V, _DTYPE[dt[0]]
+
+
+def _ce_work(head, backward: int) -> int:
+    n = C.c_int64(0)
+    _check(load().sg_softmax_ce_work(*head, backward, C.byref(n)))
+    return n.value
+
+
+def sg_softmax_ce_work(h: torch.Tensor, W: torch.Tensor, backward: bool) -> int:
+    """Bytes of work memory that sg_softmax_ce_fwd or sg_softmax_ce_bwd needs
+    for this h and W."""
+    return _ce_work(_head(h, W, tuple(_DTYPE)), int(bool(backward)))
+
+
+def sg_softmax_ce_fwd(h: torch.Tensor, W: torch.Tensor, targets, loss, lse, h_scale=None, W_scale=None,
+                      ignore_index: int = -100, smoothing: float = 0.0, work=None, status=None):
+    """loss[T] and lse[T] of the dense head with logits h W^T (see sg.h); with
+    float8_e4m3fn rows, h_scale[T] and W_scale[V] are their scales.  work: a
+    uint8 tensor of sg_softmax_ce_work bytes; one is taken from torch's
+    allocator if it is None.  status: an int32 tensor of one element."""
+    head = _head(h, W, _16BIT + (torch.float8_e4m3fn,))
+    hp, ldh, T, H, wp, ldw, V, dt = head
+    dev = h.device
+    if work is None:
+        work = torch.empty(_ce_work(head, 0), dtype=torch.uint8, device=dev)
+    _call(load().sg_softmax_ce_fwd, dev, hp, ldh, _vec(h_scale, "h_scale", T, _F32, dev), T, H, wp, ldw,
+          _vec(W_scale, "W_scale", V, _F32, dev), V, dt, _vec(targets, "targets", T, _I32, dev), ignore_index,
+          smoothing, _vec(loss, "loss", T, _F32, dev), _vec(lse, "lse", T, _F32, dev),
+          _vec(work, "work", None, (torch.uint8,), dev), work.numel(), _vec(status, "status", 1, _I32, dev))
+
+
+def sg_softmax_ce_bwd(h: torch.Tensor, W: torch.Tensor, targets, lse, dloss, dh=None, dW=None,
+                      ignore_index: int = -100, smoothing: float = 0.0, work=None, status=None):
+    """dh and dW (either may be None) from dloss[T] and the lse that
+    sg_softmax_ce_fwd wrote for the same h and W (see sg.h); work and status as
+    there."""
+    head = _head(h, W, _16BIT)
+    hp, ldh, T, H, wp, ldw, V, dt = head
+    dev = h.device
+    dhp, lddh = _mat(dh, "dh", (T, H), (h.dtype,), dev)
+    dwp, lddw = _mat(dW, "dW", (V, H), (h.dtype,), dev)
+    if work is None:
+        work = torch.empty(_ce_work(head, 1), dtype=torch.uint8, device=dev)
+    _call(load().sg_softmax_ce_bwd, dev, hp, ldh, T, H, wp, ldw, V, dt, _vec(targets, "targets", T, _I32, dev),
+          ignore_index, smoothing, _vec(lse, "lse", T, _F32, dev), _vec(dloss, "dloss", T, _F32, dev), dhp, lddh,
+          dwp, lddw, _vec(work, "work", None, (torch.uint8,), dev), work.numel(),
+          _vec(status, "status", 1, _I32, dev))

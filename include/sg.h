@@ -387,6 +387,111 @@ SG_API sg_status sg_grouping_groups(sg_grouping *g, int32_t *groups, int32_t *cl
 SG_API sg_status sg_grouping_export(sg_grouping *g, sg_bf16 *E, uint8_t *has, float *centroids, int64_t *counts,
                                     void *stream);
 
+/* ---------------------------------------------------------------- around the layer
+ * Operators next to the output layer: what turns an encoder's last block into
+ * h, and a dense softmax head over a large label set.  The paper has no
+ * counterpart; they let a training or serving program go from the block's
+ * output to the loss and back without leaving the library.
+ *
+ * Conventions: element types are sg_dtype values; a matrix is row-major with
+ * its row stride in elements (ld >= columns, so it may be a slice of a wider
+ * one); any alignment to the element is accepted, and rows that start on 16
+ * bytes are read and written faster.  Work memory is device memory of the
+ * caller, of the size that the _work call gives; its contents need not survive
+ * between calls, and calls that overlap on the GPU need one each.  Nothing is
+ * allocated, no call waits for the device, and all of them can be captured
+ * into a graph. */
+typedef enum sg_dtype {
+    SG_BF16 = 0,
+    SG_F16 = 1,
+    SG_F32 = 2,
+    SG_E4M3 = 3 /* 8-bit floats: 4 exponent and 3 fraction bits, largest 448 */
+} sg_dtype;
+
+/* sg_dropout -- y = x with elements set to zero with probability p and the
+ * others divided by the probability to stay.  The mask is a function of
+ * (seed, offset, row, column) and is never stored: the backward pass is the
+ * same call on the gradient.  Element (r, c) has 16 random bits, half-word
+ * c % 8 (the low half of a word first) of Philox4x32-10 at the counter
+ * (c / 8, r, offset low, offset high) under the key (seed low, seed high); it
+ * stays when they are >= t = round(65536 p), and is multiplied in fp32 by
+ * 65536 / (65536 - t).  p is thus rounded to a multiple of 2^-16; a dropped
+ * element is zero whatever x holds.  Take another offset for each layer and
+ * step.  dtype: SG_BF16, SG_F16 or SG_F32.  y may be x. */
+SG_API sg_status sg_dropout(const void *x, int64_t ldx, int64_t rows, int64_t cols, int32_t dtype, double p,
+                            uint64_t seed, uint64_t offset, void *y, int64_t ldy, void *stream);
+
+/* sg_add_rmsnorm_fwd -- the residual's addition and RMS norm of each row:
+ *   u = round(residual + drop(x)),  rstd = 1 / sqrt(mean(u^2) + eps),
+ *   y = u rstd weight,
+ * drop being sg_dropout with drop_p (0: x as it is) kept in fp32, and u
+ * rounded to dtype before the norm is taken of it.  Outputs, each where its
+ * pointer is given: u (the next residual, and what the backward pass reads),
+ * rstd[rows], y rounded to dtype, and y8[rows][cols] with y8_scale[rows]: y in
+ * 8 bits (SG_E4M3), y = y8 * y8_scale with y8_scale = max |y| / 448 of the row
+ * (0 for a row of zeros).  One of y and y8 is needed.  residual NULL: u =
+ * drop(x).  weight[cols] has dtype.  u may be x or residual, and y any of
+ * them.  cols <= 32768. */
+SG_API sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows,
+                                    int64_t cols, int32_t dtype, const void *weight, double eps, double drop_p,
+                                    uint64_t seed, uint64_t offset, void *u, int64_t ldu, float *rstd, void *y,
+                                    int64_t ldy, uint8_t *y8, int64_t ldy8, float *y8_scale, void *stream);
+
+/* sg_add_rmsnorm_bwd -- its gradient, from dy, u and rstd:
+ *   g = dy weight,  n = u rstd,  du = rstd (g - n mean(g n)) + du_in,
+ *   dx = drop'(du) (the same mask and factor as the forward call's),
+ *   dweight[c] = sum over rows of dy n  (fp32, in an order that is always the
+ *   same for the same sizes).
+ * du_in (may be NULL) is the gradient that reaches u by its other way, the
+ * residual; du is the gradient of residual, and of x where drop_p = 0.  dx and
+ * dweight may be NULL.  du may be dy or du_in, and dx any of them.  work (only
+ * for dweight) is aligned to 4 bytes. */
+SG_API sg_status sg_add_rmsnorm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes);
+SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_t ldu, const void *du_in,
+                                    int64_t lddu_in, int64_t rows, int64_t cols, int32_t dtype, const void *weight,
+                                    const float *rstd, double drop_p, uint64_t seed, uint64_t offset, void *du,
+                                    int64_t lddu, void *dx, int64_t lddx, float *dweight, void *work,
+                                    int64_t work_bytes, void *stream);
+
+/* sg_softmax_ce_fwd, sg_softmax_ce_bwd -- softmax cross entropy of a dense
+ * head over V labels, without its logits in memory:
+ *   z[t][v] = < h_t, W_v >          (SG_E4M3: times h_scale[t] W_scale[v])
+ *   lse[t]  = log sum_v exp z[t][v]
+ *   loss[t] = lse[t] - (1 - e) z[t][y_t] - e mean_v z[t][v],   e = smoothing
+ * and, from dloss[t] = dL / d loss[t],
+ *   g[t][v] = dloss[t] (exp(z[t][v] - lse[t]) - (1 - e) [v = y_t] - e / V)
+ *   dh[t] = sum_v g[t][v] W_v,      dW[v] = sum_t g[t][v] h_t.
+ *   h[T][H] and W[V][H] in dtype (SG_BF16, SG_F16; sg_softmax_ce_fwd also
+ *   SG_E4M3, with a scale for each row of h and of W, NULL: 1).
+ *   targets[T] int32: y_t in [0, V); a row with ignore_index has loss 0 and no
+ *   gradient (its lse is still written).  Any other value counts as
+ *   ignore_index and sets *status to SG_ERR_DATA.
+ *   loss[T], lse[T], dloss[T] fp32; dh[T][H], dW[V][H] in dtype, one of them
+ *   may be NULL.  lse is what sg_softmax_ce_fwd wrote for the same h and W.
+ * fp32 accumulation, sums and statistics in fp32.  g enters the products of dh
+ * and dW in dtype (SG_F16: times a power of two that keeps it in range).  The
+ * results are the same bits for the same call.  Rows of h or W that do not
+ * start on 16 bytes are first copied into the work memory.
+ * status (device int32, may be NULL): sticky, first error wins, SG_ERR_TIMEOUT
+ * where a bounded wait gave up and the outputs are not complete; the caller
+ * clears it.  T <= 2^24, H <= 2^20, V <= 2^30.
+ * Errors: SG_ERR_INVALID for NULL pointers, sizes below 1 (T below 0), row
+ * strides below H, smoothing outside [0, 1], work memory that is too small or
+ * not aligned to 256 bytes.  sg_softmax_ce_work wants the same h, W and strides
+ * as the call (it looks at the alignment of their rows); backward: 0 for
+ * sg_softmax_ce_fwd, 1 for sg_softmax_ce_bwd. */
+SG_API sg_status sg_softmax_ce_work(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
+                                    int64_t V, int32_t dtype, int32_t backward, int64_t *bytes);
+SG_API sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, int64_t T, int64_t H,
+                                   const void *W, int64_t ldw, const float *W_scale, int64_t V, int32_t dtype,
+                                   const int32_t *targets, int32_t ignore_index, double smoothing, float *loss,
+                                   float *lse, void *work, int64_t work_bytes, int32_t *status, void *stream);
+SG_API sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
+                                   int64_t V, int32_t dtype, const int32_t *targets, int32_t ignore_index,
+                                   double smoothing, const float *lse, const float *dloss, void *dh, int64_t lddh,
+                                   void *dW, int64_t lddw, void *work, int64_t work_bytes, int32_t *status,
+                                   void *stream);
+
 /* ---------------------------------------------------------------- timing
  * Per-kernel device timing for benchmarks: while enabled, every kernel the
  * library launches for this layout is bracketed by a pair of CUDA events

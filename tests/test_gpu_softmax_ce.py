@@ -1,0 +1,310 @@
+"""Softmax cross entropy of a dense head against its 64-bit restatement.
+
+Tolerances.  A logit is a sum of H products, exact in fp32, added in fp32 in
+steps of 16 or more: (H / 16 + 4) 2^-23 of its terms' absolute sum.  lse moves
+by no more than the largest logit error, loss by twice that; the exponentials,
+their sum and the logarithm add 1e-5 (1e-6 of a loss of a few units, several
+times).  g, the sum of three parts that may cancel, is off by (2 e_z + 3e-5) of
+its parts' absolute values and rounded to dtype (u = 2^-8 for bf16, 2^-11 for
+f16, half a unit in the last place): an element of dh and dW is off by u of its
+terms' absolute sum, by (2 e_z + 3e-5) of the sum with g's parts in its place,
+and by u from its own rounding, and by what the types cannot hold (half of
+f16's smallest step; an exponential below fp32's 2^-126 is taken as zero, times
+features below 2^6).
+Roundings that are independent of one another make less of it: over
+a whole matrix, whose two roundings have a root mean square of at most
+u / sqrt(3) each, the 2-norm of the error is below u of the 2-norm, plus the
+other parts of the bound.
+"""
+import numpy as np
+import pytest
+import torch
+
+import extreme_label_sparse_gb300 as sg
+from oracle.softmax_ce import softmax_ce
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+LEAST = {"bf16": 2.0 ** -120, "f16": 2.0 ** -25}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    sg.build()
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def rand(rows, cols, dtype, seed, std=1.0, pad=0, shift=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randn((rows, cols + pad + shift), generator=g, device="cuda") * std
+    return x.to(TYPES[dtype])[:, shift:shift + cols]
+
+
+def draw_targets(T, V, seed, ignored=0.1):
+    r = np.random.RandomState(seed)
+    y = r.randint(0, V, T)
+    y[r.rand(T) < ignored] = -100
+    return torch.tensor(y, dtype=torch.int32, device="cuda")
+
+
+def logit_error(h, W):
+    """Bound on a logit's error, row by row."""
+    H = h.shape[1]
+    return (H / 16 + 4) * 2.0 ** -23 * (np.abs(h) @ np.abs(W).T).max(1)
+
+
+def check(h, W, y, dloss, dtype, smoothing=0.0, ignore=-100, want_dh=True, want_dW=True, dW_out=None, status=None):
+    (T, H), V = h.shape, W.shape[0]
+    loss, lse = torch.full((T,), 9.0, device="cuda"), torch.full((T,), 9.0, device="cuda")
+    dh = torch.full((T, H), 9.0, dtype=h.dtype, device="cuda") if want_dh else None
+    dW = (torch.full((V, H), 9.0, dtype=h.dtype, device="cuda") if dW_out is None else dW_out) if want_dW else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(ignore_index=ignore, smoothing=smoothing, status=st)
+    sg.sg_softmax_ce_fwd(h, W, y, loss, lse, **kw)
+    sg.sg_softmax_ce_bwd(h, W, y, lse, dloss, dh, dW, **kw)
+    ref = softmax_ce(f64(h), f64(W), y.cpu().numpy(), f64(dloss), ignore, smoothing)
+    e = logit_error(f64(h), f64(W))
+    assert int(st) == (0 if status is None else status)
+    assert np.all(np.abs(f64(lse) - ref["lse"]) <= e + 1e-5)
+    assert np.all(np.abs(f64(loss) - ref["loss"]) <= 2 * e + 1e-5)
+    u = U[dtype]
+    for name, got in (("dh", dh), ("dW", dW)):
+        if got is None:
+            continue
+        got, want, terms, mag = f64(got), ref[name], ref[name + "_abs"], ref[name + "_mag"]
+        assert np.all(np.isfinite(got))
+        err = np.abs(got - want)
+        bound = u * terms + (2 * e.max() + 3e-5) * mag + u * np.abs(want) + LEAST[dtype] * (1 + 2.0 ** -14)
+        assert np.all(err <= bound), (name, (err - bound).max(), np.unravel_index((err - bound).argmax(), err.shape))
+        if dtype == "bf16" or np.sqrt(np.mean(want ** 2)) > 2.0 ** -10:  # f16: above its subnormal range
+            rest = (2 * e.max() + 3e-5) * np.linalg.norm(mag)
+            assert np.linalg.norm(err) <= u * np.linalg.norm(want) + rest, (name, np.linalg.norm(err))
+    return loss, lse, dh, dW
+
+
+SIZES = [(1, 8, 1), (1, 64, 300), (2, 72, 255), (5, 768, 256), (31, 64, 257), (64, 128, 20000), (127, 256, 1000),
+         (128, 768, 4096), (129, 64, 1000), (130, 1032, 777), (256, 320, 5003), (300, 768, 2500), (1025, 128, 1300)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", SIZES, ids=str)
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+def test_against_64_bits(size, dtype, smoothing):
+    T, H, V = size
+    h, W = rand(T, H, dtype, 1), rand(V, H, dtype, 2, 2.0 / np.sqrt(H))
+    dloss = torch.rand(T, device="cuda") + 0.5
+    check(h, W, draw_targets(T, V, 3), dloss, dtype, smoothing)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", [(1, 1, 5), (3, 7, 300), (50, 100, 1000), (140, 1001, 700), (200, 333, 1025),
+                                  (130, 1005, 600), (20, 333, 600)], ids=str)
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 1), (3, 0)])
+def test_odd_widths_strides_and_alignment(size, dtype, pad, shift):
+    T, H, V = size
+    h, W = rand(T, H, dtype, 1, 1.0, pad, shift), rand(V, H, dtype, 2, 2.0 / np.sqrt(H), pad, 0)
+    out = torch.full((V + 2, H + 3), 5.0, dtype=h.dtype, device="cuda")
+    check(h, W, draw_targets(T, V, 3), torch.ones(T, device="cuda"), dtype, 0.0, dW_out=out[1:V + 1, :H])
+    assert bool((out[0] == 5).all()) and bool((out[V + 1] == 5).all()) and bool((out[:, H:] == 5).all())
+
+
+@pytest.mark.parametrize("size", [(4096, 64, 70000), (4500, 72, 1000), (2100, 520, 66000)], ids=str)
+def test_pieces_of_the_vocabulary_and_bands_of_rows(size):
+    """More than one piece (256 MB of g hold 32768 labels of 4096 rows), more
+    than one band of 4096 rows."""
+    T, H, V = size
+    h, W = rand(T, H, "bf16", 1), rand(V, H, "bf16", 2, 3.0 / np.sqrt(H))
+    check(h, W, draw_targets(T, V, 3), torch.full((T,), 1.0 / T, device="cuda"), "bf16", 0.1)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T", [40, 200])
+def test_ignored_rows_and_small_weights(dtype, T):
+    """Rows without a target have no loss and no gradient; dloss of 1e-7 is
+    below what fp16 holds times a probability."""
+    h, W = rand(T, 128, dtype, 1), rand(900, 128, dtype, 2, 0.2)
+    y = draw_targets(T, 900, 3, 0.5)
+    dloss = torch.rand(T, device="cuda") * 1e-7
+    loss, lse, dh, dW = check(h, W, y, dloss, dtype)
+    assert not loss[y == -100].any() and not dh[y == -100].any() and bool((lse != 9).all())
+    y[:] = -100
+    loss, _, dh, dW = check(h, W, y, dloss, dtype)
+    assert not loss.any() and not dh.any() and not dW.any()
+    # another ignore_index, one of the labels
+    y = draw_targets(T, 900, 3, 0.0)
+    loss, _, dh, _ = check(h, W, y, dloss, dtype, ignore=int(y[0]))
+    assert not loss[y == y[0]].any() and not dh[y == y[0]].any()
+
+
+def test_targets_that_are_no_labels():
+    T, V = 20, 500
+    h, W = rand(T, 64, "bf16", 1), rand(V, 64, "bf16", 2, 0.25)
+    for bad in (-1, V, 2 ** 31 - 1, -2 ** 31):
+        y = draw_targets(T, V, 3)
+        y[7] = bad
+        loss, _, dh, _ = check(h, W, y, torch.ones(T, device="cuda"), "bf16", status=sg.SG_ERR_DATA)
+        assert float(loss[7]) == 0 and not dh[7].any()
+
+
+def test_large_logits_and_values_that_are_not_numbers():
+    """Logits of hundreds (exp overflows), a row with an infinity, a row with a
+    NaN: the other rows do not see them."""
+    h, W = rand(40, 64, "bf16", 1, 8.0), rand(1000, 64, "bf16", 2, 8.0)
+    y = draw_targets(40, 1000, 3, 0.0)
+    one = torch.ones(40, device="cuda")
+    check(h, W, y, one, "bf16")
+    h2 = h.clone()
+    h2[3, 5], h2[9, 0] = float("inf"), float("nan")
+    a, b = ([torch.empty(40, device="cuda") for _ in range(2)] for _ in range(2))
+    sg.sg_softmax_ce_fwd(h, W, y, *a)
+    sg.sg_softmax_ce_fwd(h2, W, y, *b)
+    keep = torch.ones(40, dtype=torch.bool, device="cuda")
+    keep[3] = keep[9] = False
+    assert torch.equal(a[0][keep], b[0][keep]) and torch.equal(a[1][keep], b[1][keep])
+    assert torch.isnan(b[1][9]) and not torch.isfinite(b[1][3])
+    dh, dh2 = torch.empty_like(h), torch.empty_like(h)
+    sg.sg_softmax_ce_bwd(h, W, y, a[1], one, dh)
+    sg.sg_softmax_ce_bwd(h2, W, y, b[1], one, dh2)
+    assert torch.equal(dh[keep], dh2[keep])
+    # an ignored row's values reach no gradient of W that is not 0 x infinity
+    y[3] = y[9] = -100
+    z = h2.clone()
+    z[3], z[9] = 1e30, -1e30
+    dW, dW0 = torch.empty_like(W), torch.empty_like(W)
+    sg.sg_softmax_ce_bwd(z, W, y, a[1], one, None, dW)
+    sg.sg_softmax_ce_bwd(h, W, y, a[1], one, None, dW0)
+    assert torch.equal(dW, dW0)
+
+
+@pytest.mark.parametrize("size", [(1, 16, 10), (1, 768, 32000), (48, 2048, 3001), (77, 100, 999), (200, 1000, 5000)],
+                         ids=str)
+@pytest.mark.parametrize("smoothing", [0.0, 0.2])
+def test_8_bit_rows(size, smoothing):
+    T, H, V = size
+    e4m3 = torch.float8_e4m3fn
+
+    def rows8(x):
+        top = x.abs().amax(1).clamp_min(1e-20)
+        return (x * (448 / top)[:, None]).to(e4m3), top / 448
+
+    h, hs = rows8(rand(T, H, "bf16", 1).float())
+    W, Ws = rows8(rand(V, H, "bf16", 2, 2.0 / np.sqrt(H)).float())
+    if T > 1:
+        hs[1] = 0  # a row of zeros
+    y = draw_targets(T, V, 3)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    for use_h, use_W in ((True, True), (False, True), (True, False)):
+        # without its scales the rows are taken as they are: small ones
+        hh = h if use_h else (h.float() / 512).to(e4m3)
+        WW = W if use_W else (W.float() / 512).to(e4m3)
+        sg.sg_softmax_ce_fwd(hh, WW, y, loss, lse, h_scale=hs if use_h else None, W_scale=Ws if use_W else None,
+                             smoothing=smoothing)
+        h6 = f64(hh) * (f64(hs)[:, None] if use_h else 1)
+        W6 = f64(WW) * (f64(Ws)[:, None] if use_W else 1)
+        ref = softmax_ce(h6, W6, y.cpu().numpy(), smoothing=smoothing)
+        e = logit_error(h6, W6)
+        assert np.all(np.abs(f64(lse) - ref["lse"]) <= e + 1e-5)
+        assert np.all(np.abs(f64(loss) - ref["loss"]) <= 2 * e + 1e-5)
+
+
+def test_gradient_against_differences():
+    """Along a direction, against central differences of the 64-bit loss: each
+    gradient element is off by at most 2^-9 of its absolute terms (two
+    roundings to f16), so the sum by 2^-9 of theirs."""
+    T, H, V, step = 33, 72, 700, 1e-6
+    h, W = rand(T, H, "f16", 1), rand(V, H, "f16", 2, 0.3)
+    y, c = draw_targets(T, V, 3), torch.rand(T, device="cuda")
+    _, _, dh, dW = check(h, W, y, c, "f16", 0.1)
+    r, at = np.random.RandomState(4), [f64(h), f64(W)]
+    ref = softmax_ce(*at, y.cpu().numpy(), f64(c), smoothing=0.1)
+    for k, (got, terms) in enumerate(((dh, ref["dh_abs"]), (dW, ref["dW_abs"]))):
+        d = r.randn(*at[k].shape)
+        lo, hi = list(at), list(at)
+        lo[k], hi[k] = at[k] - step * d, at[k] + step * d
+        diff = sum(s * (softmax_ce(*a, y.cpu().numpy(), smoothing=0.1)["loss"] * f64(c)).sum()
+                   for s, a in ((1, hi), (-1, lo))) / (2 * step)
+        assert abs((f64(got) * d).sum() - diff) <= 2.0 ** -9 * (terms * np.abs(d)).sum()
+
+
+def test_parts_of_the_gradient_and_the_same_bits_twice():
+    for T in (60, 260):
+        h, W = rand(T, 200, "bf16", 1), rand(3000, 200, "bf16", 2, 0.2)
+        y, c = draw_targets(T, 3000, 3), torch.rand(T, device="cuda")
+        a = check(h, W, y, c, "bf16")
+        b = check(h, W, y, c, "bf16")
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        only = check(h, W, y, c, "bf16", want_dW=False)
+        assert np.abs(f64(only[2]) - f64(a[2])).max() <= 2.0 ** -7 * np.abs(f64(a[2])).max()
+        assert torch.equal(check(h, W, y, c, "bf16", want_dh=False)[3], a[3])
+
+
+def test_no_rows_another_stream_and_a_graph():
+    W = rand(300, 64, "bf16", 2)
+    e, n = torch.empty((0, 64), dtype=W.dtype, device="cuda"), torch.empty(0, device="cuda")
+    dW = torch.full_like(W, 4.0)
+    sg.sg_softmax_ce_fwd(e, W, n.int(), n, n.clone())
+    sg.sg_softmax_ce_bwd(e, W, n.int(), n, n, e, dW)
+    assert not dW.any()
+    T = 150
+    h, y = rand(T, 64, "bf16", 1), draw_targets(T, 300, 3)
+    loss, lse, dh, dW = check(h, W, y, torch.ones(T, device="cuda"), "bf16")
+    out = [torch.empty_like(t) for t in (loss, lse, dh, dW)]
+    one = torch.ones(T, device="cuda")
+    work = torch.empty(max(sg.sg_softmax_ce_work(h, W, b) for b in (False, True)), dtype=torch.uint8, device="cuda")
+
+    def step():
+        sg.sg_softmax_ce_fwd(h, W, y, out[0], out[1], work=work)
+        sg.sg_softmax_ce_bwd(h, W, y, out[1], one, out[2], out[3], work=work)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step()
+    st.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(out, (loss, lse, dh, dW)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for t in out:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(out, (loss, lse, dh, dW)))
+
+
+def test_refusals():
+    h, W = rand(4, 64, "bf16", 1), rand(10, 64, "bf16", 2)
+    y, v = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+    for s in (-0.1, 1.5, float("nan")):
+        with pytest.raises(sg.SGError) as e:
+            sg.sg_softmax_ce_fwd(h, W, y, v, v.clone(), smoothing=s)
+        assert e.value.status == sg.SG_ERR_INVALID
+    with pytest.raises(sg.SGError):  # scales without 8-bit rows
+        sg.sg_softmax_ce_fwd(h, W, y, v, v.clone(), h_scale=v)
+    with pytest.raises(sg.SGError):
+        sg.sg_softmax_ce_bwd(h, W, y, v, v)  # no gradient asked for
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(sg.SGError):
+        sg.sg_softmax_ce_fwd(h, W, y, v, v.clone(), work=small)
+    with pytest.raises(sg.SGError):
+        big = torch.empty(sg.sg_softmax_ce_work(h, W, False) + 512, dtype=torch.uint8, device="cuda")
+        sg.sg_softmax_ce_fwd(h, W, y, v, v.clone(), work=big[16:])
+    with pytest.raises(TypeError):
+        sg.sg_softmax_ce_fwd(h, W.half(), y, v, v.clone())
+    with pytest.raises(TypeError):
+        sg.sg_softmax_ce_fwd(h, W, y.long(), v, v.clone())
+    with pytest.raises(TypeError):
+        sg.sg_softmax_ce_fwd(h.float(), W.float(), y, v, v.clone())
+    with pytest.raises(TypeError):
+        e4 = torch.float8_e4m3fn
+        sg.sg_softmax_ce_bwd(h.to(e4), W.to(e4), y, v, v, torch.empty_like(h.to(e4)))
+    with pytest.raises(ValueError):
+        sg.sg_softmax_ce_fwd(h, W[:, :32], y, v, v.clone())
+    with pytest.raises(ValueError):
+        sg.sg_softmax_ce_fwd(h, W, y[:3], v, v.clone())
