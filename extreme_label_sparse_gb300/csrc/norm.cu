@@ -1,11 +1,13 @@
 // Dropout and the residual's addition with RMS norm (definitions in
 // include/sg.h).  All of them are bound by memory: each input is read once and
 // each output written once.
+#include <atomic>
 #include <cmath>
 
 #include <cuda_fp8.h>
 
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 
 using namespace rows;
 
@@ -17,34 +19,87 @@ namespace {
         return code;               \
     } while (0)
 
+#define NORM_TRY(expr)          \
+    do {                        \
+        sg_status rc_ = (expr); \
+        if (rc_ != SG_OK)       \
+            return rc_;         \
+    } while (0)
+
 constexpr int kDropThreads = 256;
 constexpr int64_t kMaxCols = 32768;   // of the norm: a row lies in one CTA's registers
-constexpr int kNormParts = 152 * 4;   // row groups that sum dweight before it is joined
+constexpr int kSMs = 152;
 
 // ---------------------------------------------------------------- dropout
-// One warp per segment of 256 columns.
-template <typename T, bool VEC>
+// One warp for a segment of 256 columns: any alignment and width.
+template <typename T>
 __global__ void __launch_bounds__(kDropThreads)
-    k_dropout(const T *x, int64_t ldx, int64_t nrows, int64_t cols, const Drop d, T *y, int64_t ldy)
+    k_dropout_any(const T *x, int64_t ldx, int64_t nrows, int64_t cols, const Drop d, T *y, int64_t ldy)
 {
     const int lane = threadIdx.x & 31;
     const int64_t segs = (cols + kSeg - 1) / kSeg;
     const int64_t step = (int64_t)gridDim.x * (kDropThreads / 32);
     for (int64_t i = (int64_t)blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32; i < nrows * segs; i += step) {
         const int64_t r = i / segs, c0 = (i - r * segs) * kSeg;
-        Pack8<T> p = load8<T, VEC>(x + r * ldx, c0, lane, cols);
-        const uint32_t m = keep_lane<VEC>(d, c0, lane, (uint32_t)r);
+        Pack8<T> p = load8<T, false>(x + r * ldx, c0, lane, cols);
+        if (d.drop) {
+            const Keep<false> k(d, c0, lane, (uint32_t)r);
+            float v[8];
+            unpack8(p, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            p.v[j] = from_f<T>((m >> j) & 1u ? __fmul_rn(to_f(p.v[j]), d.scale) : 0.f);
-        store8<T, VEC>(y + r * ldy, c0, lane, cols, p);
+            for (int j = 0; j < 8; ++j)
+                v[j] = k.at(j) ? __fmul_rn(v[j], d.scale) : 0.f;
+            p = pack8<T>(v);
+        }
+        store8<T, false>(y + r * ldy, c0, lane, cols, p);
+    }
+}
+
+// Rows of whole, aligned eights: the blocks of all rows are numbered through,
+// and a thread takes U of them, kDropThreads apart, whose loads it issues
+// together.  n (blocks) is below 2^31; row = i / blks by a multiplication.
+template <typename T, int U>
+__global__ void __launch_bounds__(kDropThreads)
+    k_dropout(const T *x, int64_t ldx, uint32_t n, uint32_t blks, uint32_t magic, uint32_t shift, uint32_t row0,
+              const Drop d, T *y, int64_t ldy)
+{
+    const uint32_t i0 = blockIdx.x * (kDropThreads * U) + threadIdx.x;
+    Pack8<T> p[U];
+    uint32_t r[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t i = i0 + u * kDropThreads;
+        r[u] = blks == 1 ? i : (uint32_t)(((uint64_t)i * magic) >> 32 >> shift);
+        b[u] = i - r[u] * blks;
+        if (i < n)
+            p[u] = *reinterpret_cast<const Pack8<T> *>(x + (int64_t)r[u] * ldx + b[u] * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (i0 + u * kDropThreads >= n)
+            return;
+        if (d.drop) {
+            const Keep<true> k(d, (int64_t)b[u] * 8, 0, row0 + r[u]);
+            float v[8];
+            unpack8(p[u], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = k.at(j) ? __fmul_rn(v[j], d.scale) : 0.f;
+            p[u] = pack8<T>(v);
+        }
+        *reinterpret_cast<Pack8<T> *>(y + (int64_t)r[u] * ldy + b[u] * 8) = p[u];
     }
 }
 
 // ---------------------------------------------------------------- norm
 // Sum of a and maximum of b over the `warps` warps of a row group (all of the
-// CTA where warps > 1).  Every thread gets both.
-__device__ __forceinline__ void row_reduce(float &a, float &b, int warps, float2 *sm)
+// CTA where warps > 1).  Every thread gets both.  Successive calls take turns
+// with two buffers, so that one barrier is enough.
+struct RowSums {
+    float2 v[2][32];
+};
+
+__device__ __forceinline__ void row_reduce(float &a, float &b, int warps, RowSums &sm, int turn)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -53,17 +108,59 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, int warps, float2
     }
     if (warps == 1)
         return;
-    __syncthreads();  // the last row's values have been read
     if ((threadIdx.x & 31) == 0)
-        sm[threadIdx.x / 32] = make_float2(a, b);
+        sm.v[turn & 1][threadIdx.x / 32] = make_float2(a, b);
     __syncthreads();
     a = 0.f;
     b = 0.f;
     for (int w = 0; w < warps; ++w) {
-        a += sm[w].x;
-        b = fmaxf(b, sm[w].y);
+        a += sm.v[turn & 1][w].x;
+        b = fmaxf(b, sm.v[turn & 1][w].y);
     }
 }
+
+// A thread's pieces of the next rows on their way to shared memory: NA
+// matrices, NV pieces of eight elements each, S rows deep.  Each thread copies
+// (cp.async) exactly what it reads itself, so no barrier is needed, and rows
+// in flight take no registers.
+template <typename T, int NA, int NV, int S, int THREADS>
+struct Ring8 {
+    [[maybe_unused]] static constexpr int kPieces = sizeof(Pack8<T>) / 16;
+    static constexpr int kBytes = S * NA * NV * THREADS * (int)sizeof(Pack8<T>);
+    uint4 *base;
+
+    __device__ __forceinline__ explicit Ring8(void *smem) : base(static_cast<uint4 *>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ uint4 *at(int slot, int m, int n, int i) const
+    {
+        return base + (((slot * NA + m) * NV + n) * kPieces + i) * THREADS;
+    }
+    __device__ __forceinline__ void copy(int slot, int m, int n, const T *src) const
+    {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            tc::cp_async16(tc::smem_u32(at(slot, m, n, i)), reinterpret_cast<const uint4 *>(src) + i);
+    }
+    __device__ __forceinline__ Pack8<T> get(int slot, int m, int n) const
+    {
+        Pack8<T> p;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            reinterpret_cast<uint4 *>(&p)[i] = *at(slot, m, n, i);
+        return p;
+    }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// threads of a CTA, and CTAs to an SM that the registers are cut for
+constexpr int norm_threads(int warps) { return warps == 1 ? 256 : warps * 32; }
+constexpr int norm_ctas(int warps) { return 1024 / norm_threads(warps); }
 
 struct NormFwd {
     const void *x, *res, *w;
@@ -76,86 +173,127 @@ struct NormFwd {
 };
 
 // A row by WARPS warps (one warp: eight rows to a CTA), NV segments to a warp.
-template <typename T, bool VEC, int WARPS, int NV>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) k_norm_fwd(const NormFwd a)
+// Row groups step over the rows.
+template <typename T, bool VEC, int WARPS, int NV, int S>
+__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_fwd(const NormFwd a)
 {
-    __shared__ float2 sm[32];
+    __shared__ RowSums sm;
+    extern __shared__ uint4 dyn[];
+    const Ring8<T, 2, NV, S, norm_threads(WARPS)> ring(dyn);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int wr = WARPS == 1 ? 0 : warp;
-    const int64_t r = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
-    if (r >= a.nrows)  // whole warps, and never a part of a CTA that meets in row_reduce
-        return;
-    float v[NV][8];
-    float ss = 0.f, top = 0.f;
+    const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
+    const int64_t g = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
+    const T *ax = static_cast<const T *>(a.x), *ar = static_cast<const T *>(a.res);
+    auto fetch = [&](int64_t r, int slot) {
+        if constexpr (VEC) {
+            if (r < a.nrows) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
-        Pack8<T> p = load8<T, VEC>(static_cast<const T *>(a.x) + r * a.ldx, c0, lane, a.cols);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[n][j] = to_f(p.v[j]);
-        if (a.d.drop) {
-            const uint32_t m = keep_lane<VEC>(a.d, c0, lane, (uint32_t)r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[n][j] = (m >> j) & 1u ? __fmul_rn(v[n][j], a.d.scale) : 0.f;
+                for (int n = 0; n < NV; ++n) {
+                    const int64_t c = (int64_t)(n * WARPS + wr) * kSeg + lane * 8;
+                    if (c < a.cols) {
+                        ring.copy(slot, 0, n, ax + r * a.ldx + c);
+                        if (ar)
+                            ring.copy(slot, 1, n, ar + r * a.ldr + c);
+                    }
+                }
+            }
+            copies_commit();
         }
-        if (a.res) {
-            const Pack8<T> q = load8<T, VEC>(static_cast<const T *>(a.res) + r * a.ldr, c0, lane, a.cols);
+    };
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[n][j] = __fadd_rn(v[n][j], to_f(q.v[j]));
-        }
-        // the norm is taken of the sum as it is stored, so that the backward
-        // pass sees the same row
+    for (int i = 0; i < S; ++i)
+        fetch(g + i * groups, i);
+    Pack8<T> w[NV];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            p.v[j] = from_f<T>(v[n][j]);
-        if (a.u)
-            store8<T, VEC>(static_cast<T *>(a.u) + r * a.ldu, c0, lane, a.cols, p);
-        const Pack8<T> w = load8<T, VEC>(static_cast<const T *>(a.w), c0, lane, a.cols);
+    for (int n = 0; n < NV; ++n)
+        w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (int64_t)(n * WARPS + wr) * kSeg, lane, a.cols);
+    int turn = 0, slot = 0;
+    for (int64_t r = g; r < a.nrows; r += groups, ++turn) {
+        Pack8<T> u[NV];
+        float ss = 0.f, top = 0.f;
+        if constexpr (VEC)
+            copies_wait<S - 1>();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[n][j] = to_f(p.v[j]);
-            ss = fmaf(v[n][j], v[n][j], ss);
-            top = fmaxf(top, fabsf(v[n][j] * to_f(w.v[j])));
-        }
-    }
-    row_reduce(ss, top, WARPS, sm);
-    const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
-    // max |y| without a second reduction: rstd max |u w|
-    top *= rstd;
-    const float to8 = top == 0.f ? 0.f : 448.0f / top;
-    if (lane == 0 && wr == 0) {
-        if (a.rstd)
-            a.rstd[r] = rstd;
-        if (a.y8)
-            a.scale8[r] = top / 448.0f;
-    }
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
-        const Pack8<T> w = load8<T, VEC>(static_cast<const T *>(a.w), c0, lane, a.cols);
-        Pack8<T> p;
-        Pack8<uint8_t> q;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float y = (v[n][j] * rstd) * to_f(w.v[j]);
-            p.v[j] = from_f<T>(y);
-            q.v[j] = __nv_cvt_float_to_fp8(y * to8, __NV_SATFINITE, __NV_E4M3);
-        }
-        if (a.y)
-            store8<T, VEC>(static_cast<T *>(a.y) + r * a.ldy, c0, lane, a.cols, p);
-        if (a.y8) {
-            uint8_t *row = a.y8 + r * a.ld8;
-            if constexpr (VEC) {
-                if (c0 + lane * 8 < a.cols)
-                    *reinterpret_cast<uint2 *>(row + c0 + lane * 8) = *reinterpret_cast<const uint2 *>(&q);
-            } else {
+        for (int n = 0; n < NV; ++n) {
+            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;  // and neither has a later segment columns of this thread
+            Pack8<T> p;
+            if constexpr (VEC)
+                p = ring.get(slot, 0, n);
+            else
+                p = load8<T, VEC>(ax + r * a.ldx, c0, lane, a.cols);
+            float v[8];
+            unpack8(p, v);
+            if (a.d.drop) {
+                const Keep<VEC> k(a.d, c0, lane, (uint32_t)r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (col_of<VEC>(c0, lane, j) < a.cols)
-                        row[col_of<VEC>(c0, lane, j)] = q.v[j];
+                    v[j] = k.at(j) ? __fmul_rn(v[j], a.d.scale) : 0.f;
+            }
+            if (ar) {
+                if constexpr (VEC)
+                    p = ring.get(slot, 1, n);
+                else
+                    p = load8<T, VEC>(ar + r * a.ldr, c0, lane, a.cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = __fadd_rn(v[j], to_f(p.v[j]));
+            }
+            // the norm is taken of the sum as it is stored, so that the
+            // backward pass sees the same row
+            u[n] = pack8<T>(v);
+            unpack8(u[n], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ss = fmaf(v[j], v[j], ss);
+                top = fmaxf(top, fabsf(v[j] * to_f(w[n].v[j])));
+            }
+            if (a.u)
+                store8<T, VEC>(static_cast<T *>(a.u) + r * a.ldu, c0, lane, a.cols, u[n]);
+        }
+        fetch(r + S * groups, slot);
+        slot = slot + 1 == S ? 0 : slot + 1;
+        row_reduce(ss, top, WARPS, sm, turn);
+        const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+        // max |y| without a second reduction: rstd max |u w|
+        top *= rstd;
+        const float to8 = top == 0.f ? 0.f : 448.0f / top;
+        if (lane == 0 && wr == 0) {
+            if (a.rstd)
+                a.rstd[r] = rstd;
+            if (a.y8)
+                a.scale8[r] = top / 448.0f;
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] = (to_f(u[n].v[j]) * rstd) * to_f(w[n].v[j]);
+            if (a.y) {
+                store8<T, VEC>(static_cast<T *>(a.y) + r * a.ldy, c0, lane, a.cols, pack8<T>(y));
+            }
+            if (a.y8) {
+                uint8_t *row = a.y8 + r * a.ld8;
+                uint16_t q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j] * to8, y[2 * j + 1] * to8), __NV_SATFINITE,
+                                                    __NV_E4M3);
+                if constexpr (VEC) {
+                    *reinterpret_cast<uint2 *>(row + c0 + lane * 8) =
+                        make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (col_of<VEC>(c0, lane, j) < a.cols)
+                            row[col_of<VEC>(c0, lane, j)] = (uint8_t)(q[j / 2] >> (8 * (j & 1)));
+                }
             }
         }
     }
@@ -172,67 +310,112 @@ struct NormBwd {
 
 // Row groups of WARPS warps step over the rows; a thread keeps the sum of its
 // columns of dweight in registers until its last row.
-template <typename T, bool VEC, int WARPS, int NV>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) k_norm_bwd(const NormBwd a)
+template <typename T, bool VEC, int WARPS, int NV, int S>
+__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_bwd(const NormBwd a)
 {
-    __shared__ float2 sm[32];
+    __shared__ RowSums sm;
+    extern __shared__ uint4 dyn[];
+    const Ring8<T, 3, NV, S, norm_threads(WARPS)> ring(dyn);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int wr = WARPS == 1 ? 0 : warp;
     const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
     const int64_t g = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
+    const T *ady = static_cast<const T *>(a.dy), *au = static_cast<const T *>(a.u);
+    const T *ai = static_cast<const T *>(a.du_in);
+    auto fetch = [&](int64_t r, int slot) {
+        if constexpr (VEC) {
+            if (r < a.nrows) {
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int64_t c = (int64_t)(n * WARPS + wr) * kSeg + lane * 8;
+                    if (c < a.cols) {
+                        ring.copy(slot, 0, n, ady + r * a.lddy + c);
+                        ring.copy(slot, 1, n, au + r * a.ldu + c);
+                        if (ai)
+                            ring.copy(slot, 2, n, ai + r * a.ldi + c);
+                    }
+                }
+            }
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        fetch(g + i * groups, i);
+    Pack8<T> w[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+        w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (int64_t)(n * WARPS + wr) * kSeg, lane, a.cols);
     float dw[NV][8] = {};
-    for (int64_t r = g; r < a.nrows; r += groups) {
-        Pack8<T> dy[NV], u[NV];
+    int turn = 0, slot = 0;
+    for (int64_t r = g; r < a.nrows; r += groups, ++turn) {
         const float rstd = a.rstd[r];
         float dot = 0.f, none = 0.f;
+        if constexpr (VEC)
+            copies_wait<S - 1>();
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
-            dy[n] = load8<T, VEC>(static_cast<const T *>(a.dy) + r * a.lddy, c0, lane, a.cols);
-            u[n] = load8<T, VEC>(static_cast<const T *>(a.u) + r * a.ldu, c0, lane, a.cols);
-        }
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
-            const Pack8<T> w = load8<T, VEC>(static_cast<const T *>(a.w), c0, lane, a.cols);
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;  // and neither has a later segment columns of this thread
+            Pack8<T> dy, u;
+            if constexpr (VEC) {
+                dy = ring.get(slot, 0, n);
+                u = ring.get(slot, 1, n);
+            } else {
+                dy = load8<T, VEC>(ady + r * a.lddy, c0, lane, a.cols);
+                u = load8<T, VEC>(au + r * a.ldu, c0, lane, a.cols);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float t = to_f(dy[n].v[j]) * (to_f(u[n].v[j]) * rstd);
+                const float t = to_f(dy.v[j]) * (to_f(u.v[j]) * rstd);
                 dw[n][j] += t;
-                dot = fmaf(t, to_f(w.v[j]), dot);
+                dot = fmaf(t, to_f(w[n].v[j]), dot);
             }
         }
-        row_reduce(dot, none, WARPS, sm);
+        row_reduce(dot, none, WARPS, sm, turn);
         const float mean = dot / (float)a.cols;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
-            const Pack8<T> w = load8<T, VEC>(static_cast<const T *>(a.w), c0, lane, a.cols);
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;
+            // once more from shared memory (or, without VEC, from the caches)
+            Pack8<T> dy, u;
+            if constexpr (VEC) {
+                dy = ring.get(slot, 0, n);
+                u = ring.get(slot, 1, n);
+            } else {
+                dy = load8<T, VEC>(ady + r * a.lddy, c0, lane, a.cols);
+                u = load8<T, VEC>(au + r * a.ldu, c0, lane, a.cols);
+            }
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = rstd * (to_f(dy[n].v[j]) * to_f(w.v[j]) - (to_f(u[n].v[j]) * rstd) * mean);
-            if (a.du_in) {
-                const Pack8<T> q = load8<T, VEC>(static_cast<const T *>(a.du_in) + r * a.ldi, c0, lane, a.cols);
+                v[j] = rstd * (to_f(dy.v[j]) * to_f(w[n].v[j]) - (to_f(u.v[j]) * rstd) * mean);
+            if (ai) {
+                Pack8<T> in;
+                if constexpr (VEC)
+                    in = ring.get(slot, 2, n);
+                else
+                    in = load8<T, VEC>(ai + r * a.ldi, c0, lane, a.cols);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[j] += to_f(q.v[j]);
+                    v[j] += to_f(in.v[j]);
             }
-            Pack8<T> p;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                p.v[j] = from_f<T>(v[j]);
-            store8<T, VEC>(static_cast<T *>(a.du) + r * a.ldo, c0, lane, a.cols, p);
+            store8<T, VEC>(static_cast<T *>(a.du) + r * a.ldo, c0, lane, a.cols, pack8<T>(v));
             if (a.dx) {
                 if (a.d.drop) {
-                    const uint32_t m = keep_lane<VEC>(a.d, c0, lane, (uint32_t)r);
+                    const Keep<VEC> k(a.d, c0, lane, (uint32_t)r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        p.v[j] = from_f<T>((m >> j) & 1u ? v[j] * a.d.scale : 0.f);
+                        v[j] = k.at(j) ? v[j] * a.d.scale : 0.f;
                 }
-                store8<T, VEC>(static_cast<T *>(a.dx) + r * a.lddx, c0, lane, a.cols, p);
+                store8<T, VEC>(static_cast<T *>(a.dx) + r * a.lddx, c0, lane, a.cols, pack8<T>(v));
             }
         }
+        fetch(r + S * groups, slot);
+        slot = slot + 1 == S ? 0 : slot + 1;
     }
     if (a.part) {
 #pragma unroll
@@ -269,57 +452,130 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float *__restrict__ part
 
 // warps and segments a row of `cols` columns takes: the first shape that
 // holds it
-#define NORM_SHAPES(X) X(1, 1) X(1, 2) X(1, 4) X(4, 2) X(8, 2) X(16, 2) X(16, 4) X(32, 4)
+#define NORM_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(32, 2) X(32, 4)
+
+// shared memory beyond the default is asked for once for each kernel and
+// device (one bit of the mask)
+template <typename F>
+sg_status allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    if (bytes <= 40 << 10)  // the default is 48 KB with the static part
+        return SG_OK;
+    int dev = 0;
+    SG_TRY_CUDA(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        SG_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return SG_OK;
+}
+
+// rows on their way: as many as leave room for the CTAs that fit by registers
+template <typename T, int NA, int WARPS, int NV>
+constexpr int ring_rows()
+{
+    const int row = NA * NV * norm_threads(WARPS) * (int)sizeof(Pack8<T>);
+    const int s = (216 << 10) / norm_ctas(WARPS) / row;
+    return s > 4 ? 4 : s < 1 ? 1 : s;
+}
+
+template <typename T, bool VEC, int W, int N>
+sg_status run_fwd(const NormFwd &a, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr int S = VEC ? ring_rows<T, 2, W, N>() : 1;
+    constexpr int smem = VEC ? Ring8<T, 2, N, S, norm_threads(W)>::kBytes : 0;
+    if constexpr (smem > 226 << 10) {  // fp32 rows above 16384 columns: not one is held
+        return run_fwd<T, false, W, N>(a, st);
+    } else {
+        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * norm_ctas(W);
+        NORM_TRY(allow_smem(k_norm_fwd<T, VEC, W, N, S>, smem, done));
+        k_norm_fwd<T, VEC, W, N, S><<<(unsigned)(need < most ? need : most), norm_threads(W), smem, st>>>(a);
+        return SG_OK;
+    }
+}
+
+template <typename T, bool VEC, int W, int N>
+sg_status run_bwd(const NormBwd &a, int64_t grid, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr int S = VEC ? ring_rows<T, 3, W, N>() : 1;
+    constexpr int smem = VEC ? Ring8<T, 3, N, S, norm_threads(W)>::kBytes : 0;
+    if constexpr (smem > 226 << 10) {  // fp32 rows above 16384 columns: not one is held
+        return run_bwd<T, false, W, N>(a, grid, st);
+    } else {
+        NORM_TRY(allow_smem(k_norm_bwd<T, VEC, W, N, S>, smem, done));
+        k_norm_bwd<T, VEC, W, N, S><<<(unsigned)grid, norm_threads(W), smem, st>>>(a);
+        return SG_OK;
+    }
+}
 
 template <typename T, bool VEC>
-void launch_fwd(const NormFwd &a, cudaStream_t st)
+sg_status launch_fwd(const NormFwd &a, cudaStream_t st)
 {
-#define X(W, N)                                                                                  \
-    if (a.cols <= (int64_t)(W) * (N) * kSeg) {                                                   \
-        const int64_t grid = (W) == 1 ? ceil_div(a.nrows, 8) : a.nrows;                          \
-        k_norm_fwd<T, VEC, W, N><<<(unsigned)grid, (W) == 1 ? 256 : (W) * 32, 0, st>>>(a);       \
-        return;                                                                                  \
-    }
+#define X(W, N)                             \
+    if (a.cols <= (int64_t)(W) * (N) * kSeg) \
+        return run_fwd<T, VEC, W, N>(a, st);
     NORM_SHAPES(X)
 #undef X
+    return SG_ERR_UNSUPPORTED;  // not reached: cols <= kMaxCols
+}
+
+template <typename T, bool VEC>
+sg_status launch_bwd(const NormBwd &a, int64_t grid, cudaStream_t st)
+{
+#define X(W, N)                             \
+    if (a.cols <= (int64_t)(W) * (N) * kSeg) \
+        return run_bwd<T, VEC, W, N>(a, grid, st);
+    NORM_SHAPES(X)
+#undef X
+    return SG_ERR_UNSUPPORTED;  // not reached: cols <= kMaxCols
 }
 
 // CTAs of the backward kernel, and the row groups they make
 int64_t bwd_groups(int64_t nrows, int64_t cols, int64_t *grid)
 {
-    const bool one = cols <= 4 * kSeg;  // one warp to a row
-    const int64_t most = one ? kNormParts / 8 * 2 : kNormParts;
-    const int64_t need = one ? ceil_div(nrows, 8) : nrows;
-    *grid = need < most ? need : most;
-    return one ? *grid * 8 : *grid;
-}
-
-template <typename T, bool VEC>
-void launch_bwd(const NormBwd &a, int64_t grid, cudaStream_t st)
-{
-#define X(W, N)                                                                                  \
-    if (a.cols <= (int64_t)(W) * (N) * kSeg) {                                                   \
-        k_norm_bwd<T, VEC, W, N><<<(unsigned)grid, (W) == 1 ? 256 : (W) * 32, 0, st>>>(a);       \
-        return;                                                                                  \
-    }
+    int warps = 32;
+#define X(W, N)                                           \
+    if (warps == 32 && cols <= (int64_t)(W) * (N) * kSeg) \
+        warps = (W);
     NORM_SHAPES(X)
 #undef X
+    const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * norm_ctas(warps);
+    *grid = need < most ? need : most;
+    return warps == 1 ? *grid * 8 : *grid;
 }
 
 template <typename T>
 void launch_dropout(bool vec, const void *x, int64_t ldx, int64_t nrows, int64_t cols, const Drop &d, void *y,
                     int64_t ldy, cudaStream_t st)
 {
-    const int64_t warps = nrows * ceil_div(cols, kSeg);
-    int64_t grid = ceil_div(warps, kDropThreads / 32);
-    if (grid > (1 << 20))
-        grid = 1 << 20;
     const T *xs = static_cast<const T *>(x);
     T *ys = static_cast<T *>(y);
-    if (vec)
-        k_dropout<T, true><<<(unsigned)grid, kDropThreads, 0, st>>>(xs, ldx, nrows, cols, d, ys, ldy);
-    else
-        k_dropout<T, false><<<(unsigned)grid, kDropThreads, 0, st>>>(xs, ldx, nrows, cols, d, ys, ldy);
+    if (!vec) {
+        int64_t grid = ceil_div(nrows * ceil_div(cols, kSeg), kDropThreads / 32);
+        if (grid > (1 << 20))
+            grid = 1 << 20;
+        k_dropout_any<T><<<(unsigned)grid, kDropThreads, 0, st>>>(xs, ldx, nrows, cols, d, ys, ldy);
+        return;
+    }
+    // i / blks = (i magic) >> (32 + shift) for i < 2^31, with magic =
+    // ceil(2^(32 + shift) / blks) and 2^shift < blks <= 2^(shift + 1): the
+    // excess of magic, below blks / 2^(32 + shift) of 1 / blks, times i stays
+    // below 1 / blks
+    const uint32_t blks = (uint32_t)(cols / 8);
+    uint32_t shift = 0;
+    while ((2ull << shift) < blks)
+        ++shift;
+    const uint32_t magic = blks == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + blks - 1) / blks);
+    constexpr int U = 2;
+    const int64_t slab = ((1ll << 31) - 1) / blks;  // rows of a launch
+    for (int64_t r0 = 0; r0 < nrows; r0 += slab) {
+        const int64_t n = (nrows - r0 < slab ? nrows - r0 : slab) * blks;
+        k_dropout<T, U><<<(unsigned)ceil_div(n, kDropThreads * U), kDropThreads, 0, st>>>(
+            xs + r0 * ldx, ldx, (uint32_t)n, blks, magic, shift, (uint32_t)r0, d, ys + r0 * ldy, ldy);
+    }
 }
 
 int64_t elem_size(int32_t dtype) { return dtype == SG_F32 ? 4 : 2; }
@@ -351,13 +607,6 @@ sg_status check_mat(const char *fn, const char *name, const void *p, int64_t ld,
         NORM_FAIL(SG_ERR_INVALID, "%s: %s is not aligned to its elements", fn, name);
     return SG_OK;
 }
-
-#define NORM_TRY(expr)          \
-    do {                        \
-        sg_status rc_ = (expr); \
-        if (rc_ != SG_OK)       \
-            return rc_;         \
-    } while (0)
 
 }  // namespace
 
@@ -425,11 +674,11 @@ sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, i
     const bool vec = cols % 8 == 0 && vec_ok(x, ldx, es) && vec_ok(residual, ldr, es) && vec_ok(weight, cols, es) &&
                      vec_ok(u, ldu, es) && vec_ok(y, ldy, es) && (!y8 || (((uintptr_t)y8) % 8 == 0 && ldy8 % 8 == 0));
     if (dtype == SG_BF16)
-        vec ? launch_fwd<__nv_bfloat16, true>(a, st) : launch_fwd<__nv_bfloat16, false>(a, st);
+        NORM_TRY((vec ? launch_fwd<__nv_bfloat16, true>(a, st) : launch_fwd<__nv_bfloat16, false>(a, st)));
     else if (dtype == SG_F16)
-        vec ? launch_fwd<__half, true>(a, st) : launch_fwd<__half, false>(a, st);
+        NORM_TRY((vec ? launch_fwd<__half, true>(a, st) : launch_fwd<__half, false>(a, st)));
     else
-        vec ? launch_fwd<float, true>(a, st) : launch_fwd<float, false>(a, st);
+        NORM_TRY((vec ? launch_fwd<float, true>(a, st) : launch_fwd<float, false>(a, st)));
     SG_TRY_CUDA(cudaGetLastError());
     return SG_OK;
 }
@@ -486,11 +735,11 @@ sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_
     const bool vec = cols % 8 == 0 && vec_ok(dy, lddy, es) && vec_ok(u, ldu, es) && vec_ok(du_in, lddu_in, es) &&
                      vec_ok(weight, cols, es) && vec_ok(du, lddu, es) && vec_ok(dx, lddx, es);
     if (dtype == SG_BF16)
-        vec ? launch_bwd<__nv_bfloat16, true>(a, grid, st) : launch_bwd<__nv_bfloat16, false>(a, grid, st);
+        NORM_TRY((vec ? launch_bwd<__nv_bfloat16, true>(a, grid, st) : launch_bwd<__nv_bfloat16, false>(a, grid, st)));
     else if (dtype == SG_F16)
-        vec ? launch_bwd<__half, true>(a, grid, st) : launch_bwd<__half, false>(a, grid, st);
+        NORM_TRY((vec ? launch_bwd<__half, true>(a, grid, st) : launch_bwd<__half, false>(a, grid, st)));
     else
-        vec ? launch_bwd<float, true>(a, grid, st) : launch_bwd<float, false>(a, grid, st);
+        NORM_TRY((vec ? launch_bwd<float, true>(a, grid, st) : launch_bwd<float, false>(a, grid, st)));
     SG_TRY_CUDA(cudaGetLastError());
     if (dweight) {
         k_norm_dw<<<(unsigned)ceil_div(cols, 32), 1024, 0, st>>>(a.part, (int)groups, cols, dweight);

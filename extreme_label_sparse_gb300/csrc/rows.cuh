@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "sg_internal.cuh"
 
 namespace rows {
@@ -39,6 +41,39 @@ template <typename T>
 struct alignas(16) Pack8 {
     T v[8];
 };
+
+// all eight at once: the 16-bit types convert in pairs
+template <typename T>
+__device__ __forceinline__ void unpack8(const Pack8<T> &p, float (&v)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = to_f(p.v[j]);
+}
+
+template <typename T>
+__device__ __forceinline__ Pack8<T> pack8(const float (&v)[8])
+{
+    Pack8<T> p;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            p.v[j] = v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t &w = reinterpret_cast<uint32_t *>(&p)[j];
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+                w = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                w = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    }
+    return p;
+}
 
 // column of element j of this lane in the segment that starts at column c0
 template <bool VEC>
@@ -98,56 +133,73 @@ __device__ __forceinline__ void store8(T *row, int64_t c0, int lane, int64_t col
 // at least `drop`; the kept ones are multiplied by 65536 / (65536 - drop).
 struct Drop {
     uint32_t drop;  // 0 .. 65536; 0: no dropout
-    uint32_t k0, k1, c2, c3;
+    uint32_t below;  // drop 2^16 - 1: a word is above it if its high half stays
+    uint32_t c2, c3;
     float scale;
+    // the keys of the ten rounds: the same for all threads, so they are worked
+    // out once and read as constants
+    uint32_t k0[10], k1[10];
 };
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy
 // as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit products.
-__device__ __forceinline__ uint4 philox10(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, uint32_t k0,
-                                          uint32_t k1)
+__device__ __forceinline__ void philox10(const Drop &d, uint32_t x0, uint32_t x1, uint32_t (&w)[4])
 {
+    uint32_t x2 = d.c2, x3 = d.c3;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
         const uint64_t p = (uint64_t)x0 * 0xD2511F53u, q = (uint64_t)x2 * 0xCD9E8D57u;
-        x0 = (uint32_t)(q >> 32) ^ x1 ^ k0;
+        x0 = (uint32_t)(q >> 32) ^ x1 ^ d.k0[i];
         x1 = (uint32_t)q;
-        x2 = (uint32_t)(p >> 32) ^ x3 ^ k1;
+        x2 = (uint32_t)(p >> 32) ^ x3 ^ d.k1[i];
         x3 = (uint32_t)p;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
-    return make_uint4(x0, x1, x2, x3);
+    w[0] = x0;
+    w[1] = x1;
+    w[2] = x2;
+    w[3] = x3;
 }
 
-// bit j: element j of the eight columns 8 blk .. 8 blk + 7 of `row` stays
-__device__ __forceinline__ uint32_t keep8(const Drop &d, uint32_t blk, uint32_t row)
-{
-    const uint4 r = philox10(blk, row, d.c2, d.c3, d.k0, d.k1);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m |= ((w[i] & 0xffffu) >= d.drop ? 1u : 0u) << (2 * i);
-        m |= ((w[i] >> 16) >= d.drop ? 1u : 0u) << (2 * i + 1);
-    }
-    return m;
-}
-
-// the same for this lane's elements of a segment (every lane of the warp calls
-// it: without VEC an element's bits come from the lane of its block)
+// Which of a lane's eight elements of a segment stay.  VEC: they are the eight
+// of one block, and the block's random words are looked at as they are;
+// without it an element's bits come from the lane that drew its block, so
+// every lane of the warp makes one.  drop is not 0.
 template <bool VEC>
-__device__ __forceinline__ uint32_t keep_lane(const Drop &d, int64_t c0, int lane, uint32_t row)
-{
-    const uint32_t own = keep8(d, (uint32_t)(c0 / 8 + lane), row);
-    if constexpr (VEC)
-        return own;
-    uint32_t m = 0;
+struct Keep {
+    uint32_t w[VEC ? 4 : 1];
+    uint32_t below;
+
+    __device__ __forceinline__ Keep(const Drop &d, int64_t c0, int lane, uint32_t row)
+    {
+        uint32_t r[4];
+        philox10(d, (uint32_t)(c0 / 8) + lane, row, r);
+        below = d.below;
+        if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        m |= ((__shfl_sync(0xffffffffu, own, (lane >> 3) + 4 * j) >> (lane & 7)) & 1u) << j;
-    return m;
-}
+            for (int i = 0; i < 4; ++i)
+                w[i] = r[i];
+        } else {
+            uint32_t own = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                own |= (r[i] << 16 > below ? 1u : 0u) << (2 * i);
+                own |= (r[i] > below ? 1u : 0u) << (2 * i + 1);
+            }
+            w[0] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[0] |= ((__shfl_sync(0xffffffffu, own, (lane >> 3) + 4 * j) >> (lane & 7)) & 1u) << j;
+        }
+    }
+
+    __device__ __forceinline__ bool at(int j) const
+    {
+        if constexpr (VEC)
+            return ((j & 1) ? w[j / 2] : w[j / 2] << 16) > below;
+        else
+            return (w[0] >> j) & 1u;
+    }
+};
 
 // host: the fields of Drop, false if p is not a probability
 inline bool make_drop(double p, uint64_t seed, uint64_t offset, Drop *d)
@@ -155,10 +207,13 @@ inline bool make_drop(double p, uint64_t seed, uint64_t offset, Drop *d)
     if (!(p >= 0.0 && p <= 1.0))
         return false;
     d->drop = (uint32_t)(p * 65536.0 + 0.5);
-    d->k0 = (uint32_t)seed;
-    d->k1 = (uint32_t)(seed >> 32);
+    d->below = (uint32_t)(((uint64_t)d->drop << 16) - 1);
     d->c2 = (uint32_t)offset;
     d->c3 = (uint32_t)(offset >> 32);
+    for (uint32_t i = 0; i < 10; ++i) {
+        d->k0[i] = (uint32_t)seed + i * 0x9E3779B9u;
+        d->k1[i] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+    }
     // at drop = 65536 nothing is kept and the factor is not used
     d->scale = d->drop < 65536u ? (float)(65536.0 / (double)(65536u - d->drop)) : 0.f;
     return true;

@@ -9,6 +9,7 @@ If libsg.so has not been built the first call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import threading
 from pathlib import Path
 
@@ -498,68 +499,90 @@ def sg_rewire(layout: Layout, h, dZ, W, n_drop: int, idx_out, W_out):
 
 
 # ---------------------------------------------------------------- around the layer
+# These calls are often a few microseconds of GPU work, so their checks are
+# kept to a few attribute reads for each tensor.
 _DTYPE = {torch.bfloat16: SG_BF16, torch.float16: SG_F16, torch.float32: SG_F32, torch.float8_e4m3fn: SG_E4M3}
-_F32 = (torch.float32,)
+_E4M3 = torch.float8_e4m3fn
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _mat(t, name: str, shape, dtypes, device):
-    """(pointer, row stride) of a [rows, cols] matrix on `device` whose rows
-    are contiguous; (NULL, cols) for None."""
-    if t is None:
-        return None, shape[1]
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    rs, cs = t.stride()
-    if cs != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if rs < shape[1]:
-        if shape[0] > 1:
-            raise ValueError(f"the rows of {name} overlap")
-        rs = shape[1]
-    return t.data_ptr(), rs
-
-
-def _vec(t, name: str, n: int, dtypes, device):
-    """Pointer of a contiguous vector of n elements on `device` (None: NULL)."""
-    if t is None:
-        return None
-    p = _dev(t, name, dtypes, n)
-    if t.device != device:
-        raise ValueError(f"{name} must be on the device of the others")
-    return p
-
-
-def _rows_of(t, name: str):
+def _open(t, name: str, dtypes):
+    """(rows, columns, dtype, device index) of the matrix that the others of a
+    call go by."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    return tuple(t.shape), t.device, (t.dtype,)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dtype = t.dtype
+    if dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {dtype}, expected one of {dtypes}")
+    rows, cols = t.shape
+    return rows, cols, dtype, t.get_device()
 
 
-def _call(fn, device, *args):
-    """One library call on the current stream of `device`, which is made the
-    current device for it."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)))
+def _mat(t, name: str, rows: int, cols: int, dtype, dev: int):
+    """(pointer, row stride) of a rows x cols matrix whose rows are contiguous;
+    (NULL, cols) for None."""
+    if t is None:
+        return None, cols
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    rs, cs = t.stride()
+    if cs != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rs < cols:
+        if rows > 1:
+            raise ValueError(f"the rows of {name} overlap")
+        rs = cols
+    return t.data_ptr(), rs
+
+
+def _vec(t, name: str, n, dtype, dev: int):
+    """Pointer of a contiguous vector of n elements (None: any number); NULL
+    for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn, dev: int, *args):
+    """One library call on the current stream of device `dev`, which is made
+    the current device for it."""
+    st = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, st)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)))
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status != SG_OK:
+        raise SGError(status, last_error())
 
 
 def sg_dropout(x: torch.Tensor, p: float, seed: int, offset: int, y: torch.Tensor):
     """y = dropout(x) with the mask of (seed, offset) (see sg.h); the backward
     pass is the same call on the gradient.  y may be x."""
-    shape, dev, dt = _rows_of(x, "x")
-    xp, ldx = _mat(x, "x", shape, tuple(_DTYPE), dev)
-    yp, ldy = _mat(y, "y", shape, dt, dev)
-    _call(load().sg_dropout, dev, xp, ldx, shape[0], shape[1], _DTYPE[dt[0]], p, seed, offset, yp, ldy)
+    rows, cols, dt, dev = _open(x, "x", _FLOATS)
+    xp, ldx = _mat(x, "x", rows, cols, dt, dev)
+    yp, ldy = _mat(y, "y", rows, cols, dt, dev)
+    _call((_lib or load()).sg_dropout, dev, xp, ldx, rows, cols, _DTYPE[dt], p, seed, offset, yp, ldy)
 
 
 def sg_add_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None, u=None, rstd=None, y=None,
@@ -567,15 +590,24 @@ def sg_add_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
     """u = residual + dropout(x), y = u / rms(u) * weight; y8 with y8_scale
     hold y in 8 bits with a scale for each row.  Outputs that are None are not
     written (see sg.h)."""
-    shape, dev, dt = _rows_of(x, "x")
-    xp, ldx = _mat(x, "x", shape, tuple(_DTYPE), dev)
-    rp, ldr = _mat(residual, "residual", shape, dt, dev)
-    up, ldu = _mat(u, "u", shape, dt, dev)
-    yp, ldy = _mat(y, "y", shape, dt, dev)
-    qp, ldq = _mat(y8, "y8", shape, (torch.float8_e4m3fn,), dev)
-    _call(load().sg_add_rmsnorm_fwd, dev, xp, ldx, rp, ldr, shape[0], shape[1], _DTYPE[dt[0]],
-          _vec(weight, "weight", shape[1], dt, dev), eps, drop_p, seed, offset, up, ldu,
-          _vec(rstd, "rstd", shape[0], _F32, dev), yp, ldy, qp, ldq, _vec(y8_scale, "y8_scale", shape[0], _F32, dev))
+    rows, cols, dt, dev = _open(x, "x", _FLOATS)
+    xp, ldx = _mat(x, "x", rows, cols, dt, dev)
+    rp, ldr = _mat(residual, "residual", rows, cols, dt, dev)
+    up, ldu = _mat(u, "u", rows, cols, dt, dev)
+    yp, ldy = _mat(y, "y", rows, cols, dt, dev)
+    qp, ldq = _mat(y8, "y8", rows, cols, _E4M3, dev)
+    _call((_lib or load()).sg_add_rmsnorm_fwd, dev, xp, ldx, rp, ldr, rows, cols, _DTYPE[dt],
+          _vec(weight, "weight", cols, dt, dev), eps, drop_p, seed, offset, up, ldu,
+          _vec(rstd, "rstd", rows, torch.float32, dev), yp, ldy, qp, ldq,
+          _vec(y8_scale, "y8_scale", rows, torch.float32, dev))
+
+
+@functools.lru_cache(4096)
+def sg_add_rmsnorm_bwd_work(rows: int, cols: int) -> int:
+    """Bytes of work memory that sg_add_rmsnorm_bwd needs for dweight."""
+    n = C.c_int64(0)
+    _check(load().sg_add_rmsnorm_bwd_work(rows, cols, C.byref(n)))
+    return n.value
 
 
 def sg_add_rmsnorm_bwd(dy: torch.Tensor, u: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, du, dweight=None,
@@ -583,49 +615,47 @@ def sg_add_rmsnorm_bwd(dy: torch.Tensor, u: torch.Tensor, weight: torch.Tensor, 
     """Gradient of sg_add_rmsnorm_fwd (see sg.h).  work: a uint8 tensor of
     sg_add_rmsnorm_bwd_work bytes; one is taken from torch's allocator if it is
     None."""
-    shape, dev, dt = _rows_of(dy, "dy")
-    gp, ldg = _mat(dy, "dy", shape, tuple(_DTYPE), dev)
-    up, ldu = _mat(u, "u", shape, dt, dev)
-    ip, ldi = _mat(du_in, "du_in", shape, dt, dev)
-    op, ldo = _mat(du, "du", shape, dt, dev)
-    xp, ldx = _mat(dx, "dx", shape, dt, dev)
+    rows, cols, dt, dev = _open(dy, "dy", _FLOATS)
+    gp, ldg = _mat(dy, "dy", rows, cols, dt, dev)
+    up, ldu = _mat(u, "u", rows, cols, dt, dev)
+    ip, ldi = _mat(du_in, "du_in", rows, cols, dt, dev)
+    op, ldo = _mat(du, "du", rows, cols, dt, dev)
+    xp, ldx = _mat(dx, "dx", rows, cols, dt, dev)
     if dweight is not None and work is None:
-        work = torch.empty(sg_add_rmsnorm_bwd_work(*shape), dtype=torch.uint8, device=dev)
-    _call(load().sg_add_rmsnorm_bwd, dev, gp, ldg, up, ldu, ip, ldi, shape[0], shape[1], _DTYPE[dt[0]],
-          _vec(weight, "weight", shape[1], dt, dev), _vec(rstd, "rstd", shape[0], _F32, dev), drop_p, seed, offset,
-          op, ldo, xp, ldx, _vec(dweight, "dweight", shape[1], _F32, dev),
-          _vec(work, "work", None, (torch.uint8,), dev), 0 if work is None else work.numel())
-
-
-def sg_add_rmsnorm_bwd_work(rows: int, cols: int) -> int:
-    """Bytes of work memory that sg_add_rmsnorm_bwd needs for dweight."""
-    n = C.c_int64(0)
-    _check(load().sg_add_rmsnorm_bwd_work(rows, cols, C.byref(n)))
-    return int(n.value)
-
-
-_16BIT = (torch.bfloat16, torch.float16)
+        work = torch.empty(sg_add_rmsnorm_bwd_work(rows, cols), dtype=torch.uint8, device=dy.device)
+    _call((_lib or load()).sg_add_rmsnorm_bwd, dev, gp, ldg, up, ldu, ip, ldi, rows, cols, _DTYPE[dt],
+          _vec(weight, "weight", cols, dt, dev), _vec(rstd, "rstd", rows, torch.float32, dev), drop_p, seed, offset,
+          op, ldo, xp, ldx, _vec(dweight, "dweight", cols, torch.float32, dev),
+          _vec(work, "work", None, torch.uint8, dev), 0 if work is None else work.numel())
 
 
 def _head(h, W, dtypes):
-    """(h pointer, ldh, T, H, W pointer, ldw, V, dtype) of a dense head."""
-    (T, H), dev, dt = _rows_of(h, "h")
-    (V, _), _, _ = _rows_of(W, "W")
-    hp, ldh = _mat(h, "h", (T, H), dtypes, dev)
-    wp, ldw = _mat(W, "W", (V, H), dt, dev)
-    return hp, ldh, T, H, wp, ldw, V, _DTYPE[dt[0]]
+    """(h pointer, ldh, T, H, W pointer, ldw, V, type) of a dense head, and its
+    dtype and device index."""
+    T, H, dt, dev = _open(h, "h", dtypes)
+    hp, ldh = _mat(h, "h", T, H, dt, dev)
+    V = W.shape[0] if isinstance(W, torch.Tensor) and W.dim() == 2 else -1
+    wp, ldw = _mat(W, "W", V, H, dt, dev)
+    return (hp, ldh, T, H, wp, ldw, V, _DTYPE[dt]), dt, dev
+
+
+@functools.lru_cache(4096)
+def _ce_bytes(h16, ldh, T, H, W16, ldw, V, dt, backward) -> int:
+    n = C.c_int64(0)
+    _check(load().sg_softmax_ce_work(h16, ldh, T, H, W16, ldw, V, dt, backward, C.byref(n)))
+    return n.value
 
 
 def _ce_work(head, backward: int) -> int:
-    n = C.c_int64(0)
-    _check(load().sg_softmax_ce_work(*head, backward, C.byref(n)))
-    return n.value
+    """The size goes by the pointers' alignment alone."""
+    hp, ldh, T, H, wp, ldw, V, dt = head
+    return _ce_bytes(hp & 15, ldh, T, H, wp & 15, ldw, V, dt, backward)
 
 
 def sg_softmax_ce_work(h: torch.Tensor, W: torch.Tensor, backward: bool) -> int:
     """Bytes of work memory that sg_softmax_ce_fwd or sg_softmax_ce_bwd needs
     for this h and W."""
-    return _ce_work(_head(h, W, tuple(_DTYPE)), int(bool(backward)))
+    return _ce_work(_head(h, W, _16BIT if backward else _8OR16BIT)[0], int(bool(backward)))
 
 
 def sg_softmax_ce_fwd(h: torch.Tensor, W: torch.Tensor, targets, loss, lse, h_scale=None, W_scale=None,
@@ -634,15 +664,15 @@ def sg_softmax_ce_fwd(h: torch.Tensor, W: torch.Tensor, targets, loss, lse, h_sc
     float8_e4m3fn rows, h_scale[T] and W_scale[V] are their scales.  work: a
     uint8 tensor of sg_softmax_ce_work bytes; one is taken from torch's
     allocator if it is None.  status: an int32 tensor of one element."""
-    head = _head(h, W, _16BIT + (torch.float8_e4m3fn,))
+    head, _, dev = _head(h, W, _8OR16BIT)
     hp, ldh, T, H, wp, ldw, V, dt = head
-    dev = h.device
     if work is None:
-        work = torch.empty(_ce_work(head, 0), dtype=torch.uint8, device=dev)
-    _call(load().sg_softmax_ce_fwd, dev, hp, ldh, _vec(h_scale, "h_scale", T, _F32, dev), T, H, wp, ldw,
-          _vec(W_scale, "W_scale", V, _F32, dev), V, dt, _vec(targets, "targets", T, _I32, dev), ignore_index,
-          smoothing, _vec(loss, "loss", T, _F32, dev), _vec(lse, "lse", T, _F32, dev),
-          _vec(work, "work", None, (torch.uint8,), dev), work.numel(), _vec(status, "status", 1, _I32, dev))
+        work = torch.empty(_ce_work(head, 0), dtype=torch.uint8, device=h.device)
+    f32 = torch.float32
+    _call((_lib or load()).sg_softmax_ce_fwd, dev, hp, ldh, _vec(h_scale, "h_scale", T, f32, dev), T, H, wp, ldw,
+          _vec(W_scale, "W_scale", V, f32, dev), V, dt, _vec(targets, "targets", T, torch.int32, dev), ignore_index,
+          smoothing, _vec(loss, "loss", T, f32, dev), _vec(lse, "lse", T, f32, dev),
+          _vec(work, "work", None, torch.uint8, dev), work.numel(), _vec(status, "status", 1, torch.int32, dev))
 
 
 def sg_softmax_ce_bwd(h: torch.Tensor, W: torch.Tensor, targets, lse, dloss, dh=None, dW=None,
@@ -650,14 +680,19 @@ def sg_softmax_ce_bwd(h: torch.Tensor, W: torch.Tensor, targets, lse, dloss, dh=
     """dh and dW (either may be None) from dloss[T] and the lse that
     sg_softmax_ce_fwd wrote for the same h and W (see sg.h); work and status as
     there."""
-    head = _head(h, W, _16BIT)
+    head, dtype, dev = _head(h, W, _16BIT)
     hp, ldh, T, H, wp, ldw, V, dt = head
-    dev = h.device
-    dhp, lddh = _mat(dh, "dh", (T, H), (h.dtype,), dev)
-    dwp, lddw = _mat(dW, "dW", (V, H), (h.dtype,), dev)
+    dhp, lddh = _mat(dh, "dh", T, H, dtype, dev)
+    dwp, lddw = _mat(dW, "dW", V, H, dtype, dev)
     if work is None:
-        work = torch.empty(_ce_work(head, 1), dtype=torch.uint8, device=dev)
-    _call(load().sg_softmax_ce_bwd, dev, hp, ldh, T, H, wp, ldw, V, dt, _vec(targets, "targets", T, _I32, dev),
-          ignore_index, smoothing, _vec(lse, "lse", T, _F32, dev), _vec(dloss, "dloss", T, _F32, dev), dhp, lddh,
-          dwp, lddw, _vec(work, "work", None, (torch.uint8,), dev), work.numel(),
-          _vec(status, "status", 1, _I32, dev))
+        work = torch.empty(_ce_work(head, 1), dtype=torch.uint8, device=h.device)
+    f32 = torch.float32
+    _call((_lib or load()).sg_softmax_ce_bwd, dev, hp, ldh, T, H, wp, ldw, V, dt,
+          _vec(targets, "targets", T, torch.int32, dev), ignore_index, smoothing, _vec(lse, "lse", T, f32, dev),
+          _vec(dloss, "dloss", T, f32, dev), dhp, lddh, dwp, lddw, _vec(work, "work", None, torch.uint8, dev),
+          work.numel(), _vec(status, "status", 1, torch.int32, dev))
+
+
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+_16BIT = (torch.bfloat16, torch.float16)
+_8OR16BIT = _16BIT + (_E4M3,)

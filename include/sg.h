@@ -469,8 +469,8 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  *   loss[T], lse[T], dloss[T] fp32; dh[T][H], dW[V][H] in dtype, one of them
  *   may be NULL.  lse is what sg_softmax_ce_fwd wrote for the same h and W.
  * fp32 accumulation, sums and statistics in fp32.  g enters the products of dh
- * and dW in dtype (SG_F16: times a power of two that keeps it in range).  The
- * results are the same bits for the same call.  Rows of h or W that do not
+ * and dW in dtype, times a factor that suits its largest element (taken out of
+ * the fp32 sums).  The results are the same bits for the same call.  Rows of h or W that do not
  * start on 16 bytes are first copied into the work memory.
  * status (device int32, may be NULL): sticky, first error wins, SG_ERR_TIMEOUT
  * where a bounded wait gave up and the outputs are not complete; the caller
