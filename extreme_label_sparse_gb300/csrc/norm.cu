@@ -26,7 +26,7 @@ namespace {
             return rc_;         \
     } while (0)
 
-constexpr int kDropThreads = 256;
+constexpr int kDropThreads = 256, kDropCtas = 6, kDropU = 4;
 constexpr int64_t kMaxCols = 32768;   // of the norm: a row lies in one CTA's registers
 constexpr int kSMs = 152;
 
@@ -56,30 +56,40 @@ __global__ void __launch_bounds__(kDropThreads)
 }
 
 // Rows of whole, aligned eights: the blocks of all rows are numbered through,
-// and a thread takes U of them, kDropThreads apart, whose loads it issues
+// and a thread takes kDropU of them, kDropThreads apart, whose loads it issues
 // together.  n (blocks) is below 2^31; row = i / blks by a multiplication.
-template <typename T, int U>
-__global__ void __launch_bounds__(kDropThreads)
+// DENSE: no gaps between rows.  The copy alone would take as long as long as
+// loads stay ahead of the rounds (about 140 instructions for eight elements):
+// four at once and 1536 threads to an SM reach it, 79 us for 32768 x 4096 bf16
+// (6.8 TB/s); two at once take 86, a loop with the next load ahead 102.
+template <typename T, bool DENSE>
+__global__ void __launch_bounds__(kDropThreads, kDropCtas)
     k_dropout(const T *x, int64_t ldx, uint32_t n, uint32_t blks, uint32_t magic, uint32_t shift, uint32_t row0,
               const Drop d, T *y, int64_t ldy)
 {
-    const uint32_t i0 = blockIdx.x * (kDropThreads * U) + threadIdx.x;
-    Pack8<T> p[U];
-    uint32_t r[U], b[U];
+    const uint32_t i0 = blockIdx.x * (kDropThreads * kDropU) + threadIdx.x;
+    auto row_of = [&](uint32_t i) { return blks == 1 ? i : (uint32_t)(((uint64_t)i * magic) >> 32 >> shift); };
+    auto at = [&](uint32_t i, int64_t ld) {
+        if (DENSE)
+            return (int64_t)i * 8;
+        const uint32_t r = row_of(i);
+        return r * ld + (i - r * blks) * 8;
+    };
+    Pack8<T> p[kDropU];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kDropU; ++u) {
         const uint32_t i = i0 + u * kDropThreads;
-        r[u] = blks == 1 ? i : (uint32_t)(((uint64_t)i * magic) >> 32 >> shift);
-        b[u] = i - r[u] * blks;
         if (i < n)
-            p[u] = *reinterpret_cast<const Pack8<T> *>(x + (int64_t)r[u] * ldx + b[u] * 8);
+            p[u] = load_pack(x + at(i, ldx));
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (i0 + u * kDropThreads >= n)
+    for (int u = 0; u < kDropU; ++u) {
+        const uint32_t i = i0 + u * kDropThreads;
+        if (i >= n)
             return;
         if (d.drop) {
-            const Keep<true> k(d, (int64_t)b[u] * 8, 0, row0 + r[u]);
+            const uint32_t r = row_of(i);
+            const Keep<true> k(d, (int64_t)(i - r * blks) * 8, 0, row0 + r);
             float v[8];
             unpack8(p[u], v);
 #pragma unroll
@@ -87,35 +97,41 @@ __global__ void __launch_bounds__(kDropThreads)
                 v[j] = k.at(j) ? __fmul_rn(v[j], d.scale) : 0.f;
             p[u] = pack8<T>(v);
         }
-        *reinterpret_cast<Pack8<T> *>(y + (int64_t)r[u] * ldy + b[u] * 8) = p[u];
+        store_pack(y + at(i, ldy), p[u]);
     }
 }
 
 // ---------------------------------------------------------------- norm
-// Sum of a and maximum of b over the `warps` warps of a row group (all of the
-// CTA where warps > 1).  Every thread gets both.  Successive calls take turns
+// Sum of a (and, if MAX, maximum of b) over the WARPS warps of a row group (all of
+// the CTA where WARPS > 1).  Every thread gets both.  Successive calls take turns
 // with two buffers, so that one barrier is enough.
 struct RowSums {
     float2 v[2][32];
 };
 
-__device__ __forceinline__ void row_reduce(float &a, float &b, int warps, RowSums &sm, int turn)
+template <int WARPS, bool MAX>
+__device__ __forceinline__ void row_reduce(float &a, float &b, RowSums &sm, int turn)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
-        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        if (MAX)
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
     }
-    if (warps == 1)
-        return;
-    if ((threadIdx.x & 31) == 0)
-        sm.v[turn & 1][threadIdx.x / 32] = make_float2(a, b);
-    __syncthreads();
-    a = 0.f;
-    b = 0.f;
-    for (int w = 0; w < warps; ++w) {
-        a += sm.v[turn & 1][w].x;
-        b = fmaxf(b, sm.v[turn & 1][w].y);
+    if constexpr (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0)
+            sm.v[turn & 1][threadIdx.x / 32] = make_float2(a, b);
+        __syncthreads();
+        // a lane takes a warp's values, and the shuffles above once more
+        const float2 t = sm.v[turn & 1][threadIdx.x % WARPS];
+        a = t.x;
+        b = t.y;
+#pragma unroll
+        for (int o = WARPS / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            if (MAX)
+                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
     }
 }
 
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
         }
         fetch(r + S * groups, slot);
         slot = slot + 1 == S ? 0 : slot + 1;
-        row_reduce(ss, top, WARPS, sm, turn);
+        row_reduce<WARPS, true>(ss, top, sm, turn);
         const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
         // max |y| without a second reduction: rstd max |u w|
         top *= rstd;
@@ -368,13 +384,15 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float t = to_f(dy.v[j]) * (to_f(u.v[j]) * rstd);
-                dw[n][j] += t;
+                const float t = to_f(dy.v[j]) * to_f(u.v[j]);
+                dw[n][j] = fmaf(t, rstd, dw[n][j]);
                 dot = fmaf(t, to_f(w[n].v[j]), dot);
             }
         }
-        row_reduce(dot, none, WARPS, sm, turn);
-        const float mean = dot / (float)a.cols;
+        row_reduce<WARPS, false>(dot, none, sm, turn);
+        // du = rstd (dy w - n mean(dy w n)) with n = u rstd:
+        // (rstd w) dy - back u, back = rstd^3 mean(dy w u)
+        const float back = rstd * rstd * rstd * (dot / (float)a.cols);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
@@ -390,19 +408,21 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
                 u = load8<T, VEC>(au + r * a.ldu, c0, lane, a.cols);
             }
             float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = rstd * (to_f(dy.v[j]) * to_f(w[n].v[j]) - (to_f(u.v[j]) * rstd) * mean);
             if (ai) {
                 Pack8<T> in;
                 if constexpr (VEC)
                     in = ring.get(slot, 2, n);
                 else
                     in = load8<T, VEC>(ai + r * a.ldi, c0, lane, a.cols);
+                unpack8(in, v);
+            } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[j] += to_f(in.v[j]);
+                    v[j] = 0.f;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = fmaf(to_f(w[n].v[j]) * rstd, to_f(dy.v[j]), fmaf(-back, to_f(u.v[j]), v[j]));
             store8<T, VEC>(static_cast<T *>(a.du) + r * a.ldo, c0, lane, a.cols, pack8<T>(v));
             if (a.dx) {
                 if (a.d.drop) {
@@ -569,12 +589,16 @@ void launch_dropout(bool vec, const void *x, int64_t ldx, int64_t nrows, int64_t
     while ((2ull << shift) < blks)
         ++shift;
     const uint32_t magic = blks == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + blks - 1) / blks);
-    constexpr int U = 2;
-    const int64_t slab = ((1ll << 31) - 1) / blks;  // rows of a launch
+    const int64_t slab = ((1ll << 31) - 1 - kDropThreads * kDropU) / blks;  // rows of a launch
     for (int64_t r0 = 0; r0 < nrows; r0 += slab) {
         const int64_t n = (nrows - r0 < slab ? nrows - r0 : slab) * blks;
-        k_dropout<T, U><<<(unsigned)ceil_div(n, kDropThreads * U), kDropThreads, 0, st>>>(
-            xs + r0 * ldx, ldx, (uint32_t)n, blks, magic, shift, (uint32_t)r0, d, ys + r0 * ldy, ldy);
+        const unsigned grid = (unsigned)ceil_div(n, kDropThreads * kDropU);
+        if (ldx == cols && ldy == cols)
+            k_dropout<T, true><<<grid, kDropThreads, 0, st>>>(xs + r0 * ldx, ldx, (uint32_t)n, blks, magic, shift,
+                                                              (uint32_t)r0, d, ys + r0 * ldy, ldy);
+        else
+            k_dropout<T, false><<<grid, kDropThreads, 0, st>>>(xs + r0 * ldx, ldx, (uint32_t)n, blks, magic, shift,
+                                                               (uint32_t)r0, d, ys + r0 * ldy, ldy);
     }
 }
 

@@ -42,6 +42,25 @@ struct alignas(16) Pack8 {
     T v[8];
 };
 
+// eight aligned elements, in accesses of 16 bytes
+template <typename T>
+__device__ __forceinline__ Pack8<T> load_pack(const T *src)
+{
+    Pack8<T> p;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(p) / 16; ++i)
+        reinterpret_cast<uint4 *>(&p)[i] = reinterpret_cast<const uint4 *>(src)[i];
+    return p;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pack(T *dst, const Pack8<T> &p)
+{
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(p) / 16; ++i)
+        reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(&p)[i];
+}
+
 // all eight at once: the 16-bit types convert in pairs
 template <typename T>
 __device__ __forceinline__ void unpack8(const Pack8<T> &p, float (&v)[8])
@@ -88,13 +107,8 @@ __device__ __forceinline__ Pack8<T> load8(const T *row, int64_t c0, int lane, in
 {
     Pack8<T> p;
     if constexpr (VEC) {
-        if (c0 + lane * 8 < cols) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(row + c0 + lane * 8);
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(p) / 16; ++i)
-                reinterpret_cast<uint4 *>(&p)[i] = src[i];
-            return p;
-        }
+        if (c0 + lane * 8 < cols)
+            return load_pack(row + c0 + lane * 8);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             p.v[j] = from_f<T>(0.f);
@@ -112,12 +126,8 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T *row, int64_t c0, int lane, int64_t cols, const Pack8<T> &p)
 {
     if constexpr (VEC) {
-        if (c0 + lane * 8 < cols) {
-            uint4 *dst = reinterpret_cast<uint4 *>(row + c0 + lane * 8);
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(p) / 16; ++i)
-                dst[i] = reinterpret_cast<const uint4 *>(&p)[i];
-        }
+        if (c0 + lane * 8 < cols)
+            store_pack(row + c0 + lane * 8, p);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
