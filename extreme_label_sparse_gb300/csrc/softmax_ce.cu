@@ -111,13 +111,13 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
     if constexpr (MODE != kGrad) {
         // bands of kBand row tiles; inside a band the row tile runs fastest,
         // so W is read from memory once for a band
-        const int64_t l = (int64_t)i * C + c;
-        if (l >= (int64_t)a.nm * a.nn)
+        const uint32_t l = (uint32_t)i * C + c;
+        if (l >= (uint32_t)(a.nm * a.nn))  // below 2^31
             return false;
-        const int64_t per = (int64_t)kBand * a.nn;
-        const int b = (int)(l / per), r = (int)(l - b * per);
-        const int mc = min(kBand, a.nm - b * kBand);
-        const int n = r / mc;
+        const uint32_t per = kBand * a.nn;
+        const uint32_t b = a.nm <= kBand ? 0 : l / per, r = l - b * per;
+        const uint32_t mc = min(kBand, a.nm - b * kBand);
+        const uint32_t n = r / mc;
         t.kind = 0;
         t.m0 = (b * kBand + (r - n * mc)) * BM;
         t.n0 = n * kBN;
@@ -365,10 +365,17 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                             v[x] *= hs * (a.W_scale && cc + x < left ? __ldg(a.W_scale + col0 + cc + x) : 1.f);
                     }
                     if (tgt >= cc && tgt < cc + 32) {
+                        // in this form so that v stays in registers (an index
+                        // known only at run time would put it into memory,
+                        // for every chunk)
                         float z = 0.f;
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
-                            z += x == tgt - cc ? v[x] : 0.f;
+                            asm("{\n\t.reg .pred p;\n\t"
+                                "setp.eq.s32 p, %2, %3;\n\t"
+                                "@p mov.f32 %0, %1;\n\t}"
+                                : "+f"(z)
+                                : "f"(v[x]), "r"(tgt - cc), "r"(x));
                         a.ztgt[row] = z;
                     }
                     if (a.zsum) {
@@ -510,8 +517,10 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 const uint32_t bar = smem_u32(&c.tempty[buf]);
+                // the accumulator's values are in registers already (wait::ld):
+                // nothing in memory has to be visible with this arrival
                 if constexpr (CG == 2)
-                    mbar_arrive_remote(mapa(bar, 0));
+                    mbar_arrive_remote_relaxed(mapa(bar, 0));
                 else
                     mbar_arrive(bar);
             }
@@ -815,9 +824,10 @@ sg_status check_ce(const char *fn, const void *h, int64_t ldh, int64_t T, int64_
     if (T < 0 || H < 1 || V < 1)
         CE_FAIL(SG_ERR_INVALID, "%s: need T >= 0, H >= 1 and V >= 1 (T=%lld H=%lld V=%lld)", fn, (long long)T,
                 (long long)H, (long long)V);
-    if (T > (1 << 24) || H > (1 << 20) || V > (1ll << 30))
-        CE_FAIL(SG_ERR_UNSUPPORTED, "%s: T=%lld, H=%lld or V=%lld is above 2^24, 2^20 or 2^30", fn, (long long)T,
-                (long long)H, (long long)V);
+    // the last: tiles are counted in 31 bits
+    if (T > (1 << 24) || H > (1 << 20) || V > (1ll << 30) || ceil_div(T, 128) * ceil_div(V, 128) >= (1ll << 31))
+        CE_FAIL(SG_ERR_UNSUPPORTED, "%s: T=%lld, H=%lld, V=%lld or T V is above 2^24, 2^20, 2^30 or 2^45", fn,
+                (long long)T, (long long)H, (long long)V);
     if (ldh < H || ldw < H)
         CE_FAIL(SG_ERR_INVALID, "%s: a row stride (%lld, %lld) is below H=%lld", fn, (long long)ldh, (long long)ldw,
                 (long long)H);

@@ -474,7 +474,7 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  * start on 16 bytes are first copied into the work memory.
  * status (device int32, may be NULL): sticky, first error wins, SG_ERR_TIMEOUT
  * where a bounded wait gave up and the outputs are not complete; the caller
- * clears it.  T <= 2^24, H <= 2^20, V <= 2^30.
+ * clears it.  T <= 2^24, H <= 2^20, V <= 2^30, T V < 2^45.
  * Errors: SG_ERR_INVALID for NULL pointers, sizes below 1 (T below 0), row
  * strides below H, smoothing outside [0, 1], work memory that is too small or
  * not aligned to 256 bytes.  sg_softmax_ce_work wants the same h, W and strides
