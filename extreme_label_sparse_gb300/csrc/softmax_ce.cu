@@ -80,19 +80,19 @@ struct CeArgs {
     // kLse
     const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
     const int32_t *targets;
-    float2 *part;         // [slot][Tp] running maximum (of z log2 e) and sum
-    float *zsum;          // [slot][Tp] sum of z, or NULL
+    float2 *part;         // running maximum (of z log2 e) and sum: [row][slot] for one row tile, else [slot][row]
+    float *zsum;          // the same for the sum of z, or NULL
     float *ztgt;          // [T] the target's logit
     int32_t Tp, ignore;
     // kProb
-    const float *lse, *dloss, *gscale;  // gscale: factor of g
-    float smooth;
+    const float *lse, *dloss;
+    float *gscale;        // factor of g and its inverse, written by the first CTA
+    float smooth, full;   // full: see g_scale
     // kGrad: dh units first (rows x features x pieces of K), then dW tiles
     int32_t dh_tiles, dh_nn, dh_split, dh_kb;  // tiles, tiles along H, pieces, K blocks in all
     int32_t dw_tiles, dw_nn, dw_hi, dw_lo, dw_nk;
     int32_t first;        // the piece is the first: dh sums start from zero
     float *acc;           // dh sums, [unit][CTA][column / 4][128 rows][4]
-    const float *ginv;    // 1 / gscale
     uint16_t *dW;         // where dW's rows do not suit TMA, else NULL
     int64_t lddW;
     int32_t *status;
@@ -190,6 +190,42 @@ __device__ __forceinline__ void stage_words(uint8_t *stg, int lane, int word0, c
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
+// Factor of g before it is rounded to 16 bits; the products' epilogues take it
+// out again.  It brings the largest |dloss| (1 - e), the target's part of g, to
+// just `full` (1, or 2^14 in fp16, whose range would not hold dloss = 1 / T
+// times a probability).  With the same dloss in every row, as in a mean, all
+// targets' parts are then a little below a power of two, where a rounding is
+// smallest against its value; without it they would all be rounded the same
+// way at wherever 1 / T falls (measured at T = 777, fp16, e = 0.1: 4.3e-4 of
+// error in dh instead of 2.7e-4 by the output's own rounding).  The epilogue
+// warps of every CTA work it out while the first tile is under way.
+__device__ __forceinline__ float g_scale(const CeArgs &a, float *sm)
+{
+    float top = 0.f;
+    for (int t = threadIdx.x; t < a.T; t += kEpiWarps * 32) {
+        const float v = fabsf(a.dloss[t]);
+        if (v < INFINITY)
+            top = fmaxf(top, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0)
+        sm[threadIdx.x / 32] = top;
+    named_bar(1, kEpiWarps * 32);
+    for (int w = 0; w < kEpiWarps; ++w)
+        top = fmaxf(top, sm[w]);
+    // |g| <= |dloss|: with a factor of at least 1/2, g stays below 2 full
+    top *= fmaxf(1.f - a.smooth, 0.5f);
+    const bool plain = !(top >= 1e-30f && top <= 1e30f);
+    const float s = plain ? 1.f : a.full / top;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.gscale[0] = s;
+        a.gscale[1] = plain ? 1.f : top / a.full;
+    }
+    return s;
+}
+
 // maps: kLse, kProb: A = h, B = W, out = g (kProb); kGrad: g, W, h, out = dW
 template <int CG, int MODE, bool F8>
 __global__ void __launch_bounds__(kCeThreads, 1)
@@ -200,6 +236,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     constexpr int NS = K::NS;
     constexpr int KE = F8 ? 128 : 64;  // elements of a K block
     __shared__ CeCtl c;
+    __shared__ float sm_top[kEpiWarps];
     extern __shared__ uint8_t dsm[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_rank() : 0;
@@ -226,6 +263,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     if constexpr (CG == 2)
         cluster_sync();
     tc_fence_after();
+    grid_wait();
+    grid_go();
     const uint32_t tbase = c.tmem;
     volatile int *abort_flag = &c.abort_flag;
     Tile t;
@@ -321,6 +360,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         uint8_t *stg = dsm + (base - smem_u32(dsm)) + NS * K::kStage + warp * kStgWarp;
         const uint32_t stg_s = smem_u32(stg);
         float m2 = -INFINITY, s = 0.f, zs = 0.f;
+        [[maybe_unused]] float scale = 1.f;
+        if constexpr (MODE == kProb)
+            scale = g_scale(a, sm_top);
         int it = 0;
         for (int i = 0; tile_at<CG, MODE>(a, cl, i, t); ++i) {
             if (t.nk == 0)
@@ -341,7 +383,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     if constexpr (MODE == kProb) {
                         l2 = a.lse[row] * kLog2e;
                         if (live)
-                            cf = a.dloss[row] * a.gscale[0];
+                            cf = a.dloss[row] * scale;
                         else
                             l2 = INFINITY;
                     } else if constexpr (F8) {
@@ -472,7 +514,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         }
                     }
                 } else {
-                    const float inv = a.ginv[0];
+                    const float inv = a.gscale[1];
                     const int64_t row0 = (int64_t)a.v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
 #pragma unroll 1
                     for (int cc = 0; cc < kBN / 2; cc += 32) {
@@ -528,7 +570,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         }
         if constexpr (MODE == kLse) {
             if (a.nm == 1) {
-                const int64_t at = (int64_t)(cl * 2 + half) * a.Tp + row_in;
+                const int64_t at = (int64_t)row_in * (2 * K::C) + cl * 2 + half;
                 a.part[at] = make_float2(m2, s);
                 if (a.zsum)
                     a.zsum[at] = zs;
@@ -549,120 +591,144 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 }
 
 // ---------------------------------------------------------------- small kernels
-// lse and loss of 32 rows from their partial maxima and sums
-__global__ void __launch_bounds__(1024)
-    k_ce_join(const float2 *__restrict__ part, const float *__restrict__ zsum, const float *__restrict__ ztgt,
-              int slots, int Tp, int T, int V, const int32_t *__restrict__ targets, int ignore, float smooth,
-              float *__restrict__ loss, float *__restrict__ lse, int32_t *status)
+// one more partial maximum (of z log2 e) and sum
+__device__ __forceinline__ void join_one(float &m, float &s, float2 p)
+{
+    const float mn = fmaxf(m, p.x), ms = mn == -INFINITY ? 0.f : mn;
+    s = s * exp2f(m - ms) + p.y * exp2f(p.x - ms);
+    m = mn;
+}
+
+struct JoinArgs {
+    const float2 *part;
+    const float *zsum, *ztgt;
+    const int32_t *targets;
+    float *loss, *lse;
+    int32_t *status;
+    int32_t slots, Tp, T, V, ignore;
+    float smooth;
+};
+
+__device__ __forceinline__ void join_out(const JoinArgs &a, int t, float m, float s, float zs)
+{
+    const float l = (m + log2f(s)) * kLn2;
+    a.lse[t] = l;
+    const int y = a.targets[t];
+    float out = 0.f;
+    if (y >= 0 && y < a.V && y != a.ignore) {
+        out = l - (1.f - a.smooth) * a.ztgt[t];
+        if (a.zsum)
+            out -= a.smooth * (zs / (float)a.V);
+    } else if (y != a.ignore && a.status) {
+        sg_flag(a.status, SG_ERR_DATA);
+    }
+    a.loss[t] = out;
+}
+
+// lse and loss of 32 rows from their partial maxima and sums, [slot][row]
+__global__ void __launch_bounds__(1024) k_ce_join(const JoinArgs a)
 {
     __shared__ float2 sm[32][33];
     __shared__ float sz[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int t = blockIdx.x * 32 + lane;  // below Tp, a multiple of 128
     float m = -INFINITY, s = 0.f, zs = 0.f;
-    for (int i = warp; i < slots; i += 32) {
-        const float2 p = part[(int64_t)i * Tp + t];
-        const float mn = fmaxf(m, p.x), ms = mn == -INFINITY ? 0.f : mn;
-        s = s * exp2f(m - ms) + p.y * exp2f(p.x - ms);
-        m = mn;
-        if (zsum)
-            zs += zsum[(int64_t)i * Tp + t];
+    grid_wait();
+    for (int i = warp; i < a.slots; i += 32) {
+        join_one(m, s, a.part[(int64_t)i * a.Tp + t]);
+        if (a.zsum)
+            zs += a.zsum[(int64_t)i * a.Tp + t];
     }
     sm[warp][lane] = make_float2(m, s);
     sz[warp][lane] = zs;
     __syncthreads();
-    if (warp != 0 || t >= T)
+    if (warp != 0 || t >= a.T)
         return;
     for (int w = 1; w < 32; ++w) {
-        const float2 p = sm[w][lane];
-        const float mn = fmaxf(m, p.x), ms = mn == -INFINITY ? 0.f : mn;
-        s = s * exp2f(m - ms) + p.y * exp2f(p.x - ms);
-        m = mn;
+        join_one(m, s, sm[w][lane]);
         zs += sz[w][lane];
     }
-    const float l = (m + log2f(s)) * kLn2;
-    lse[t] = l;
-    const int y = targets[t];
-    float out = 0.f;
-    if (y >= 0 && y < V && y != ignore) {
-        out = l - (1.f - smooth) * ztgt[t];
-        if (zsum)
-            out -= smooth * (zs / (float)V);
-    } else if (y != ignore && status) {
-        sg_flag(status, SG_ERR_DATA);
-    }
-    loss[t] = out;
+    join_out(a, t, m, s, zs);
 }
 
-// Factor of g before it is rounded to 16 bits; the products' epilogues take it
-// out again.  It brings the largest |dloss| (1 - e), the target's part of g, to
-// just `full` (1, or 2^14 in fp16, whose range would not hold dloss = 1 / T
-// times a probability).  With the same dloss in every row, as in a mean, all
-// targets' parts are then a little below a power of two, where a rounding is
-// smallest against its value; without it they would all be rounded the same
-// way at wherever 1 / T falls (measured at T = 777, fp16, e = 0.1: 4.3e-4 of
-// error in dh instead of 2.7e-4 by the output's own rounding).
-__global__ void __launch_bounds__(1024)
-    k_ce_gscale(const float *__restrict__ dloss, int T, float hit, float full, float *__restrict__ out)
+// the same for one row tile, [row][slot]: a CTA for a row, whose slots (at most
+// 3 x 128) are loaded together
+__global__ void __launch_bounds__(128) k_ce_join_row(const JoinArgs a)
 {
-    __shared__ float sm[32];
-    float top = 0.f;
-    for (int t = threadIdx.x; t < T; t += 1024) {
-        const float v = fabsf(dloss[t]);
-        if (v < INFINITY)
-            top = fmaxf(top, v);
+    __shared__ float sm[3][4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = blockIdx.x;
+    float2 p[3];
+    float zs = 0.f;
+    grid_wait();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const int i = threadIdx.x + 128 * j;
+        const bool in = i < a.slots;
+        p[j] = in ? a.part[(int64_t)t * a.slots + i] : make_float2(-INFINITY, 0.f);
+        if (a.zsum)
+            zs += in ? a.zsum[(int64_t)t * a.slots + i] : 0.f;
     }
+    float m = fmaxf(fmaxf(p[0].x, p[1].x), p[2].x);
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0)
-        sm[threadIdx.x / 32] = top;
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0)
+        sm[0][warp] = m;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 32; ++w)
-            top = fmaxf(top, sm[w]);
-        // |g| <= |dloss|: with hit >= 1/2, g stays below 2 full
-        top *= hit;
-        const bool plain = !(top >= 1e-30f && top <= 1e30f);
-        out[0] = plain ? 1.f : full / top;
-        out[1] = plain ? 1.f : top / full;
+    m = fmaxf(fmaxf(sm[0][0], sm[0][1]), fmaxf(sm[0][2], sm[0][3]));
+    const float ms = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        s += p[j].y * exp2f(p[j].x - ms);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        zs += __shfl_xor_sync(0xffffffffu, zs, o);
     }
+    if (lane == 0) {
+        sm[1][warp] = s;
+        sm[2][warp] = zs;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        join_out(a, t, m, (sm[1][0] + sm[1][1]) + (sm[1][2] + sm[1][3]),
+                 (sm[2][0] + sm[2][1]) + (sm[2][2] + sm[2][3]));
 }
 
-// dh = the sum of its pieces, 32 rows x 64 columns to a CTA
+// dh = the sum of its pieces, 32 rows x 32 columns to a CTA, a warp for four
+// columns
 template <int CG>
 __global__ void __launch_bounds__(256)
-    k_ce_dh(const float4 *__restrict__ acc, int tiles, int nn, int split, int T, int H, const float *ginv, int f16,
-            uint16_t *__restrict__ dh, int64_t lddh)
+    k_ce_dh(const float4 *__restrict__ acc, int tiles, int nn, int split, int T, int H,
+            const float *__restrict__ gscale, int f16, uint16_t *__restrict__ dh, int64_t lddh)
 {
-    __shared__ uint16_t sm[32][66];
+    __shared__ uint16_t sm[32][34];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int x = blockIdx.x / (CG * 4), rq = blockIdx.x % (CG * 4);  // tile, 32-row quarter of it
-    const int row0 = x / nn * Cfg<CG>::BM + rq * 32, col0 = x % nn * kBN + blockIdx.y * 64;
+    const int x = blockIdx.x / (CG * 4), rq = blockIdx.x % (CG * 4);  // tile, 32-row part of it
+    const int row0 = x / nn * Cfg<CG>::BM + rq * 32, col0 = x % nn * kBN + blockIdx.y * 32;
     if (row0 >= T || col0 >= H)
         return;
-    const float inv = ginv[0];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int c4 = warp * 2 + j;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < split; ++s) {
-            const int64_t u = (int64_t)s * tiles + x;
-            const float4 o =
-                acc[((u * CG + rq / 4) * (kBN / 4) + blockIdx.y * 16 + c4) * 128 + (rq & 3) * 32 + lane];
-            v.x += o.x;
-            v.y += o.y;
-            v.z += o.z;
-            v.w += o.w;
-        }
-        *reinterpret_cast<uint32_t *>(&sm[lane][c4 * 4]) = pack16(v.x * inv, v.y * inv, f16);
-        *reinterpret_cast<uint32_t *>(&sm[lane][c4 * 4 + 2]) = pack16(v.z * inv, v.w * inv, f16);
+    grid_wait();
+    const float inv = gscale[1];
+    const float4 *src =
+        acc + (((int64_t)x * CG + rq / 4) * (kBN / 4) + blockIdx.y * 8 + warp) * 128 + (rq & 3) * 32 + lane;
+    const int64_t step = (int64_t)tiles * CG * (kBN / 4) * 128;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < split; ++s) {
+        const float4 o = src[s * step];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
     }
+    *reinterpret_cast<uint32_t *>(&sm[lane][warp * 4]) = pack16(v.x * inv, v.y * inv, f16);
+    *reinterpret_cast<uint32_t *>(&sm[lane][warp * 4 + 2]) = pack16(v.z * inv, v.w * inv, f16);
     __syncthreads();
     for (int r = warp; r < 32 && row0 + r < T; r += 8)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (col0 + lane + 32 * j < H)
-                dh[(int64_t)(row0 + r) * lddh + col0 + lane + 32 * j] = sm[r][lane + 32 * j];
+        if (col0 + lane < H)
+            dh[(int64_t)(row0 + r) * lddh + col0 + lane] = sm[r][lane];
 }
 
 // rows that do not start on 16 bytes, copied to a stride that does
@@ -709,9 +775,37 @@ sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, i
     return SG_OK;
 }
 
+// `after`: the kernel before it in the stream is one of this call's, which this
+// one may overlap
+template <typename... P, typename... A>
+sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, bool after, cudaStream_t st,
+                 A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    cfg.attrs = at;
+    cfg.numAttrs = 0;
+    if (cluster > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+        at[cfg.numAttrs].val.clusterDim.y = 1;
+        at[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    if (after) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    SG_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return SG_OK;
+}
+
 template <int CG, int MODE, bool F8>
 sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CUtensorMap &dW,
-                    const CeArgs &a, cudaStream_t st)
+                    const CeArgs &a, bool after, cudaStream_t st)
 {
     // once for each device (one bit of the mask)
     static std::atomic<uint64_t> done{0};
@@ -723,20 +817,8 @@ sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMa
                                          (int)Cfg<CG>::kSmem));
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(Cfg<CG>::C * CG);
-    cfg.blockDim = dim3(kCeThreads);
-    cfg.dynamicSmemBytes = Cfg<CG>::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    SG_TRY_CUDA(cudaLaunchKernelEx(&cfg, k_ce<CG, MODE, F8>, h, W, g, dW, a));
-    return SG_OK;
+    return launch(k_ce<CG, MODE, F8>, dim3(Cfg<CG>::C * CG), kCeThreads, (int)Cfg<CG>::kSmem, CG, after, st, h, W, g,
+                  dW, a);
 }
 
 // One call's tiles and the places of its work memory
@@ -756,8 +838,10 @@ struct Plan {
 
 bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
 
-// K blocks that a tile's epilogue costs where its own product is shorter
-int64_t tile_cost(int64_t nk) { return (nk > 6 ? nk : 6) + 1; }
+// Time of a tile or dh unit of nk K blocks, in half K blocks: a tile that is
+// shorter than its output takes to reach memory (2 K blocks of a CTA, 4 of a
+// pair) costs that, and each has a little of its own.
+int64_t tile_cost(int64_t nk, int CG) { return 2 * (nk > 2 * CG ? nk : 2 * CG) + 1; }
 
 void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
                int32_t dtype, bool backward, Plan *p)
@@ -798,10 +882,10 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     p->dh_nn = ceil_div(H, kBN);
     p->dh_tiles = p->nm * p->dh_nn;
     // split K of dh until its units and the dW tiles fill the clusters evenly
-    const int64_t kb = ceil_div(V < Vc ? V : Vc, 64), dw = ceil_div(Vc, p->BM) * p->dh_nn * tile_cost(ceil_div(T, 64));
+    const int64_t kb = ceil_div(V < Vc ? V : Vc, 64), dw = ceil_div(Vc, p->BM) * p->dh_nn * tile_cost(ceil_div(T, 64), p->CG);
     double best = 0;
     for (int64_t n = 1; n <= kb && n <= 64; ++n) {
-        const int64_t units = p->dh_tiles * n, cost = tile_cost(ceil_div(kb, n)) + 2;
+        const int64_t units = p->dh_tiles * n, cost = tile_cost(ceil_div(kb, n), p->CG) + 2;
         const double even = (double)(units * cost + dw) / p->C;
         const double last = (double)(ceil_div(units, p->C) * cost);
         const double span = (even > last ? even : last) * (1.0 + 0.002 * (double)n);
@@ -927,16 +1011,18 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     a.Tp = (int32_t)p.Tp;
     a.status = status;
     if (dtype == SG_E4M3)
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, a, st))
-                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, a, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, a, false, st))
+                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, a, false, st)));
     else
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, a, st))
-                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, a, st)));
-    k_ce_join<<<(unsigned)ceil_div(T, 32), 1024, 0, st>>>(a.part, a.zsum, a.ztgt, (int)p.slots, (int)p.Tp, (int)T,
-                                                          (int)V, targets, ignore_index, (float)smoothing, loss, lse,
-                                                          status);
-    SG_TRY_CUDA(cudaGetLastError());
-    return SG_OK;
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, a, false, st))
+                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, a, false, st)));
+    JoinArgs j;
+    j.part = a.part, j.zsum = a.zsum, j.ztgt = a.ztgt, j.targets = targets, j.loss = loss, j.lse = lse;
+    j.status = status, j.slots = (int32_t)p.slots, j.Tp = a.Tp, j.T = a.T, j.V = a.V, j.ignore = ignore_index;
+    j.smooth = (float)smoothing;
+    if (p.nm == 1)
+        return launch(k_ce_join_row, dim3((unsigned)T), 128, 0, 1, true, st, j);
+    return launch(k_ce_join, dim3((unsigned)ceil_div(T, 32)), 1024, 0, 1, true, st, j);
 }
 
 sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
@@ -997,42 +1083,34 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     a.dW = dW && !dw_tma ? static_cast<uint16_t *>(dW) : nullptr;
     a.lddW = lddw;
     a.status = status;
-    float *gs = reinterpret_cast<float *>(w8 + p.o_gs);
-    k_ce_gscale<<<1, 1024, 0, st>>>(dloss, (int)T, (float)(smoothing < 0.5 ? 1.0 - smoothing : 0.5),
-                                    dtype == SG_F16 ? 16384.f : 1.f, gs);
-    SG_TRY_CUDA(cudaGetLastError());
-    a.gscale = gs;
-    a.ginv = gs + 1;
+    a.gscale = reinterpret_cast<float *>(w8 + p.o_gs);
+    a.full = dtype == SG_F16 ? 16384.f : 1.f;
     for (int64_t v0 = 0; v0 < V; v0 += p.Vc) {
         const int64_t vc = V - v0 < p.Vc ? V - v0 : p.Vc;
         a.v0 = (int32_t)v0;
         a.first = v0 == 0;
         a.nn = (int32_t)ceil_div(vc, kBN);
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kProb, false>(mh, mW, mgs, mdW, a, st))
-                         : (launch_ce<2, kProb, false>(mh, mW, mgs, mdW, a, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kProb, false>(mh, mW, mgs, mdW, a, v0 > 0, st))
+                         : (launch_ce<2, kProb, false>(mh, mW, mgs, mdW, a, v0 > 0, st)));
         a.dh_kb = (int32_t)ceil_div(vc, 64);
         a.dw_tiles = dW ? (int32_t)(ceil_div(vc, p.BM) * p.dh_nn) : 0;
         // turns of dW tiles so that all clusters end at about the same time
         const int64_t units = (int64_t)a.dh_tiles * p.split, hi = units % p.C;
-        const int64_t less = dh ? ceil_div(tile_cost(ceil_div(a.dh_kb, p.split)) + 2, tile_cost(a.dw_nk)) : 0;
+        const int64_t less = dh ? ceil_div(tile_cost(ceil_div(a.dh_kb, p.split), p.CG) + 2, tile_cost(a.dw_nk, p.CG)) : 0;
         int64_t q_hi = hi ? (a.dw_tiles - less * (p.C - hi)) / p.C : 0;
         if (q_hi < 0)
             q_hi = 0;
         a.dw_hi = (int32_t)q_hi;
         a.dw_lo = (int32_t)(q_hi + ceil_div(a.dw_tiles - q_hi * p.C > 0 ? a.dw_tiles - q_hi * p.C : 0, p.C - hi));
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mh, mW, mg, mdW, a, st))
-                         : (launch_ce<2, kGrad, false>(mh, mW, mg, mdW, a, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mh, mW, mg, mdW, a, true, st))
+                         : (launch_ce<2, kGrad, false>(mh, mW, mg, mdW, a, true, st)));
     }
     if (dh) {
-        const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), kBN / 64);
+        const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), kBN / 32);
         const float4 *acc = reinterpret_cast<const float4 *>(a.acc);
-        if (p.CG == 1)
-            k_ce_dh<1><<<grid, 256, 0, st>>>(acc, (int)p.dh_tiles, (int)p.dh_nn, (int)p.split, (int)T, (int)H, a.ginv,
-                                             a.f16, static_cast<uint16_t *>(dh), lddh);
-        else
-            k_ce_dh<2><<<grid, 256, 0, st>>>(acc, (int)p.dh_tiles, (int)p.dh_nn, (int)p.split, (int)T, (int)H, a.ginv,
-                                             a.f16, static_cast<uint16_t *>(dh), lddh);
-        SG_TRY_CUDA(cudaGetLastError());
+        return launch(p.CG == 1 ? k_ce_dh<1> : k_ce_dh<2>, grid, 256, 0, 1, true, st, acc, (int)p.dh_tiles,
+                      (int)p.dh_nn, (int)p.split, (int)T, (int)H, (const float *)a.gscale, (int)a.f16,
+                      static_cast<uint16_t *>(dh), lddh);
     }
     return SG_OK;
 }

@@ -452,6 +452,15 @@ __device__ __forceinline__ void red_add_v4(float *dst, float a, float b, float c
                  : "memory");
 }
 
+// ------------------------------------------------------------------ launches that overlap
+// A kernel launched with programmatic stream serialization may start while the
+// kernel before it still runs.  grid_wait returns when that kernel has ended
+// and its writes are visible; every CTA calls it before it touches what the
+// earlier kernel reads or writes (returns at once in an ordinary launch).
+// grid_go lets the next kernel's CTAs in as soon as there is room for them.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ CTA pairs
 // tcgen05 operations of one CTA (CG = 1) or of the pair of a 2-CTA cluster
 // (CG = 2).  A pair's MMA is issued by one thread of the rank-0 CTA; its A and
