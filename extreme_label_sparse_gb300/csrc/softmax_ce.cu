@@ -89,8 +89,9 @@ struct CeArgs {
     float *gscale;        // factor of g and its inverse, written by the first CTA
     float smooth, full;   // full: see g_scale
     // kGrad: dh units first (rows x features x pieces of K), then dW tiles
-    int32_t dh_tiles, dh_nn, dh_split, dh_kb;  // tiles, tiles along H, pieces, K blocks in all
-    int32_t dw_tiles, dw_nn, dw_hi, dw_lo, dw_nk;
+    int32_t nh;           // tiles along H
+    int32_t dh_tiles, dh_split, dh_kb, dh_each, dh_hi;  // tiles, pieces of K, K blocks; units of a cluster
+    int32_t dw_tiles, dw_hi, dw_lo, dw_nk;
     int32_t first;        // the piece is the first: dh sums start from zero
     float *acc;           // dh sums, [unit][CTA][column / 4][128 rows][4]
     uint16_t *dW;         // where dW's rows do not suit TMA, else NULL
@@ -126,34 +127,35 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
         t.unit = n;
         return true;
     } else {
-        const int units = a.dh_tiles * a.dh_split;
-        const int hi = units % C;  // clusters below `hi` have one dh unit more
-        const int mine = units / C + (c < hi ? 1 : 0);
-        if (i < mine) {
-            const int u = i * C + c, s = u / a.dh_tiles, x = u - s * a.dh_tiles;
+        const uint32_t hi = a.dh_hi;  // clusters below it have one dh unit more
+        const uint32_t mine = a.dh_each + ((uint32_t)c < hi ? 1 : 0);
+        if ((uint32_t)i < mine) {
+            const uint32_t u = (uint32_t)i * C + c, s = u / (uint32_t)a.dh_tiles, x = u - s * a.dh_tiles;
+            const uint32_t m = x / (uint32_t)a.nh;
             t.kind = 1;
-            t.m0 = x / a.dh_nn * BM;
-            t.n0 = x % a.dh_nn * kBN;
+            t.m0 = m * BM;
+            t.n0 = (x - m * a.nh) * kBN;
             t.k0 = (int)((int64_t)s * a.dh_kb / a.dh_split);
             t.nk = (int)((int64_t)(s + 1) * a.dh_kb / a.dh_split) - t.k0;
             t.unit = u;
             return true;
         }
-        i -= mine;
+        const uint32_t j = (uint32_t)i - mine;
         // dW tiles in turn over the clusters; those with one dh unit more take
         // only the first dw_hi turns
-        int64_t l;
-        if (i < a.dw_hi)
-            l = (int64_t)i * C + c;
-        else if (i < a.dw_lo && c >= hi)
-            l = (int64_t)a.dw_hi * C + (int64_t)(i - a.dw_hi) * (C - hi) + (c - hi);
+        uint32_t l;
+        if (j < (uint32_t)a.dw_hi)
+            l = j * C + c;
+        else if (j < (uint32_t)a.dw_lo && (uint32_t)c >= hi)
+            l = a.dw_hi * C + (j - a.dw_hi) * (C - hi) + (c - hi);
         else
             return false;
-        if (l >= a.dw_tiles)
+        if (l >= (uint32_t)a.dw_tiles)
             return false;
+        const uint32_t m = l / (uint32_t)a.nh;
         t.kind = 2;
-        t.m0 = (int)(l / a.dw_nn) * BM;
-        t.n0 = (int)(l % a.dw_nn) * kBN;
+        t.m0 = m * BM;
+        t.n0 = (l - m * a.nh) * kBN;
         t.k0 = 0;
         t.nk = a.dw_nk;
         t.unit = 0;
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         [[maybe_unused]] float scale = 1.f;
         if constexpr (MODE == kProb)
             scale = g_scale(a, sm_top);
+        if constexpr (MODE == kGrad)
+            scale = a.gscale[1];
         int it = 0;
         for (int i = 0; tile_at<CG, MODE>(a, cl, i, t); ++i) {
             if (t.nk == 0)
@@ -514,7 +518,6 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         }
                     }
                 } else {
-                    const float inv = a.gscale[1];
                     const int64_t row0 = (int64_t)a.v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
 #pragma unroll 1
                     for (int cc = 0; cc < kBN / 2; cc += 32) {
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         uint32_t w[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            w[x] = pack16(v[2 * x] * inv, v[2 * x + 1] * inv, a.f16);
+                            w[x] = pack16(v[2 * x] * scale, v[2 * x + 1] * scale, a.f16);
                         if ((cc & 32) == 0) {
                             if (lane == 0)
                                 bulk_wait_read<0>();
@@ -1075,7 +1078,7 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     a.lse = lse;
     a.dloss = dloss;
     a.smooth = (float)smoothing;
-    a.dh_nn = a.dw_nn = (int32_t)p.dh_nn;
+    a.nh = (int32_t)p.dh_nn;
     a.dh_split = (int32_t)p.split;
     a.dh_tiles = dh ? (int32_t)p.dh_tiles : 0;
     a.dw_nk = (int32_t)ceil_div(T, 64);
@@ -1096,6 +1099,8 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
         a.dw_tiles = dW ? (int32_t)(ceil_div(vc, p.BM) * p.dh_nn) : 0;
         // turns of dW tiles so that all clusters end at about the same time
         const int64_t units = (int64_t)a.dh_tiles * p.split, hi = units % p.C;
+        a.dh_each = (int32_t)(units / p.C);
+        a.dh_hi = (int32_t)hi;
         const int64_t less = dh ? ceil_div(tile_cost(ceil_div(a.dh_kb, p.split), p.CG) + 2, tile_cost(a.dw_nk, p.CG)) : 0;
         int64_t q_hi = hi ? (a.dw_tiles - less * (p.C - hi)) / p.C : 0;
         if (q_hi < 0)
