@@ -5,11 +5,9 @@
 //   dh = g W,  dW = g^T h.
 // The logits never reach memory.  Forward: one matrix product whose epilogue
 // reduces each tile of logits to a running maximum and sum per row; a small
-// kernel joins them.  Backward: the vocabulary goes by in pieces.  The product
-// is taken again, its epilogue turning a piece's logits into g (16 bits, a few
-// pieces of it held at a time), and the two gradient products follow a few
-// pieces behind, so that they find the piece's W and g in the L2 cache: all in
-// one launch, whose CTAs wait for one another's pieces by counters.
+// kernel joins them.  Backward, over pieces of the vocabulary: the product
+// again, its epilogue turning logits into g (16 bits, one piece of it held at
+// a time), then one launch with the tiles of both gradient products.
 //
 // All three products share one kernel: a persistent CTA, or a pair of CTAs on
 // one 256 x 256 tile where there are more than 128 rows, walks a list of
@@ -22,7 +20,6 @@
 
 #include <atomic>
 #include <cmath>
-#include <cstdlib>
 
 #include "sg_internal.cuh"
 #include "tc_common.cuh"
@@ -49,10 +46,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kSMs = 152;
 constexpr int kEpiWarps = 8;
-constexpr int kCeThreads = 32 * (kEpiWarps + 4);
+constexpr int kCeThreads = 32 * (kEpiWarps + 2);
 constexpr int kBN = 256;                 // tile columns
 constexpr uint32_t kBox = 8192;          // one TMA box: 64 rows of 128 bytes
-constexpr uint32_t kStgWarp = 32 * 17 * 4;  // an epilogue warp's 32 x 32 outputs, rows 4 bytes apart
+constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's output box: 32 rows of 128 bytes
 constexpr int kBand = 16;                // row tiles that walk the vocabulary together
 
 template <int CG>
@@ -64,255 +61,115 @@ struct Cfg {
     static constexpr uint32_t kStage = kA + kB;
     static constexpr int NS = CG == 2 ? 6 : 4;
     static constexpr uint32_t kSmem = NS * kStage + kEpiWarps * kStgWarp + 1024;
+    static constexpr int C = kSMs / CG;            // clusters
 };
 
-enum Mode { kLse = 0, kBwd = 1 };
-
-struct CeArgs {
-    int32_t T, V, H;      // rows, vocabulary, features
-    int32_t C;            // clusters of the launch
-    int32_t nm, nn, nk;   // tiles of the logits (rows, columns; of a piece in kBwd), K blocks
-    int32_t f16;          // 16-bit operands are fp16, not bf16
-    const int32_t *targets;
-    int32_t ignore;
-    int32_t *status;
-    // kLse
-    const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
-    float2 *part;         // running maximum (of z log2 e) and sum: [row][slot] for one row tile, else [slot][row]
-    float *zsum;          // the same for the sum of z, or NULL
-    float *ztgt;          // [T] the target's logit
-    int32_t Tp;
-    // kBwd
-    const float *lse, *dloss;
-    float *gscale;        // factor of g and its inverse, written by the first CTA
-    float smooth, full;   // full: see g_scale
-    int32_t pieces, Vc, lag, ring;  // of the vocabulary; the gradients follow `lag` behind, g is held `ring` deep
-    int32_t nh;           // tiles along H
-    int32_t dh_tiles, dh_split, dh_units;  // tiles, pieces of K, their product (0: no dh)
-    int32_t dw, dw_nk;    // dW wanted; K blocks
-    int32_t dw_more;      // dW tiles that a cluster with one dh unit less takes before the others share the rest
-    float *acc;           // dh sums, [unit][CTA][column / 4][128 rows][4]
-    uint16_t *g, *dW;
-    int64_t ldg, lddW;
-    int32_t dw_align;     // bytes that dW's rows start on: 32, 16 or 2 (any)
-    uint32_t *g_done, *w_done;  // for each piece: CTAs that have stored a tile of g, gradient tiles that have read it
-};
-
-struct Tile {
-    int kind;  // 0: logits, 1: dh, 2: dW
-    int m0, n0, k0, nk, unit, piece;
-};
-
-// The tiles of cluster c, in the order in which each of its warps takes them.
-// In kBwd phase p has the logits of piece p and then the gradients of piece p -
-// lag.  A dh unit stays with one cluster through all pieces, which adds to its
-// sums in order; the other tiles go round the clusters, each kind going on
-// from one piece to the next where it stopped.
-template <int CG, int MODE>
-struct Walk {
-    uint32_t c, j = 0;
-    int phase = 0, stage = 0;
-
-    __device__ __forceinline__ explicit Walk(int cluster) : c((uint32_t)cluster) {}
-
-    // the j-th of this cluster's tiles in a round that starts at tile `from` of
-    // the kind
-    __device__ __forceinline__ uint32_t turn(const CeArgs &a, uint32_t from) const
-    {
-        const uint32_t C = a.C, at = from % C;
-        return (c >= at ? c - at : c + C - at) + j * C;
-    }
-
-    __device__ __forceinline__ bool next(const CeArgs &a, Tile &t)
-    {
-        constexpr int BM = Cfg<CG>::BM;
-        if constexpr (MODE == kLse) {
-            // bands of kBand row tiles; inside a band the row tile runs
-            // fastest, so W is read from memory once for a band
-            const uint32_t l = j++ * a.C + c;
-            if (l >= (uint32_t)(a.nm * a.nn))  // below 2^31
-                return false;
-            const uint32_t per = kBand * a.nn;
-            const uint32_t b = a.nm <= kBand ? 0 : l / per, r = l - b * per;
-            const uint32_t mc = min(kBand, a.nm - b * kBand);
-            const uint32_t n = r / mc;
-            t.kind = 0;
-            t.m0 = (b * kBand + (r - n * mc)) * BM;
-            t.n0 = n * kBN;
-            t.k0 = 0;
-            t.nk = a.nk;
-            t.unit = n;
-            t.piece = 0;
-            return true;
-        } else {
-            for (; phase < a.pieces + a.lag; ++phase, stage = 0, j = 0) {
-                if (stage == 0) {
-                    if (phase < a.pieces) {
-                        const int left = a.V - phase * a.Vc;
-                        const uint32_t n_p = a.nm * (phase + 1 < a.pieces ? a.nn : (left + kBN - 1) / kBN);
-                        const uint32_t r = turn(a, (uint32_t)phase * (uint32_t)(a.nm * a.nn));
-                        if (r < n_p) {
-                            const uint32_t n = r / (uint32_t)a.nm;
-                            t.kind = 0;
-                            t.m0 = (r - n * a.nm) * BM;
-                            t.n0 = n * kBN;
-                            t.k0 = 0;
-                            t.nk = a.nk;
-                            t.unit = 0;
-                            t.piece = phase;
-                            ++j;
-                            return true;
-                        }
-                    }
-                    stage = 1;
-                    j = 0;
-                }
-                const int q = phase - a.lag;
-                if (q < 0)
-                    continue;
-                const int vc = min(a.Vc, a.V - q * a.Vc);
-                t.piece = q;
-                if (stage == 1) {
-                    const int kb = (vc + 63) / 64;
-                    for (uint32_t u = c + j * a.C; u < (uint32_t)a.dh_units; u += a.C) {
-                        ++j;
-                        const uint32_t s = u / (uint32_t)a.dh_tiles, x = u - s * a.dh_tiles;
-                        const uint32_t m = x / (uint32_t)a.nh;
-                        t.k0 = (int)(s * kb / (uint32_t)a.dh_split);  // below 64 x 2^24
-                        t.nk = (int)((s + 1) * kb / (uint32_t)a.dh_split) - t.k0;
-                        if (t.nk == 0)  // a short last piece
-                            continue;
-                        t.kind = 1;
-                        t.m0 = m * BM;
-                        t.n0 = (x - m * a.nh) * kBN;
-                        t.unit = u;
-                        return true;
-                    }
-                    stage = 2;
-                    j = 0;
-                }
-                if (!a.dw)
-                    continue;
-                const uint32_t tiles = (vc + BM - 1) / BM * a.nh, hi = (uint32_t)a.dh_units % a.C;
-                const uint32_t first = min(tiles, a.dw_more * (a.C - hi));
-                uint32_t l;
-                if (stage == 2) {
-                    l = j * (a.C - hi) + (c - hi);
-                    if (j < (uint32_t)a.dw_more && c >= hi && l < first) {
-                        ++j;
-                    } else {
-                        stage = 3;
-                        j = 0;
-                    }
-                }
-                if (stage == 3) {
-                    const uint32_t all = (a.Vc + BM - 1) / BM * a.nh;
-                    l = first + turn(a, (uint32_t)q * (all - min(all, a.dw_more * (a.C - hi))));
-                    if (l >= tiles)
-                        continue;
-                    ++j;
-                }
-                const uint32_t m = l / (uint32_t)a.nh;
-                t.kind = 2;
-                t.m0 = m * BM;
-                t.n0 = (l - m * a.nh) * kBN;
-                t.k0 = 0;
-                t.nk = a.dw_nk;
-                t.unit = 0;
-                return true;
-            }
-            return false;
-        }
-    }
-};
-
-constexpr int kTiles = 4;  // tiles known ahead
+enum Mode { kLse = 0, kProb = 1, kGrad = 2 };
 
 struct CeCtl {
     uint64_t full[6], empty[6], tfull[2], tempty[2];
-    uint64_t tile_full[kTiles], tile_empty[kTiles], stored[kTiles];
-    Tile tiles[kTiles];
     uint32_t tmem;
     int abort_flag;
 };
 
-// The tiles as one warp works them out (several divisions each) for the others,
-// which only read them: done by each warp for itself, the thread that issues
-// the MMAs would leave the tensor cores waiting between tiles (a fifth of the
-// time of the backward pass at 4096 x 2048 x 32000).
-struct Tiles {
-    Ring r;
-
-    // by the lanes in `mask` of a warp; false at the end, or where a wait gave up
-    __device__ __forceinline__ bool next(CeCtl &c, Tile &t, uint32_t mask, volatile int *abort_flag, int32_t *status)
-    {
-        if (!__all_sync(mask, mbar_wait(smem_u32(&c.tile_full[r.i]), r.ph, abort_flag, status)))
-            return false;
-        t = c.tiles[r.i];
-        __syncwarp(mask);
-        if ((threadIdx.x & 31) == 0)
-            mbar_arrive(smem_u32(&c.tile_empty[r.i]));
-        r.next(kTiles);
-        return t.kind >= 0;
-    }
+struct CeArgs {
+    int32_t T, V, H;      // rows, vocabulary, features
+    int32_t v0;           // first vocabulary row of the piece
+    int32_t nm, nn, nk;   // tiles of the logits (rows, columns of the piece), K blocks
+    int32_t f16;          // 16-bit operands are fp16, not bf16
+    // kLse
+    const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
+    const int32_t *targets;
+    float2 *part;         // running maximum (of z log2 e) and sum: [row][slot] for one row tile, else [slot][row]
+    float *zsum;          // the same for the sum of z, or NULL
+    float *ztgt;          // [T] the target's logit
+    int32_t Tp, ignore;
+    // kProb
+    const float *lse, *dloss;
+    float *gscale;        // factor of g and its inverse, written by the first CTA
+    float smooth, full;   // full: see g_scale
+    // kGrad: dh units first (rows x features x pieces of K), then dW tiles
+    int32_t nh;           // tiles along H
+    int32_t dh_tiles, dh_split, dh_kb, dh_each, dh_hi;  // tiles, pieces of K, K blocks; units of a cluster
+    int32_t dw_tiles, dw_hi, dw_lo, dw_nk;
+    int32_t first;        // the piece is the first: dh sums start from zero
+    float *acc;           // dh sums, [unit][CTA][column / 4][128 rows][4]
+    uint16_t *dW;         // where dW's rows do not suit TMA, else NULL
+    int64_t lddW;
+    int32_t *status;
 };
 
-// Bounded wait for a counter that other CTAs of the launch add to, before TMA
-// copies of what they wrote (or over what they read).
-__device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t want, volatile int *abort_flag,
-                                           int32_t *status)
+struct Tile {
+    int kind;  // 0: logits, 1: dh, 2: dW
+    int m0, n0, k0, nk, unit;
+};
+
+// tile i of cluster c
+template <int CG, int MODE>
+__device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
 {
-    const uint64_t t0 = global_ns();
-    for (uint32_t n = 1;; ++n) {
-        uint32_t v;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-        if (v >= want)
-            break;
-        if (*abort_flag)
+    constexpr int C = Cfg<CG>::C, BM = Cfg<CG>::BM;
+    if constexpr (MODE != kGrad) {
+        // bands of kBand row tiles; inside a band the row tile runs fastest,
+        // so W is read from memory once for a band
+        const uint32_t l = (uint32_t)i * C + c;
+        if (l >= (uint32_t)(a.nm * a.nn))  // below 2^31
             return false;
-        if ((n & 15u) == 0 && global_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            if (status)
-                sg_flag(status, SG_ERR_TIMEOUT);
-            return false;
+        const uint32_t per = kBand * a.nn;
+        const uint32_t b = a.nm <= kBand ? 0 : l / per, r = l - b * per;
+        const uint32_t mc = min(kBand, a.nm - b * kBand);
+        const uint32_t n = r / mc;
+        t.kind = 0;
+        t.m0 = (b * kBand + (r - n * mc)) * BM;
+        t.n0 = n * kBN;
+        t.k0 = 0;
+        t.nk = a.nk;
+        t.unit = n;
+        return true;
+    } else {
+        const uint32_t hi = a.dh_hi;  // clusters below it have one dh unit more
+        const uint32_t mine = a.dh_each + ((uint32_t)c < hi ? 1 : 0);
+        if ((uint32_t)i < mine) {
+            const uint32_t u = (uint32_t)i * C + c, s = u / (uint32_t)a.dh_tiles, x = u - s * a.dh_tiles;
+            const uint32_t m = x / (uint32_t)a.nh;
+            t.kind = 1;
+            t.m0 = m * BM;
+            t.n0 = (x - m * a.nh) * kBN;
+            t.k0 = (int)((int64_t)s * a.dh_kb / a.dh_split);
+            t.nk = (int)((int64_t)(s + 1) * a.dh_kb / a.dh_split) - t.k0;
+            t.unit = u;
+            return true;
         }
-        __nanosleep(64);
+        const uint32_t j = (uint32_t)i - mine;
+        // dW tiles in turn over the clusters; those with one dh unit more take
+        // only the first dw_hi turns
+        uint32_t l;
+        if (j < (uint32_t)a.dw_hi)
+            l = j * C + c;
+        else if (j < (uint32_t)a.dw_lo && (uint32_t)c >= hi)
+            l = a.dw_hi * C + (j - a.dw_hi) * (C - hi) + (c - hi);
+        else
+            return false;
+        if (l >= (uint32_t)a.dw_tiles)
+            return false;
+        const uint32_t m = l / (uint32_t)a.nh;
+        t.kind = 2;
+        t.m0 = m * BM;
+        t.n0 = (l - m * a.nh) * kBN;
+        t.k0 = 0;
+        t.nk = a.dw_nk;
+        t.unit = 0;
+        return true;
     }
-    asm volatile("fence.proxy.async;" ::: "memory");
-    return true;
 }
 
-// One more.  PUBLISH: all writes that this thread knows of come before it (they
-// have to be seen everywhere first, which takes a microsecond or two).
-template <bool PUBLISH>
-__device__ __forceinline__ void add_count(uint32_t *p)
-{
-    if constexpr (PUBLISH)
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
-    else
-        asm volatile("red.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
-}
-
-// Descriptors of an operand's tile at shared address `base`: the low word, to
-// which stages (bytes / 16) and K steps are added, the high word, and the step.
 // K-major: rows of 128 bytes of K, 8 rows to a swizzle atom.  MN-major: boxes
-// of 64 rows (128 bytes) by 64 K, kBox apart.  Worked out once for a tile: the
-// thread that issues the MMAs has little time for each.
-struct OpDesc {
-    uint32_t lo, hi, step;
-
-    __device__ __forceinline__ OpDesc(uint32_t base, bool mn)
-    {
-        const uint64_t d = sdesc(base, mn ? kBox : 16, 1024, kLayoutSW128);
-        lo = (uint32_t)d;
-        hi = (uint32_t)(d >> 32);
-        step = mn ? 2048 / 16 : 32 / 16;
-    }
-    __device__ __forceinline__ uint64_t at(uint32_t stage, int ks) const
-    {
-        return (uint64_t)hi << 32 | (lo + stage + ks * step);
-    }
-};
+// of 64 rows (128 bytes) by 64 K, kBox apart.
+__device__ __forceinline__ uint64_t op_desc(uint32_t tile, bool mn, int ks)
+{
+    return mn ? sdesc(tile + (uint32_t)ks * 2048, kBox, 1024, kLayoutSW128)
+              : sdesc(tile + (uint32_t)ks * 32, 16, 1024, kLayoutSW128);
+}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -324,6 +181,15 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16)
 {
     return f16 ? pack2_f16(a, b) : pack2(a, b);
+}
+
+// 64 columns (32 packed words) of this warp's 32 rows into its swizzled box
+__device__ __forceinline__ void stage_words(uint8_t *stg, int lane, int word0, const uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(stg + lane * 128 + ((((word0 >> 2) + i) ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
 // Factor of g before it is rounded to 16 bits; the products' epilogues take it
@@ -362,10 +228,11 @@ __device__ __forceinline__ float g_scale(const CeArgs &a, float *sm)
     return s;
 }
 
+// maps: kLse, kProb: A = h, B = W, out = g (kProb); kGrad: g, W, h, out = dW
 template <int CG, int MODE, bool F8>
 __global__ void __launch_bounds__(kCeThreads, 1)
     k_ce(const __grid_constant__ CUtensorMap m_h, const __grid_constant__ CUtensorMap m_W,
-         const __grid_constant__ CUtensorMap m_g, const CeArgs a)
+         const __grid_constant__ CUtensorMap m_g, const __grid_constant__ CUtensorMap m_dW, const CeArgs a)
 {
     using K = Cfg<CG>;
     constexpr int NS = K::NS;
@@ -386,11 +253,6 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c.tfull[b]), 1);
             mbar_init(smem_u32(&c.tempty[b]), CG * kEpiWarps);
-        }
-        for (int i = 0; i < kTiles; ++i) {
-            mbar_init(smem_u32(&c.tile_full[i]), 1);
-            mbar_init(smem_u32(&c.tile_empty[i]), kEpiWarps + 1 + (rank == 0) + (MODE == kBwd));
-            mbar_init(smem_u32(&c.stored[i]), kEpiWarps);
         }
         fence_mbar_init();
     }
@@ -414,22 +276,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         if (lane == 0) {
             Ring r;
             bool ok = true;
-            int seen = -1;  // last piece whose g was waited for
-            for (Tiles tiles; ok && tiles.next(c, t, 1u, abort_flag, a.status);) {
+            for (int i = 0; ok && tile_at<CG, MODE>(a, cl, i, t); ++i) {
                 const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
                 const CUtensorMap *ma = t.kind ? &m_g : &m_h, *mb = t.kind == 2 ? &m_h : &m_W;
-                // columns of g start at the piece's place, rows of W at the piece
-                const int g_col = MODE == kBwd && t.kind ? t.piece % a.ring * a.Vc : 0;
-                const int b_row = MODE == kBwd && t.kind != 2 ? t.piece * a.Vc : 0;
-                const int am = t.m0 + rank * 128 + (a_mn ? g_col : 0), bn = t.n0 + rank * 128;
-                if (MODE == kBwd && t.kind && t.piece != seen) {
-                    const int left = min(a.Vc, a.V - t.piece * a.Vc);
-                    seen = t.piece;
-                    ok = wait_count(a.g_done + seen, (uint32_t)(a.nm * ((left + kBN - 1) / kBN)) * CG,
-                                    abort_flag, a.status);
-                    if (!ok)
-                        break;
-                }
+                const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
+                const int b_row = t.kind == 2 ? 0 : a.v0;  // rows of W start at the piece
                 for (int kb = 0; kb < t.nk; ++kb) {
                     if (!mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, a.status)) {
                         ok = false;
@@ -444,8 +295,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     const int k = (t.k0 + kb) * KE;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        tma_load_2d_cg<CG>(st + j * kBox, ma, a_mn ? am + 64 * j : g_col + k, a_mn ? k : am + 64 * j,
-                                           bar);
+                        tma_load_2d_cg<CG>(st + j * kBox, ma, a_mn ? am + 64 * j : k, a_mn ? k : am + 64 * j, bar);
 #pragma unroll
                     for (int j = 0; j < K::BRows / 64; ++j)
                         tma_load_2d_cg<CG>(st + K::kA + j * kBox, mb, b_mn ? bn + 64 * j : k,
@@ -468,11 +318,12 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             Ring r;
             int it = 0;
             bool ok = true;
-            for (Tiles tiles; ok && tiles.next(c, t, 0xffffffffu, abort_flag, a.status);) {
+            for (int i = 0; ok && tile_at<CG, MODE>(a, cl, i, t); ++i) {
+                if (t.nk == 0)
+                    continue;
                 const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
                 const uint32_t idesc = (F8 || a.f16 ? idesc_f16(K::BM, kBN, a_mn, b_mn)
                                                     : idesc_bf16(K::BM, kBN, a_mn, b_mn));
-                const OpDesc da(base, a_mn), db(base + K::kA, b_mn);
                 const int buf = it & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tempty[buf]),
                                                                ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.status));
@@ -486,11 +337,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         break;
                     tc_fence_after();
                     if (lane == 0) {
-                        const uint32_t st = (uint32_t)r.i * (K::kStage / 16);
+                        const uint32_t st = base + (uint32_t)r.i * K::kStage;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_cg<CG, F8>(tbase + buf * kBN, da.at(st, ks), db.at(st, ks), idesc,
-                                           (kb > 0 || ks > 0) ? 1u : 0u);
+                            mma_cg<CG, F8>(tbase + buf * kBN, op_desc(st, a_mn, ks), op_desc(st + K::kA, b_mn, ks),
+                                           idesc, (kb > 0 || ks > 0) ? 1u : 0u);
                         mma_commit_cg<CG>(smem_u32(&c.empty[r.i]));
                     }
                     __syncwarp();
@@ -502,107 +353,54 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 ++it;
             }
         }
-    } else if (warp == kEpiWarps + 2) {
-        // ---------------------------------------------------------- tiles
-        if (lane == 0) {
-            Ring r;
-            Walk<CG, MODE> walk(cl);
-            for (bool more = true; more; r.next(kTiles)) {
-                more = walk.next(a, t);
-                if (!more)
-                    t.kind = -1;
-                if (!mbar_wait(smem_u32(&c.tile_empty[r.i]), r.ph ^ 1u, abort_flag, a.status))
-                    break;
-                c.tiles[r.i] = t;
-                mbar_arrive(smem_u32(&c.tile_full[r.i]));
-            }
-        }
-        __syncwarp();
-    } else if (warp == kEpiWarps + 3) {
-        // ---------------------------------------------------------- signals
-        // tells the other CTAs of each tile of g that the epilogue warps have
-        // stored
-        if (MODE == kBwd && lane == 0) {
-            Ring r;
-            uint32_t ph = 0;  // phase of stored, a bit for each place
-            while (mbar_wait(smem_u32(&c.tile_full[r.i]), r.ph, abort_flag, a.status)) {
-                t = c.tiles[r.i];
-                if (t.kind < 0)
-                    break;
-                if (t.kind == 0) {
-                    if (!mbar_wait(smem_u32(&c.stored[r.i]), (ph >> r.i) & 1u, abort_flag, a.status))
-                        break;
-                    ph ^= 1u << r.i;
-                    add_count<true>(a.g_done + t.piece);
-                }
-                mbar_arrive(smem_u32(&c.tile_empty[r.i]));
-                r.next(kTiles);
-            }
-        }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
         // a warp reads its quarter of the TMEM lanes (tile rows) and one half
         // of the tile's columns; a thread has one row
         const int q = warp & 3, half = warp >> 2;
         const int row_in = rank * 128 + q * 32 + lane;
-        [[maybe_unused]] uint32_t *stg =
-            reinterpret_cast<uint32_t *>(dsm + (base - smem_u32(dsm)) + NS * K::kStage + warp * kStgWarp);
+        uint8_t *stg = dsm + (base - smem_u32(dsm)) + NS * K::kStage + warp * kStgWarp;
+        const uint32_t stg_s = smem_u32(stg);
         float m2 = -INFINITY, s = 0.f, zs = 0.f;
-        [[maybe_unused]] float scale = 1.f, inv = 1.f;
-        [[maybe_unused]] int freed = a.ring - 1;  // g of pieces up to this may be written
-        if constexpr (MODE == kBwd) {
+        [[maybe_unused]] float scale = 1.f;
+        if constexpr (MODE == kProb)
             scale = g_scale(a, sm_top);
-            inv = 1.f / scale;
-        }
+        if constexpr (MODE == kGrad)
+            scale = a.gscale[1];
         int it = 0;
-        Tiles tiles;
-        for (;;) {
-            [[maybe_unused]] const int slot = tiles.r.i;
-            if (!tiles.next(c, t, 0xffffffffu, abort_flag, a.status))
-                break;
+        for (int i = 0; tile_at<CG, MODE>(a, cl, i, t); ++i) {
+            if (t.nk == 0)
+                continue;
             const int buf = it & 1;
             const int row = t.m0 + row_in;              // row of the tile's A operand
             const int col0 = t.n0 + half * (kBN / 2);   // first column of this warp
-            const int v0 = MODE == kBwd ? t.piece * a.Vc : 0;
             const uint32_t tm = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kBN + half * (kBN / 2));
             // what the row needs, before the wait
             int tgt = -1;
             [[maybe_unused]] float cf = 0.f, l2 = 0.f, hs = 1.f;
-            if (MODE == kLse || t.kind == 0) {
+            if constexpr (MODE != kGrad) {
                 if (row < a.T) {
                     const int y = a.targets[row];
                     const bool live = y != a.ignore && y >= 0 && y < a.V;
                     if (live)
-                        tgt = y - v0 - col0;  // this warp's column of the target, if it has it
-                    if constexpr (MODE == kBwd) {
+                        tgt = y - a.v0 - col0;  // this warp's column of the target, if it has it
+                    if constexpr (MODE == kProb) {
                         l2 = a.lse[row] * kLog2e;
                         if (live)
                             cf = a.dloss[row] * scale;
+                        else
+                            l2 = INFINITY;
                     } else if constexpr (F8) {
                         hs = a.h_scale ? a.h_scale[row] : 1.f;
                     }
-                }
-                if (MODE == kBwd && t.piece > freed) {
-                    // the place of this piece's g was another's
-                    bool ok = true;
-                    if (lane == 0)
-                        ok = wait_count(a.w_done + t.piece - a.ring, (uint32_t)(a.dh_units + (a.dw ? (a.Vc + K::BM - 1) / K::BM * a.nh : 0)),
-                                        abort_flag, a.status);
-                    if (!__all_sync(0xffffffffu, ok))
-                        break;
-                    freed = t.piece;
                 }
             }
             if (!__all_sync(0xffffffffu,
                             mbar_wait_cluster(smem_u32(&c.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, a.status)))
                 break;
             tc_fence_after();
-            // all of a gradient tile's operands have been read
-            if (MODE == kBwd && t.kind && threadIdx.x == 0 && rank == 0)
-                add_count<false>(a.w_done + t.piece);
             if constexpr (MODE == kLse) {
-                const int left = a.V - col0;  // columns of the vocabulary from col0 on
+                const int left = a.V - a.v0 - col0;  // columns of the vocabulary from col0 on
 #pragma unroll 1
                 for (int cc = 0; cc < kBN / 2; cc += 32) {
                     float v[32];
@@ -660,9 +458,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     m2 = -INFINITY;
                     s = zs = 0.f;
                 }
-            } else if (t.kind == 0) {
-                const int left = a.V - v0 - col0;
-                const int g_col = t.piece % a.ring * a.Vc + col0;
+            } else if constexpr (MODE == kProb) {
+                const int left = a.V - a.v0 - col0;
                 const float off = cf * (a.smooth / (float)a.V), hit = cf * (1.f - a.smooth);
 #pragma unroll 1
                 for (int cc = 0; cc < kBN / 2; cc += 32) {
@@ -686,15 +483,23 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 16; ++x)
                         w[x] = pack16(v[2 * x], v[2 * x + 1], a.f16);
-                    if (row < a.T) {
-                        uint16_t *dst = a.g + (int64_t)row * a.ldg + g_col + cc;
-                        st_global32(dst, w);
-                        st_global32(dst + 16, w + 8);
+                    if ((cc & 32) == 0) {
+                        if (lane == 0)
+                            bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    stage_words(stg, lane, (cc & 32) / 2, w);
+                    if (cc & 32) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0 && row < a.T) {  // lane 0 has the warp's first row
+                            tma_store_2d(&m_g, col0 + cc - 32, row, stg_s);
+                            bulk_commit();
+                        }
                     }
                 }
             } else {
                 if (t.kind == 1) {
-                    // always this thread's own sums, one piece after the other
                     float4 *acc = reinterpret_cast<float4 *>(a.acc) +
                                   ((int64_t)(t.unit * CG + rank) * (kBN / 4) + half * (kBN / 8)) * 128 + q * 32 + lane;
 #pragma unroll 1
@@ -704,14 +509,16 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
                             float4 *p = acc + (cc / 4 + x) * 128;
-                            if (t.piece == 0)
-                                *p = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                            else
-                                red_add_v4(&p->x, v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                            float4 o = a.first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+                            o.x += v[4 * x];
+                            o.y += v[4 * x + 1];
+                            o.z += v[4 * x + 2];
+                            o.w += v[4 * x + 3];
+                            *p = o;
                         }
                     }
                 } else {
-                    const int64_t row0 = (int64_t)v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
+                    const int64_t row0 = (int64_t)a.v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
 #pragma unroll 1
                     for (int cc = 0; cc < kBN / 2; cc += 32) {
                         float v[32];
@@ -719,37 +526,34 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         uint32_t w[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            w[x] = pack16(v[2 * x] * inv, v[2 * x + 1] * inv, a.f16);
-                        const int x0 = col0 + cc;
-                        if (a.dw_align == 32) {
-                            if (row0 + lane < a.V) {
-                                uint16_t *dst = a.dW + (row0 + lane) * a.lddW + x0;
-                                if (x0 < a.H)
-                                    st_global32(dst, w);
-                                if (x0 + 16 < a.H)
-                                    st_global32(dst + 16, w + 8);
-                            }
-                        } else if (a.dw_align == 16) {
-                            if (row0 + lane < a.V) {
-                                uint16_t *dst = a.dW + (row0 + lane) * a.lddW + x0;
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    if (x0 + 8 * x < a.H)
-                                        *reinterpret_cast<uint4 *>(dst + 8 * x) =
-                                            make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                            w[x] = pack16(v[2 * x] * scale, v[2 * x + 1] * scale, a.f16);
+                        if ((cc & 32) == 0) {
+                            if (lane == 0)
+                                bulk_wait_read<0>();
+                            __syncwarp();
+                        }
+                        stage_words(stg, lane, (cc & 32) / 2, w);
+                        if ((cc & 32) == 0)
+                            continue;
+                        const int x0 = col0 + cc - 32;
+                        if (!a.dW) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0 && row0 < a.V && x0 < a.H) {
+                                tma_store_2d(&m_dW, x0, (int)row0, stg_s);
+                                bulk_commit();
                             }
                         } else {
-                            // rows on any boundary: through shared memory, so
-                            // that a warp writes a row at a time
-                            __syncwarp();
-#pragma unroll
-                            for (int x = 0; x < 16; ++x)
-                                stg[lane * 17 + x] = w[x];
                             __syncwarp();
                             for (int r = 0; r < 32 && row0 + r < a.V; ++r)
-                                if (x0 + lane < a.H)
-                                    a.dW[(row0 + r) * a.lddW + x0 + lane] =
-                                        reinterpret_cast<const uint16_t *>(stg + r * 17)[lane];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int e = lane + 32 * j;
+                                    if (x0 + e < a.H)
+                                        a.dW[(row0 + r) * a.lddW + x0 + e] = *reinterpret_cast<const uint16_t *>(
+                                            stg + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+                                }
+                            __syncwarp();
                         }
                     }
                 }
@@ -764,20 +568,20 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     mbar_arrive_remote_relaxed(mapa(bar, 0));
                 else
                     mbar_arrive(bar);
-                if (MODE == kBwd && t.kind == 0)
-                    mbar_arrive(smem_u32(&c.stored[slot]));
             }
-            __syncwarp();
             ++it;
         }
         if constexpr (MODE == kLse) {
             if (a.nm == 1) {
-                const int64_t at = (int64_t)row_in * (2 * a.C) + cl * 2 + half;
+                const int64_t at = (int64_t)row_in * (2 * K::C) + cl * 2 + half;
                 a.part[at] = make_float2(m2, s);
                 if (a.zsum)
                     a.zsum[at] = zs;
             }
         }
+        if (lane == 0)
+            bulk_wait<0>();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -943,9 +747,10 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- host
 std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode_ce{nullptr};
 
-// row-major matrix in boxes of 64 rows x 128 bytes, 128-byte swizzle
+// row-major matrix in boxes of 64 rows x 128 bytes (or box_rows), 128-byte
+// swizzle
 sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int elem,
-                 const char *what)
+                 uint32_t box_rows, const char *what)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = g_encode_ce.load(std::memory_order_acquire);
     if (!enc) {
@@ -962,7 +767,7 @@ sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, i
     }
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
-    cuuint32_t box[2] = {128u / (uint32_t)elem, 64u};
+    cuuint32_t box[2] = {128u / (uint32_t)elem, box_rows};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
                            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -974,17 +779,17 @@ sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, i
 }
 
 // `after`: the kernel before it in the stream is one of this call's, which this
-// one may overlap; `together`: its CTAs wait for one another
+// one may overlap
 template <typename... P, typename... A>
-sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, bool after,
-                 bool together, cudaStream_t st, A... args)
+sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, bool after, cudaStream_t st,
+                 A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[3];
+    cudaLaunchAttribute at[2];
     cfg.attrs = at;
     cfg.numAttrs = 0;
     if (cluster > 1) {
@@ -997,68 +802,41 @@ sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int clu
         at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
-    if (together) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeCooperative;
-        at[cfg.numAttrs++].val.cooperative = 1;
-    }
     SG_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
     return SG_OK;
 }
 
-// clusters of CG CTAs that run at the same time (the backward kernel's wait for
-// one another), and the kernel made ready for the current device
 template <int CG, int MODE, bool F8>
-sg_status prepare_ce(int *clusters)
+sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CUtensorMap &dW,
+                    const CeArgs &a, bool after, cudaStream_t st)
 {
-    static std::atomic<int> known[64];  // by device
+    // once for each device (one bit of the mask)
+    static std::atomic<uint64_t> done{0};
     int dev = 0;
     SG_TRY_CUDA(cudaGetDevice(&dev));
-    int n = known[dev & 63].load(std::memory_order_acquire);
-    if (n == 0) {
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
         SG_TRY_CUDA(cudaFuncSetAttribute(k_ce<CG, MODE, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Cfg<CG>::kSmem));
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kSMs / CG * CG);
-        cfg.blockDim = dim3(kCeThreads);
-        cfg.dynamicSmemBytes = Cfg<CG>::kSmem;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = CG;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        SG_TRY_CUDA(cudaOccupancyMaxActiveClusters(&n, k_ce<CG, MODE, F8>, &cfg));
-        if (n < 1)
-            CE_FAIL(SG_ERR_CUDA, "no cluster of %d CTAs of the softmax kernel fits this device", CG);
-        if (n > kSMs / CG)
-            n = kSMs / CG;
-        known[dev & 63].store(n, std::memory_order_release);
+        done.fetch_or(bit, std::memory_order_relaxed);
     }
-    *clusters = n;
-    return SG_OK;
-}
-
-template <int CG, int MODE, bool F8>
-sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CeArgs &a,
-                    cudaStream_t st)
-{
-    return launch(k_ce<CG, MODE, F8>, dim3((unsigned)a.C * CG), kCeThreads, (int)Cfg<CG>::kSmem, CG, false,
-                  MODE == kBwd, st, h, W, g, a);
+    return launch(k_ce<CG, MODE, F8>, dim3(Cfg<CG>::C * CG), kCeThreads, (int)Cfg<CG>::kSmem, CG, after, st, h, W, g,
+                  dW, a);
 }
 
 // One call's tiles and the places of its work memory
 struct Plan {
-    int es = 2, CG = 1, BM = 128, C = 1;
+    int es = 2, CG = 1, BM = 128, C = kSMs;
     bool pack_h = false, pack_W = false;
     int64_t ldp = 0;             // row stride of the packed copies
     int64_t nm = 0, Tp = 0;
     // forward
     int64_t slots = 0;
     // backward
-    int64_t Vc = 0, pieces = 0, lag = 0, ring = 0;
-    int64_t dh_nn = 0, dh_tiles = 0, split = 1, dw_more = 0;
+    int64_t Vc = 0, nn = 0;      // vocabulary of a piece, its tiles
+    int64_t dh_nn = 0, dh_tiles = 0, split = 1;
     // byte offsets
-    int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_count = 0, o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
+    int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
 };
 
 bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
@@ -1068,18 +846,13 @@ bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) 
 // pair) costs that, and each has a little of its own.
 int64_t tile_cost(int64_t nk, int CG) { return 2 * (nk > 2 * CG ? nk : 2 * CG) + 1; }
 
-sg_status make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
-                    int32_t dtype, bool backward, Plan *p)
+void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
+               int32_t dtype, bool backward, Plan *p)
 {
     p->es = dtype == SG_E4M3 ? 1 : 2;
     p->CG = T > 128 ? 2 : 1;
     p->BM = 128 * p->CG;
-    if (backward)
-        CE_TRY(p->CG == 1 ? (prepare_ce<1, kBwd, false>(&p->C)) : (prepare_ce<2, kBwd, false>(&p->C)));
-    else if (dtype == SG_E4M3)
-        CE_TRY(p->CG == 1 ? (prepare_ce<1, kLse, true>(&p->C)) : (prepare_ce<2, kLse, true>(&p->C)));
-    else
-        CE_TRY(p->CG == 1 ? (prepare_ce<1, kLse, false>(&p->C)) : (prepare_ce<2, kLse, false>(&p->C)));
+    p->C = kSMs / p->CG;
     p->pack_h = !tma_ok(h, ldh, p->es);
     p->pack_W = !tma_ok(W, ldw, p->es);
     p->ldp = ceil_div(H * p->es, 16) * 16 / p->es;
@@ -1099,44 +872,34 @@ sg_status make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void
         p->o_part = take(p->slots * p->Tp * 8);
         p->o_zsum = take(p->slots * p->Tp * 4);
         p->o_ztgt = take(T * 4);
-        return SG_OK;
+        return;
     }
-    int64_t Vc = (getenv("SG_W") ? atoll(getenv("SG_W")) : (24ll << 20)) / (2 * H) / kBN * kBN;
+    // a piece of g holds at most 256 MB
+    int64_t Vc = (256ll << 20) / 2 / T / kBN * kBN;
     if (Vc < kBN)
         Vc = kBN;
-    const int64_t most = (getenv("SG_G") ? atoll(getenv("SG_G")) : (64ll << 20)) / (2 * T) / kBN * kBN;
-    if (Vc > most)
-        Vc = most < kBN ? kBN : most;
-    const int64_t all = ceil_div(V, kBN) * kBN;
-    if (Vc > all)
-        Vc = all;
+    if (Vc > ceil_div(V, kBN) * kBN)
+        Vc = ceil_div(V, kBN) * kBN;
     p->Vc = Vc;
-    p->pieces = ceil_div(V, Vc);
-    p->lag = getenv("SG_L") ? atoll(getenv("SG_L")) : 1;
-    p->ring = p->lag + 2 < p->pieces ? p->lag + 2 : p->pieces;
+    p->nn = Vc / kBN;
     p->dh_nn = ceil_div(H, kBN);
     p->dh_tiles = p->nm * p->dh_nn;
-    // split K of dh until its units leave room for the other tiles' even share
-    const int64_t kb = ceil_div(V < Vc ? V : Vc, 64), nk = ceil_div(H, 64), tk = ceil_div(T, 64);
-    const int64_t logit = p->nm * (Vc / kBN) * tile_cost(nk, p->CG);
-    const int64_t dw = ceil_div(Vc, p->BM) * p->dh_nn * tile_cost(tk, p->CG);
+    // split K of dh until its units and the dW tiles fill the clusters evenly
+    const int64_t kb = ceil_div(V < Vc ? V : Vc, 64), dw = ceil_div(Vc, p->BM) * p->dh_nn * tile_cost(ceil_div(T, 64), p->CG);
     double best = 0;
     for (int64_t n = 1; n <= kb && n <= 64; ++n) {
         const int64_t units = p->dh_tiles * n, cost = tile_cost(ceil_div(kb, n), p->CG) + 2;
-        const double even = (double)(units * cost + dw + logit) / p->C;
-        const double last = (double)(ceil_div(units, p->C) * cost) + (double)logit / p->C;
+        const double even = (double)(units * cost + dw) / p->C;
+        const double last = (double)(ceil_div(units, p->C) * cost);
         const double span = (even > last ? even : last) * (1.0 + 0.002 * (double)n);
         if (n == 1 || span < best) {
             best = span;
             p->split = n;
         }
     }
-    p->dw_more = (tile_cost(ceil_div(kb, p->split), p->CG) + 2) / tile_cost(tk, p->CG);
-    p->o_count = take(p->pieces * 8);
     p->o_gs = take(8);
-    p->o_g = take(T * p->ring * Vc * 2);
+    p->o_g = take(T * Vc * 2);
     p->o_acc = take(p->dh_tiles * p->split * p->BM * kBN * 4);
-    return SG_OK;
 }
 
 sg_status check_ce(const char *fn, const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
@@ -1186,8 +949,8 @@ sg_status operand_maps(const Plan &p, const void *h, int64_t ldh, int64_t T, int
     if (p.pack_W)
         packed(W, ldw, V, p.o_W);
     SG_TRY_CUDA(cudaGetLastError());
-    CE_TRY(map_of(mh, h, H, T, ldh, p.es, "h"));
-    return map_of(mW, W, H, V, ldw, p.es, "W");
+    CE_TRY(map_of(mh, h, H, T, ldh, p.es, 64, "h"));
+    return map_of(mW, W, H, V, ldw, p.es, 64, "W");
 }
 
 }  // namespace
@@ -1203,7 +966,7 @@ sg_status sg_softmax_ce_work(const void *h, int64_t ldh, int64_t T, int64_t H, c
     CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, backward != 0));
     Plan p;
     if (T > 0)
-        CE_TRY(make_plan(h, ldh, T, H, W, ldw, V, dtype, backward != 0, &p));
+        make_plan(h, ldh, T, H, W, ldw, V, dtype, backward != 0, &p);
     *bytes = p.bytes;
     return SG_OK;
 }
@@ -1225,7 +988,7 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     if (T == 0)
         return SG_OK;
     Plan p;
-    CE_TRY(make_plan(h, ldh, T, H, W, ldw, V, dtype, false, &p));
+    make_plan(h, ldh, T, H, W, ldw, V, dtype, false, &p);
     if (!work || work_bytes < p.bytes || ((uintptr_t)work & 255) != 0)
         CE_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_softmax_ce_work), aligned to 256", fn,
                 (long long)p.bytes);
@@ -1237,7 +1000,6 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     a.T = (int32_t)T;
     a.V = (int32_t)V;
     a.H = (int32_t)H;
-    a.C = p.C;
     a.nm = (int32_t)p.nm;
     a.nn = (int32_t)ceil_div(V, kBN);
     a.nk = (int32_t)ceil_div(H * p.es, 128);
@@ -1252,18 +1014,18 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     a.Tp = (int32_t)p.Tp;
     a.status = status;
     if (dtype == SG_E4M3)
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, a, st))
-                         : (launch_ce<2, kLse, true>(mh, mW, mh, a, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, a, false, st))
+                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, a, false, st)));
     else
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, a, st))
-                         : (launch_ce<2, kLse, false>(mh, mW, mh, a, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, a, false, st))
+                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, a, false, st)));
     JoinArgs j;
     j.part = a.part, j.zsum = a.zsum, j.ztgt = a.ztgt, j.targets = targets, j.loss = loss, j.lse = lse;
     j.status = status, j.slots = (int32_t)p.slots, j.Tp = a.Tp, j.T = a.T, j.V = a.V, j.ignore = ignore_index;
     j.smooth = (float)smoothing;
     if (p.nm == 1)
-        return launch(k_ce_join_row, dim3((unsigned)T), 128, 0, 1, true, false, st, j);
-    return launch(k_ce_join, dim3((unsigned)ceil_div(T, 32)), 1024, 0, 1, true, false, st, j);
+        return launch(k_ce_join_row, dim3((unsigned)T), 128, 0, 1, true, st, j);
+    return launch(k_ce_join, dim3((unsigned)ceil_div(T, 32)), 1024, 0, 1, true, st, j);
 }
 
 sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
@@ -1287,58 +1049,71 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
         return SG_OK;
     }
     Plan p;
-    CE_TRY(make_plan(h, ldh, T, H, W, ldw, V, dtype, true, &p));
+    make_plan(h, ldh, T, H, W, ldw, V, dtype, true, &p);
     if (!work || work_bytes < p.bytes || ((uintptr_t)work & 255) != 0)
         CE_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_softmax_ce_work), aligned to 256", fn,
                 (long long)p.bytes);
     uint8_t *w8 = static_cast<uint8_t *>(work);
-    CUtensorMap mh, mW, mg;
+    CUtensorMap mh, mW, mg, mgs, mdW;
     CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, st));
-    CE_TRY(map_of(&mg, w8 + p.o_g, p.ring * p.Vc, T, p.ring * p.Vc, 2, "g"));
+    // g: [T][Vc], loaded in boxes of 64 rows, stored in boxes of 32
+    CE_TRY(map_of(&mg, w8 + p.o_g, p.Vc, T, p.Vc, 2, 64, "g"));
+    CE_TRY(map_of(&mgs, w8 + p.o_g, p.Vc, T, p.Vc, 2, 32, "g"));
+    // a TMA store ends on a multiple of 16 bytes: with other widths it would
+    // write past a row's end
+    const bool dw_tma = dW && tma_ok(dW, lddw, 2) && H % 8 == 0;
+    if (dw_tma)
+        CE_TRY(map_of(&mdW, dW, H, V, lddw, 2, 32, "dW"));
+    else
+        mdW = mgs;
     CeArgs a = {};
     a.T = (int32_t)T;
     a.V = (int32_t)V;
     a.H = (int32_t)H;
-    a.C = p.C;
     a.nm = (int32_t)p.nm;
-    a.nn = (int32_t)(p.Vc / kBN);
     a.nk = (int32_t)ceil_div(H, 64);
     a.f16 = dtype == SG_F16;
     a.targets = targets;
     a.ignore = ignore_index;
-    a.status = status;
     a.lse = lse;
     a.dloss = dloss;
-    a.gscale = reinterpret_cast<float *>(w8 + p.o_gs);
     a.smooth = (float)smoothing;
-    a.full = dtype == SG_F16 ? 16384.f : 1.f;
-    a.pieces = (int32_t)p.pieces;
-    a.Vc = (int32_t)p.Vc;
-    a.lag = (int32_t)p.lag;
-    a.ring = (int32_t)p.ring;
     a.nh = (int32_t)p.dh_nn;
-    a.dh_tiles = (int32_t)p.dh_tiles;
     a.dh_split = (int32_t)p.split;
-    a.dh_units = dh ? (int32_t)(p.dh_tiles * p.split) : 0;
-    a.dw = dW != nullptr;
+    a.dh_tiles = dh ? (int32_t)p.dh_tiles : 0;
     a.dw_nk = (int32_t)ceil_div(T, 64);
-    a.dw_more = dh ? (int32_t)p.dw_more : 0;
     a.acc = reinterpret_cast<float *>(w8 + p.o_acc);
-    a.g = reinterpret_cast<uint16_t *>(w8 + p.o_g);
-    a.ldg = p.ring * p.Vc;
-    a.dW = static_cast<uint16_t *>(dW);
+    a.dW = dW && !dw_tma ? static_cast<uint16_t *>(dW) : nullptr;
     a.lddW = lddw;
-    const uintptr_t bits = (uintptr_t)dW | (uintptr_t)(lddw * 2) | (uintptr_t)(H * 2);
-    a.dw_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 2;
-    a.g_done = reinterpret_cast<uint32_t *>(w8 + p.o_count);
-    a.w_done = a.g_done + p.pieces;
-    SG_TRY_CUDA(cudaMemsetAsync(a.g_done, 0, (size_t)p.pieces * 8, st));
-    CE_TRY(p.CG == 1 ? (launch_ce<1, kBwd, false>(mh, mW, mg, a, st))
-                     : (launch_ce<2, kBwd, false>(mh, mW, mg, a, st)));
+    a.status = status;
+    a.gscale = reinterpret_cast<float *>(w8 + p.o_gs);
+    a.full = dtype == SG_F16 ? 16384.f : 1.f;
+    for (int64_t v0 = 0; v0 < V; v0 += p.Vc) {
+        const int64_t vc = V - v0 < p.Vc ? V - v0 : p.Vc;
+        a.v0 = (int32_t)v0;
+        a.first = v0 == 0;
+        a.nn = (int32_t)ceil_div(vc, kBN);
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kProb, false>(mh, mW, mgs, mdW, a, v0 > 0, st))
+                         : (launch_ce<2, kProb, false>(mh, mW, mgs, mdW, a, v0 > 0, st)));
+        a.dh_kb = (int32_t)ceil_div(vc, 64);
+        a.dw_tiles = dW ? (int32_t)(ceil_div(vc, p.BM) * p.dh_nn) : 0;
+        // turns of dW tiles so that all clusters end at about the same time
+        const int64_t units = (int64_t)a.dh_tiles * p.split, hi = units % p.C;
+        a.dh_each = (int32_t)(units / p.C);
+        a.dh_hi = (int32_t)hi;
+        const int64_t less = dh ? ceil_div(tile_cost(ceil_div(a.dh_kb, p.split), p.CG) + 2, tile_cost(a.dw_nk, p.CG)) : 0;
+        int64_t q_hi = hi ? (a.dw_tiles - less * (p.C - hi)) / p.C : 0;
+        if (q_hi < 0)
+            q_hi = 0;
+        a.dw_hi = (int32_t)q_hi;
+        a.dw_lo = (int32_t)(q_hi + ceil_div(a.dw_tiles - q_hi * p.C > 0 ? a.dw_tiles - q_hi * p.C : 0, p.C - hi));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mh, mW, mg, mdW, a, true, st))
+                         : (launch_ce<2, kGrad, false>(mh, mW, mg, mdW, a, true, st)));
+    }
     if (dh) {
         const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), kBN / 32);
         const float4 *acc = reinterpret_cast<const float4 *>(a.acc);
-        return launch(p.CG == 1 ? k_ce_dh<1> : k_ce_dh<2>, grid, 256, 0, 1, true, false, st, acc, (int)p.dh_tiles,
+        return launch(p.CG == 1 ? k_ce_dh<1> : k_ce_dh<2>, grid, 256, 0, 1, true, st, acc, (int)p.dh_tiles,
                       (int)p.dh_nn, (int)p.split, (int)T, (int)H, (const float *)a.gscale, (int)a.f16,
                       static_cast<uint16_t *>(dh), lddh);
     }

@@ -548,11 +548,13 @@ __device__ __forceinline__ void tma_load_2d_cg(uint32_t dst, const CUtensorMap *
             : "memory");
 }
 
-// 32 bytes to a 32-byte aligned address: a whole sector by one thread
-__device__ __forceinline__ void st_global32(void *p, const uint32_t *w)
+// tile of shared memory -> global memory (parts outside the map are left
+// out), tracked by this thread's bulk groups; x and y are not negative
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     (uint64_t)map),
+                 "r"(x), "r"(y), "r"(src)
                  : "memory");
 }
 
