@@ -49,7 +49,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kCeThreads = 32 * (kEpiWarps + 2);
 constexpr int kBN = 256;                 // tile columns
 constexpr uint32_t kBox = 8192;          // one TMA box: 64 rows of 128 bytes
-constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's output box: 32 rows of 128 bytes
+constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's outputs on their way: two boxes of 32 x 32
 constexpr int kBand = 16;                // row tiles that walk the vocabulary together
 
 template <int CG>
@@ -163,13 +163,26 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
     }
 }
 
+// Descriptors of an operand's tile at shared address `base`: the low word, to
+// which stages (bytes / 16) and K steps are added, the high word, and the step.
 // K-major: rows of 128 bytes of K, 8 rows to a swizzle atom.  MN-major: boxes
-// of 64 rows (128 bytes) by 64 K, kBox apart.
-__device__ __forceinline__ uint64_t op_desc(uint32_t tile, bool mn, int ks)
-{
-    return mn ? sdesc(tile + (uint32_t)ks * 2048, kBox, 1024, kLayoutSW128)
-              : sdesc(tile + (uint32_t)ks * 32, 16, 1024, kLayoutSW128);
-}
+// of 64 rows (128 bytes) by 64 K, kBox apart.  Worked out once for a tile: the
+// thread that issues the MMAs has little time for each.
+struct OpDesc {
+    uint32_t lo, hi, step;
+
+    __device__ __forceinline__ OpDesc(uint32_t base, bool mn)
+    {
+        const uint64_t d = sdesc(base, mn ? kBox : 16, 1024, kLayoutSW128);
+        lo = (uint32_t)d;
+        hi = (uint32_t)(d >> 32);
+        step = mn ? 2048 / 16 : 32 / 16;
+    }
+    __device__ __forceinline__ uint64_t at(uint32_t stage, int ks) const
+    {
+        return (uint64_t)hi << 32 | (lo + stage + ks * step);
+    }
+};
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -183,13 +196,26 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16)
     return f16 ? pack2_f16(a, b) : pack2(a, b);
 }
 
-// 64 columns (32 packed words) of this warp's 32 rows into its swizzled box
-__device__ __forceinline__ void stage_words(uint8_t *stg, int lane, int word0, const uint32_t (&w)[16])
+// 32 columns (16 packed words) of this warp's 32 rows to global memory by TMA,
+// from one of its two boxes while the other is filled: rows of 64 bytes, their
+// 16-byte units swizzled.  Lane 0 issues the store, if `in`.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, bool in, uint8_t *box, int lane,
+                                          const uint32_t (&w)[16])
 {
+    if (lane == 0)
+        bulk_wait_read<1>();
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(stg + lane * 128 + ((((word0 >> 2) + i) ^ (lane & 7)) << 4)) =
+        *reinterpret_cast<uint4 *>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+        if (in)
+            tma_store_2d(map, x, y, smem_u32(box));
+        bulk_commit();
+    }
 }
 
 // Factor of g before it is rounded to 16 bits; the products' epilogues take it
@@ -324,6 +350,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
                 const uint32_t idesc = (F8 || a.f16 ? idesc_f16(K::BM, kBN, a_mn, b_mn)
                                                     : idesc_bf16(K::BM, kBN, a_mn, b_mn));
+                const OpDesc da(base, a_mn), db(base + K::kA, b_mn);
                 const int buf = it & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tempty[buf]),
                                                                ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.status));
@@ -337,11 +364,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         break;
                     tc_fence_after();
                     if (lane == 0) {
-                        const uint32_t st = base + (uint32_t)r.i * K::kStage;
+                        const uint32_t st = (uint32_t)r.i * (K::kStage / 16);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_cg<CG, F8>(tbase + buf * kBN, op_desc(st, a_mn, ks), op_desc(st + K::kA, b_mn, ks),
-                                           idesc, (kb > 0 || ks > 0) ? 1u : 0u);
+                            mma_cg<CG, F8>(tbase + buf * kBN, da.at(st, ks), db.at(st, ks), idesc,
+                                           (kb > 0 || ks > 0) ? 1u : 0u);
                         mma_commit_cg<CG>(smem_u32(&c.empty[r.i]));
                     }
                     __syncwarp();
@@ -360,7 +387,6 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const int q = warp & 3, half = warp >> 2;
         const int row_in = rank * 128 + q * 32 + lane;
         uint8_t *stg = dsm + (base - smem_u32(dsm)) + NS * K::kStage + warp * kStgWarp;
-        const uint32_t stg_s = smem_u32(stg);
         float m2 = -INFINITY, s = 0.f, zs = 0.f;
         [[maybe_unused]] float scale = 1.f;
         if constexpr (MODE == kProb)
@@ -461,10 +487,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             } else if constexpr (MODE == kProb) {
                 const int left = a.V - a.v0 - col0;
                 const float off = cf * (a.smooth / (float)a.V), hit = cf * (1.f - a.smooth);
-#pragma unroll 1
-                for (int cc = 0; cc < kBN / 2; cc += 32) {
-                    float v[32];
-                    tmem_ld_chunk<32>(tm + cc, v);
+                auto out = [&](float (&v)[32], int cc) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
                         v[x] = cf == 0.f ? 0.f : fmaf(ex2(fmaf(v[x], kLog2e, -l2)), cf, -off);
@@ -483,29 +506,21 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 16; ++x)
                         w[x] = pack16(v[2 * x], v[2 * x + 1], a.f16);
-                    if ((cc & 32) == 0) {
-                        if (lane == 0)
-                            bulk_wait_read<0>();
-                        __syncwarp();
-                    }
-                    stage_words(stg, lane, (cc & 32) / 2, w);
-                    if (cc & 32) {
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0 && row < a.T) {  // lane 0 has the warp's first row
-                            tma_store_2d(&m_g, col0 + cc - 32, row, stg_s);
-                            bulk_commit();
-                        }
-                    }
+                    // lane 0 has the warp's first row
+                    store_box(&m_g, col0 + cc, row, row < a.T, stg + (cc & 32) * (kStgWarp / 64), lane, w);
+                };
+#pragma unroll 1
+                for (int cc = 0; cc < kBN / 2; cc += 64) {
+                    float v[32], u[32];
+                    tmem_ld_chunk2<32>(tm + cc, tm + cc + 32, v, u);
+                    out(v, cc);
+                    out(u, cc + 32);
                 }
             } else {
                 if (t.kind == 1) {
                     float4 *acc = reinterpret_cast<float4 *>(a.acc) +
                                   ((int64_t)(t.unit * CG + rank) * (kBN / 4) + half * (kBN / 8)) * 128 + q * 32 + lane;
-#pragma unroll 1
-                    for (int cc = 0; cc < kBN / 2; cc += 32) {
-                        float v[32];
-                        tmem_ld_chunk<32>(tm + cc, v);
+                    auto out = [&](const float (&v)[32], int cc) {
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
                             float4 *p = acc + (cc / 4 + x) * 128;
@@ -516,45 +531,46 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                             o.w += v[4 * x + 3];
                             *p = o;
                         }
+                    };
+#pragma unroll 1
+                    for (int cc = 0; cc < kBN / 2; cc += 64) {
+                        float v[32], u[32];
+                        tmem_ld_chunk2<32>(tm + cc, tm + cc + 32, v, u);
+                        out(v, cc);
+                        out(u, cc + 32);
                     }
                 } else {
                     const int64_t row0 = (int64_t)a.v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
-#pragma unroll 1
-                    for (int cc = 0; cc < kBN / 2; cc += 32) {
-                        float v[32];
-                        tmem_ld_chunk<32>(tm + cc, v);
+                    auto out = [&](const float (&v)[32], int cc) {
                         uint32_t w[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
                             w[x] = pack16(v[2 * x] * scale, v[2 * x + 1] * scale, a.f16);
-                        if ((cc & 32) == 0) {
-                            if (lane == 0)
-                                bulk_wait_read<0>();
-                            __syncwarp();
-                        }
-                        stage_words(stg, lane, (cc & 32) / 2, w);
-                        if ((cc & 32) == 0)
-                            continue;
-                        const int x0 = col0 + cc - 32;
+                        const int x0 = col0 + cc;
                         if (!a.dW) {
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0 && row0 < a.V && x0 < a.H) {
-                                tma_store_2d(&m_dW, x0, (int)row0, stg_s);
-                                bulk_commit();
-                            }
+                            store_box(&m_dW, x0, (int)row0, row0 < a.V && x0 < a.H, stg + (cc & 32) * (kStgWarp / 64),
+                                      lane, w);
                         } else {
+                            // rows on any boundary: through shared memory, so
+                            // that a warp writes a row at a time
+                            uint32_t *rows = reinterpret_cast<uint32_t *>(stg);
+                            __syncwarp();
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                rows[lane * 17 + x] = w[x];
                             __syncwarp();
                             for (int r = 0; r < 32 && row0 + r < a.V; ++r)
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const int e = lane + 32 * j;
-                                    if (x0 + e < a.H)
-                                        a.dW[(row0 + r) * a.lddW + x0 + e] = *reinterpret_cast<const uint16_t *>(
-                                            stg + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
-                                }
-                            __syncwarp();
+                                if (x0 + lane < a.H)
+                                    a.dW[(row0 + r) * a.lddW + x0 + lane] =
+                                        reinterpret_cast<const uint16_t *>(rows + r * 17)[lane];
                         }
+                    };
+#pragma unroll 1
+                    for (int cc = 0; cc < kBN / 2; cc += 64) {
+                        float v[32], u[32];
+                        tmem_ld_chunk2<32>(tm + cc, tm + cc + 32, v, u);
+                        out(v, cc);
+                        out(u, cc + 32);
                     }
                 }
             }
@@ -747,10 +763,10 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- host
 std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode_ce{nullptr};
 
-// row-major matrix in boxes of 64 rows x 128 bytes (or box_rows), 128-byte
-// swizzle
+// row-major matrix in boxes of 64 rows x 128 bytes, 128-byte swizzle; `out`:
+// 32 rows x 64 bytes, 64-byte swizzle
 sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int elem,
-                 uint32_t box_rows, const char *what)
+                 const char *what, bool out = false)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = g_encode_ce.load(std::memory_order_acquire);
     if (!enc) {
@@ -767,12 +783,12 @@ sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, i
     }
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
-    cuuint32_t box[2] = {128u / (uint32_t)elem, box_rows};
+    cuuint32_t box[2] = {(out ? 64u : 128u) / (uint32_t)elem, out ? 32u : 64u};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
                            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         CE_FAIL(SG_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
     return SG_OK;
@@ -949,8 +965,8 @@ sg_status operand_maps(const Plan &p, const void *h, int64_t ldh, int64_t T, int
     if (p.pack_W)
         packed(W, ldw, V, p.o_W);
     SG_TRY_CUDA(cudaGetLastError());
-    CE_TRY(map_of(mh, h, H, T, ldh, p.es, 64, "h"));
-    return map_of(mW, W, H, V, ldw, p.es, 64, "W");
+    CE_TRY(map_of(mh, h, H, T, ldh, p.es, "h"));
+    return map_of(mW, W, H, V, ldw, p.es, "W");
 }
 
 }  // namespace
@@ -1056,14 +1072,14 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     uint8_t *w8 = static_cast<uint8_t *>(work);
     CUtensorMap mh, mW, mg, mgs, mdW;
     CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, st));
-    // g: [T][Vc], loaded in boxes of 64 rows, stored in boxes of 32
-    CE_TRY(map_of(&mg, w8 + p.o_g, p.Vc, T, p.Vc, 2, 64, "g"));
-    CE_TRY(map_of(&mgs, w8 + p.o_g, p.Vc, T, p.Vc, 2, 32, "g"));
+    // g: [T][Vc], loaded in boxes of 64 rows, stored in boxes of 32 x 32
+    CE_TRY(map_of(&mg, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g"));
+    CE_TRY(map_of(&mgs, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g", true));
     // a TMA store ends on a multiple of 16 bytes: with other widths it would
     // write past a row's end
     const bool dw_tma = dW && tma_ok(dW, lddw, 2) && H % 8 == 0;
     if (dw_tma)
-        CE_TRY(map_of(&mdW, dW, H, V, lddw, 2, 32, "dW"));
+        CE_TRY(map_of(&mdW, dW, H, V, lddw, 2, "dW", true));
     else
         mdW = mgs;
     CeArgs a = {};
