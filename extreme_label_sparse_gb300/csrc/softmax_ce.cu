@@ -76,6 +76,10 @@ struct CeArgs {
     int32_t T, V, H;      // rows, vocabulary, features
     int32_t v0;           // first vocabulary row of the piece
     int32_t nm, nn, nk;   // tiles of the logits (rows, columns of the piece), K blocks
+    int32_t bw;           // columns of a tile of logits
+    int32_t ab, an;       // rows of a box of A by its rows (h; g in dh's product), and boxes: rows past them
+                          // stay unset, and their results unused
+    int32_t kt;           // rows of a box of g and h in dW's product, whose K they are
     int32_t f16;          // 16-bit operands are fp16, not bf16
     // kLse
     const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
@@ -121,7 +125,7 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
         const uint32_t n = r / mc;
         t.kind = 0;
         t.m0 = (b * kBand + (r - n * mc)) * BM;
-        t.n0 = n * kBN;
+        t.n0 = n * a.bw;
         t.k0 = 0;
         t.nk = a.nk;
         t.unit = n;
@@ -254,11 +258,13 @@ __device__ __forceinline__ float g_scale(const CeArgs &a, float *sm)
     return s;
 }
 
-// maps: kLse, kProb: A = h, B = W, out = g (kProb); kGrad: g, W, h, out = dW
+// kLse, kProb: A = m_h, B = m_W, out = m_g (kProb).  kGrad: dh from A = m_g (by
+// rows), B = m_W; dW from A = m_gk (by columns), B = m_h, out = m_dW.
 template <int CG, int MODE, bool F8>
 __global__ void __launch_bounds__(kCeThreads, 1)
     k_ce(const __grid_constant__ CUtensorMap m_h, const __grid_constant__ CUtensorMap m_W,
-         const __grid_constant__ CUtensorMap m_g, const __grid_constant__ CUtensorMap m_dW, const CeArgs a)
+         const __grid_constant__ CUtensorMap m_g, const __grid_constant__ CUtensorMap m_gk,
+         const __grid_constant__ CUtensorMap m_dW, const CeArgs a)
 {
     using K = Cfg<CG>;
     constexpr int NS = K::NS;
@@ -303,30 +309,67 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             Ring r;
             bool ok = true;
             for (int i = 0; ok && tile_at<CG, MODE>(a, cl, i, t); ++i) {
-                const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
-                const CUtensorMap *ma = t.kind ? &m_g : &m_h, *mb = t.kind == 2 ? &m_h : &m_W;
-                const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
-                const int b_row = t.kind == 2 ? 0 : a.v0;  // rows of W start at the piece
-                for (int kb = 0; kb < t.nk; ++kb) {
-                    if (!mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = base + (uint32_t)r.i * K::kStage;
-                    uint32_t bar = smem_u32(&c.full[r.i]);
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(bar, CG * K::kStage);
+                const int am = t.m0 + rank * 128;
+                // a pair has more than 128 rows: whole boxes
+                const int ab = CG == 2 ? 64 : a.ab, an = CG == 2 ? 2 : a.an, kt = CG == 2 ? 64 : a.kt;
+                // the next free stage, which is to receive `bytes` in all CTAs
+                auto stage = [&](uint32_t bytes, uint32_t *bar) {
+                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, a.status);
+                    *bar = smem_u32(&c.full[r.i]);
+                    if (ok && rank == 0)
+                        mbar_arrive_expect_tx(*bar, bytes);
                     if constexpr (CG == 2)
-                        bar = mapa(bar, 0);
-                    const int k = (t.k0 + kb) * KE;
+                        *bar = mapa(*bar, 0);
+                    return base + (uint32_t)r.i * K::kStage;
+                };
+                // one loop for each product: the thread has some 500 cycles
+                // for a K block
+                uint32_t bar;
+                if (MODE != kGrad) {
+                    const int bh = a.bw / 2;  // with two CTAs, B's rows of one; else half of them
+                    const int bn = a.v0 + t.n0 + rank * bh;
+                    const uint32_t bytes = CG * 128 * (an * ab + a.bw / CG), a2 = ab * 128, b2 = bh * 128;
+                    const bool two = an == 2;
+                    for (int k = 0; k < t.nk * KE; k += KE, r.next(NS)) {
+                        const uint32_t st = stage(bytes, &bar);
+                        if (!ok)
+                            break;
+                        tma_load_2d_cg<CG>(st, &m_h, k, am, bar);
+                        if (two)
+                            tma_load_2d_cg<CG>(st + a2, &m_h, k, am + ab, bar);
+                        tma_load_2d_cg<CG>(st + K::kA, &m_W, k, bn, bar);
+                        if (CG == 1)
+                            tma_load_2d_cg<CG>(st + K::kA + b2, &m_W, k, bn + bh, bar);
+                    }
+                } else if (t.kind == 1) {
+                    const int bn = t.n0 + rank * 128, k1 = (t.k0 + t.nk) * KE;
+                    const uint32_t bytes = CG * 128 * (an * ab + K::BRows), a2 = ab * 128;
+                    const bool two = an == 2;
+                    for (int k = t.k0 * KE; k < k1; k += KE, r.next(NS)) {
+                        const uint32_t st = stage(bytes, &bar);
+                        if (!ok)
+                            break;
+                        tma_load_2d_cg<CG>(st, &m_g, k, am, bar);
+                        if (two)
+                            tma_load_2d_cg<CG>(st + a2, &m_g, k, am + ab, bar);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        tma_load_2d_cg<CG>(st + j * kBox, ma, a_mn ? am + 64 * j : k, a_mn ? k : am + 64 * j, bar);
+                        for (int j = 0; j < K::BRows / 64; ++j)
+                            tma_load_2d_cg<CG>(st + K::kA + j * kBox, &m_W, bn + 64 * j, a.v0 + k, bar);
+                    }
+                } else {
+                    const int bn = t.n0 + rank * 128;
+                    const uint32_t bytes = CG * 128 * (2 + K::BRows / 64) * kt;
+                    for (int k = 0; k < t.nk * KE; k += KE, r.next(NS)) {
+                        const uint32_t st = stage(bytes, &bar);
+                        if (!ok)
+                            break;
 #pragma unroll
-                    for (int j = 0; j < K::BRows / 64; ++j)
-                        tma_load_2d_cg<CG>(st + K::kA + j * kBox, mb, b_mn ? bn + 64 * j : k,
-                                           b_mn ? b_row + k : b_row + bn + 64 * j, bar);
-                    r.next(NS);
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_2d_cg<CG>(st + j * kBox, &m_gk, am + 64 * j, k, bar);
+#pragma unroll
+                        for (int j = 0; j < K::BRows / 64; ++j)
+                            tma_load_2d_cg<CG>(st + K::kA + j * kBox, &m_h, bn + 64 * j, k, bar);
+                    }
                 }
             }
             if (!ok) {
@@ -348,8 +391,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 if (t.nk == 0)
                     continue;
                 const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
-                const uint32_t idesc = (F8 || a.f16 ? idesc_f16(K::BM, kBN, a_mn, b_mn)
-                                                    : idesc_bf16(K::BM, kBN, a_mn, b_mn));
+                const int bn = MODE == kGrad ? kBN : a.bw;
+                const uint32_t idesc =
+                    F8 || a.f16 ? idesc_f16(K::BM, bn, a_mn, b_mn) : idesc_bf16(K::BM, bn, a_mn, b_mn);
                 const OpDesc da(base, a_mn), db(base + K::kA, b_mn);
                 const int buf = it & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tempty[buf]),
@@ -366,9 +410,12 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     if (lane == 0) {
                         const uint32_t st = (uint32_t)r.i * (K::kStage / 16);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
+                        for (int ks = 0; ks < 4; ++ks) {
+                            if (MODE == kGrad && CG == 1 && a_mn && ks * 16 >= a.kt)
+                                break;
                             mma_cg<CG, F8>(tbase + buf * kBN, da.at(st, ks), db.at(st, ks), idesc,
                                            (kb > 0 || ks > 0) ? 1u : 0u);
+                        }
                         mma_commit_cg<CG>(smem_u32(&c.empty[r.i]));
                     }
                     __syncwarp();
@@ -399,8 +446,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 continue;
             const int buf = it & 1;
             const int row = t.m0 + row_in;              // row of the tile's A operand
-            const int col0 = t.n0 + half * (kBN / 2);   // first column of this warp
-            const uint32_t tm = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kBN + half * (kBN / 2));
+            const int cols = MODE == kGrad ? kBN / 2 : a.bw / 2;  // of this warp, and the first of them
+            const int col0 = t.n0 + half * cols;
+            const uint32_t tm = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kBN + half * cols);
             // what the row needs, before the wait
             int tgt = -1;
             [[maybe_unused]] float cf = 0.f, l2 = 0.f, hs = 1.f;
@@ -408,7 +456,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 if (row < a.T) {
                     const int y = a.targets[row];
                     const bool live = y != a.ignore && y >= 0 && y < a.V;
-                    if (live)
+                    if (live && y - a.v0 - col0 < cols)
                         tgt = y - a.v0 - col0;  // this warp's column of the target, if it has it
                     if constexpr (MODE == kProb) {
                         l2 = a.lse[row] * kLog2e;
@@ -426,9 +474,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 break;
             tc_fence_after();
             if constexpr (MODE == kLse) {
-                const int left = a.V - a.v0 - col0;  // columns of the vocabulary from col0 on
+                const int left = min(cols, a.V - a.v0 - col0);  // columns of this warp that are labels
 #pragma unroll 1
-                for (int cc = 0; cc < kBN / 2; cc += 32) {
+                for (int cc = 0; cc < cols; cc += 32) {
                     float v[32];
                     tmem_ld_chunk<32>(tm + cc, v);
                     if constexpr (F8) {
@@ -510,7 +558,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     store_box(&m_g, col0 + cc, row, row < a.T, stg + (cc & 32) * (kStgWarp / 64), lane, w);
                 };
 #pragma unroll 1
-                for (int cc = 0; cc < kBN / 2; cc += 64) {
+                for (int cc = 0; cc < cols; cc += 64) {
                     float v[32], u[32];
                     tmem_ld_chunk2<32>(tm + cc, tm + cc + 32, v, u);
                     out(v, cc);
@@ -763,10 +811,10 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- host
 std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode_ce{nullptr};
 
-// row-major matrix in boxes of 64 rows x 128 bytes, 128-byte swizzle; `out`:
-// 32 rows x 64 bytes, 64-byte swizzle
+// row-major matrix in boxes of box_rows x 128 bytes, 128-byte swizzle;
+// `narrow`: 64 bytes, 64-byte swizzle
 sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int elem,
-                 const char *what, bool out = false)
+                 const char *what, uint32_t box_rows = 64, bool narrow = false)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = g_encode_ce.load(std::memory_order_acquire);
     if (!enc) {
@@ -783,11 +831,11 @@ sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, i
     }
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
-    cuuint32_t box[2] = {(out ? 64u : 128u) / (uint32_t)elem, out ? 32u : 64u};
+    cuuint32_t box[2] = {(narrow ? 64u : 128u) / (uint32_t)elem, box_rows};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
                            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         CE_FAIL(SG_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
@@ -823,8 +871,8 @@ sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int clu
 }
 
 template <int CG, int MODE, bool F8>
-sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CUtensorMap &dW,
-                    const CeArgs &a, bool after, cudaStream_t st)
+sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CUtensorMap &gk,
+                    const CUtensorMap &dW, const CeArgs &a, bool after, cudaStream_t st)
 {
     // once for each device (one bit of the mask)
     static std::atomic<uint64_t> done{0};
@@ -837,7 +885,7 @@ sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMa
         done.fetch_or(bit, std::memory_order_relaxed);
     }
     return launch(k_ce<CG, MODE, F8>, dim3(Cfg<CG>::C * CG), kCeThreads, (int)Cfg<CG>::kSmem, CG, after, st, h, W, g,
-                  dW, a);
+                  gk, dW, a);
 }
 
 // One call's tiles and the places of its work memory
@@ -845,11 +893,12 @@ struct Plan {
     int es = 2, CG = 1, BM = 128, C = kSMs;
     bool pack_h = false, pack_W = false;
     int64_t ldp = 0;             // row stride of the packed copies
-    int64_t nm = 0, Tp = 0;
+    int64_t nm = 0, Tp = 0, bw = kBN;
+    int64_t ab = 64, an = 2, kt = 64;  // boxes: see CeArgs
     // forward
     int64_t slots = 0;
     // backward
-    int64_t Vc = 0, nn = 0;      // vocabulary of a piece, its tiles
+    int64_t Vc = 0;              // vocabulary of a piece
     int64_t dh_nn = 0, dh_tiles = 0, split = 1;
     // byte offsets
     int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
@@ -861,6 +910,24 @@ bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) 
 // shorter than its output takes to reach memory (2 K blocks of a CTA, 4 of a
 // pair) costs that, and each has a little of its own.
 int64_t tile_cost(int64_t nk, int CG) { return 2 * (nk > 2 * CG ? nk : 2 * CG) + 1; }
+
+// Columns of the forward pass's tiles: the width, a multiple of 16, at which the
+// clusters' last turn is fullest.  The time of a tile goes by the rows of W
+// that it loads and, with two CTAs, whose tiles are bound by the L2 cache, by
+// those of h too; it has a little of its own.  (T = 1, H = 2048, V = 128000:
+// 572 tiles of 224 on 152 CTAs take 87 us, 500 of 256 take 90.)
+int64_t tile_width(int64_t nm, int64_t V, int CG, int C)
+{
+    int64_t best = kBN, least = 0;
+    for (int64_t w = kBN; w >= 128; w -= 16) {
+        const int64_t cost = ceil_div(nm * ceil_div(V, w), C) * (w + (CG == 2 ? 272 : 40));
+        if (w == kBN || cost < least) {
+            best = w;
+            least = cost;
+        }
+    }
+    return best;
+}
 
 void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
                int32_t dtype, bool backward, Plan *p)
@@ -874,6 +941,15 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     p->ldp = ceil_div(H * p->es, 16) * 16 / p->es;
     p->nm = ceil_div(T, p->BM);
     p->Tp = p->nm * p->BM;
+    // only the rows that there are: copying boxes of 64 rows of which few exist
+    // takes longer than the rest of a stage (forward pass, T = 1, H = 2048, V =
+    // 128000: 103 us with two such boxes, 87 with one of 8)
+    if (T <= 128) {
+        p->an = T <= 64 ? 1 : 2;
+        p->ab = ceil_div(ceil_div(T, p->an), 8) * 8;
+    }
+    if (T < 64)
+        p->kt = ceil_div(T, 16) * 16;
     auto take = [&](int64_t n) {
         const int64_t at = p->bytes;
         p->bytes += ceil_div(n, 256) * 256;
@@ -884,7 +960,8 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     if (p->pack_W)
         p->o_W = take(V * p->ldp * p->es);
     if (!backward) {
-        p->slots = 2 * (p->nm == 1 ? (int64_t)p->C : ceil_div(V, kBN));
+        p->bw = tile_width(p->nm, V, p->CG, p->C);
+        p->slots = 2 * (p->nm == 1 ? (int64_t)p->C : ceil_div(V, p->bw));
         p->o_part = take(p->slots * p->Tp * 8);
         p->o_zsum = take(p->slots * p->Tp * 4);
         p->o_ztgt = take(T * 4);
@@ -897,7 +974,6 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     if (Vc > ceil_div(V, kBN) * kBN)
         Vc = ceil_div(V, kBN) * kBN;
     p->Vc = Vc;
-    p->nn = Vc / kBN;
     p->dh_nn = ceil_div(H, kBN);
     p->dh_tiles = p->nm * p->dh_nn;
     // split K of dh until its units and the dW tiles fill the clusters evenly
@@ -948,9 +1024,10 @@ void pack(const void *src, int64_t ld, int64_t rows, int64_t cols, void *dst, in
                                                  static_cast<E *>(dst), ldd);
 }
 
-// maps of h and W, packed first where their rows need it
+// maps of h and W (mh, mW: in the logits' tiles; mhk, mWk: as K rows), packed
+// first where their rows need it
 sg_status operand_maps(const Plan &p, const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
-                       int64_t V, uint8_t *work, CUtensorMap *mh, CUtensorMap *mW, cudaStream_t st)
+                       int64_t V, uint8_t *work, CUtensorMap *mh, CUtensorMap *mW, CUtensorMap *mhk, CUtensorMap *mWk, cudaStream_t st)
 {
     auto packed = [&](const void *&src, int64_t &ld, int64_t rows, int64_t at) {
         if (p.es == 1)
@@ -965,8 +1042,12 @@ sg_status operand_maps(const Plan &p, const void *h, int64_t ldh, int64_t T, int
     if (p.pack_W)
         packed(W, ldw, V, p.o_W);
     SG_TRY_CUDA(cudaGetLastError());
-    CE_TRY(map_of(mh, h, H, T, ldh, p.es, "h"));
-    return map_of(mW, W, H, V, ldw, p.es, "W");
+    if (mhk) {
+        CE_TRY(map_of(mhk, h, H, T, ldh, p.es, "h", (uint32_t)p.kt));
+        CE_TRY(map_of(mWk, W, H, V, ldw, p.es, "W"));
+    }
+    CE_TRY(map_of(mh, h, H, T, ldh, p.es, "h", (uint32_t)p.ab));
+    return map_of(mW, W, H, V, ldw, p.es, "W", (uint32_t)p.bw / 2);
 }
 
 }  // namespace
@@ -1011,13 +1092,17 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t *w8 = static_cast<uint8_t *>(work);
     CUtensorMap mh, mW;
-    CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, st));
+    CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, nullptr, nullptr, st));
     CeArgs a = {};
     a.T = (int32_t)T;
     a.V = (int32_t)V;
     a.H = (int32_t)H;
     a.nm = (int32_t)p.nm;
-    a.nn = (int32_t)ceil_div(V, kBN);
+    a.nn = (int32_t)ceil_div(V, p.bw);
+    a.bw = (int32_t)p.bw;
+    a.ab = (int32_t)p.ab;
+    a.an = (int32_t)p.an;
+    a.kt = (int32_t)p.kt;
     a.nk = (int32_t)ceil_div(H * p.es, 128);
     a.f16 = dtype == SG_F16;
     a.h_scale = h_scale;
@@ -1030,11 +1115,11 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     a.Tp = (int32_t)p.Tp;
     a.status = status;
     if (dtype == SG_E4M3)
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, a, false, st))
-                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, a, false, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, mh, a, false, st))
+                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, mh, a, false, st)));
     else
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, a, false, st))
-                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, a, false, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, mh, a, false, st))
+                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, mh, a, false, st)));
     JoinArgs j;
     j.part = a.part, j.zsum = a.zsum, j.ztgt = a.ztgt, j.targets = targets, j.loss = loss, j.lse = lse;
     j.status = status, j.slots = (int32_t)p.slots, j.Tp = a.Tp, j.T = a.T, j.V = a.V, j.ignore = ignore_index;
@@ -1070,16 +1155,17 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
         CE_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_softmax_ce_work), aligned to 256", fn,
                 (long long)p.bytes);
     uint8_t *w8 = static_cast<uint8_t *>(work);
-    CUtensorMap mh, mW, mg, mgs, mdW;
-    CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, st));
-    // g: [T][Vc], loaded in boxes of 64 rows, stored in boxes of 32 x 32
-    CE_TRY(map_of(&mg, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g"));
-    CE_TRY(map_of(&mgs, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g", true));
+    CUtensorMap mh, mW, mhk, mWk, mg, mgk, mgs, mdW;
+    CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, &mhk, &mWk, st));
+    // g: [T][Vc], loaded by rows and by columns, stored in boxes of 32 x 32
+    CE_TRY(map_of(&mg, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g", (uint32_t)p.ab));
+    CE_TRY(map_of(&mgk, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g", (uint32_t)p.kt));
+    CE_TRY(map_of(&mgs, w8 + p.o_g, p.Vc, T, p.Vc, 2, "g", 32, true));
     // a TMA store ends on a multiple of 16 bytes: with other widths it would
     // write past a row's end
     const bool dw_tma = dW && tma_ok(dW, lddw, 2) && H % 8 == 0;
     if (dw_tma)
-        CE_TRY(map_of(&mdW, dW, H, V, lddw, 2, "dW", true));
+        CE_TRY(map_of(&mdW, dW, H, V, lddw, 2, "dW", 32, true));
     else
         mdW = mgs;
     CeArgs a = {};
@@ -1087,6 +1173,10 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     a.V = (int32_t)V;
     a.H = (int32_t)H;
     a.nm = (int32_t)p.nm;
+    a.bw = (int32_t)p.bw;
+    a.ab = (int32_t)p.ab;
+    a.an = (int32_t)p.an;
+    a.kt = (int32_t)p.kt;
     a.nk = (int32_t)ceil_div(H, 64);
     a.f16 = dtype == SG_F16;
     a.targets = targets;
@@ -1108,9 +1198,9 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
         const int64_t vc = V - v0 < p.Vc ? V - v0 : p.Vc;
         a.v0 = (int32_t)v0;
         a.first = v0 == 0;
-        a.nn = (int32_t)ceil_div(vc, kBN);
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kProb, false>(mh, mW, mgs, mdW, a, v0 > 0, st))
-                         : (launch_ce<2, kProb, false>(mh, mW, mgs, mdW, a, v0 > 0, st)));
+        a.nn = (int32_t)ceil_div(vc, p.bw);
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kProb, false>(mh, mW, mgs, mgs, mgs, a, v0 > 0, st))
+                         : (launch_ce<2, kProb, false>(mh, mW, mgs, mgs, mgs, a, v0 > 0, st)));
         a.dh_kb = (int32_t)ceil_div(vc, 64);
         a.dw_tiles = dW ? (int32_t)(ceil_div(vc, p.BM) * p.dh_nn) : 0;
         // turns of dW tiles so that all clusters end at about the same time
@@ -1123,8 +1213,8 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
             q_hi = 0;
         a.dw_hi = (int32_t)q_hi;
         a.dw_lo = (int32_t)(q_hi + ceil_div(a.dw_tiles - q_hi * p.C > 0 ? a.dw_tiles - q_hi * p.C : 0, p.C - hi));
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mh, mW, mg, mdW, a, true, st))
-                         : (launch_ce<2, kGrad, false>(mh, mW, mg, mdW, a, true, st)));
+        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st))
+                         : (launch_ce<2, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st)));
     }
     if (dh) {
         const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), kBN / 32);
