@@ -26,37 +26,40 @@ namespace {
             return rc_;         \
     } while (0)
 
-constexpr int kDropThreads = 256, kDropCtas = 6, kDropU = 4;
+constexpr int kDropThreads = 256, kDropCtas = 6;
+constexpr int drop_u(int size) { return size == 4 ? 2 : 4; }  // blocks of a thread: 64 bytes
 constexpr int64_t kMaxCols = 32768;   // of the norm: a row lies in one CTA's registers
 constexpr int kSMs = 152;
 
 // ---------------------------------------------------------------- dropout
-// One warp for a segment of 256 columns: any alignment and width.
+// One warp for a segment of 256 columns: any alignment and width.  segs
+// (segments of a row) times rows is below 2^31.
 template <typename T>
-__global__ void __launch_bounds__(kDropThreads)
-    k_dropout_any(const T *x, int64_t ldx, int64_t nrows, int64_t cols, const Drop d, T *y, int64_t ldy)
+__global__ void __launch_bounds__(kDropThreads, kDropCtas)
+    k_dropout_any(const T *x, int64_t ldx, uint32_t nseg, uint32_t segs, int cols, uint32_t row0, const Drop d, T *y,
+                  int64_t ldy)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t segs = (cols + kSeg - 1) / kSeg;
-    const int64_t step = (int64_t)gridDim.x * (kDropThreads / 32);
-    for (int64_t i = (int64_t)blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32; i < nrows * segs; i += step) {
-        const int64_t r = i / segs, c0 = (i - r * segs) * kSeg;
-        Pack8<T> p = load8<T, false>(x + r * ldx, c0, lane, cols);
-        if (d.drop) {
-            const Keep<false> k(d, c0, lane, (uint32_t)r);
-            float v[8];
-            unpack8(p, v);
+    const uint32_t i = blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32;
+    if (i >= nseg)
+        return;
+    const uint32_t r = i / segs;
+    const int c0 = (int)(i - r * segs) * kSeg;
+    Pack8<T> p = load8<T, false>(x + r * ldx, c0, lane, cols);
+    if (d.drop) {
+        const Keep<false> k(d, c0, lane, row0 + r);
+        float v[8];
+        unpack8(p, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = k.at(j) ? __fmul_rn(v[j], d.scale) : 0.f;
-            p = pack8<T>(v);
-        }
-        store8<T, false>(y + r * ldy, c0, lane, cols, p);
+        for (int j = 0; j < 8; ++j)
+            v[j] = k.at(j) ? __fmul_rn(v[j], d.scale) : 0.f;
+        p = pack8<T>(v);
     }
+    store8<T, false>(y + r * ldy, c0, lane, cols, p);
 }
 
 // Rows of whole, aligned eights: the blocks of all rows are numbered through,
-// and a thread takes kDropU of them, kDropThreads apart, whose loads it issues
+// and a thread takes U of them, kDropThreads apart, whose loads it issues
 // together.  n (blocks) is below 2^31; row = i / blks by a multiplication.
 // DENSE: no gaps between rows.  The copy alone would take as long as long as
 // loads stay ahead of the rounds (about 140 instructions for eight elements):
@@ -67,7 +70,8 @@ __global__ void __launch_bounds__(kDropThreads, kDropCtas)
     k_dropout(const T *x, int64_t ldx, uint32_t n, uint32_t blks, uint32_t magic, uint32_t shift, uint32_t row0,
               const Drop d, T *y, int64_t ldy)
 {
-    const uint32_t i0 = blockIdx.x * (kDropThreads * kDropU) + threadIdx.x;
+    constexpr int U = drop_u(sizeof(T));
+    const uint32_t i0 = blockIdx.x * (kDropThreads * U) + threadIdx.x;
     auto row_of = [&](uint32_t i) { return blks == 1 ? i : (uint32_t)(((uint64_t)i * magic) >> 32 >> shift); };
     auto at = [&](uint32_t i, int64_t ld) {
         if (DENSE)
@@ -75,21 +79,21 @@ __global__ void __launch_bounds__(kDropThreads, kDropCtas)
         const uint32_t r = row_of(i);
         return r * ld + (i - r * blks) * 8;
     };
-    Pack8<T> p[kDropU];
+    Pack8<T> p[U];
 #pragma unroll
-    for (int u = 0; u < kDropU; ++u) {
+    for (int u = 0; u < U; ++u) {
         const uint32_t i = i0 + u * kDropThreads;
         if (i < n)
             p[u] = load_pack(x + at(i, ldx));
     }
 #pragma unroll
-    for (int u = 0; u < kDropU; ++u) {
+    for (int u = 0; u < U; ++u) {
         const uint32_t i = i0 + u * kDropThreads;
         if (i >= n)
             return;
         if (d.drop) {
             const uint32_t r = row_of(i);
-            const Keep<true> k(d, (int64_t)(i - r * blks) * 8, 0, row0 + r);
+            const Keep<true> k(d, (int)(i - r * blks) * 8, 0, row0 + r);
             float v[8];
             unpack8(p[u], v);
 #pragma unroll
@@ -153,8 +157,13 @@ struct Ring8 {
     __device__ __forceinline__ void copy(int slot, int m, int n, const T *src) const
     {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            tc::cp_async16(tc::smem_u32(at(slot, m, n, i)), reinterpret_cast<const uint4 *>(src) + i);
+        for (int i = 0; i < kPieces; ++i) {
+            const uint32_t dst = tc::smem_u32(at(slot, m, n, i));
+            if constexpr (kPieces == 2)
+                tc::cp_async16_l1(dst, reinterpret_cast<const uint4 *>(src) + i);
+            else
+                tc::cp_async16(dst, reinterpret_cast<const uint4 *>(src) + i);
+        }
     }
     __device__ __forceinline__ Pack8<T> get(int slot, int m, int n) const
     {
@@ -176,14 +185,19 @@ __device__ __forceinline__ void copies_wait()
 
 // threads of a CTA, and CTAs to an SM that the registers are cut for
 constexpr int norm_threads(int warps) { return warps == 1 ? 256 : warps * 32; }
-constexpr int norm_ctas(int warps) { return 1024 / norm_threads(warps); }
+constexpr int norm_ctas(int warps, int size)
+{
+    const int n = (size == 4 ? 512 : 1024) / norm_threads(warps);
+    return n < 1 ? 1 : n;
+}
 
 struct NormFwd {
     const void *x, *res, *w;
     void *u, *y;
     uint8_t *y8;
     float *rstd, *scale8;
-    int64_t ldx, ldr, ldu, ldy, ld8, nrows, cols;
+    int64_t ldx, ldr, ldu, ldy, ld8, nrows;
+    int cols;
     float eps;
     Drop d;
 };
@@ -191,7 +205,7 @@ struct NormFwd {
 // A row by WARPS warps (one warp: eight rows to a CTA), NV segments to a warp.
 // Row groups step over the rows.
 template <typename T, bool VEC, int WARPS, int NV, int S>
-__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_fwd(const NormFwd a)
+__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T))) k_norm_fwd(const NormFwd a)
 {
     __shared__ RowSums sm;
     extern __shared__ uint4 dyn[];
@@ -206,7 +220,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
             if (r < a.nrows) {
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
-                    const int64_t c = (int64_t)(n * WARPS + wr) * kSeg + lane * 8;
+                    const int c = (n * WARPS + wr) * kSeg + lane * 8;
                     if (c < a.cols) {
                         ring.copy(slot, 0, n, ax + r * a.ldx + c);
                         if (ar)
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
     Pack8<T> w[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n)
-        w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (int64_t)(n * WARPS + wr) * kSeg, lane, a.cols);
+        w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (n * WARPS + wr) * kSeg, lane, a.cols);
     int turn = 0, slot = 0;
     for (int64_t r = g; r < a.nrows; r += groups, ++turn) {
         Pack8<T> u[NV];
@@ -232,7 +246,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
             copies_wait<S - 1>();
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
+            const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;  // and neither has a later segment columns of this thread
             Pack8<T> p;
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
         }
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
+            const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;
             float y[8];
@@ -320,14 +334,15 @@ struct NormBwd {
     const float *rstd;
     void *du, *dx;
     float *part;  // [row groups][cols], or NULL: no dweight
-    int64_t lddy, ldu, ldi, ldo, lddx, nrows, cols;
+    int64_t lddy, ldu, ldi, ldo, lddx, nrows;
+    int cols;
     Drop d;
 };
 
 // Row groups of WARPS warps step over the rows; a thread keeps the sum of its
 // columns of dweight in registers until its last row.
 template <typename T, bool VEC, int WARPS, int NV, int S>
-__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_bwd(const NormBwd a)
+__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T))) k_norm_bwd(const NormBwd a)
 {
     __shared__ RowSums sm;
     extern __shared__ uint4 dyn[];
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
             if (r < a.nrows) {
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
-                    const int64_t c = (int64_t)(n * WARPS + wr) * kSeg + lane * 8;
+                    const int c = (n * WARPS + wr) * kSeg + lane * 8;
                     if (c < a.cols) {
                         ring.copy(slot, 0, n, ady + r * a.lddy + c);
                         ring.copy(slot, 1, n, au + r * a.ldu + c);
@@ -361,7 +376,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
     Pack8<T> w[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n)
-        w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (int64_t)(n * WARPS + wr) * kSeg, lane, a.cols);
+        w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (n * WARPS + wr) * kSeg, lane, a.cols);
     float dw[NV][8] = {};
     int turn = 0, slot = 0;
     for (int64_t r = g; r < a.nrows; r += groups, ++turn) {
@@ -371,7 +386,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
             copies_wait<S - 1>();
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
+            const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;  // and neither has a later segment columns of this thread
             Pack8<T> dy, u;
@@ -395,7 +410,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
         const float back = rstd * rstd * rstd * (dot / (float)a.cols);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int64_t c0 = (int64_t)(n * WARPS + wr) * kSeg;
+            const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;
             // once more from shared memory (or, without VEC, from the caches)
@@ -442,9 +457,9 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS)) k_norm_
         for (int n = 0; n < NV; ++n)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int64_t c = col_of<VEC>((int64_t)(n * WARPS + wr) * kSeg, lane, j);
+                const int c = col_of<VEC>((n * WARPS + wr) * kSeg, lane, j);
                 if (c < a.cols)
-                    a.part[g * a.cols + c] = dw[n][j];
+                    a.part[g * (int64_t)a.cols + c] = dw[n][j];
             }
     }
 }
@@ -496,7 +511,7 @@ template <typename T, int NA, int WARPS, int NV>
 constexpr int ring_rows()
 {
     const int row = NA * NV * norm_threads(WARPS) * (int)sizeof(Pack8<T>);
-    const int s = (216 << 10) / norm_ctas(WARPS) / row;
+    const int s = (216 << 10) / norm_ctas(WARPS, sizeof(T)) / row;
     return s > 4 ? 4 : s < 1 ? 1 : s;
 }
 
@@ -509,7 +524,7 @@ sg_status run_fwd(const NormFwd &a, cudaStream_t st)
     if constexpr (smem > 226 << 10) {  // fp32 rows above 16384 columns: not one is held
         return run_fwd<T, false, W, N>(a, st);
     } else {
-        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * norm_ctas(W);
+        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * norm_ctas(W, sizeof(T));
         NORM_TRY(allow_smem(k_norm_fwd<T, VEC, W, N, S>, smem, done));
         k_norm_fwd<T, VEC, W, N, S><<<(unsigned)(need < most ? need : most), norm_threads(W), smem, st>>>(a);
         return SG_OK;
@@ -554,7 +569,7 @@ sg_status launch_bwd(const NormBwd &a, int64_t grid, cudaStream_t st)
 }
 
 // CTAs of the backward kernel, and the row groups they make
-int64_t bwd_groups(int64_t nrows, int64_t cols, int64_t *grid)
+int64_t bwd_groups(int64_t nrows, int64_t cols, int size, int64_t *grid)
 {
     int warps = 32;
 #define X(W, N)                                           \
@@ -562,7 +577,7 @@ int64_t bwd_groups(int64_t nrows, int64_t cols, int64_t *grid)
         warps = (W);
     NORM_SHAPES(X)
 #undef X
-    const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * norm_ctas(warps);
+    const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * norm_ctas(warps, size);
     *grid = need < most ? need : most;
     return warps == 1 ? *grid * 8 : *grid;
 }
@@ -574,10 +589,12 @@ void launch_dropout(bool vec, const void *x, int64_t ldx, int64_t nrows, int64_t
     const T *xs = static_cast<const T *>(x);
     T *ys = static_cast<T *>(y);
     if (!vec) {
-        int64_t grid = ceil_div(nrows * ceil_div(cols, kSeg), kDropThreads / 32);
-        if (grid > (1 << 20))
-            grid = 1 << 20;
-        k_dropout_any<T><<<(unsigned)grid, kDropThreads, 0, st>>>(xs, ldx, nrows, cols, d, ys, ldy);
+        const int64_t segs = ceil_div(cols, kSeg), slab = ((1ll << 31) - 1) / segs;  // rows of a launch
+        for (int64_t r0 = 0; r0 < nrows; r0 += slab) {
+            const int64_t n = (nrows - r0 < slab ? nrows - r0 : slab) * segs;
+            k_dropout_any<T><<<(unsigned)ceil_div(n, kDropThreads / 32), kDropThreads, 0, st>>>(
+                xs + r0 * ldx, ldx, (uint32_t)n, (uint32_t)segs, (int)cols, (uint32_t)r0, d, ys + r0 * ldy, ldy);
+        }
         return;
     }
     // i / blks = (i magic) >> (32 + shift) for i < 2^31, with magic =
@@ -589,10 +606,11 @@ void launch_dropout(bool vec, const void *x, int64_t ldx, int64_t nrows, int64_t
     while ((2ull << shift) < blks)
         ++shift;
     const uint32_t magic = blks == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + blks - 1) / blks);
-    const int64_t slab = ((1ll << 31) - 1 - kDropThreads * kDropU) / blks;  // rows of a launch
+    constexpr int U = drop_u(sizeof(T));
+    const int64_t slab = ((1ll << 31) - 1 - kDropThreads * U) / blks;  // rows of a launch
     for (int64_t r0 = 0; r0 < nrows; r0 += slab) {
         const int64_t n = (nrows - r0 < slab ? nrows - r0 : slab) * blks;
-        const unsigned grid = (unsigned)ceil_div(n, kDropThreads * kDropU);
+        const unsigned grid = (unsigned)ceil_div(n, kDropThreads * U);
         if (ldx == cols && ldy == cols)
             k_dropout<T, true><<<grid, kDropThreads, 0, st>>>(xs + r0 * ldx, ldx, (uint32_t)n, blks, magic, shift,
                                                               (uint32_t)r0, d, ys + r0 * ldy, ldy);
@@ -614,9 +632,9 @@ sg_status check_rows(const char *fn, int64_t nrows, int64_t cols, int32_t dtype)
     if (nrows < 0 || cols < 1)
         NORM_FAIL(SG_ERR_INVALID, "%s: need rows >= 0 and cols >= 1 (rows=%lld cols=%lld)", fn, (long long)nrows,
                   (long long)cols);
-    if (nrows > INT32_MAX || cols > INT32_MAX)
-        NORM_FAIL(SG_ERR_UNSUPPORTED, "%s: rows and cols must be below 2^31 (rows=%lld cols=%lld)", fn,
-                  (long long)nrows, (long long)cols);
+    if (nrows > INT32_MAX || cols > (1 << 30))
+        NORM_FAIL(SG_ERR_UNSUPPORTED, "%s: rows=%lld or cols=%lld is above 2^31 - 1 or 2^30", fn, (long long)nrows,
+                  (long long)cols);
     return SG_OK;
 }
 
@@ -691,10 +709,10 @@ sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, i
     if (rows == 0)
         return SG_OK;
     a.x = x, a.res = residual, a.w = weight, a.u = u, a.y = y, a.y8 = y8, a.rstd = rstd, a.scale8 = y8_scale;
-    a.ldx = ldx, a.ldr = ldr, a.ldu = ldu, a.ldy = ldy, a.ld8 = ldy8, a.nrows = rows, a.cols = cols;
+    a.ldx = ldx, a.ldr = ldr, a.ldu = ldu, a.ldy = ldy, a.ld8 = ldy8, a.nrows = rows, a.cols = (int)cols;
     a.eps = (float)eps;
     cudaStream_t st = (cudaStream_t)stream;
-    // 8-bit rows are written in pieces of 8 bytes: half the 16 that vec_ok asks
+    // 8-bit rows are written in pieces of 8 bytes
     const bool vec = cols % 8 == 0 && vec_ok(x, ldx, es) && vec_ok(residual, ldr, es) && vec_ok(weight, cols, es) &&
                      vec_ok(u, ldu, es) && vec_ok(y, ldy, es) && (!y8 || (((uintptr_t)y8) % 8 == 0 && ldy8 % 8 == 0));
     if (dtype == SG_BF16)
@@ -716,7 +734,7 @@ sg_status sg_add_rmsnorm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes)
     if (cols > kMaxCols)
         NORM_FAIL(SG_ERR_UNSUPPORTED, "%s: cols=%lld is above %lld", fn, (long long)cols, (long long)kMaxCols);
     int64_t grid;
-    *bytes = bwd_groups(rows, cols, &grid) * cols * 4;
+    *bytes = bwd_groups(rows, cols, 2, &grid) * cols * 4;  // the type with the most groups
     return SG_OK;
 }
 
@@ -749,13 +767,13 @@ sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_
         return SG_OK;
     }
     int64_t grid;
-    const int64_t groups = bwd_groups(rows, cols, &grid);
+    const int64_t groups = bwd_groups(rows, cols, (int)es, &grid);
     if (dweight && (!work || work_bytes < groups * cols * 4 || ((uintptr_t)work) % 4 != 0))
         NORM_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_add_rmsnorm_bwd_work), aligned to 4", fn,
                   (long long)(groups * cols * 4));
     a.dy = dy, a.u = u, a.w = weight, a.du_in = du_in, a.rstd = rstd, a.du = du, a.dx = dx;
     a.part = dweight ? static_cast<float *>(work) : nullptr;
-    a.lddy = lddy, a.ldu = ldu, a.ldi = lddu_in, a.ldo = lddu, a.lddx = lddx, a.nrows = rows, a.cols = cols;
+    a.lddy = lddy, a.ldu = ldu, a.ldi = lddu_in, a.ldo = lddu, a.lddx = lddx, a.nrows = rows, a.cols = (int)cols;
     const bool vec = cols % 8 == 0 && vec_ok(dy, lddy, es) && vec_ok(u, ldu, es) && vec_ok(du_in, lddu_in, es) &&
                      vec_ok(weight, cols, es) && vec_ok(du, lddu, es) && vec_ok(dx, lddx, es);
     if (dtype == SG_BF16)

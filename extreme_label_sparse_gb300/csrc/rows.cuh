@@ -2,8 +2,8 @@
 // (dropout, RMS norm), and the counter-based random bits of dropout.
 //
 // A warp takes segments of 256 columns of a row, eight elements to a lane.
-// VEC: the lane's elements are contiguous (16-byte accesses); needs rows that
-// start on 16 bytes and a whole number of eights.  Otherwise the lane takes
+// VEC: the lane's elements are contiguous; needs rows that start on eight
+// elements' bytes and a whole number of eights.  Otherwise the lane takes
 // columns lane, lane + 32, ...: any alignment and width, still whole sectors.
 #pragma once
 
@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "sg_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace rows {
 
@@ -42,7 +43,8 @@ struct alignas(16) Pack8 {
     T v[8];
 };
 
-// eight aligned elements, in accesses of 16 bytes
+// eight aligned elements: 16 bytes in one access; 32 (fp32) in two loads, which
+// meet in L1, and one store, since halves of a sector would each go to L2
 template <typename T>
 __device__ __forceinline__ Pack8<T> load_pack(const T *src)
 {
@@ -56,9 +58,10 @@ __device__ __forceinline__ Pack8<T> load_pack(const T *src)
 template <typename T>
 __device__ __forceinline__ void store_pack(T *dst, const Pack8<T> &p)
 {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(p) / 16; ++i)
-        reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(&p)[i];
+    if constexpr (sizeof(p) == 32)
+        tc::st_global32(dst, reinterpret_cast<const uint32_t *>(&p));
+    else
+        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(&p);
 }
 
 // all eight at once: the 16-bit types convert in pairs
@@ -96,14 +99,14 @@ __device__ __forceinline__ Pack8<T> pack8(const float (&v)[8])
 
 // column of element j of this lane in the segment that starts at column c0
 template <bool VEC>
-__device__ __forceinline__ int64_t col_of(int64_t c0, int lane, int j)
+__device__ __forceinline__ int col_of(int c0, int lane, int j)
 {
     return VEC ? c0 + lane * 8 + j : c0 + lane + 32 * j;
 }
 
 // elements past `cols` read as zero
 template <typename T, bool VEC>
-__device__ __forceinline__ Pack8<T> load8(const T *row, int64_t c0, int lane, int64_t cols)
+__device__ __forceinline__ Pack8<T> load8(const T *row, int c0, int lane, int cols)
 {
     Pack8<T> p;
     if constexpr (VEC) {
@@ -113,27 +116,37 @@ __device__ __forceinline__ Pack8<T> load8(const T *row, int64_t c0, int lane, in
         for (int j = 0; j < 8; ++j)
             p.v[j] = from_f<T>(0.f);
     } else {
+        const T *at = row + c0 + lane;
+        if (c0 + kSeg <= cols) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t c = col_of<VEC>(c0, lane, j);
-            p.v[j] = c < cols ? row[c] : from_f<T>(0.f);
+            for (int j = 0; j < 8; ++j)
+                p.v[j] = at[32 * j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                p.v[j] = col_of<VEC>(c0, lane, j) < cols ? at[32 * j] : from_f<T>(0.f);
         }
     }
     return p;
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *row, int64_t c0, int lane, int64_t cols, const Pack8<T> &p)
+__device__ __forceinline__ void store8(T *row, int c0, int lane, int cols, const Pack8<T> &p)
 {
     if constexpr (VEC) {
         if (c0 + lane * 8 < cols)
             store_pack(row + c0 + lane * 8, p);
     } else {
+        T *at = row + c0 + lane;
+        if (c0 + kSeg <= cols) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t c = col_of<VEC>(c0, lane, j);
-            if (c < cols)
-                row[c] = p.v[j];
+            for (int j = 0; j < 8; ++j)
+                at[32 * j] = p.v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col_of<VEC>(c0, lane, j) < cols)
+                    at[32 * j] = p.v[j];
         }
     }
 }
@@ -179,7 +192,7 @@ struct Keep {
     uint32_t w[VEC ? 4 : 1];
     uint32_t below;
 
-    __device__ __forceinline__ Keep(const Drop &d, int64_t c0, int lane, uint32_t row)
+    __device__ __forceinline__ Keep(const Drop &d, int c0, int lane, uint32_t row)
     {
         uint32_t r[4];
         philox10(d, (uint32_t)(c0 / 8) + lane, row, r);
@@ -229,10 +242,11 @@ inline bool make_drop(double p, uint64_t seed, uint64_t offset, Drop *d)
     return true;
 }
 
-// host: a matrix can be taken in 16-byte pieces (a NULL one does not hinder)
+// host: a matrix can be taken in pieces of eight elements (a NULL one does not
+// hinder)
 inline bool vec_ok(const void *p, int64_t ld, int64_t elem)
 {
-    return !p || ((((uintptr_t)p) & 15) == 0 && (ld * elem) % 16 == 0);
+    return !p || (((uintptr_t)p) % (8 * elem) == 0 && ld % 8 == 0);
 }
 
 }  // namespace rows

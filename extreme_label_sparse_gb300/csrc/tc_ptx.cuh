@@ -232,6 +232,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// the same through L1, where the other half of a 32-byte sector is asked for
+// right after
+__device__ __forceinline__ void cp_async16_l1(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // arrive on `bar` once every cp.async this thread issued so far has landed
 // (the arrival counts toward the barrier's expected count)
 __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar)
@@ -449,6 +456,14 @@ __device__ __forceinline__ void red_add_v4(float *dst, float a, float b, float c
 {
     asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(a), "f"(b), "f"(c),
                  "f"(d)
+                 : "memory");
+}
+
+// 32 bytes to a 32-byte aligned address: a whole sector by one thread
+__device__ __forceinline__ void st_global32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
 
