@@ -50,6 +50,7 @@ constexpr int kCeThreads = 32 * (kEpiWarps + 2);
 constexpr int kBN = 256;                 // tile columns
 constexpr uint32_t kBox = 8192;          // one TMA box: 64 rows of 128 bytes
 constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's outputs on their way: two boxes of 32 x 32
+constexpr int kJoinThreads = 128;
 constexpr int kBand = 16;                // row tiles that walk the vocabulary together
 
 template <int CG>
@@ -84,10 +85,11 @@ struct CeArgs {
     // kLse
     const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
     const int32_t *targets;
-    float2 *part;         // running maximum (of z log2 e) and sum: [row][slot] for one row tile, else [slot][row]
+    float2 *part;         // [Tp][slots] running maximum (of z log2 e) and sum
     float *zsum;          // the same for the sum of z, or NULL
+    int32_t slots;
     float *ztgt;          // [T] the target's logit
-    int32_t Tp, ignore;
+    int32_t ignore;
     // kProb
     const float *lse, *dloss;
     float *gscale;        // factor of g and its inverse, written by the first CTA
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 // one row tile: the running values cover all tiles of this
                 // CTA; else they are written out for every tile
                 if (a.nm > 1) {
-                    const int64_t at = (int64_t)(t.unit * 2 + half) * a.Tp + row;
+                    const int64_t at = (int64_t)row * a.slots + t.unit * 2 + half;
                     a.part[at] = make_float2(m2, s);
                     if (a.zsum)
                         a.zsum[at] = zs;
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         }
         if constexpr (MODE == kLse) {
             if (a.nm == 1) {
-                const int64_t at = (int64_t)row_in * (2 * K::C) + cl * 2 + half;
+                const int64_t at = (int64_t)row_in * a.slots + cl * 2 + half;
                 a.part[at] = make_float2(m2, s);
                 if (a.zsum)
                     a.zsum[at] = zs;
@@ -672,7 +674,7 @@ struct JoinArgs {
     const int32_t *targets;
     float *loss, *lse;
     int32_t *status;
-    int32_t slots, Tp, T, V, ignore;
+    int32_t slots, V, ignore;
     float smooth;
 };
 
@@ -692,62 +694,39 @@ __device__ __forceinline__ void join_out(const JoinArgs &a, int t, float m, floa
     a.loss[t] = out;
 }
 
-// lse and loss of 32 rows from their partial maxima and sums, [slot][row]
-__global__ void __launch_bounds__(1024) k_ce_join(const JoinArgs a)
+// lse and loss of a row, a CTA each, from its partial maxima and sums
+__global__ void __launch_bounds__(kJoinThreads) k_ce_join(const JoinArgs a)
 {
-    __shared__ float2 sm[32][33];
-    __shared__ float sz[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int t = blockIdx.x * 32 + lane;  // below Tp, a multiple of 128
+    constexpr int NW = kJoinThreads / 32;
+    __shared__ float sm[3][NW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = blockIdx.x;
+    const float2 *part = a.part + (int64_t)t * a.slots;
     float m = -INFINITY, s = 0.f, zs = 0.f;
     grid_wait();
-    for (int i = warp; i < a.slots; i += 32) {
-        join_one(m, s, a.part[(int64_t)i * a.Tp + t]);
-        if (a.zsum)
-            zs += a.zsum[(int64_t)i * a.Tp + t];
-    }
-    sm[warp][lane] = make_float2(m, s);
-    sz[warp][lane] = zs;
-    __syncthreads();
-    if (warp != 0 || t >= a.T)
-        return;
-    for (int w = 1; w < 32; ++w) {
-        join_one(m, s, sm[w][lane]);
-        zs += sz[w][lane];
-    }
-    join_out(a, t, m, s, zs);
-}
-
-// the same for one row tile, [row][slot]: a CTA for a row, whose slots (at most
-// 3 x 128) are loaded together
-__global__ void __launch_bounds__(128) k_ce_join_row(const JoinArgs a)
-{
-    __shared__ float sm[3][4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = blockIdx.x;
-    float2 p[3];
-    float zs = 0.f;
-    grid_wait();
+    for (int i0 = threadIdx.x; i0 < a.slots; i0 += 4 * kJoinThreads) {
+        // four loads under way together
+        float2 p[4];
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        const int i = threadIdx.x + 128 * j;
-        const bool in = i < a.slots;
-        p[j] = in ? a.part[(int64_t)t * a.slots + i] : make_float2(-INFINITY, 0.f);
-        if (a.zsum)
-            zs += in ? a.zsum[(int64_t)t * a.slots + i] : 0.f;
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kJoinThreads;
+            p[j] = i < a.slots ? part[i] : make_float2(-INFINITY, 0.f);
+            if (a.zsum)
+                zs += i < a.slots ? a.zsum[(int64_t)t * a.slots + i] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            join_one(m, s, p[j]);
     }
-    float m = fmaxf(fmaxf(p[0].x, p[1].x), p[2].x);
+    float top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0)
-        sm[0][warp] = m;
+        sm[0][warp] = top;
     __syncthreads();
-    m = fmaxf(fmaxf(sm[0][0], sm[0][1]), fmaxf(sm[0][2], sm[0][3]));
-    const float ms = m == -INFINITY ? 0.f : m;
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-        s += p[j].y * exp2f(p[j].x - ms);
+    for (int w = 0; w < NW; ++w)
+        top = fmaxf(top, sm[0][w]);
+    s *= exp2f(m - (top == -INFINITY ? 0.f : top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -758,9 +737,13 @@ __global__ void __launch_bounds__(128) k_ce_join_row(const JoinArgs a)
         sm[2][warp] = zs;
     }
     __syncthreads();
-    if (threadIdx.x == 0)
-        join_out(a, t, m, (sm[1][0] + sm[1][1]) + (sm[1][2] + sm[1][3]),
-                 (sm[2][0] + sm[2][1]) + (sm[2][2] + sm[2][3]));
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < NW; ++w) {
+            s += sm[1][w];
+            zs += sm[2][w];
+        }
+        join_out(a, t, top, s, zs);
+    }
 }
 
 // dh = the sum of its pieces, 32 rows x 32 columns to a CTA, a warp for four
@@ -1112,7 +1095,7 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     a.part = reinterpret_cast<float2 *>(w8 + p.o_part);
     a.zsum = smoothing > 0 ? reinterpret_cast<float *>(w8 + p.o_zsum) : nullptr;
     a.ztgt = reinterpret_cast<float *>(w8 + p.o_ztgt);
-    a.Tp = (int32_t)p.Tp;
+    a.slots = (int32_t)p.slots;
     a.status = status;
     if (dtype == SG_E4M3)
         CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, mh, a, false, st))
@@ -1122,11 +1105,9 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
                          : (launch_ce<2, kLse, false>(mh, mW, mh, mh, mh, a, false, st)));
     JoinArgs j;
     j.part = a.part, j.zsum = a.zsum, j.ztgt = a.ztgt, j.targets = targets, j.loss = loss, j.lse = lse;
-    j.status = status, j.slots = (int32_t)p.slots, j.Tp = a.Tp, j.T = a.T, j.V = a.V, j.ignore = ignore_index;
+    j.status = status, j.slots = a.slots, j.V = a.V, j.ignore = ignore_index;
     j.smooth = (float)smoothing;
-    if (p.nm == 1)
-        return launch(k_ce_join_row, dim3((unsigned)T), 128, 0, 1, true, st, j);
-    return launch(k_ce_join, dim3((unsigned)ceil_div(T, 32)), 1024, 0, 1, true, st, j);
+    return launch(k_ce_join, dim3((unsigned)T), kJoinThreads, 0, 1, true, st, j);
 }
 
 sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,

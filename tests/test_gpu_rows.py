@@ -250,3 +250,18 @@ def test_refusals():
     with pytest.raises(sg.SGError) as e:
         sg.sg_add_rmsnorm_fwd(wide, wide[0], 1e-6, y=wide)
     assert e.value.status == sg.SG_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(5003, 768), (4999, 520), (10001, 1024)], ids=str)
+def test_norm_of_many_rows(shape, dtype):
+    """Enough rows that every row group takes several, and (513 to 768 columns)
+    the shape of one warp to a row."""
+    x, res, w = fwd_inputs(shape, dtype, 0, 0)
+    u, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(shape[0], device="cuda")
+    sg.sg_add_rmsnorm_fwd(x, w, 1e-5, residual=res, u=u, rstd=rstd, y=y, drop_p=0.3, seed=SEED, offset=OFFSET)
+    want_u = torch.from_numpy(orc.dropout(f32(x), 0.3, SEED, OFFSET) + f32(res)).to(x.dtype)
+    assert torch.equal(u.cpu(), want_u)
+    want, r = orc.add_rmsnorm(f64(u), f64(w), 1e-5)
+    assert np.all(np.abs(f64(rstd) - r) <= 1e-5 * r)
+    close(y, want, dtype, np.abs(want))
