@@ -6,8 +6,8 @@
 
 #include <cuda_fp8.h>
 
+#include "launch.cuh"
 #include "rows.cuh"
-#include "tc_ptx.cuh"
 
 using namespace rows;
 
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T
     const int wr = WARPS == 1 ? 0 : warp;
     const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
     const int64_t g = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
+    tc::grid_go();
     const T *ady = static_cast<const T *>(a.dy), *au = static_cast<const T *>(a.u);
     const T *ai = static_cast<const T *>(a.du_in);
     auto fetch = [&](int64_t r, int slot) {
@@ -464,20 +465,27 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T
     }
 }
 
-// dweight[c] = the sum of its parts, in a fixed order
+// dweight[c] = the sum of its parts, in a fixed order: eight columns (a sector)
+// to a CTA, whose threads take 128 parts at a time
 __global__ void __launch_bounds__(1024) k_norm_dw(const float *__restrict__ part, int nparts, int64_t cols,
                                                   float *__restrict__ dw)
 {
-    __shared__ float sm[32][33];
+    __shared__ float sm[32][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t c = (int64_t)blockIdx.x * 8 + (lane & 7);
     float s = 0.f;
-    if (c < cols)
-        for (int i = warp; i < nparts; i += 32)
+    tc::grid_wait();
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = threadIdx.x / 8; i < nparts; i += 128)
             s += part[i * cols + c];
-    sm[warp][lane] = s;
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (lane < 8)
+        sm[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < cols) {
+    if (threadIdx.x < 8 && c < cols) {
         s = 0.f;
         for (int i = 0; i < 32; ++i)
             s += sm[i][lane];
@@ -790,10 +798,9 @@ sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_
     else
         NORM_TRY((vec ? launch_bwd<float, true>(a, grid, st) : launch_bwd<float, false>(a, grid, st)));
     SG_TRY_CUDA(cudaGetLastError());
-    if (dweight) {
-        k_norm_dw<<<(unsigned)ceil_div(cols, 32), 1024, 0, st>>>(a.part, (int)groups, cols, dweight);
-        SG_TRY_CUDA(cudaGetLastError());
-    }
+    if (dweight)
+        return launch(k_norm_dw, dim3((unsigned)ceil_div(cols, 8)), 1024, 0, 1, true, st, (const float *)a.part,
+                      (int)groups, cols, dweight);
     return SG_OK;
 }
 

@@ -21,7 +21,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "sg_internal.cuh"
+#include "launch.cuh"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -746,39 +746,61 @@ __global__ void __launch_bounds__(kJoinThreads) k_ce_join(const JoinArgs a)
     }
 }
 
-// dh = the sum of its pieces, 32 rows x 32 columns to a CTA, a warp for four
-// columns
-template <int CG>
+// dh = the sum of its pieces.  A CTA has 32 rows and 32 / PARTS columns; a warp
+// four of the columns and every PARTS-th piece, whose loads are under way
+// together.  (Many pieces mean few tiles: 23 pieces of 128 x 768 took 14 us
+// with one warp to all of a column's pieces.)
+template <int CG, int PARTS>
 __global__ void __launch_bounds__(256)
     k_ce_dh(const float4 *__restrict__ acc, int tiles, int nn, int split, int T, int H,
             const float *__restrict__ gscale, int f16, uint16_t *__restrict__ dh, int64_t lddh)
 {
-    __shared__ uint16_t sm[32][34];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    constexpr int N4 = 8 / PARTS;  // fours of columns
+    __shared__ float4 sm[PARTS][N4][32];
+    __shared__ uint16_t rows[32][4 * N4 + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c4 = warp % N4, part = warp / N4;
     const int x = blockIdx.x / (CG * 4), rq = blockIdx.x % (CG * 4);  // tile, 32-row part of it
-    const int row0 = x / nn * Cfg<CG>::BM + rq * 32, col0 = x % nn * kBN + blockIdx.y * 32;
+    const int row0 = x / nn * Cfg<CG>::BM + rq * 32, col0 = x % nn * kBN + blockIdx.y * 4 * N4;
+    grid_wait();
     if (row0 >= T || col0 >= H)
         return;
-    grid_wait();
     const float inv = gscale[1];
     const float4 *src =
-        acc + (((int64_t)x * CG + rq / 4) * (kBN / 4) + blockIdx.y * 8 + warp) * 128 + (rq & 3) * 32 + lane;
+        acc + (((int64_t)x * CG + rq / 4) * (kBN / 4) + blockIdx.y * N4 + c4) * 128 + (rq & 3) * 32 + lane;
     const int64_t step = (int64_t)tiles * CG * (kBN / 4) * 128;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int s = 0; s < split; ++s) {
+    for (int s = part; s < split; s += PARTS) {
         const float4 o = src[s * step];
         v.x += o.x;
         v.y += o.y;
         v.z += o.z;
         v.w += o.w;
     }
-    *reinterpret_cast<uint32_t *>(&sm[lane][warp * 4]) = pack16(v.x * inv, v.y * inv, f16);
-    *reinterpret_cast<uint32_t *>(&sm[lane][warp * 4 + 2]) = pack16(v.z * inv, v.w * inv, f16);
+    if constexpr (PARTS > 1) {
+        sm[part][c4][lane] = v;
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int i = 1; i < PARTS; ++i) {
+                const float4 o = sm[i][c4][lane];
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+        }
+    }
+    if (part == 0) {
+        *reinterpret_cast<uint32_t *>(&rows[lane][c4 * 4]) = pack16(v.x * inv, v.y * inv, f16);
+        *reinterpret_cast<uint32_t *>(&rows[lane][c4 * 4 + 2]) = pack16(v.z * inv, v.w * inv, f16);
+    }
     __syncthreads();
-    for (int r = warp; r < 32 && row0 + r < T; r += 8)
-        if (col0 + lane < H)
-            dh[(int64_t)(row0 + r) * lddh + col0 + lane] = sm[r][lane];
+    for (int i = threadIdx.x; i < 32 * 4 * N4; i += 256) {
+        const int r = i / (4 * N4), c = i % (4 * N4);
+        if (row0 + r < T && col0 + c < H)
+            dh[(int64_t)(row0 + r) * lddh + col0 + c] = rows[r][c];
+    }
 }
 
 // rows that do not start on 16 bytes, copied to a stride that does
@@ -822,34 +844,6 @@ sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, i
                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         CE_FAIL(SG_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
-    return SG_OK;
-}
-
-// `after`: the kernel before it in the stream is one of this call's, which this
-// one may overlap
-template <typename... P, typename... A>
-sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, bool after, cudaStream_t st,
-                 A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    cfg.attrs = at;
-    cfg.numAttrs = 0;
-    if (cluster > 1) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
-        at[cfg.numAttrs].val.clusterDim.y = 1;
-        at[cfg.numAttrs++].val.clusterDim.z = 1;
-    }
-    if (after) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    SG_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
     return SG_OK;
 }
 
@@ -1198,11 +1192,13 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
                          : (launch_ce<2, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st)));
     }
     if (dh) {
-        const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), kBN / 32);
+        const int parts = p.split >= 8 ? 4 : 1;
+        const dim3 grid((unsigned)(p.dh_tiles * p.CG * 4), (unsigned)(kBN / 32 * parts));
         const float4 *acc = reinterpret_cast<const float4 *>(a.acc);
-        return launch(p.CG == 1 ? k_ce_dh<1> : k_ce_dh<2>, grid, 256, 0, 1, true, st, acc, (int)p.dh_tiles,
-                      (int)p.dh_nn, (int)p.split, (int)T, (int)H, (const float *)a.gscale, (int)a.f16,
-                      static_cast<uint16_t *>(dh), lddh);
+        return launch(p.CG == 1 ? (parts == 4 ? k_ce_dh<1, 4> : k_ce_dh<1, 1>)
+                                : (parts == 4 ? k_ce_dh<2, 4> : k_ce_dh<2, 1>),
+                      grid, 256, 0, 1, true, st, acc, (int)p.dh_tiles, (int)p.dh_nn, (int)p.split, (int)T, (int)H,
+                      (const float *)a.gscale, (int)a.f16, static_cast<uint16_t *>(dh), lddh);
     }
     return SG_OK;
 }
