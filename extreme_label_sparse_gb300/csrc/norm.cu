@@ -465,27 +465,31 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T
     }
 }
 
-// dweight[c] = the sum of its parts, in a fixed order: eight columns (a sector)
-// to a CTA, whose threads take 128 parts at a time
+// dweight[c] = the sum of its parts, in a fixed order: NC columns to a CTA,
+// whose threads take 1024 / NC parts at a time.  Eight columns (a sector) give
+// enough CTAs where there are few columns (65536 x 256, whole backward pass: 32
+// us, 37 with 32 columns), 32 read whole lines (16384 x 4096: 123 us, 125).
+template <int NC>
 __global__ void __launch_bounds__(1024) k_norm_dw(const float *__restrict__ part, int nparts, int64_t cols,
                                                   float *__restrict__ dw)
 {
-    __shared__ float sm[32][8];
+    __shared__ float sm[32][NC];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t c = (int64_t)blockIdx.x * 8 + (lane & 7);
+    const int64_t c = (int64_t)blockIdx.x * NC + lane % NC;
     float s = 0.f;
     tc::grid_wait();
     if (c < cols) {
 #pragma unroll 4
-        for (int i = threadIdx.x / 8; i < nparts; i += 128)
+        for (int i = threadIdx.x / NC; i < nparts; i += 1024 / NC)
             s += part[i * cols + c];
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 8);
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
-    if (lane < 8)
+#pragma unroll
+    for (int o = NC; o < 32; o *= 2)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane < NC)
         sm[warp][lane] = s;
     __syncthreads();
-    if (threadIdx.x < 8 && c < cols) {
+    if (threadIdx.x < NC && c < cols) {
         s = 0.f;
         for (int i = 0; i < 32; ++i)
             s += sm[i][lane];
@@ -799,8 +803,9 @@ sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_
         NORM_TRY((vec ? launch_bwd<float, true>(a, grid, st) : launch_bwd<float, false>(a, grid, st)));
     SG_TRY_CUDA(cudaGetLastError());
     if (dweight)
-        return launch(k_norm_dw, dim3((unsigned)ceil_div(cols, 8)), 1024, 0, 1, true, st, (const float *)a.part,
-                      (int)groups, cols, dweight);
+        return launch(cols < 2048 ? k_norm_dw<8> : k_norm_dw<32>,
+                      dim3((unsigned)ceil_div(cols, cols < 2048 ? 8 : 32)), 1024, 0, 1, true, st,
+                      (const float *)a.part, (int)groups, cols, dweight);
     return SG_OK;
 }
 
