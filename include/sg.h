@@ -429,7 +429,7 @@ SG_API sg_status sg_dropout(const void *x, int64_t ldx, int64_t rows, int64_t co
  * pointer is given: u (the next residual, and what the backward pass reads),
  * rstd[rows], y rounded to dtype, and y8[rows][cols] with y8_scale[rows]: y in
  * 8 bits (SG_E4M3), y = y8 * y8_scale with y8_scale = max |y| / 448 of the row
- * (0 for a row of zeros).  One of y and y8 is needed.  residual NULL: u =
+ * (at least 2^-126; 0 for a row of zeros).  One of y and y8 is needed.  residual NULL: u =
  * drop(x).  weight[cols] has dtype.  u may be x or residual, and y any of
  * them.  cols <= 32768. */
 SG_API sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows,

@@ -141,6 +141,35 @@ def test_norm_of_zero_rows_and_of_values_that_are_not_numbers():
     assert torch.isnan(y[1]).all()
 
 
+def test_norm_to_8_bits_of_the_smallest_rows():
+    # y of 2^-137 to 2^-107: where max |y| / 448 or its inverse leave fp32's normal numbers
+    x = rand(31, 512, "f32", 5)
+    x[:, 7] = 0
+    y, y8 = torch.empty_like(x), torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.empty(31, device="cuda")
+    for i in range(31):
+        w = torch.full((512,), 2.0 ** (i - 137), device="cuda")
+        sg.sg_add_rmsnorm_fwd(x[i:i + 1], w, 1e-6, y=y[i:i + 1], y8=y8[i:i + 1], y8_scale=scale[i:i + 1])
+    # y itself is rounded to a multiple of 2^-149
+    got, want, s = f64(y8) * f64(scale)[:, None], f64(y), f64(scale)[:, None]
+    assert np.all(s >= 2.0 ** -126)
+    assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -4 + 1e-5) + s * 2.0 ** -10 + 2.0 ** -148)
+
+
+@pytest.mark.parametrize("unit", (1e-15, 1e15))
+def test_norm_backward_of_rows_of_other_scales(unit):
+    dy, u = rand(8, 520, "f32", 1), unit * rand(8, 520, "f32", 2)
+    w = torch.ones(520, device="cuda")
+    rstd = (1 / np.sqrt((f64(u) ** 2).mean(1))).astype(np.float32)
+    rstd = torch.from_numpy(rstd).cuda()
+    du = torch.empty_like(dy)
+    sg.sg_add_rmsnorm_bwd(dy, u, w, rstd, du)
+    want, _ = orc.add_rmsnorm_grad(f64(dy), f64(u), f64(w), f64(rstd), 0 * f64(dy))
+    r = f64(rstd)[:, None]
+    g, n = np.abs(f64(dy)), np.abs(f64(u)) * r
+    close(du, want, "f32", r * (g + n * (g * n).mean(1, keepdims=True)))
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("shape", SHAPES + [(700, 264), (5000, 40), (1300, 2056), (3, 16384), (2, 20001)], ids=str)
 @pytest.mark.parametrize("pad,shift,p", [(0, 0, 0.0), (8, 0, 0.3), (3, 1, 0.3)])
