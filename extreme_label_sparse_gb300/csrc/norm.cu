@@ -185,13 +185,22 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// threads of a CTA, and CTAs to an SM that the registers are cut for
+// threads of a CTA, and CTAs to an SM that the registers are cut for: 1024
+// threads of 64 registers, or 512 of 128
 constexpr int norm_threads(int warps) { return warps == 1 ? 256 : warps * 32; }
-constexpr int norm_ctas(int warps, int size)
+constexpr int norm_ctas(int warps, bool few)
 {
-    const int n = (size == 4 ? 512 : 1024) / norm_threads(warps);
+    const int n = (few ? 512 : 1024) / norm_threads(warps);
     return n < 1 ? 1 : n;
 }
+// The forward kernel takes 512 with fp32 and with three segments to a warp,
+// which lack registers otherwise (65536 x 768 bf16 to 8 bits with dropout: 68
+// us, 81 with 1024; 16384 x 4096 to 8 bits, two segments: 79 us, 75 with 1024).
+constexpr int fwd_ctas(int warps, int nv, int size) { return norm_ctas(warps, size == 4 || nv == 3); }
+// The backward kernel's eights take 512 in all types: its sums of dweight spill
+// otherwise (16384 x 4096 bf16 with dropout: 107 us, 124 with 1024).  Single
+// elements, with no ring of rows, want the warps (32768 x 1001: 96 us, 140).
+constexpr int bwd_ctas(bool vec, int warps, int size) { return norm_ctas(warps, size == 4 || vec); }
 
 struct NormFwd {
     const void *x, *res, *w;
@@ -213,7 +222,7 @@ struct NormFwd {
 // 128 x 768).  No barrier but the sum's own; from 257 columns on a row takes
 // several warps, so that its registers let 1024 threads be on an SM.
 template <typename T, bool VEC, int WARPS, int NV, int S>
-__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T))) k_norm_fwd(const NormFwd a)
+__global__ void __launch_bounds__(norm_threads(WARPS), fwd_ctas(WARPS, NV, sizeof(T))) k_norm_fwd(const NormFwd a)
 {
     __shared__ RowSums sm;
     extern __shared__ uint4 dyn[];
@@ -351,11 +360,11 @@ struct NormBwd {
 // Row groups of WARPS warps step over the rows; a thread keeps the sum of its
 // columns of dweight in registers until its last row, and the groups' sums are
 // joined by k_norm_dw.  Both uses of dy and u are served from shared memory, so
-// memory is read once: 16384 x 4096 bf16 with du_in and dropout, 671 MB, 123
-// us (5.5 TB/s; 189 us with loads into registers).  Three inputs and two outputs
-// to a row leave two or three rows under way on an SM's 1024 threads.
+// memory is read once: 16384 x 4096 bf16 with du_in and dropout, 671 MB, 107
+// us (6.3 TB/s; 189 us with loads into registers, 139 with rstd read in its own
+// turn).
 template <typename T, bool VEC, int WARPS, int NV, int S>
-__global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T))) k_norm_bwd(const NormBwd a)
+__global__ void __launch_bounds__(norm_threads(WARPS), bwd_ctas(VEC, WARPS, sizeof(T))) k_norm_bwd(const NormBwd a)
 {
     __shared__ RowSums sm;
     extern __shared__ uint4 dyn[];
@@ -393,8 +402,22 @@ __global__ void __launch_bounds__(norm_threads(WARPS), norm_ctas(WARPS, sizeof(T
         w[n] = load8<T, VEC>(static_cast<const T *>(a.w), (n * WARPS + wr) * kSeg, lane, a.cols);
     float dw[NV][8] = {};
     int turn = 0, slot = 0;
+    // rstd is read ahead, or each row would begin with a wait for it: one row, or
+    // with four segments, which have few rows to a CTA, 32 rows at a time by the
+    // lanes (16384 x 4096 bf16: 107 us, 110 by the lanes; 4096 x 16384: 139, 114)
+    constexpr bool kLanes = NV == 4;
+    float next = kLanes || g >= a.nrows ? 0.f : a.rstd[g];
     for (int64_t r = g; r < a.nrows; r += groups, ++turn) {
-        const float rstd = a.rstd[r];
+        float rstd;
+        if constexpr (kLanes) {
+            if ((turn & 31) == 0)
+                next = r + lane * groups < a.nrows ? a.rstd[r + lane * groups] : 0.f;
+            rstd = __shfl_sync(0xffffffffu, next, turn & 31);
+        } else {
+            rstd = next;
+            if (r + groups < a.nrows)
+                next = a.rstd[r + groups];
+        }
         float dot = 0.f, none = 0.f;
         if constexpr (VEC)
             copies_wait<S - 1>();
@@ -514,6 +537,9 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float *__restrict__ part
 // warps and segments a row of `cols` columns takes: the first shape that
 // holds it
 #define NORM_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(32, 2) X(32, 4)
+// of the backward kernel's eights: with its sums of dweight, 1024 threads of
+// two segments lack registers (4096 x 16384 bf16: 114 us, 148 with X(32, 2))
+#define NORM_SHAPES_BWD8(X) X(1, 1) X(1, 2) X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(16, 4) X(32, 4)
 
 // shared memory beyond the default is asked for once for each kernel and
 // device (one bit of the mask)
@@ -534,10 +560,10 @@ sg_status allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done)
 
 // rows on their way: as many as leave room for the CTAs that fit by registers
 template <typename T, int NA, int WARPS, int NV>
-constexpr int ring_rows()
+constexpr int ring_rows(int ctas)
 {
     const int row = NA * NV * norm_threads(WARPS) * (int)sizeof(Pack8<T>);
-    const int s = (216 << 10) / norm_ctas(WARPS, sizeof(T)) / row;
+    const int s = (216 << 10) / ctas / row;
     return s > 4 ? 4 : s < 1 ? 1 : s;
 }
 
@@ -545,12 +571,12 @@ template <typename T, bool VEC, int W, int N>
 sg_status run_fwd(const NormFwd &a, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr int S = VEC ? ring_rows<T, 2, W, N>() : 1;
+    constexpr int S = VEC ? ring_rows<T, 2, W, N>(fwd_ctas(W, N, sizeof(T))) : 1;
     constexpr int smem = VEC ? Ring8<T, 2, N, S, norm_threads(W)>::kBytes : 0;
     if constexpr (smem > 226 << 10) {  // fp32 rows above 16384 columns: not one is held
         return run_fwd<T, false, W, N>(a, st);
     } else {
-        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * norm_ctas(W, sizeof(T));
+        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * fwd_ctas(W, N, sizeof(T));
         NORM_TRY(allow_smem(k_norm_fwd<T, VEC, W, N, S>, smem, done));
         k_norm_fwd<T, VEC, W, N, S><<<(unsigned)(need < most ? need : most), norm_threads(W), smem, st>>>(a);
         return SG_OK;
@@ -561,7 +587,7 @@ template <typename T, bool VEC, int W, int N>
 sg_status run_bwd(const NormBwd &a, int64_t grid, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr int S = VEC ? ring_rows<T, 3, W, N>() : 1;
+    constexpr int S = VEC ? ring_rows<T, 3, W, N>(bwd_ctas(true, W, sizeof(T))) : 1;
     constexpr int smem = VEC ? Ring8<T, 3, N, S, norm_threads(W)>::kBytes : 0;
     if constexpr (smem > 226 << 10) {  // fp32 rows above 16384 columns: not one is held
         return run_bwd<T, false, W, N>(a, grid, st);
@@ -577,9 +603,9 @@ sg_status launch_fwd(const NormFwd &a, cudaStream_t st)
 {
     // 513 to 768 columns: one warp to a row leaves none of its lanes without
     // work and needs no barrier, but takes twice as long for one row.  65536 x
-    // 768 bf16 to 8 bits with dropout: 80 us, 101 by four warps; 128 rows: 4.7
+    // 768 bf16 to 8 bits with dropout: 68 us, 101 by four warps; 128 rows: 4.7
     // and 2.4 us.  So it is taken when there are rows for all warps.
-    if (VEC && a.cols > 2 * kSeg && a.cols <= 3 * kSeg && a.nrows >= (int64_t)kSMs * norm_ctas(1, sizeof(T)) * 8)
+    if (VEC && a.cols > 2 * kSeg && a.cols <= 3 * kSeg && a.nrows >= (int64_t)kSMs * fwd_ctas(1, 3, sizeof(T)) * 8)
         return run_fwd<T, VEC, 1, 3>(a, st);
 #define X(W, N)                             \
     if (a.cols <= (int64_t)(W) * (N) * kSeg) \
@@ -595,21 +621,29 @@ sg_status launch_bwd(const NormBwd &a, int64_t grid, cudaStream_t st)
 #define X(W, N)                             \
     if (a.cols <= (int64_t)(W) * (N) * kSeg) \
         return run_bwd<T, VEC, W, N>(a, grid, st);
-    NORM_SHAPES(X)
+    if constexpr (VEC) {
+        NORM_SHAPES_BWD8(X)
+    } else {
+        NORM_SHAPES(X)
+    }
 #undef X
     return SG_ERR_UNSUPPORTED;  // not reached: cols <= kMaxCols
 }
 
 // CTAs of the backward kernel, and the row groups they make
-int64_t bwd_groups(int64_t nrows, int64_t cols, int size, int64_t *grid)
+int64_t bwd_groups(bool vec, int64_t nrows, int64_t cols, int size, int64_t *grid)
 {
     int warps = 32;
 #define X(W, N)                                           \
     if (warps == 32 && cols <= (int64_t)(W) * (N) * kSeg) \
         warps = (W);
-    NORM_SHAPES(X)
+    if (vec) {
+        NORM_SHAPES_BWD8(X)
+    } else {
+        NORM_SHAPES(X)
+    }
 #undef X
-    const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * norm_ctas(warps, size);
+    const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * bwd_ctas(vec, warps, size);
     *grid = need < most ? need : most;
     return warps == 1 ? *grid * 8 : *grid;
 }
@@ -766,8 +800,12 @@ sg_status sg_add_rmsnorm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes)
     if (cols > kMaxCols)
         NORM_FAIL(SG_ERR_UNSUPPORTED, "%s: cols=%lld is above %lld", fn, (long long)cols, (long long)kMaxCols);
     int64_t grid;
-    const int64_t g2 = bwd_groups(rows, cols, 2, &grid), g4 = bwd_groups(rows, cols, 4, &grid);
-    *bytes = (g2 > g4 ? g2 : g4) * cols * 4;  // of the type with the most groups
+    int64_t most = 0;  // groups of any type and mapping
+    for (int i = 0; i < 4; ++i) {
+        const int64_t n = bwd_groups(i & 1, rows, cols, i & 2 ? 2 : 4, &grid);
+        most = n > most ? n : most;
+    }
+    *bytes = most * cols * 4;
     return SG_OK;
 }
 
@@ -799,16 +837,16 @@ sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_
             SG_TRY_CUDA(cudaMemsetAsync(dweight, 0, (size_t)cols * 4, st));
         return SG_OK;
     }
+    const bool vec = cols % 8 == 0 && vec_ok(dy, lddy, es) && vec_ok(u, ldu, es) && vec_ok(du_in, lddu_in, es) &&
+                     vec_ok(weight, cols, es) && vec_ok(du, lddu, es) && vec_ok(dx, lddx, es);
     int64_t grid;
-    const int64_t groups = bwd_groups(rows, cols, (int)es, &grid);
+    const int64_t groups = bwd_groups(vec, rows, cols, (int)es, &grid);
     if (dweight && (!work || work_bytes < groups * cols * 4 || ((uintptr_t)work) % 4 != 0))
         NORM_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_add_rmsnorm_bwd_work), aligned to 4", fn,
                   (long long)(groups * cols * 4));
     a.dy = dy, a.u = u, a.w = weight, a.du_in = du_in, a.rstd = rstd, a.du = du, a.dx = dx;
     a.part = dweight ? static_cast<float *>(work) : nullptr;
     a.lddy = lddy, a.ldu = ldu, a.ldi = lddu_in, a.ldo = lddu, a.lddx = lddx, a.nrows = rows, a.cols = (int)cols;
-    const bool vec = cols % 8 == 0 && vec_ok(dy, lddy, es) && vec_ok(u, ldu, es) && vec_ok(du_in, lddu_in, es) &&
-                     vec_ok(weight, cols, es) && vec_ok(du, lddu, es) && vec_ok(dx, lddx, es);
     if (dtype == SG_BF16)
         NORM_TRY((vec ? launch_bwd<__nv_bfloat16, true>(a, grid, st) : launch_bwd<__nv_bfloat16, false>(a, grid, st)));
     else if (dtype == SG_F16)
