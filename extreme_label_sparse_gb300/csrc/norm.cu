@@ -147,8 +147,8 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, RowSums &sm, int 
 // in flight take no registers.
 template <typename T, int NA, int NV, int S, int THREADS>
 struct Ring8 {
-    [[maybe_unused]] static constexpr int kPieces = sizeof(Pack8<T>) / 16;
-    static constexpr int kBytes = S * NA * NV * THREADS * (int)sizeof(Pack8<T>);
+    static constexpr int kPieces = sizeof(Pack8<T>) / 16;
+    static constexpr int kBytes = S * NA * NV * kPieces * THREADS * 16;
     uint4 *base;
 
     __device__ __forceinline__ explicit Ring8(void *smem) : base(static_cast<uint4 *>(smem) + threadIdx.x) {}
@@ -219,8 +219,8 @@ struct NormFwd {
 // their way to shared memory meanwhile, since a CTA that waits for its row's
 // sum would otherwise have nothing in flight (16384 x 4096 bf16, sum and 8-bit
 // outputs: 100 us with loads into registers, now 74.5 us, 6.3 TB/s; 2.4 us for
-// 128 x 768).  No barrier but the sum's own; from 257 columns on a row takes
-// several warps, so that its registers let 1024 threads be on an SM.
+// 128 x 768).  No barrier but the sum's own; wide rows take several
+// warps, so that a thread has at most two segments in registers.
 template <typename T, bool VEC, int WARPS, int NV, int S>
 __global__ void __launch_bounds__(norm_threads(WARPS), fwd_ctas(WARPS, NV, sizeof(T))) k_norm_fwd(const NormFwd a)
 {
@@ -576,7 +576,16 @@ sg_status run_fwd(const NormFwd &a, cudaStream_t st)
     if constexpr (smem > 226 << 10) {  // fp32 rows above 16384 columns: not one is held
         return run_fwd<T, false, W, N>(a, st);
     } else {
-        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * fwd_ctas(W, N, sizeof(T));
+        // Half the CTAs where only 16-bit rows are written and none of dropout's
+        // work waits to be hidden: memory takes the rows faster the fewer are
+        // read and written at a time, while two segments to a thread are enough
+        // under way (16384 x 4096 bf16: 81 us, 97 with all; with dropout 104, 96;
+        // to 8 bits 82, 75; 32768 x 1024, one segment: 55, 49).  Rows that fit
+        // the L2 cache take all (1024 x 4096: 7.9 us, 8.5 with half).
+        constexpr int kCtas = fwd_ctas(W, N, sizeof(T));
+        const bool half = VEC && sizeof(T) == 2 && N > 1 && kCtas > 1 && !a.y8 && !a.d.drop &&
+                          a.nrows * a.cols >= 8 << 20;  // 64 MB in and out
+        const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * (half ? kCtas / 2 : kCtas);
         NORM_TRY(allow_smem(k_norm_fwd<T, VEC, W, N, S>, smem, done));
         k_norm_fwd<T, VEC, W, N, S><<<(unsigned)(need < most ? need : most), norm_threads(W), smem, st>>>(a);
         return SG_OK;
