@@ -294,3 +294,47 @@ def test_norm_of_many_rows(shape, dtype):
     want, r = orc.add_rmsnorm(f64(u), f64(w), 1e-5)
     assert np.all(np.abs(f64(rstd) - r) <= 1e-5 * r)
     close(y, want, dtype, np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(16501, 512), (11003, 768), (2050, 4096)], ids=str)
+def test_norm_of_many_rows_in_16_bits_without_dropout(shape, dtype):
+    x, res, w = fwd_inputs(shape, dtype, 0, 0)
+    u, y = torch.empty_like(x), torch.empty_like(x)
+    sg.sg_add_rmsnorm_fwd(x, w, 1e-5, residual=res, u=u, y=y)
+    assert torch.equal(u, (x.float() + res.float()).to(x.dtype))
+    want, _ = orc.add_rmsnorm(f64(u), f64(w), 1e-5)
+    close(y, want, dtype, np.abs(want))
+
+
+def test_norm_backward_of_many_wide_rows():
+    """More than 32 rows to a row group of four segments to a warp."""
+    rows, cols = 5003, 8200
+    dy, u = rand(rows, cols, "bf16", 1), rand(rows, cols, "bf16", 2)
+    w = (1 + 0.2 * rand(1, cols, "f32", 3)).bfloat16().reshape(-1)
+    rstd = (1 + torch.rand(rows, device="cuda")) / 2
+    du, dw = torch.empty_like(dy), torch.empty(cols, device="cuda")
+    sg.sg_add_rmsnorm_bwd(dy, u, w, rstd, du, dw)
+    r, n = rstd.double()[:, None], u.double() * rstd.double()[:, None]
+    g = dy.double() * w.double()
+    want = r * (g - n * (g * n).mean(1, keepdim=True))
+    slack = r * (g.abs() + n.abs() * (g * n).abs().mean(1, keepdim=True))
+    close(du, want.cpu().numpy(), "bf16", slack.cpu().numpy())
+    t = dy.double() * n
+    close(dw, t.sum(0).cpu().numpy(), "f32", 2 * t.abs().sum(0).cpu().numpy())
+
+
+def test_dropout_beyond_two_to_the_31_elements():
+    """The mask goes by row and column alone: the first columns as a matrix of
+    their own get the same one."""
+    rows, cols = (1 << 21) + 5, 1032
+    x = torch.ones((rows, cols), dtype=torch.bfloat16, device="cuda")
+    y, part = torch.zeros_like(x), torch.zeros((rows, 8), dtype=x.dtype, device="cuda")
+    sg.sg_dropout(x, 0.5, SEED, OFFSET, y)
+    sg.sg_dropout(x[:, :8], 0.5, SEED, OFFSET, part)
+    assert torch.equal(y[:, :8], part)
+    assert torch.equal(part[:4].cpu(), torch.from_numpy(orc.dropout(np.ones((4, 8), np.float32), 0.5, SEED,
+                                                                    OFFSET)).bfloat16())
+    # standard deviation of the mean of 10^6 of them: 5e-4
+    for at in (0, rows // 2, rows - 1000):
+        assert abs(float((y[at:at + 1000] != 0).float().mean()) - 0.5) < 5e-3

@@ -308,3 +308,52 @@ def test_refusals():
         sg.sg_softmax_ce_fwd(h, W[:, :32], y, v, v.clone())
     with pytest.raises(ValueError):
         sg.sg_softmax_ce_fwd(h, W, y[:3], v, v.clone())
+
+
+def test_weights_of_more_than_two_to_the_31_elements():
+    """A block of 512 labels, many times over: every copy has the block's
+    logits, so lse is the block's plus the logarithm of their number."""
+    T, H, V0, n = 5, 2048, 512, 2051
+    V = V0 * n
+    h, block = rand(T, H, "bf16", 1), rand(V0, H, "bf16", 2, 2.0 / np.sqrt(H))
+    W = block.repeat(n, 1)
+    y = torch.tensor([3, V - 1, V - V0, -100, V // 2], dtype=torch.int32, device="cuda")
+    dloss = torch.rand(T, device="cuda") + 0.5
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dh, dW = torch.empty_like(h), torch.empty_like(W)
+    sg.sg_softmax_ce_fwd(h, W, y, loss, lse)
+    sg.sg_softmax_ce_bwd(h, W, y, lse, dloss, dh, dW)
+    hd, bd = f64(h), f64(block)
+    e = logit_error(hd, bd)
+    z = hd @ bd.T
+    want = np.log(np.exp(z).sum(1)) + np.log(n)
+    at = y.cpu().numpy()
+    live = at >= 0
+    assert np.all(np.abs(f64(lse) - want) <= e + 1e-5)
+    zt = z[np.arange(T), np.where(live, at % V0, 0)]
+    assert np.all(np.abs(f64(loss) - np.where(live, want - zt, 0)) <= 2 * e + 1e-5)
+    c = np.where(live, f64(dloss), 0)[:, None]
+    p = c * np.exp(z - want[:, None])  # g, but for the targets' part
+    rel = 2 * e.max() + 3e-5
+    u = U["bf16"]
+    # dW: in every copy the same but for the targets' rows
+    plain = p.T @ hd
+    bound = (2 * u + rel) * (p.T @ np.abs(hd)) + LEAST["bf16"] * 2
+    rows = dW.view(n, V0, H)
+    other = torch.ones((n, V0), dtype=torch.bool, device="cuda")
+    for t in np.flatnonzero(live):
+        other[at[t] // V0, at[t] % V0] = False
+        want_row = plain[at[t] % V0] - c[t] * hd[t]
+        row_bound = bound[at[t] % V0] + (2 * u + rel) * c[t] * np.abs(hd[t])
+        assert np.all(np.abs(f64(dW[int(at[t])]) - want_row) <= row_bound)
+    for i in (0, 1, n // 2, n - 2, n - 1):
+        err = np.abs(f64(rows[i]) - plain)
+        assert np.all((err <= bound)[other[i].cpu().numpy()])
+    for i in range(1, n):  # and the same bits
+        same = (rows[i].view(torch.int16) == rows[1].view(torch.int16)).all(1)
+        assert bool((same | ~other[i] | ~other[1]).all())
+    # dh: the sum over all copies
+    wt = bd[np.where(live, at % V0, 0)]
+    want_h = n * (p @ bd) - c * wt
+    terms = n * (p @ np.abs(bd)) + c * np.abs(wt)
+    assert np.all(np.abs(f64(dh) - want_h) <= (2 * u + rel) * terms + LEAST["bf16"] * 2)
