@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(256)
 {
     constexpr int N4 = 8 / PARTS;  // fours of columns
     __shared__ float4 sm[PARTS][N4][32];
-    __shared__ uint16_t rows[32][4 * N4 + 2];
+    __shared__ uint32_t rows[32][2 * N4 + 1];  // two columns to a word
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c4 = warp % N4, part = warp / N4;
     const int x = blockIdx.x / (CG * 4), rq = blockIdx.x % (CG * 4);  // tile, 32-row part of it
     const int row0 = x / nn * Cfg<CG>::BM + rq * 32, col0 = x % nn * kBN + blockIdx.y * 4 * N4;
@@ -807,14 +807,14 @@ __global__ void __launch_bounds__(256)
         }
     }
     if (part == 0) {
-        *reinterpret_cast<uint32_t *>(&rows[lane][c4 * 4]) = pack16(v.x * inv, v.y * inv, f16);
-        *reinterpret_cast<uint32_t *>(&rows[lane][c4 * 4 + 2]) = pack16(v.z * inv, v.w * inv, f16);
+        rows[lane][c4 * 2] = pack16(v.x * inv, v.y * inv, f16);
+        rows[lane][c4 * 2 + 1] = pack16(v.z * inv, v.w * inv, f16);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * 4 * N4; i += 256) {
         const int r = i / (4 * N4), c = i % (4 * N4);
         if (row0 + r < T && col0 + c < H)
-            dh[(int64_t)(row0 + r) * lddh + col0 + c] = rows[r][c];
+            dh[(int64_t)(row0 + r) * lddh + col0 + c] = reinterpret_cast<const uint16_t *>(rows[r])[c];
     }
 }
 
