@@ -237,8 +237,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, 
     }
 }
 
+// whether the row of target y has a loss and a gradient
+__device__ __forceinline__ bool is_live(const CeArgs &a, int y) { return y != a.ignore && y >= 0 && y < a.V; }
+
 // Factor of g before it is rounded to 16 bits; the products' epilogues take it
-// out again.  It brings the largest |dloss| (1 - e), the target's part of g, to
+// out again.  It brings the largest |dloss| (1 - e) of the rows that have a
+// gradient (what the others hold may be anything), the target's part of g, to
 // just `full` (1, or 2^14 in fp16, whose range would not hold dloss = 1 / T
 // times a probability).  With the same dloss in every row, as in a mean, all
 // targets' parts are then a little below a power of two, where a rounding is
@@ -251,7 +255,7 @@ __device__ __forceinline__ float g_scale(const CeArgs &a, float *sm)
     float top = 0.f;
     for (int t = threadIdx.x; t < a.T; t += kEpiWarps * 32) {
         const float v = fabsf(a.dloss[t]);
-        if (v < INFINITY)
+        if (v < INFINITY && is_live(a, a.targets[t]))
             top = fmaxf(top, v);
     }
 #pragma unroll
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             if constexpr (MODE != kGrad) {
                 if (row < a.T) {
                     const int y = a.targets[row];
-                    const bool live = y != a.ignore && y >= 0 && y < a.V;
+                    const bool live = is_live(a, y);
                     if (live && y - a.v0 - col0 < cols)
                         tgt = y - a.v0 - col0;  // this warp's column of the target, if it has it
                     if constexpr (MODE == kProb) {

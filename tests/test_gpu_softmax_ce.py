@@ -357,3 +357,68 @@ def test_weights_of_more_than_two_to_the_31_elements():
     want_h = n * (p @ bd) - c * wt
     terms = n * (p @ np.abs(bd)) + c * np.abs(wt)
     assert np.all(np.abs(f64(dh) - want_h) <= (2 * u + rel) * terms + LEAST["bf16"] * 2)
+
+
+@pytest.mark.parametrize("T", [64, 96, 200])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_dloss_of_rows_without_a_target_has_no_effect(dtype, T):
+    """Whatever dloss holds where a row is ignored or its target is no label,
+    the gradients are the same bits."""
+    V = 5000
+    h, W = rand(T, 128, dtype, 1), rand(V, 128, dtype, 2, 0.2)
+    y = draw_targets(T, V, 3, 0.3)
+    y[1], y[2] = -100, V  # ignored, no label
+    dead = (y < 0) | (y >= V)
+    base = torch.full((T,), 1.0 / T, device="cuda")
+    lse, status = torch.empty(T, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sg_softmax_ce_fwd(h, W, y, torch.empty_like(lse), lse, status=status)
+    got = []
+    for left in (0.0, 1e6, 1e20, -1e9, float("inf"), float("nan")):
+        dh, dW = torch.empty_like(h), torch.empty_like(W)
+        sg.sg_softmax_ce_bwd(h, W, y, lse, torch.where(dead, left, base), dh, dW, status=status)
+        got.append((dh, dW))
+    assert got[0][0][~dead].any() and not got[0][0][dead].any()
+    for dh, dW in got[1:]:
+        assert torch.equal(dh, got[0][0]) and torch.equal(dW, got[0][1])
+
+
+@pytest.mark.parametrize("T", [96, 300])
+@pytest.mark.parametrize("weights", ["mean", "spread"])
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+def test_f16_gradients_of_small_weights(T, weights, smoothing):
+    """dloss of 1 / T, or over three orders of magnitude, where a probability
+    times dloss is below what f16 holds well: with a factor that brings the
+    largest dloss to 2^13 at least, an element of g is off by at most u of its
+    value and half a subnormal step, 2^-25, over the factor.  Rounding errors
+    that lie anywhere in such an interval have 1 / sqrt(3) of it as root mean
+    square, and those of different elements are independent, so the squares of
+    the sums' errors add up.  The output's own rounding is measured; features
+    and weights are scaled so that it is one of normal numbers.  A tenth more
+    for what a sample of errors differs from its mean."""
+    H, V = 64, 2000
+    y = draw_targets(T, V, 3)
+    dloss = torch.full((T,), 1.0 / T, device="cuda")
+    if weights == "spread":
+        g = torch.Generator(device="cuda")
+        g.manual_seed(4)
+        dloss = dloss * 10.0 ** (-3 * torch.rand(T, generator=g, device="cuda"))
+    for up in (2.0 ** -6, 2.0 ** 6):  # dh of normal numbers, dW of normal numbers
+        h, W = rand(T, H, "f16", 1, up), rand(V, H, "f16", 2, 2.0 / np.sqrt(H) / up)
+        loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        dh, dW = torch.empty_like(h), torch.empty_like(W)
+        sg.sg_softmax_ce_fwd(h, W, y, loss, lse, smoothing=smoothing)
+        sg.sg_softmax_ce_bwd(h, W, y, lse, dloss, dh, dW, smoothing=smoothing)
+        hd, Wd, at, c = f64(h), f64(W), y.cpu().numpy(), f64(dloss)
+        ref = softmax_ce(hd, Wd, at, c, smoothing=smoothing)
+        z = hd @ Wd.T
+        p = np.exp(z - ref["lse"][:, None]) - smoothing / V
+        live = at >= 0
+        p[live, at[live]] -= 1 - smoothing
+        p *= np.where(live, c, 0)[:, None]
+        off2 = (U["f16"] ** 2 * p ** 2 + (2.0 ** -25 * c.max() / 2 ** 13) ** 2) / 3 * live[:, None]
+        e = 2 * logit_error(hd, Wd).max() + 3e-5
+        name, got, mean2 = (("dh", dh, (off2 @ Wd ** 2).sum()), ("dW", dW, (off2.T @ hd ** 2).sum()))[up > 1]
+        want = ref[name]
+        own = np.linalg.norm(want.astype(np.float16).astype(np.float64) - want)
+        err = np.linalg.norm(f64(got) - want)
+        assert err <= 1.1 * np.sqrt(own ** 2 + mean2) + e * np.linalg.norm(ref[name + "_mag"]), (name, err, own)
