@@ -249,14 +249,20 @@ __device__ __forceinline__ bool is_live(const CeArgs &a, int y) { return y != a.
 // smallest against its value; without it they would all be rounded the same
 // way at wherever 1 / T falls (measured at T = 777, fp16, e = 0.1: 4.3e-4 of
 // error in dh instead of 2.7e-4 by the output's own rounding).  The epilogue
-// warps of every CTA work it out while the first tile is under way.
+// warps of every CTA work it out while the first tile is under way; those of
+// the first one report targets that are no labels.
 __device__ __forceinline__ float g_scale(const CeArgs &a, float *sm)
 {
     float top = 0.f;
     for (int t = threadIdx.x; t < a.T; t += kEpiWarps * 32) {
         const float v = fabsf(a.dloss[t]);
-        if (v < INFINITY && is_live(a, a.targets[t]))
-            top = fmaxf(top, v);
+        const int y = a.targets[t];
+        if (is_live(a, y)) {
+            if (v < INFINITY)
+                top = fmaxf(top, v);
+        } else if (y != a.ignore && a.status && blockIdx.x == 0) {
+            sg_flag(a.status, SG_ERR_DATA);
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)

@@ -422,3 +422,18 @@ def test_f16_gradients_of_small_weights(T, weights, smoothing):
         own = np.linalg.norm(want.astype(np.float16).astype(np.float64) - want)
         err = np.linalg.norm(f64(got) - want)
         assert err <= 1.1 * np.sqrt(own ** 2 + mean2) + e * np.linalg.norm(ref[name + "_mag"]), (name, err, own)
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_backward_call_reports_targets_that_are_no_labels(T):
+    """By itself: its status word is another than the forward call's."""
+    V = 500
+    h, W, v = rand(T, 64, "bf16", 1), rand(V, 64, "bf16", 2, 0.25), torch.ones(T, device="cuda")
+    for bad in (-1, V, 2 ** 31 - 1, -2 ** 31):
+        y = draw_targets(T, V, 3)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sg.sg_softmax_ce_bwd(h, W, y, v, v, torch.empty_like(h), status=status)
+        assert int(status) == 0
+        y[T - 1] = bad
+        sg.sg_softmax_ce_bwd(h, W, y, v, v, torch.empty_like(h), status=status)
+        assert int(status) == sg.SG_ERR_DATA
