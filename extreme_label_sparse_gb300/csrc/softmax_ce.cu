@@ -1138,7 +1138,7 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     const char *fn = "sg_softmax_ce_bwd";
     NvtxRange nvtx_(fn);
     CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, true));
-    if (!W || (T && (!h || !targets || !lse || !dloss)) || (!dh && !dW))
+    if (!W || (T && (!h || !targets || !lse || !dloss || (!dh && !dW))))
         CE_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
     if (!(smoothing >= 0.0 && smoothing <= 1.0))
         CE_FAIL(SG_ERR_INVALID, "%s: smoothing=%g is outside [0, 1]", fn, smoothing);

@@ -83,3 +83,13 @@ def test_softmax_refusals_and_work(lib):
     args = list(bwd)
     args[13] = args[15] = None
     assert lib.sg_softmax_ce_bwd(*args) == INVALID
+
+
+def test_softmax_backward_of_no_rows_with_dh_alone(lib):
+    """No rows: dh has no elements, so its pointer may be NULL, and without dW
+    there is nothing to do."""
+    args = [None, 64, 0, 64, P, 64, 1000, sgpkg.SG_BF16, None, -100, 0.0, None, None, None, 64, None, 64, None, 0, None,
+            None]
+    assert lib.sg_softmax_ce_bwd(*args) == 0, sgpkg.last_error()
+    args[2] = 1
+    assert lib.sg_softmax_ce_bwd(*args) == INVALID
