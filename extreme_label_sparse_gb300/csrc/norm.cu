@@ -725,6 +725,14 @@ sg_status check_mat(const char *fn, const char *name, const void *p, int64_t ld,
     return SG_OK;
 }
 
+// fp32 vectors
+sg_status check_vec(const char *fn, const char *name, const void *p)
+{
+    if (((uintptr_t)p) % 4 != 0)
+        NORM_FAIL(SG_ERR_INVALID, "%s: %s is not aligned to its elements", fn, name);
+    return SG_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -778,6 +786,8 @@ sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, i
     NORM_TRY(check_mat(fn, "u", u, ldu, cols, es));
     NORM_TRY(check_mat(fn, "y", y, ldy, cols, es));
     NORM_TRY(check_mat(fn, "y8", y8, ldy8, cols, 1));
+    NORM_TRY(check_vec(fn, "rstd", rstd));
+    NORM_TRY(check_vec(fn, "y8_scale", y8_scale));
     NormFwd a;
     if (!make_drop(drop_p, seed, offset, &a.d))
         NORM_FAIL(SG_ERR_INVALID, "%s: drop_p=%g is not a probability", fn, drop_p);
@@ -837,6 +847,8 @@ sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_
     NORM_TRY(check_mat(fn, "weight", weight, cols, cols, es));
     NORM_TRY(check_mat(fn, "du", du, lddu, cols, es));
     NORM_TRY(check_mat(fn, "dx", dx, lddx, cols, es));
+    NORM_TRY(check_vec(fn, "rstd", rstd));
+    NORM_TRY(check_vec(fn, "dweight", dweight));
     NormBwd a;
     if (!make_drop(drop_p, seed, offset, &a.d))
         NORM_FAIL(SG_ERR_INVALID, "%s: drop_p=%g is not a probability", fn, drop_p);

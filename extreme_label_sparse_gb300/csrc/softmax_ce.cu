@@ -1019,6 +1019,13 @@ sg_status check_ce(const char *fn, const void *h, int64_t ldh, int64_t T, int64_
     return SG_OK;
 }
 
+// whether vectors of 32-bit elements (any of them may be NULL) are aligned to them
+template <typename... P>
+bool aligned4(const P *...p)
+{
+    return (((uintptr_t)p | ...) & 3) == 0;
+}
+
 template <typename E>
 void pack(const void *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t ldd, cudaStream_t st)
 {
@@ -1081,6 +1088,8 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, false));
     if (!W || (T && (!h || !targets || !loss || !lse)))
         CE_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
+    if (!aligned4(h_scale, W_scale, targets, loss, lse, status))
+        CE_FAIL(SG_ERR_INVALID, "%s: a vector or status is not aligned to its elements", fn);
     if ((h_scale || W_scale) && dtype != SG_E4M3)
         CE_FAIL(SG_ERR_INVALID, "%s: scales go with SG_E4M3 rows only", fn);
     if (!(smoothing >= 0.0 && smoothing <= 1.0))
@@ -1140,6 +1149,8 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     CE_TRY(check_ce(fn, h, ldh, T, H, W, ldw, V, dtype, true));
     if (!W || (T && (!h || !targets || !lse || !dloss || (!dh && !dW))))
         CE_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
+    if (!aligned4(targets, lse, dloss, status))
+        CE_FAIL(SG_ERR_INVALID, "%s: a vector or status is not aligned to its elements", fn);
     if (!(smoothing >= 0.0 && smoothing <= 1.0))
         CE_FAIL(SG_ERR_INVALID, "%s: smoothing=%g is outside [0, 1]", fn, smoothing);
     if ((dh && (lddh < H || (uintptr_t)dh % 2 != 0)) || (dW && (lddw < H || (uintptr_t)dW % 2 != 0)))

@@ -396,7 +396,8 @@ SG_API sg_status sg_grouping_export(sg_grouping *g, sg_bf16 *E, uint8_t *has, fl
  * Conventions: element types are sg_dtype values; a matrix is row-major with
  * its row stride in elements (ld >= columns, so it may be a slice of a wider
  * one); any alignment to the element is accepted, and rows that start on 16
- * bytes are read and written faster.  Work memory is device memory of the
+ * bytes are read and written faster.  Vectors are contiguous and aligned to
+ * their elements (SG_ERR_INVALID otherwise).  Work memory is device memory of the
  * caller, of the size that the _work call gives; its contents need not survive
  * between calls, and calls that overlap on the GPU need one each.  Nothing is
  * allocated, no call waits for the device, and all of them can be captured

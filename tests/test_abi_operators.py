@@ -93,3 +93,24 @@ def test_softmax_backward_of_no_rows_with_dh_alone(lib):
     assert lib.sg_softmax_ce_bwd(*args) == 0, sgpkg.last_error()
     args[2] = 1
     assert lib.sg_softmax_ce_bwd(*args) == INVALID
+
+
+def test_vectors_off_their_elements_are_refused(lib):
+    """Each fp32 or int32 vector by itself, two bytes off its elements."""
+    off, bf = C.c_void_p(258), sgpkg.SG_BF16
+    calls = (
+        (lib.sg_add_rmsnorm_fwd, [P, 8, None, 8, 4, 8, bf, P, 1e-6, 0.0, 1, 2, None, 8, P, P, 8, P, 8, P, None],
+         (14, 19)),
+        (lib.sg_add_rmsnorm_bwd, [P, 8, P, 8, None, 8, 4, 8, bf, P, P, 0.0, 1, 2, P, 8, None, 8, P, P, 1 << 30, None],
+         (10, 18, 19)),
+        (lib.sg_softmax_ce_fwd, [P, 64, P, 4, 64, P, 64, P, 1000, sgpkg.SG_E4M3, P, -100, 0.0, P, P, P, 1 << 40, P, None],
+         (2, 7, 10, 13, 14, 17)),
+        (lib.sg_softmax_ce_bwd, [P, 64, 4, 64, P, 64, 1000, bf, P, -100, 0.0, P, P, P, 64, P, 64, P, 1 << 40, P, None],
+         (8, 11, 12, 19)),
+    )
+    for call, ok, places in calls:
+        for at in places:
+            args = list(ok)
+            args[at] = off
+            assert call(*args) == INVALID, (call.__name__, at, sgpkg.last_error())
+            assert "align" in sgpkg.last_error()
