@@ -442,10 +442,11 @@ __global__ void __launch_bounds__(norm_threads(WARPS), bwd_ctas(VEC, WARPS, size
             }
         }
         row_reduce<WARPS, false>(dot, none, sm, turn);
-        // du = rstd (dy w - n mean(dy w n)) with n = u rstd:
-        // (rstd w) dy - back u, back = rstd^3 mean(dy w u) in an order that
-        // keeps rows of any scale within the range of fp32
-        const float back = dot / (float)a.cols * rstd * rstd * rstd;
+        // du = rstd (dy w - n mean(dy w n)): (rstd w) dy - back n with n = u
+        // rstd, back = rstd mean(dy w n).  Neither a square of u nor one of rstd
+        // is a part of it without the other, which leaves rows of values from
+        // 1e-36 to 1e34 within the range of fp32.
+        const float back = dot / (float)a.cols * rstd * rstd;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c0 = (n * WARPS + wr) * kSeg;
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), bwd_ctas(VEC, WARPS, size
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = fmaf(to_f(w[n].v[j]) * rstd, to_f(dy.v[j]), fmaf(-back, to_f(u.v[j]), v[j]));
+                v[j] = fmaf(to_f(w[n].v[j]) * rstd, to_f(dy.v[j]), fmaf(-back, to_f(u.v[j]) * rstd, v[j]));
             store8<T, VEC>(static_cast<T *>(a.du) + r * a.ldo, c0, lane, a.cols, pack8<T>(v));
             if (a.dx) {
                 if (a.d.drop) {

@@ -338,3 +338,19 @@ def test_dropout_beyond_two_to_the_31_elements():
     # standard deviation of the mean of 10^6 of them: 5e-4
     for at in (0, rows // 2, rows - 1000):
         assert abs(float((y[at:at + 1000] != 0).float().mean()) - 0.5) < 5e-3
+
+
+@pytest.mark.parametrize("unit", (1e-36, 1e-30, 1e-20, 1e20, 1e30, 1e34))
+@pytest.mark.parametrize("dtype,cols", [("f32", 520), ("f32", 301), ("bf16", 520), ("bf16", 8200)])
+def test_norm_backward_of_rows_of_extreme_scales(dtype, cols, unit):
+    """Rows whose squares fp32 cannot hold, but whose rstd it can."""
+    dy, u = rand(5, cols, dtype, 1), (unit * rand(5, cols, "f32", 2)).to(TYPES[dtype])
+    w = (1 + 0.2 * rand(1, cols, "f32", 3)).to(TYPES[dtype]).reshape(-1)
+    rstd = torch.from_numpy((1 / np.sqrt((f64(u) ** 2).mean(1))).astype(np.float32)).cuda()
+    du, dw = torch.empty_like(dy), torch.empty(cols, device="cuda")
+    sg.sg_add_rmsnorm_bwd(dy, u, w, rstd, du, dw)
+    want, want_w = orc.add_rmsnorm_grad(f64(dy), f64(u), f64(w), f64(rstd))
+    r = f64(rstd)[:, None]
+    g, n = np.abs(f64(dy) * f64(w)), np.abs(f64(u)) * r
+    close(du, want, dtype, r * (g + n * (g * n).mean(1, keepdims=True)))
+    close(dw, want_w, "f32", (np.abs(f64(dy)) * n).sum(0) * 2)
