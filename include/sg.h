@@ -432,7 +432,10 @@ SG_API sg_status sg_dropout(const void *x, int64_t ldx, int64_t rows, int64_t co
  * 8 bits (SG_E4M3), y = y8 * y8_scale with y8_scale = max |y| / 448 of the row
  * (at least 2^-126; 0 for a row of zeros).  One of y and y8 is needed.  residual NULL: u =
  * drop(x).  weight[cols] has dtype.  u may be x or residual, and y any of
- * them.  cols <= 32768. */
+ * them.  cols <= 32768.
+ * The sum of u^2 is formed in fp32 as it is: rows of a root mean square of up
+ * to 1e19 / sqrt(cols), and above 1e-18 where eps is smaller than its square.
+ * Beyond, rstd is 0 or infinite, and y = u rstd weight follows it. */
 SG_API sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows,
                                     int64_t cols, int32_t dtype, const void *weight, double eps, double drop_p,
                                     uint64_t seed, uint64_t offset, void *u, int64_t ldu, float *rstd, void *y,
@@ -444,7 +447,8 @@ SG_API sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *resi
  *   dweight[c] = sum over rows of dy n  (fp32, in an order that is always the
  *   same for the same sizes).
  * du_in (may be NULL) is the gradient that reaches u by its other way, the
- * residual; du is the gradient of residual, and of x where drop_p = 0.  dx and
+ * residual; du is the gradient of residual, and of x where drop_p = 0.  Values
+ * of u may lie anywhere between 1e-36 and 1e34.  dx and
  * dweight may be NULL.  du may be dy or du_in, and dx any of them.  work (only
  * for dweight) is aligned to 4 bytes. */
 SG_API sg_status sg_add_rmsnorm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes);

@@ -354,3 +354,24 @@ def test_norm_backward_of_rows_of_extreme_scales(dtype, cols, unit):
     g, n = np.abs(f64(dy) * f64(w)), np.abs(f64(u)) * r
     close(du, want, dtype, r * (g + n * (g * n).mean(1, keepdims=True)))
     close(dw, want_w, "f32", (np.abs(f64(dy)) * n).sum(0) * 2)
+
+
+@pytest.mark.parametrize("dtype,cols", [("f32", 520), ("f32", 301), ("bf16", 301), ("bf16", 700), ("bf16", 32768)])
+def test_norm_forward_of_rows_at_the_ends_of_its_range(dtype, cols):
+    """Root mean squares of 1e-18 and 1e19 / sqrt(cols); a row beyond keeps to
+    itself, with the rstd that its fp32 sum gives."""
+    far = 1e19 / np.sqrt(cols)
+    units = np.array([1.0, 1e-18, 1e-17, far / 2, far, 1.0, 1e21, 1e-30, 1.0])
+    x = rand(9, cols, "f32", 1)
+    x = x / x.square().mean(1, keepdim=True).sqrt() * torch.tensor(units, device="cuda").float()[:, None]
+    x = x.to(TYPES[dtype])
+    w = (1 + 0.2 * rand(1, cols, "f32", 3)).to(TYPES[dtype]).reshape(-1)
+    y, rstd = torch.empty_like(x), torch.empty(9, device="cuda")
+    for eps in (0.0, 1e-30):
+        sg.sg_add_rmsnorm_fwd(x, w, eps, rstd=rstd, y=y)
+        ok = np.array([True] * 6 + [False, False, True])
+        want, r = orc.add_rmsnorm(f64(x), f64(w), float(np.float32(eps)))
+        assert np.all(np.abs(f64(rstd) - r)[ok] <= 1e-5 * r[ok])
+        close(y[torch.from_numpy(ok).cuda()], want[ok], dtype, np.abs(want[ok]))
+        assert float(rstd[6]) == 0 and not y[6].any()
+        assert eps > 0 or float(rstd[7]) == float("inf")
