@@ -96,9 +96,9 @@ struct CeArgs {
     int32_t kt;           // rows of a box of g and h in dW's product, whose K they are
     int32_t f16;          // 16-bit operands are fp16, not bf16
     // kLse
-    const float *h_scale, *W_scale;  // fp8: scale per row, or NULL
+    const float *h_scale, *W_scale;  // fp8: scale per row (W: from row v0 on), or NULL
     const int32_t *targets;
-    float2 *part;         // [Tp][slots] running maximum (of z log2 e) and sum
+    float2 *part;         // [tile rows][slots] running maximum (of z log2 e) and sum
     float *zsum;          // the same for the sum of z, or NULL
     int32_t slots;
     float *ztgt;          // [T] the target's logit
@@ -699,6 +699,9 @@ struct JoinArgs {
     int32_t *status;
     int32_t slots, V, ignore;
     float smooth;
+    float2 *run;  // what the pieces of the vocabulary before this one came to
+    float *zrun;
+    int32_t first, last;  // of the pieces
 };
 
 __device__ __forceinline__ void join_out(const JoinArgs &a, int t, float m, float s, float zs)
@@ -767,7 +770,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_ce_join(const JoinArgs a)
             s += sm[1][w];
             zs += sm[2][w];
         }
-        join_out(a, t, top, s, zs);
+        if (!a.first) {
+            join_one(top, s, a.run[t]);
+            zs += a.zrun[t];
+        }
+        if (a.last) {
+            join_out(a, t, top, s, zs);
+        } else {
+            a.run[t] = make_float2(top, s);
+            a.zrun[t] = zs;
+        }
     }
 }
 
@@ -895,15 +907,16 @@ struct Plan {
     int es = 2, CG = 1, BM = 128, C = kSMs;
     bool pack_h = false, pack_W = false;
     int64_t ldp = 0;             // row stride of the packed copies
-    int64_t nm = 0, Tp = 0, bw = kBN;
+    int64_t nm = 0, bw = kBN;
     int64_t ab = 64, an = 2, kt = 64;  // boxes: see CeArgs
-    // forward
-    int64_t slots = 0;
+    // forward: rows of a band, vocabulary of a piece
+    int64_t Tb = 0, Vb = 0;
     // backward
     int64_t Vc = 0;              // vocabulary of a piece
     int64_t dh_nn = 0, dh_tiles = 0, split = 1;
     // byte offsets
-    int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
+    int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_run = 0, o_zrun = 0;
+    int64_t o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
 };
 
 bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
@@ -931,6 +944,21 @@ int64_t tile_width(int64_t nm, int64_t V, int CG, int C)
     return best;
 }
 
+constexpr int64_t kPartBytes = 256ll << 20;
+
+// partial results of a row in a launch over `rows` rows and `vocab` labels: a
+// running one for each half of a cluster's tiles, or, where a cluster meets
+// several row tiles, one for each half tile; and of all rows
+int64_t slot_count(const Plan &p, int64_t rows, int64_t vocab)
+{
+    return 2 * (rows <= p.BM ? (int64_t)p.C : ceil_div(vocab, p.bw));
+}
+
+int64_t part_count(const Plan &p, int64_t rows, int64_t vocab)
+{
+    return slot_count(p, rows, vocab) * ceil_div(rows, p.BM) * p.BM;
+}
+
 void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
                int32_t dtype, bool backward, Plan *p)
 {
@@ -942,7 +970,6 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     p->pack_W = !tma_ok(W, ldw, p->es);
     p->ldp = ceil_div(H * p->es, 16) * 16 / p->es;
     p->nm = ceil_div(T, p->BM);
-    p->Tp = p->nm * p->BM;
     // only the rows that there are: copying boxes of 64 rows of which few exist
     // takes longer than the rest of a stage (forward pass, T = 1, H = 2048, V =
     // 128000: 103 us with two such boxes, 87 with one of 8)
@@ -963,10 +990,25 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
         p->o_W = take(V * p->ldp * p->es);
     if (!backward) {
         p->bw = tile_width(p->nm, V, p->CG, p->C);
-        p->slots = 2 * (p->nm == 1 ? (int64_t)p->C : ceil_div(V, p->bw));
-        p->o_part = take(p->slots * p->Tp * 8);
-        p->o_zsum = take(p->slots * p->Tp * 4);
-        p->o_ztgt = take(T * 4);
+        // The partial results of a band of rows, 12 bytes for a row and half tile,
+        // are at most kPartBytes: whole bands of kBand row tiles, which read W once
+        // each anyway, and where not one fits, pieces of the vocabulary.
+        const int64_t band = kBand * p->BM;
+        p->Tb = T;
+        p->Vb = V;
+        if (part_count(*p, T, V) * 12 > kPartBytes) {
+            p->Tb = kPartBytes / 12 / slot_count(*p, T, V) / band * band;
+            if (p->Tb == 0) {
+                p->Tb = T < band ? T : band;
+                p->Vb = kPartBytes / 24 / (ceil_div(p->Tb, p->BM) * p->BM) * p->bw;
+                p->o_run = take(p->Tb * 8);
+                p->o_zrun = take(p->Tb * 4);
+            }
+        }
+        const int64_t parts = part_count(*p, p->Tb, p->Vb);
+        p->o_part = take(parts * 8);
+        p->o_zsum = take(parts * 4);
+        p->o_ztgt = take(p->Tb * 4);
         return;
     }
     // a piece of g holds at most 256 MB (or 256 labels), whatever V: memory that a training
@@ -1035,8 +1077,8 @@ void pack(const void *src, int64_t ld, int64_t rows, int64_t cols, void *dst, in
 }
 
 // maps of h and W (mh, mW: in the logits' tiles; mhk, mWk: as K rows), packed
-// first where their rows need it
-sg_status operand_maps(const Plan &p, const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
+// first where their rows need it; h and ldh become those of the copy then
+sg_status operand_maps(const Plan &p, const void *&h, int64_t &ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
                        int64_t V, uint8_t *work, CUtensorMap *mh, CUtensorMap *mW, CUtensorMap *mhk, CUtensorMap *mWk, cudaStream_t st)
 {
     auto packed = [&](const void *&src, int64_t &ld, int64_t rows, int64_t at) {
@@ -1106,37 +1148,52 @@ sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, in
     CUtensorMap mh, mW;
     CE_TRY(operand_maps(p, h, ldh, T, H, W, ldw, V, w8, &mh, &mW, nullptr, nullptr, st));
     CeArgs a = {};
-    a.T = (int32_t)T;
     a.V = (int32_t)V;
     a.H = (int32_t)H;
-    a.nm = (int32_t)p.nm;
-    a.nn = (int32_t)ceil_div(V, p.bw);
     a.bw = (int32_t)p.bw;
     a.ab = (int32_t)p.ab;
     a.an = (int32_t)p.an;
     a.kt = (int32_t)p.kt;
     a.nk = (int32_t)ceil_div(H * p.es, 128);
     a.f16 = dtype == SG_F16;
-    a.h_scale = h_scale;
-    a.W_scale = W_scale;
-    a.targets = targets;
     a.ignore = ignore_index;
     a.part = reinterpret_cast<float2 *>(w8 + p.o_part);
     a.zsum = smoothing > 0 ? reinterpret_cast<float *>(w8 + p.o_zsum) : nullptr;
     a.ztgt = reinterpret_cast<float *>(w8 + p.o_ztgt);
-    a.slots = (int32_t)p.slots;
     a.status = status;
-    if (dtype == SG_E4M3)
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, mh, a, false, st))
-                         : (launch_ce<2, kLse, true>(mh, mW, mh, mh, mh, a, false, st)));
-    else
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, mh, a, false, st))
-                         : (launch_ce<2, kLse, false>(mh, mW, mh, mh, mh, a, false, st)));
-    JoinArgs j;
-    j.part = a.part, j.zsum = a.zsum, j.ztgt = a.ztgt, j.targets = targets, j.loss = loss, j.lse = lse;
-    j.status = status, j.slots = a.slots, j.V = a.V, j.ignore = ignore_index;
+    JoinArgs j = {};
+    j.part = a.part, j.zsum = a.zsum, j.ztgt = a.ztgt;
+    j.status = status, j.V = a.V, j.ignore = ignore_index;
     j.smooth = (float)smoothing;
-    return launch(k_ce_join, dim3((unsigned)T), kJoinThreads, 0, 1, true, st, j);
+    j.run = reinterpret_cast<float2 *>(w8 + p.o_run), j.zrun = reinterpret_cast<float *>(w8 + p.o_zrun);
+    for (int64_t t0 = 0; t0 < T; t0 += p.Tb) {
+        const int64_t rows = T - t0 < p.Tb ? T - t0 : p.Tb;
+        if (p.Tb < T)
+            CE_TRY(map_of(&mh, static_cast<const uint8_t *>(h) + t0 * ldh * p.es, H, rows, ldh, p.es, "h",
+                          (uint32_t)p.ab));
+        a.T = (int32_t)rows;
+        a.nm = (int32_t)ceil_div(rows, p.BM);
+        a.h_scale = h_scale ? h_scale + t0 : nullptr;
+        a.targets = j.targets = targets + t0;
+        j.loss = loss + t0, j.lse = lse + t0;
+        for (int64_t v0 = 0; v0 < V; v0 += p.Vb) {
+            const int64_t vc = V - v0 < p.Vb ? V - v0 : p.Vb;
+            const bool after = t0 > 0 || v0 > 0;
+            a.v0 = (int32_t)v0;
+            a.W_scale = W_scale ? W_scale + v0 : nullptr;
+            a.nn = (int32_t)ceil_div(vc, p.bw);
+            a.slots = j.slots = (int32_t)slot_count(p, rows, vc);
+            j.first = v0 == 0, j.last = v0 + vc == V;
+            if (dtype == SG_E4M3)
+                CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, true>(mh, mW, mh, mh, mh, a, after, st))
+                                 : (launch_ce<2, kLse, true>(mh, mW, mh, mh, mh, a, after, st)));
+            else
+                CE_TRY(p.CG == 1 ? (launch_ce<1, kLse, false>(mh, mW, mh, mh, mh, a, after, st))
+                                 : (launch_ce<2, kLse, false>(mh, mW, mh, mh, mh, a, after, st)));
+            CE_TRY(launch(k_ce_join, dim3((unsigned)rows), kJoinThreads, 0, 1, true, st, j));
+        }
+    }
+    return SG_OK;
 }
 
 sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,

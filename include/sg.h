@@ -484,7 +484,10 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  * strides below H, smoothing outside [0, 1], work memory that is too small or
  * not aligned to 256 bytes.  sg_softmax_ce_work wants the same h, W and strides
  * as the call (it looks at the alignment of their rows); backward: 0 for
- * sg_softmax_ce_fwd, 1 for sg_softmax_ce_bwd. */
+ * sg_softmax_ce_fwd, 1 for sg_softmax_ce_bwd.  Beside copies of h and W the
+ * forward call needs at most 256 MB and 16 bytes a row (more rows or labels are
+ * taken in turns), the backward call a piece of g (256 MB, or 256 labels where
+ * that is more) and fp32 sums of dh for each piece of its split vocabulary. */
 SG_API sg_status sg_softmax_ce_work(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
                                     int64_t V, int32_t dtype, int32_t backward, int64_t *bytes);
 SG_API sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, int64_t T, int64_t H,

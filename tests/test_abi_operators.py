@@ -114,3 +114,13 @@ def test_vectors_off_their_elements_are_refused(lib):
             args[at] = off
             assert call(*args) == INVALID, (call.__name__, at, sgpkg.last_error())
             assert "align" in sgpkg.last_error()
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 64, 1 << 30), (300, 64, 1 << 30), (8192, 512, 262144), (65536, 512, 262144),
+                                   (1 << 20, 64, 1 << 20), (1 << 24, 64, 1 << 20), (1 << 24, 64, 100)])
+def test_forward_work_memory_is_bounded(lib, T, H, V):
+    """Partial results of at most 256 MB, and 4 to 16 bytes a row (rows here
+    start on 16 bytes, so nothing is copied)."""
+    n = C.c_int64(-1)
+    assert lib.sg_softmax_ce_work(P, H, T, H, P, H, V, sgpkg.SG_BF16, 0, C.byref(n)) == 0
+    assert 0 < n.value <= (256 << 20) + 16 * T + 4096

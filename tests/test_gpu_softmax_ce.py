@@ -437,3 +437,50 @@ def test_backward_call_reports_targets_that_are_no_labels(T):
         y[T - 1] = bad
         sg.sg_softmax_ce_bwd(h, W, y, v, v, torch.empty_like(h), status=status)
         assert int(status) == sg.SG_ERR_DATA
+
+
+def forward64(h, W, y, smoothing, hs=None, Ws=None, piece=16384):
+    """loss, lse and the bound on a logit's error of each row, in 64 bits on the
+    device, a piece of the vocabulary at a time."""
+    h = h.double() if hs is None else h.float().double() * hs.double()[:, None]
+    T, V = h.shape[0], W.shape[0]
+    lse = torch.full((T,), -float("inf"), dtype=torch.float64, device="cuda")
+    total, top, at = (torch.zeros(T, dtype=torch.float64, device="cuda") for _ in range(3))
+    for v0 in range(0, V, piece):
+        w = W[v0:v0 + piece].float().double()
+        if Ws is not None:
+            w = w * Ws[v0:v0 + piece].double()[:, None]
+        z = h @ w.t()
+        lse = torch.logaddexp(lse, torch.logsumexp(z, 1))
+        total += z.sum(1)
+        here = (y >= v0) & (y < v0 + piece)
+        at = torch.where(here, z.gather(1, (y.long() - v0).clamp(0, z.shape[1] - 1)[:, None])[:, 0], at)
+        top = torch.maximum(top, (h.abs() @ w.abs().t()).amax(1))
+    loss = lse - (1 - smoothing) * at - smoothing * total / V
+    return torch.where(y >= 0, loss, 0.0), lse, (h.shape[1] / 16 + 4) * 2.0 ** -23 * top
+
+
+@pytest.mark.parametrize("T,H,V,dtype", [(45000, 64, 66000, "bf16"), (5000, 16, 768100, "e4m3"),
+                                         (4300, 8, 710000, "f16"), (600, 16, 3900000, "e4m3")])
+def test_forward_in_bands_of_rows_and_pieces_of_the_vocabulary(T, H, V, dtype):
+    """Sizes whose partial results do not fit the work memory at once: bands of
+    rows (the last one short), pieces of the vocabulary, and both."""
+    y = draw_targets(T, V, 3)
+    y[:2] = torch.tensor([0, V - 1])
+    hs = Ws = None
+    if dtype == "e4m3":
+        g = torch.Generator(device="cuda")
+        g.manual_seed(5)
+        h, W = (rand(n, H, "f16", s, 16.0).float().to(torch.float8_e4m3fn) for n, s in ((T, 1), (V, 2)))
+        hs, Ws = ((0.5 + torch.rand(n, generator=g, device="cuda")) / 24 for n in (T, V))
+    else:
+        h, W = rand(T, H, dtype, 1), rand(V, H, dtype, 2, 2.0 / np.sqrt(H))
+    assert sg.sg_softmax_ce_work(h, W, False) <= (256 << 20) + 16 * T + 4096
+    loss, lse, status = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.zeros(1, dtype=torch.int32,
+                                                                                                  device="cuda")
+    for smoothing in (0.0, 0.1):
+        sg.sg_softmax_ce_fwd(h, W, y, loss, lse, h_scale=hs, W_scale=Ws, smoothing=smoothing, status=status)
+        want, want_lse, e = forward64(h, W, y, smoothing, hs, Ws)
+        assert int(status) == 0
+        assert bool(((lse.double() - want_lse).abs() <= e + 1e-5).all())
+        assert bool(((loss.double() - want).abs() <= 2 * e + 1e-5).all())
