@@ -397,10 +397,10 @@ sg_status sg_device_status(int32_t *code)
         SG_TRY_CUDA(cudaMemcpy(&c, lo->status, sizeof(int32_t), cudaMemcpyDeviceToHost));
         if (c != SG_OK) {
             *code = c;
-            break;
+            return SG_OK;
         }
     }
-    return SG_OK;
+    return sg_softmax_ce_status(code, 0);
 }
 
 // ---------------------------------------------------------------- positives

@@ -237,6 +237,11 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, 
     }
 }
 
+// errors of calls that were given no status word
+__device__ int32_t g_ce_status;
+
+__device__ __forceinline__ int32_t *status_of(int32_t *status) { return status ? status : &g_ce_status; }
+
 // whether the row of target y has a loss and a gradient
 __device__ __forceinline__ bool is_live(const CeArgs &a, int y) { return y != a.ignore && y >= 0 && y < a.V; }
 
@@ -260,8 +265,8 @@ __device__ __forceinline__ float g_scale(const CeArgs &a, float *sm)
         if (is_live(a, y)) {
             if (v < INFINITY)
                 top = fmaxf(top, v);
-        } else if (y != a.ignore && a.status && blockIdx.x == 0) {
-            sg_flag(a.status, SG_ERR_DATA);
+        } else if (y != a.ignore && blockIdx.x == 0) {
+            sg_flag(status_of(a.status), SG_ERR_DATA);
         }
     }
 #pragma unroll
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 const int ab = CG == 2 ? 64 : a.ab, an = CG == 2 ? 2 : a.an, kt = CG == 2 ? 64 : a.kt;
                 // the next free stage, which is to receive `bytes` in all CTAs
                 auto stage = [&](uint32_t bytes, uint32_t *bar) {
-                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, a.status);
+                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status_of(a.status));
                     *bar = smem_u32(&c.full[r.i]);
                     if (ok && rank == 0)
                         mbar_arrive_expect_tx(*bar, bytes);
@@ -422,13 +427,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 const OpDesc da(base, a_mn), db(base + K::kA, b_mn);
                 const int buf = it & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tempty[buf]),
-                                                               ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.status));
+                                                               ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, status_of(a.status)));
                 if (!ok)
                     break;
                 tc_fence_after();
                 for (int kb = 0; kb < t.nk; ++kb) {
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait_cluster(smem_u32(&c.full[r.i]), r.ph, abort_flag, a.status));
+                                    mbar_wait_cluster(smem_u32(&c.full[r.i]), r.ph, abort_flag, status_of(a.status)));
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 }
             }
             if (!__all_sync(0xffffffffu,
-                            mbar_wait_cluster(smem_u32(&c.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, a.status)))
+                            mbar_wait_cluster(smem_u32(&c.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, status_of(a.status))))
                 break;
             tc_fence_after();
             if constexpr (MODE == kLse) {
@@ -714,8 +719,8 @@ __device__ __forceinline__ void join_out(const JoinArgs &a, int t, float m, floa
         out = l - (1.f - a.smooth) * a.ztgt[t];
         if (a.zsum)
             out -= a.smooth * (zs / (float)a.V);
-    } else if (y != a.ignore && a.status) {
-        sg_flag(a.status, SG_ERR_DATA);
+    } else if (y != a.ignore) {
+        sg_flag(status_of(a.status), SG_ERR_DATA);
     }
     a.loss[t] = out;
 }
@@ -1105,6 +1110,20 @@ sg_status operand_maps(const Plan &p, const void *&h, int64_t &ldh, int64_t T, i
 }  // namespace
 
 extern "C" {
+
+sg_status sg_softmax_ce_status(int32_t *code, int32_t clear)
+{
+    const char *fn = "sg_softmax_ce_status";
+    if (!code)
+        CE_FAIL(SG_ERR_INVALID, "%s: code is NULL", fn);
+    *code = SG_OK;
+    SG_TRY_CUDA(cudaDeviceSynchronize());
+    SG_TRY_CUDA(cudaMemcpyFromSymbol(code, g_ce_status, sizeof(int32_t)));
+    const int32_t none = SG_OK;
+    if (clear && *code != SG_OK)
+        SG_TRY_CUDA(cudaMemcpyToSymbol(g_ce_status, &none, sizeof(int32_t)));
+    return SG_OK;
+}
 
 sg_status sg_softmax_ce_work(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw, int64_t V,
                              int32_t dtype, int32_t backward, int64_t *bytes)

@@ -91,6 +91,7 @@ def load():
             "sg_add_rmsnorm_bwd": ([P, i64, P, i64, P, i64, i64, i64, i32, P, P, f64, u64, u64, P, i64, P, i64, P, P,
                                     i64, P], C.c_int),
             "sg_softmax_ce_work": ([P, i64, i64, i64, P, i64, i64, i32, i32, C.POINTER(i64)], C.c_int),
+            "sg_softmax_ce_status": ([C.POINTER(i32), i32], C.c_int),
             "sg_softmax_ce_fwd": ([P, i64, P, i64, i64, P, i64, P, i64, i32, P, i32, f64, P, P, P, i64, P, P],
                                   C.c_int),
             "sg_softmax_ce_bwd": ([P, i64, i64, i64, P, i64, i64, i32, P, i32, f64, P, P, P, i64, P, i64, P, i64, P,
@@ -216,7 +217,8 @@ def sg_layout_status(layout: Layout, clear: bool = True) -> int:
 
 def sg_device_status() -> int:
     """First non-zero status word among the live layouts of the current
-    device (0 if none); reads without clearing."""
+    device, else that of sg_softmax_ce_status (0 if none); reads without
+    clearing."""
     code = C.c_int32(0)
     _check(load().sg_device_status(C.byref(code)))
     return int(code.value)
@@ -658,12 +660,21 @@ def sg_softmax_ce_work(h: torch.Tensor, W: torch.Tensor, backward: bool) -> int:
     return _ce_work(_head(h, W, _16BIT if backward else _8OR16BIT)[0], int(bool(backward)))
 
 
+def sg_softmax_ce_status(clear: bool = True) -> int:
+    """The status word of the current device's softmax cross entropy calls that
+    were given none of their own (0: no error); waits for the device."""
+    code = C.c_int32(0)
+    _check(load().sg_softmax_ce_status(C.byref(code), int(bool(clear))))
+    return int(code.value)
+
+
 def sg_softmax_ce_fwd(h: torch.Tensor, W: torch.Tensor, targets, loss, lse, h_scale=None, W_scale=None,
                       ignore_index: int = -100, smoothing: float = 0.0, work=None, status=None):
     """loss[T] and lse[T] of the dense head with logits h W^T (see sg.h); with
     float8_e4m3fn rows, h_scale[T] and W_scale[V] are their scales.  work: a
     uint8 tensor of sg_softmax_ce_work bytes; one is taken from torch's
-    allocator if it is None.  status: an int32 tensor of one element."""
+    allocator if it is None.  status: an int32 tensor of one element; errors go
+    to the device's word (sg_softmax_ce_status) if it is None."""
     head, _, dev = _head(h, W, _8OR16BIT)
     hp, ldh, T, H, wp, ldw, V, dt = head
     if work is None:

@@ -163,8 +163,10 @@ SG_API sg_status sg_layout_status(sg_layout *layout, int32_t *code, int32_t clea
 
 /* The device-wide view of the same words: waits for the current device, then
  * sets *code to the first non-zero status word among the live layouts built on
- * that device (in the order they were built), or SG_OK.  Clears nothing: a
- * layout's word is reset with sg_layout_status(..., clear = 1).  Returns
+ * that device (in the order they were built), else to that of the softmax cross
+ * entropy calls without one of their own (sg_softmax_ce_status), or SG_OK.
+ * Clears nothing: a layout's word is reset with sg_layout_status(..., clear =
+ * 1).  Returns
  * SG_ERR_INVALID for a NULL `code` and SG_ERR_CUDA if the device reports an
  * error.  Thread-safe against concurrent build and free. */
 SG_API sg_status sg_device_status(int32_t *code);
@@ -477,9 +479,10 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  * and dW in dtype, times a factor that suits its largest element (taken out of
  * the fp32 sums).  The results are the same bits for the same call.  Rows of h or W that do not
  * start on 16 bytes are first copied into the work memory.
- * status (device int32, may be NULL): sticky, first error wins, SG_ERR_TIMEOUT
- * where a bounded wait gave up and the outputs are not complete; the caller
- * clears it.  T <= 2^24, H <= 2^20, V <= 2^30, T V < 2^45.
+ * status (device int32): sticky, first error wins, SG_ERR_TIMEOUT where a
+ * bounded wait gave up and the outputs are not complete; the caller clears it.
+ * NULL: the device's word, which sg_softmax_ce_status reads (it waits for the
+ * device) and, if `clear`, resets.  T <= 2^24, H <= 2^20, V <= 2^30, T V < 2^45.
  * Errors: SG_ERR_INVALID for NULL pointers, sizes below 1 (T below 0), row
  * strides below H, smoothing outside [0, 1], work memory that is too small or
  * not aligned to 256 bytes.  sg_softmax_ce_work wants the same h, W and strides
@@ -490,6 +493,7 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  * that is more) and fp32 sums of dh for each piece of its split vocabulary. */
 SG_API sg_status sg_softmax_ce_work(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
                                     int64_t V, int32_t dtype, int32_t backward, int64_t *bytes);
+SG_API sg_status sg_softmax_ce_status(int32_t *code, int32_t clear);
 SG_API sg_status sg_softmax_ce_fwd(const void *h, int64_t ldh, const float *h_scale, int64_t T, int64_t H,
                                    const void *W, int64_t ldw, const float *W_scale, int64_t V, int32_t dtype,
                                    const int32_t *targets, int32_t ignore_index, double smoothing, float *loss,

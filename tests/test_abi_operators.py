@@ -124,3 +124,7 @@ def test_forward_work_memory_is_bounded(lib, T, H, V):
     n = C.c_int64(-1)
     assert lib.sg_softmax_ce_work(P, H, T, H, P, H, V, sgpkg.SG_BF16, 0, C.byref(n)) == 0
     assert 0 < n.value <= (256 << 20) + 16 * T + 4096
+
+
+def test_softmax_status_wants_a_place(lib):
+    assert lib.sg_softmax_ce_status(None, 1) == INVALID

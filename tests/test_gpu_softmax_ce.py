@@ -484,3 +484,26 @@ def test_forward_in_bands_of_rows_and_pieces_of_the_vocabulary(T, H, V, dtype):
         assert int(status) == 0
         assert bool(((lse.double() - want_lse).abs() <= e + 1e-5).all())
         assert bool(((loss.double() - want).abs() <= 2 * e + 1e-5).all())
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_errors_of_calls_without_a_status_word_are_kept(T):
+    """In the device's word, by both calls, until it is cleared."""
+    V = 500
+    h, W, v = rand(T, 64, "bf16", 1), rand(V, 64, "bf16", 2, 0.25), torch.ones(T, device="cuda")
+    good = draw_targets(T, V, 3)
+    bad = good.clone()
+    bad[T // 2] = V
+    out = [torch.empty(T, device="cuda") for _ in range(2)]
+    sg.sg_softmax_ce_status()
+    for call in (lambda y: sg.sg_softmax_ce_fwd(h, W, y, *out), lambda y: sg.sg_softmax_ce_bwd(h, W, y, v, v, torch.empty_like(h))):
+        call(good)
+        assert sg.sg_softmax_ce_status() == 0
+        call(bad)
+        call(good)
+        assert sg.sg_device_status() == sg.SG_ERR_DATA  # which does not clear it
+        assert sg.sg_softmax_ce_status(clear=False) == sg.SG_ERR_DATA
+        assert sg.sg_softmax_ce_status() == sg.SG_ERR_DATA and sg.sg_softmax_ce_status() == 0
+    own = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sg_softmax_ce_fwd(h, W, bad, *out, status=own)
+    assert int(own) == sg.SG_ERR_DATA and sg.sg_softmax_ce_status() == 0
