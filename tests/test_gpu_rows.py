@@ -375,3 +375,81 @@ def test_norm_forward_of_rows_at_the_ends_of_its_range(dtype, cols):
         close(y[torch.from_numpy(ok).cuda()], want[ok], dtype, np.abs(want[ok]))
         assert float(rstd[6]) == 0 and not y[6].any()
         assert eps > 0 or float(rstd[7]) == float("inf")
+
+
+@pytest.mark.parametrize("dtype,shape", [("bf16", (700, 1024)), ("f32", (300, 4096)), ("f16", (501, 333)),
+                                         ("bf16", (40, 20000))])
+def test_outputs_written_over_inputs(dtype, shape):
+    """The same bits as with outputs of their own, for every input that an output
+    may be."""
+    rows, cols = shape
+    x, res, w = fwd_inputs(shape, dtype, 0, 0)
+    drop = dict(drop_p=0.25, seed=SEED, offset=OFFSET)
+    u, y = torch.empty_like(x), torch.empty_like(x)
+    sg.sg_add_rmsnorm_fwd(x, w, 1e-5, residual=res, u=u, y=y, **drop)
+    for over_u, over_y in (("x", "residual"), ("residual", "x"), ("residual", "own"), ("x", "own"), ("own", "x"),
+                           ("own", "residual")):
+        t = {"x": x.clone(), "residual": res.clone()}
+        own = torch.empty_like(x)
+        a, b = t.get(over_u, own), t.get(over_y, own)
+        sg.sg_add_rmsnorm_fwd(t["x"], w, 1e-5, residual=t["residual"], u=a, y=b, **drop)
+        assert torch.equal(a, u) and torch.equal(b, y)
+    for over in ("x", "residual"):  # u not asked for
+        t = {"x": x.clone(), "residual": res.clone()}
+        sg.sg_add_rmsnorm_fwd(t["x"], w, 1e-5, residual=t["residual"], y=t[over], **drop)
+        assert torch.equal(t[over], y)
+    dy, du_in = rand(*shape, dtype, 3), rand(*shape, dtype, 4)
+    rstd = torch.rsqrt(u.float().square().mean(1) + 1e-5)
+    du, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(cols, device="cuda")
+    sg.sg_add_rmsnorm_bwd(dy, u, w, rstd, du, dw, du_in=du_in, dx=dx, **drop)
+    for over_du, over_dx in (("dy", "du_in"), ("du_in", "dy"), ("dy", "own"), ("du_in", "own"), ("own", "dy"),
+                             ("own", "du_in")):
+        t = {"dy": dy.clone(), "du_in": du_in.clone()}
+        own, dw2 = torch.empty_like(x), torch.empty_like(dw)
+        a, b = t.get(over_du, own), t.get(over_dx, own)
+        sg.sg_add_rmsnorm_bwd(t["dy"], u, w, rstd, a, dw2, du_in=t["du_in"], dx=b, **drop)
+        assert torch.equal(a, du) and torch.equal(b, dx) and torch.equal(dw2, dw)
+
+
+def test_rows_on_two_streams_at_once():
+    """Each stream's outputs are those of its calls alone."""
+    cases = []
+    for seed in (1, 2):
+        dy, u = rand(4000, 2048, "bf16", seed), rand(4000, 2048, "bf16", seed + 2)
+        rstd, w = torch.rand(4000, device="cuda") + 0.5, rand(1, 2048, "bf16", 5).reshape(-1)
+        outs = [[torch.empty_like(u), torch.empty(2048, device="cuda"), torch.empty_like(u), torch.empty_like(u)]
+                for _ in range(2)]
+        cases.append((dy, u, rstd, w, outs, torch.cuda.Stream()))
+
+    def step(case, i):
+        dy, u, rstd, w, outs, _ = case
+        du, dw, y, d = outs[i]
+        sg.sg_add_rmsnorm_bwd(dy, u, w, rstd, du, dw)
+        sg.sg_add_rmsnorm_fwd(dy, w, 1e-6, residual=u, y=y)
+        sg.sg_dropout(dy, 0.5, SEED, OFFSET, d)
+
+    for case in cases:
+        step(case, 0)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for case in cases:
+            with torch.cuda.stream(case[5]):
+                step(case, 1)
+    torch.cuda.synchronize()
+    for case in cases:
+        assert all(torch.equal(a, b) for a, b in zip(*case[4]))
+
+
+@pytest.mark.parametrize("shape", [(1, 8), (3, 768), (1000, 264), (4001, 1001), (700, 20000)], ids=str)
+def test_what_work_memory_of_dweight_holds_does_not_matter(shape):
+    rows, cols = shape
+    dy, u = rand(*shape, "bf16", 1), rand(*shape, "bf16", 2)
+    w, rstd = torch.ones(cols, dtype=dy.dtype, device="cuda"), torch.rand(rows, device="cuda") + 0.5
+    got = []
+    for fill in (0, 255):
+        work = torch.full((sg.sg_add_rmsnorm_bwd_work(rows, cols),), fill, dtype=torch.uint8, device="cuda")
+        du, dw = torch.empty_like(dy), torch.empty(cols, device="cuda")
+        sg.sg_add_rmsnorm_bwd(dy, u, w, rstd, du, dw, work=work)
+        got.append((du, dw))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())

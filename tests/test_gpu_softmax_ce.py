@@ -507,3 +507,92 @@ def test_errors_of_calls_without_a_status_word_are_kept(T):
     own = torch.zeros(1, dtype=torch.int32, device="cuda")
     sg.sg_softmax_ce_fwd(h, W, bad, *out, status=own)
     assert int(own) == sg.SG_ERR_DATA and sg.sg_softmax_ce_status() == 0
+
+
+# width of the forward pass's tiles: (labels at which it is taken with one row
+# tile of a pair of CTAs, with two, with one row tile of one CTA)
+WIDTHS = {144: (9753, 4886, 19550), 160: (11014, 5515, 21975), 176: (12178, 6107, 24400), 192: (13439, 6736, 26825),
+          208: (14603, 7328, 29250), 224: (15864, 7957, 31675), 240: (17028, 8549, 34100)}
+
+
+@pytest.mark.parametrize("width", list(WIDTHS))
+@pytest.mark.parametrize("place,T", [(0, 130), (1, 300), (2, 70)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "e4m3"])
+def test_forward_tiles_between_128_and_256_columns(width, place, T, dtype):
+    """Where a warp's half of a tile is no whole number of its 32-column chunks;
+    targets on both sides of the halves' ends, in the first tiles and the last."""
+    V, H = WIDTHS[width][place], 72
+    y = draw_targets(T, V, 3)
+    ends = np.array([0, width // 2 - 1, width // 2, width - 1])
+    ends = np.concatenate([ends, ends + width, ends + V // width * width, [V - 1]])
+    y[:len(ends)] = torch.tensor(np.where(ends < V, ends, 0), dtype=torch.int32)
+    hs = Ws = None
+    if dtype == "e4m3":
+        h, W = (rand(n, 80, "f16", s, 16.0).float().to(torch.float8_e4m3fn) for n, s in ((T, 1), (V, 2)))
+        hs, Ws = ((0.5 + torch.rand(n, device="cuda")) / 48 for n in (T, V))
+    else:
+        h, W = rand(T, H, dtype, 1), rand(V, H, dtype, 2, 2.0 / np.sqrt(H))
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    for smoothing in (0.0, 0.1):
+        sg.sg_softmax_ce_fwd(h, W, y, loss, lse, h_scale=hs, W_scale=Ws, smoothing=smoothing)
+        want, want_lse, e = forward64(h, W, y, smoothing, hs, Ws)
+        assert bool(((lse.double() - want_lse).abs() <= e + 1e-5).all())
+        assert bool(((loss.double() - want).abs() <= 2 * e + 1e-5).all())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", [(65, 72, 1000), (72, 333, 600), (80, 256, 3000), (96, 768, 2500), (105, 64, 257),
+                                  (112, 320, 5003), (113, 128, 700)], ids=str)
+def test_two_boxes_of_fewer_than_64_rows(size, dtype):
+    T, H, V = size
+    h, W = rand(T, H, dtype, 1), rand(V, H, dtype, 2, 2.0 / np.sqrt(H))
+    check(h, W, draw_targets(T, V, 3), torch.rand(T, device="cuda") + 0.5, dtype, 0.1)
+
+
+def test_two_streams_at_once():
+    """Calls with work memory of their own, on the GPU together."""
+    cases = []
+    for T, H, V, seed in ((100, 512, 30000, 1), (600, 512, 30000, 2)):
+        h, W = rand(T, H, "bf16", seed), rand(V, H, "bf16", seed + 2, 2.0 / np.sqrt(H))
+        y, dloss = draw_targets(T, V, seed), torch.rand(T, device="cuda")
+        outs = [[torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(h), torch.empty_like(W)]
+                for _ in range(2)]
+        cases.append((h, W, y, dloss, outs, torch.cuda.Stream()))
+
+    def step(case, i):
+        h, W, y, dloss, outs, _ = case
+        loss, lse, dh, dW = outs[i]
+        sg.sg_softmax_ce_fwd(h, W, y, loss, lse, smoothing=0.1)
+        sg.sg_softmax_ce_bwd(h, W, y, lse, dloss, dh, dW, smoothing=0.1)
+
+    for case in cases:
+        step(case, 0)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for case in cases:
+            with torch.cuda.stream(case[5]):
+                step(case, 1)
+    torch.cuda.synchronize()
+    for case in cases:
+        assert all(torch.equal(a, b) for a, b in zip(*case[4]))
+
+
+@pytest.mark.parametrize("size", [(1, 64, 3000), (17, 1001, 5000), (96, 256, 20000), (128, 768, 131072), (777, 1000, 9001),
+                                  (4096, 128, 70000), (5000, 16, 768100)], ids=str)
+def test_what_work_memory_holds_does_not_matter(size):
+    """Zeros or NaNs, also between the calls: the same bits."""
+    T, H, V = size
+    h, W = rand(T, H, "bf16", 1), rand(V, H, "bf16", 2, 2.0 / np.sqrt(H))
+    y, dloss = draw_targets(T, V, 3), torch.rand(T, device="cuda")
+    got = []
+    for fill in (0, 255):
+        out = [torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(h), torch.empty_like(W)]
+        for backward in (False, True):
+            work = torch.full((sg.sg_softmax_ce_work(h, W, backward),), fill, dtype=torch.uint8, device="cuda")
+            if backward:
+                sg.sg_softmax_ce_bwd(h, W, y, out[1], dloss, out[2], out[3], smoothing=0.1, work=work)
+            else:
+                sg.sg_softmax_ce_fwd(h, W, y, out[0], out[1], smoothing=0.1, work=work)
+        got.append(out)
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())
