@@ -1,6 +1,8 @@
 // Dropout and the residual's addition with RMS norm (definitions in
 // include/sg.h).  All of them are bound by memory: each input is read once and
-// each output written once.
+// each output written once, but for the backward kernel's rows that are not
+// whole, aligned eights, of which dy and u are read twice (mostly from the
+// caches the second time).
 #include <atomic>
 #include <cmath>
 
@@ -199,7 +201,8 @@ constexpr int norm_ctas(int warps, bool few)
 constexpr int fwd_ctas(int warps, int nv, int size) { return norm_ctas(warps, size == 4 || nv == 3); }
 // The backward kernel's eights take 512 in all types: its sums of dweight spill
 // otherwise (16384 x 4096 bf16 with dropout: 107 us, 124 with 1024).  Single
-// elements, with no ring of rows, want the warps (32768 x 1001: 96 us, 140).
+// elements, with no ring of rows, want the warps even though their 64 registers
+// spill at most widths (32768 x 1001 with dropout: 97 us, 140 with 512).
 constexpr int bwd_ctas(bool vec, int warps, int size) { return norm_ctas(warps, size == 4 || vec); }
 
 struct NormFwd {

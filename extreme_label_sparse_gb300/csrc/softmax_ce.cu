@@ -5,7 +5,8 @@
 //   dh = g W,  dW = g^T h.
 // The logits never reach memory.  Forward: one matrix product whose epilogue
 // reduces each tile of logits to a running maximum and sum per row; a small
-// kernel joins them.  Backward, over pieces of the vocabulary: the product
+// kernel joins them.  (Where those would take more than 256 MB, bands of rows
+// and pieces of the vocabulary in turn.)  Backward, over pieces of the vocabulary: the product
 // again, its epilogue turning logits into g (16 bits, one piece of it held at
 // a time), then one launch with the tiles of both gradient products.
 //
@@ -18,8 +19,9 @@
 //
 // What bounds it.  Few rows: reading W, once in the forward pass and twice in
 // the backward one (for the logits and for dh), and writing dW.  128 x 768 x
-// 131072 bf16: forward 35.5 us (5.7 TB/s), backward 121 us (201 MB of W twice,
-// 201 MB of dW, 34 MB of g written and read twice: 5.8 TB/s).  Many rows: the
+// 131072 bf16: forward 36 us (5.7 TB/s), backward 121 to 131 us from card to
+// card (201 MB of W twice, 201 MB of dW, 34 MB of g written and read twice: up
+// to 5.8 TB/s).  Many rows: the
 // tensor cores.  4096 x 2048 x 128000 bf16: forward 1.1 to 1.2 ms (1.8 to 2.0
 // PFLOP/s as the power limit lets the clock), forward and backward 5.13 ms with
 // the logits worked out twice (1.67 PFLOP/s).  Between: tiles of a short K,

@@ -397,8 +397,11 @@ SG_API sg_status sg_grouping_export(sg_grouping *g, sg_bf16 *E, uint8_t *has, fl
  *
  * Conventions: element types are sg_dtype values; a matrix is row-major with
  * its row stride in elements (ld >= columns, so it may be a slice of a wider
- * one); any alignment to the element is accepted, and rows that start on 16
- * bytes are read and written faster.  Vectors are contiguous and aligned to
+ * one); any alignment to the element is accepted.  Dropout and the norm are
+ * faster (by up to two) where the columns are a whole number of eights and the
+ * rows of all matrices of the call start on 16 bytes (32 in fp32), softmax cross
+ * entropy where the rows of h and W start on 16 bytes and H is a whole number
+ * of eights.  Vectors are contiguous and aligned to
  * their elements (SG_ERR_INVALID otherwise).  Work memory is device memory of the
  * caller, of the size that the _work call gives; its contents need not survive
  * between calls, and calls that overlap on the GPU need one each.  Nothing is
@@ -432,9 +435,9 @@ SG_API sg_status sg_dropout(const void *x, int64_t ldx, int64_t rows, int64_t co
  * pointer is given: u (the next residual, and what the backward pass reads),
  * rstd[rows], y rounded to dtype, and y8[rows][cols] with y8_scale[rows]: y in
  * 8 bits (SG_E4M3), y = y8 * y8_scale with y8_scale = max |y| / 448 of the row
- * (at least 2^-126; 0 for a row of zeros).  One of y and y8 is needed.  residual NULL: u =
- * drop(x).  weight[cols] has dtype.  u may be x or residual, and y any of
- * them.  cols <= 32768.
+ * (at least 2^-126; 0 for a row of zeros).  One of y and y8 is needed.
+ * residual NULL: u = drop(x).  weight[cols] has dtype.  u may be x or residual,
+ * and y any of them.  cols <= 32768.
  * The sum of u^2 is formed in fp32 as it is: rows of a root mean square of up
  * to 1e19 / sqrt(cols), and above 1e-18 where eps is smaller than its square.
  * Beyond, rstd is 0 or infinite, and y = u rstd weight follows it. */
@@ -450,9 +453,9 @@ SG_API sg_status sg_add_rmsnorm_fwd(const void *x, int64_t ldx, const void *resi
  *   same for the same sizes).
  * du_in (may be NULL) is the gradient that reaches u by its other way, the
  * residual; du is the gradient of residual, and of x where drop_p = 0.  Values
- * of u may lie anywhere between 1e-36 and 1e34.  dx and
- * dweight may be NULL.  du may be dy or du_in, and dx any of them.  work (only
- * for dweight) is aligned to 4 bytes. */
+ * of u may lie anywhere between 1e-36 and 1e34.  dx and dweight may be NULL.
+ * du may be dy or du_in, and dx any of them.  work (only for dweight) is
+ * aligned to 4 bytes. */
 SG_API sg_status sg_add_rmsnorm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes);
 SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u, int64_t ldu, const void *du_in,
                                     int64_t lddu_in, int64_t rows, int64_t cols, int32_t dtype, const void *weight,
@@ -471,13 +474,15 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  *   h[T][H] and W[V][H] in dtype (SG_BF16, SG_F16; sg_softmax_ce_fwd also
  *   SG_E4M3, with a scale for each row of h and of W, NULL: 1).
  *   targets[T] int32: y_t in [0, V); a row with ignore_index has loss 0 and no
- *   gradient (its lse is still written).  Any other value counts as
- *   ignore_index and sets *status to SG_ERR_DATA.
+ *   gradient, whatever its dloss (its lse is still written).  Its g is 0, which
+ *   its features and W have to be finite for: 0 h_t is part of dW.  Any other
+ *   value counts as ignore_index and sets *status to SG_ERR_DATA, in either
+ *   call.
  *   loss[T], lse[T], dloss[T] fp32; dh[T][H], dW[V][H] in dtype, one of them
  *   may be NULL.  lse is what sg_softmax_ce_fwd wrote for the same h and W.
  * fp32 accumulation, sums and statistics in fp32.  g enters the products of dh
- * and dW in dtype, times a factor that suits its largest element (taken out of
- * the fp32 sums).  The results are the same bits for the same call.  Rows of h or W that do not
+ * and dW in dtype, times a factor that suits its largest element, by the dloss
+ * of the rows that have a gradient (taken out of the fp32 sums).  The results are the same bits for the same call.  Rows of h or W that do not
  * start on 16 bytes are first copied into the work memory.
  * status (device int32): sticky, first error wins, SG_ERR_TIMEOUT where a
  * bounded wait gave up and the outputs are not complete; the caller clears it.
