@@ -66,6 +66,17 @@ constexpr int kBN = 256;                 // tile columns
 constexpr uint32_t kBox = 8192;          // one TMA box: 64 rows of 128 bytes
 constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's outputs on their way: two boxes of 32 x 32
 constexpr int kJoinThreads = 128;
+// K blocks that are summed in the tensor cores' accumulator alone.  It rounds each
+// step's sum toward zero, which takes about 6e-9 of a sum of terms of one sign for
+// each of them (in one sum, dW of 2^17 rows was 7.6e-4 too small, of 2^20 rows
+// 6e-3).  Longer sums are taken in parts, which are added in fp32, rounded to
+// nearest.  dW, whose terms may well have one sign, in parts of 16384 rows: 1e-4,
+// half of fp16's rounding (40000 x 1024 x 60000 bf16 backward: 11.75 ms, 11.45
+// in one sum).  dh, whose terms have the signs of a column of W, in parts of at
+// most 65536 labels (with 16384, 777 x 1000 x 50021 backward takes 253 us, not
+// 234).
+constexpr int kDwBlocks = 256, kDhBlocks = 1024;
+constexpr int kMaxSplit = 64;            // parts of dh's K
 constexpr int kBand = 16;                // row tiles that walk the vocabulary together
 
 template <int CG>
@@ -80,7 +91,9 @@ struct Cfg {
     static constexpr int C = kSMs / CG;            // clusters
 };
 
-enum Mode { kLse = 0, kProb = 1, kGrad = 2 };
+// kGradLong: kGrad whose dW sums, of more than kDwBlocks K blocks, are taken in parts
+enum Mode { kLse = 0, kProb = 1, kGrad = 2, kGradLong = 3 };
+constexpr bool is_grad(int mode) { return mode >= kGrad; }
 
 struct CeCtl {
     uint64_t full[6], empty[6], tfull[2], tempty[2];
@@ -113,8 +126,10 @@ struct CeArgs {
     int32_t nh;           // tiles along H
     int32_t dh_tiles, dh_split, dh_kb, dh_each, dh_hi;  // tiles, pieces of K, K blocks; units of a cluster
     int32_t dw_tiles, dw_hi, dw_lo, dw_nk;
+    int32_t dw_segs;      // parts of a dW tile's K
     int32_t first;        // the piece is the first: dh sums start from zero
     float *acc;           // dh sums, [unit][CTA][column / 4][128 rows][4]
+    float *dw_acc;        // the same of a cluster's dW tile, where dw_segs > 1
     uint16_t *dW;         // where dW's rows do not suit TMA, else NULL
     int64_t lddW;
     int32_t *status;
@@ -122,7 +137,7 @@ struct CeArgs {
 
 struct Tile {
     int kind;  // 0: logits, 1: dh, 2: dW
-    int m0, n0, k0, nk, unit;
+    int m0, n0, k0, nk, unit, seg;
 };
 
 // tile i of cluster c
@@ -130,7 +145,7 @@ template <int CG, int MODE>
 __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
 {
     constexpr int C = Cfg<CG>::C, BM = Cfg<CG>::BM;
-    if constexpr (MODE != kGrad) {
+    if constexpr (!is_grad(MODE)) {
         // bands of kBand row tiles; inside a band the row tile runs fastest,
         // so W is read from memory once for a band
         const uint32_t l = (uint32_t)i * C + c;
@@ -150,6 +165,7 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
     } else {
         const uint32_t hi = a.dh_hi;  // clusters below it have one dh unit more
         const uint32_t mine = a.dh_each + ((uint32_t)c < hi ? 1 : 0);
+        constexpr bool LONG = MODE == kGradLong;
         if ((uint32_t)i < mine) {
             const uint32_t u = (uint32_t)i * C + c, s = u / (uint32_t)a.dh_tiles, x = u - s * a.dh_tiles;
             const uint32_t m = x / (uint32_t)a.nh;
@@ -161,7 +177,7 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
             t.unit = u;
             return true;
         }
-        const uint32_t j = (uint32_t)i - mine;
+        const uint32_t jj = (uint32_t)i - mine, segs = LONG ? a.dw_segs : 1, j = LONG ? jj / segs : jj;
         // dW tiles in turn over the clusters; those with one dh unit more take
         // only the first dw_hi turns
         uint32_t l;
@@ -180,6 +196,11 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
         t.k0 = 0;
         t.nk = a.dw_nk;
         t.unit = 0;
+        if (LONG) {
+            t.seg = (int)(jj - j * segs);
+            t.k0 = (int)((int64_t)a.dw_nk * t.seg / a.dw_segs);
+            t.nk = (int)((int64_t)a.dw_nk * (t.seg + 1) / a.dw_segs) - t.k0;
+        }
         return true;
     }
 }
@@ -301,6 +322,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     using K = Cfg<CG>;
     constexpr int NS = K::NS;
     constexpr int KE = F8 ? 128 : 64;  // elements of a K block
+    constexpr bool LONG = MODE == kGradLong;
     __shared__ CeCtl c;
     __shared__ float sm_top[kEpiWarps];
     extern __shared__ uint8_t dsm[];
@@ -357,7 +379,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 // one loop for each product: the thread has some 500 cycles
                 // for a K block
                 uint32_t bar;
-                if (MODE != kGrad) {
+                if (!is_grad(MODE)) {
                     const int bh = a.bw / 2;  // with two CTAs, B's rows of one; else half of them
                     const int bn = a.v0 + t.n0 + rank * bh;
                     const uint32_t bytes = CG * 128 * (an * ab + a.bw / CG), a2 = ab * 128, b2 = bh * 128;
@@ -391,7 +413,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 } else {
                     const int bn = t.n0 + rank * 128;
                     const uint32_t bytes = CG * 128 * (2 + K::BRows / 64) * kt;
-                    for (int k = 0; k < t.nk * KE; k += KE, r.next(NS)) {
+                    for (int k = LONG ? t.k0 * KE : 0, k1 = k + t.nk * KE; k < k1; k += KE, r.next(NS)) {
                         const uint32_t st = stage(bytes, &bar);
                         if (!ok)
                             break;
@@ -423,7 +445,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 if (t.nk == 0)
                     continue;
                 const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
-                const int bn = MODE == kGrad ? kBN : a.bw;
+                const int bn = is_grad(MODE) ? kBN : a.bw;
                 const uint32_t idesc =
                     F8 || a.f16 ? idesc_f16(K::BM, bn, a_mn, b_mn) : idesc_bf16(K::BM, bn, a_mn, b_mn);
                 const OpDesc da(base, a_mn), db(base + K::kA, b_mn);
@@ -443,7 +465,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         const uint32_t st = (uint32_t)r.i * (K::kStage / 16);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
-                            if (MODE == kGrad && CG == 1 && a_mn && ks * 16 >= a.kt)
+                            if (is_grad(MODE) && CG == 1 && a_mn && ks * 16 >= a.kt)
                                 break;
                             mma_cg<CG, F8>(tbase + buf * kBN, da.at(st, ks), db.at(st, ks), idesc,
                                            (kb > 0 || ks > 0) ? 1u : 0u);
@@ -470,7 +492,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         [[maybe_unused]] float scale = 1.f;
         if constexpr (MODE == kProb)
             scale = g_scale(a, sm_top);
-        if constexpr (MODE == kGrad)
+        if constexpr (is_grad(MODE))
             scale = a.gscale[1];
         int it = 0;
         for (int i = 0; tile_at<CG, MODE>(a, cl, i, t); ++i) {
@@ -478,13 +500,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 continue;
             const int buf = it & 1;
             const int row = t.m0 + row_in;              // row of the tile's A operand
-            const int cols = MODE == kGrad ? kBN / 2 : a.bw / 2;  // of this warp, and the first of them
+            const int cols = is_grad(MODE) ? kBN / 2 : a.bw / 2;  // of this warp, and the first of them
             const int col0 = t.n0 + half * cols;
             const uint32_t tm = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kBN + half * cols);
             // what the row needs, before the wait
             int tgt = -1;
             [[maybe_unused]] float cf = 0.f, l2 = 0.f, hs = 1.f;
-            if constexpr (MODE != kGrad) {
+            if constexpr (!is_grad(MODE)) {
                 if (row < a.T) {
                     const int y = a.targets[row];
                     const bool live = is_live(a, y);
@@ -597,9 +619,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     out(u, cc + 32);
                 }
             } else {
+                // a thread's place among the sums of its unit or tile
+                const int mine = (half * (kBN / 8)) * 128 + q * 32 + lane;
                 if (t.kind == 1) {
                     float4 *acc = reinterpret_cast<float4 *>(a.acc) +
-                                  ((int64_t)(t.unit * CG + rank) * (kBN / 4) + half * (kBN / 8)) * 128 + q * 32 + lane;
+                                  (int64_t)(t.unit * CG + rank) * (kBN / 4) * 128 + mine;
                     auto out = [&](const float (&v)[32], int cc) {
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
@@ -621,7 +645,26 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     }
                 } else {
                     const int64_t row0 = (int64_t)a.v0 + t.m0 + rank * 128 + q * 32;  // the warp's first row of dW
-                    auto out = [&](const float (&v)[32], int cc) {
+                    const bool done = !LONG || t.seg == a.dw_segs - 1;
+                    auto out = [&](float (&v)[32], int cc) {
+                        if constexpr (LONG) {
+                            float4 *acc = reinterpret_cast<float4 *>(a.dw_acc) +
+                                          (int64_t)(cl * CG + rank) * (kBN / 4) * 128 + mine + (cc / 4) * 128;
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                if (t.seg > 0) {
+                                    const float4 o = acc[x * 128];
+                                    v[4 * x] += o.x;
+                                    v[4 * x + 1] += o.y;
+                                    v[4 * x + 2] += o.z;
+                                    v[4 * x + 3] += o.w;
+                                }
+                                if (!done)
+                                    acc[x * 128] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                            }
+                            if (!done)
+                                return;
+                        }
                         uint32_t w[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
@@ -923,7 +966,7 @@ struct Plan {
     int64_t dh_nn = 0, dh_tiles = 0, split = 1;
     // byte offsets
     int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_run = 0, o_zrun = 0;
-    int64_t o_gs = 0, o_g = 0, o_acc = 0, bytes = 0;
+    int64_t o_gs = 0, o_g = 0, o_acc = 0, o_dw = 0, bytes = 0;
 };
 
 bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
@@ -1023,20 +1066,24 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     int64_t Vc = (256ll << 20) / 2 / T / kBN * kBN;
     if (Vc < kBN)
         Vc = kBN;
+    if (Vc > kMaxSplit * kDhBlocks * 64)
+        Vc = kMaxSplit * kDhBlocks * 64;
     if (Vc > ceil_div(V, kBN) * kBN)
         Vc = ceil_div(V, kBN) * kBN;
     p->Vc = Vc;
     p->dh_nn = ceil_div(H, kBN);
     p->dh_tiles = p->nm * p->dh_nn;
-    // split K of dh until its units and the dW tiles fill the clusters evenly
+    // split K of dh until its units and the dW tiles fill the clusters evenly,
+    // and into parts of at most kDhBlocks
     const int64_t kb = ceil_div(V < Vc ? V : Vc, 64), dw = ceil_div(Vc, p->BM) * p->dh_nn * tile_cost(ceil_div(T, 64), p->CG);
     double best = 0;
-    for (int64_t n = 1; n <= kb && n <= 64; ++n) {
+    const int64_t least = ceil_div(kb, kDhBlocks);
+    for (int64_t n = least; n <= kb && n <= kMaxSplit; ++n) {
         const int64_t units = p->dh_tiles * n, cost = tile_cost(ceil_div(kb, n), p->CG) + 2;
         const double even = (double)(units * cost + dw) / p->C;
         const double last = (double)(ceil_div(units, p->C) * cost);
         const double span = (even > last ? even : last) * (1.0 + 0.002 * (double)n);
-        if (n == 1 || span < best) {
+        if (n == least || span < best) {
             best = span;
             p->split = n;
         }
@@ -1044,6 +1091,8 @@ void make_plan(const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, 
     p->o_gs = take(8);
     p->o_g = take(T * Vc * 2);
     p->o_acc = take(p->dh_tiles * p->split * p->BM * kBN * 4);
+    if (ceil_div(T, 64) > kDwBlocks)
+        p->o_dw = take((int64_t)p->C * p->BM * kBN * 4);
 }
 
 sg_status check_ce(const char *fn, const void *h, int64_t ldh, int64_t T, int64_t H, const void *W, int64_t ldw,
@@ -1278,7 +1327,9 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
     a.dh_split = (int32_t)p.split;
     a.dh_tiles = dh ? (int32_t)p.dh_tiles : 0;
     a.dw_nk = (int32_t)ceil_div(T, 64);
+    a.dw_segs = (int32_t)ceil_div(a.dw_nk, kDwBlocks);
     a.acc = reinterpret_cast<float *>(w8 + p.o_acc);
+    a.dw_acc = reinterpret_cast<float *>(w8 + p.o_dw);
     a.dW = dW && !dw_tma ? static_cast<uint16_t *>(dW) : nullptr;
     a.lddW = lddw;
     a.status = status;
@@ -1303,8 +1354,11 @@ sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_t H, co
             q_hi = 0;
         a.dw_hi = (int32_t)q_hi;
         a.dw_lo = (int32_t)(q_hi + ceil_div(a.dw_tiles - q_hi * p.C > 0 ? a.dw_tiles - q_hi * p.C : 0, p.C - hi));
-        CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st))
-                         : (launch_ce<2, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st)));
+        if (a.dw_segs > 1)  // more than 128 rows: pairs
+            CE_TRY((launch_ce<2, kGradLong, false>(mhk, mWk, mg, mgk, mdW, a, true, st)));
+        else
+            CE_TRY(p.CG == 1 ? (launch_ce<1, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st))
+                             : (launch_ce<2, kGrad, false>(mhk, mWk, mg, mgk, mdW, a, true, st)));
     }
     if (dh) {
         const int parts = p.split >= 8 ? 4 : 1;

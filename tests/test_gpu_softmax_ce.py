@@ -596,3 +596,71 @@ def test_what_work_memory_holds_does_not_matter(size):
         got.append(out)
     for a, b in zip(*got):
         assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+def gradients64(h, W, y, lse, dloss, smoothing, rows, labels):
+    """dh, dW in 64 bits on the device, in pieces of that many rows and labels,
+    and their sums with the absolute values of g's parts."""
+    T, V = h.shape[0], W.shape[0]
+    dh, dhm = (torch.zeros(h.shape, dtype=torch.float64, device="cuda") for _ in range(2))
+    dW, dWm = (torch.zeros(W.shape, dtype=torch.float64, device="cuda") for _ in range(2))
+    for t0 in range(0, T, rows):
+        t = slice(t0, t0 + rows)
+        hd, yt = h[t].double(), y[t].long()
+        c = torch.where(yt >= 0, dloss[t].double(), 0.0)[:, None]
+        for v0 in range(0, V, labels):
+            v = slice(v0, v0 + labels)
+            w = W[v].double()
+            p = torch.exp(hd @ w.t() - lse[t][:, None])
+            hit = torch.zeros_like(p)
+            here = (yt >= v0) & (yt < v0 + labels)
+            hit.scatter_(1, (yt - v0).clamp(0, p.shape[1] - 1)[:, None], here.double()[:, None] * (1 - smoothing))
+            g, mag = (p - hit - smoothing / V) * c, (p + hit + smoothing / V) * c
+            dh[t] += g @ w
+            dW[v] += g.t() @ hd
+            dhm[t] += mag @ w.abs()
+            dWm[v] += mag.t() @ hd.abs()
+    return dh, dW, dhm, dWm
+
+
+def test_weight_gradients_of_very_many_rows():
+    """Sums of 2^21 products of one sign.  The tensor cores' accumulator rounds
+    toward zero, by 2^-24 of the sum so far on average for a step of 16 of them;
+    the sum so far is half the sum on average: 2^-13 where 65536 are summed
+    there (fewer are), 2^-8 if all of them were."""
+    T, H, V, targets = (1 << 21) + 77, 64, 100, 5
+    h, W = rand(T, H, "f16", 1).abs(), rand(V, H, "f16", 2, 2.0 / np.sqrt(H))
+    y = draw_targets(T, targets, 3)
+    loss, lse, dloss = (torch.full((T,), 64.0 / T, device="cuda") for _ in range(3))
+    dh, dW, status = torch.empty_like(h), torch.empty_like(W), torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sg_softmax_ce_fwd(h, W, y, loss, lse, status=status)
+    sg.sg_softmax_ce_bwd(h, W, y, lse, dloss, dh, dW, status=status)
+    _, lse64, e = forward64(h, W, y, 0.0)
+    want_h, want, mag_h, mag = gradients64(h, W, y, lse64, dloss, 0.0, 1 << 18, V)
+    assert int(status) == 0
+    rest = 2 * float(e.max()) + 3e-5
+    err = (dW.double() - want)[targets:].norm() / want[targets:].norm()
+    assert float(err) <= U["f16"] + rest + 2.0 ** -13
+    # dh is below f16's normal numbers: half its smallest step
+    err, least = (dh.double() - want_h).norm(), LEAST["f16"] * np.sqrt(want_h.numel())
+    assert float(err) <= U["f16"] * float(want_h.norm()) + rest * float(mag_h.norm()) + least
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 64, 4861730), (300, 1024, 417619), (1000, 2048, 136845)])
+def test_feature_gradients_of_long_sums(T, H, V):
+    """More than 65536 labels to a piece of dh's sum; the last size with a second
+    piece of the vocabulary."""
+    h, W = rand(T, H, "f16", 1), rand(V, H, "f16", 2, 2.0 / np.sqrt(H))
+    y = draw_targets(T, V, 3, 0.0)
+    loss, lse, dloss = (torch.full((T,), 1.0 / T, device="cuda") for _ in range(3))
+    dh, dW, status = torch.empty_like(h), torch.empty_like(W), torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sg_softmax_ce_fwd(h, W, y, loss, lse, smoothing=0.1, status=status)
+    sg.sg_softmax_ce_bwd(h, W, y, lse, dloss, dh, dW, smoothing=0.1, status=status)
+    _, lse64, e = forward64(h, W, y, 0.1)
+    want_h, want_W, mag_h, mag_W = gradients64(h, W, y, lse64, dloss, 0.1, T, 1 << 16)
+    assert int(status) == 0
+    rest = 2 * float(e.max()) + 3e-5 + 2.0 ** -13
+    for got, want, mag in ((dh, want_h, mag_h), (dW, want_W, mag_W)):
+        # an element of dW may be below f16's normal numbers
+        bound = U["f16"] * want.norm() + rest * mag.norm() + LEAST["f16"] * np.sqrt(want.numel())
+        assert float((got.double() - want).norm()) <= float(bound)
