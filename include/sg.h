@@ -482,7 +482,9 @@ SG_API sg_status sg_add_rmsnorm_bwd(const void *dy, int64_t lddy, const void *u,
  *   may be NULL.  lse is what sg_softmax_ce_fwd wrote for the same h and W.
  * fp32 accumulation (the tensor cores round their sums toward zero: about 6e-9
  * of a sum of terms of one sign for each, which is why dW is summed in parts of
- * 16384 rows and dh in parts of 65536 labels), sums and statistics in fp32.  g enters the products of dh
+ * 16384 rows and dh in parts of 65536 labels; a logit is one such sum, and lse of
+ * ordinary 16-bit rows is off by about 5e-10 H of it), sums and statistics in
+ * fp32.  g enters the products of dh
  * and dW in dtype, times a factor that suits its largest element, by the dloss
  * of the rows that have a gradient (taken out of the fp32 sums).  The results are the same bits for the same call.  Rows of h or W that do not
  * start on 16 bytes are first copied into the work memory.

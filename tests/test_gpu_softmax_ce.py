@@ -664,3 +664,12 @@ def test_feature_gradients_of_long_sums(T, H, V):
         # an element of dW may be below f16's normal numbers
         bound = U["f16"] * want.norm() + rest * mag.norm() + LEAST["f16"] * np.sqrt(want.numel())
         assert float((got.double() - want).norm()) <= float(bound)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", [(1, 1600, 300), (20, 2048, 5000), (100, 4096, 1300), (128, 1544, 3001), (130, 2048, 9753),
+                                  (300, 3080, 2500), (700, 5000, 777), (9, 1601, 1000), (200, 2049, 600)], ids=str)
+def test_many_features(size, dtype):
+    T, H, V = size
+    h, W = rand(T, H, dtype, 1), rand(V, H, dtype, 2, 2.0 / np.sqrt(H))
+    check(h, W, draw_targets(T, V, 3), torch.rand(T, device="cuda") + 0.5, dtype, 0.1)
