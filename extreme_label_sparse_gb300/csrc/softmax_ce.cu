@@ -30,17 +30,11 @@
 // Keeping g for a second use in the L2 cache, with both gradients trailing the
 // logits inside one launch, was not faster than two launches over pieces of the
 // vocabulary (128 x 768 x 131072: 137 to 166 us): a CTA's own turns then add up.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <cmath>
 
 #include "launch.cuh"
-#include "tc_common.cuh"
-#include "tc_ptx.cuh"
-
-using namespace tc;
+#include "tc_tile.cuh"
 
 namespace {
 
@@ -63,8 +57,6 @@ constexpr int kSMs = 152;
 constexpr int kEpiWarps = 8;
 constexpr int kCeThreads = 32 * (kEpiWarps + 2);
 constexpr int kBN = 256;                 // tile columns
-constexpr uint32_t kBox = 8192;          // one TMA box: 64 rows of 128 bytes
-constexpr uint32_t kStgWarp = 4096;      // an epilogue warp's outputs on their way: two boxes of 32 x 32
 constexpr int kJoinThreads = 128;
 // K blocks that are summed in the tensor cores' accumulator alone.  It rounds each
 // step's sum toward zero, which takes about 6e-9 of a sum of terms of one sign for
@@ -205,59 +197,11 @@ __device__ __forceinline__ bool tile_at(const CeArgs &a, int c, int i, Tile &t)
     }
 }
 
-// Descriptors of an operand's tile at shared address `base`: the low word, to
-// which stages (bytes / 16) and K steps are added, the high word, and the step.
-// K-major: rows of 128 bytes of K, 8 rows to a swizzle atom.  MN-major: boxes
-// of 64 rows (128 bytes) by 64 K, kBox apart.  Worked out once for a tile: the
-// thread that issues the MMAs has little time for each.
-struct OpDesc {
-    uint32_t lo, hi, step;
-
-    __device__ __forceinline__ OpDesc(uint32_t base, bool mn)
-    {
-        const uint64_t d = sdesc(base, mn ? kBox : 16, 1024, kLayoutSW128);
-        lo = (uint32_t)d;
-        hi = (uint32_t)(d >> 32);
-        step = mn ? 2048 / 16 : 32 / 16;
-    }
-    __device__ __forceinline__ uint64_t at(uint32_t stage, int ks) const
-    {
-        return (uint64_t)hi << 32 | (lo + stage + ks * step);
-    }
-};
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16)
-{
-    return f16 ? pack2_f16(a, b) : pack2(a, b);
-}
-
-// 32 columns (16 packed words) of this warp's 32 rows to global memory by TMA,
-// from one of its two boxes while the other is filled: rows of 64 bytes, their
-// 16-byte units swizzled.  Lane 0 issues the store, if `in`.
-__device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, bool in, uint8_t *box, int lane,
-                                          const uint32_t (&w)[16])
-{
-    if (lane == 0)
-        bulk_wait_read<1>();
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) {
-        if (in)
-            tma_store_2d(map, x, y, smem_u32(box));
-        bulk_commit();
-    }
 }
 
 // errors of calls that were given no status word
@@ -901,39 +845,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host
-std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode_ce{nullptr};
-
-// row-major matrix in boxes of box_rows x 128 bytes, 128-byte swizzle;
-// `narrow`: 64 bytes, 64-byte swizzle
-sg_status map_of(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int elem,
-                 const char *what, uint32_t box_rows = 64, bool narrow = false)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 enc = g_encode_ce.load(std::memory_order_acquire);
-    if (!enc) {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess || !fn) {
-            cudaGetLastError();
-            CE_FAIL(SG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-        }
-        enc = (PFN_cuTensorMapEncodeTiled_v12000)fn;
-        g_encode_ce.store(enc, std::memory_order_release);
-    }
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
-    cuuint32_t box[2] = {(narrow ? 64u : 128u) / (uint32_t)elem, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = enc(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
-                           const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        CE_FAIL(SG_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
-    return SG_OK;
-}
-
 template <int CG, int MODE, bool F8>
 sg_status launch_ce(const CUtensorMap &h, const CUtensorMap &W, const CUtensorMap &g, const CUtensorMap &gk,
                     const CUtensorMap &dW, const CeArgs &a, bool after, cudaStream_t st)
@@ -968,8 +879,6 @@ struct Plan {
     int64_t o_h = 0, o_W = 0, o_part = 0, o_zsum = 0, o_ztgt = 0, o_run = 0, o_zrun = 0;
     int64_t o_gs = 0, o_g = 0, o_acc = 0, o_dw = 0, bytes = 0;
 };
-
-bool tma_ok(const void *p, int64_t ld, int64_t es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
 
 // Time of a tile or dh unit of nk K blocks, in half K blocks: a tile that is
 // shorter than its output takes to reach memory (2 K blocks of a CTA, 4 of a
