@@ -17,5 +17,6 @@ from .sg import (  # noqa: F401
     sg_grouping_kmeans_init, sg_grouping_set_centroids, sg_grouping_kmeans_batch, sg_grouping_groups,
     sg_grouping_export, sg_rewire, SG_BF16, SG_F16, SG_F32, SG_E4M3, sg_dropout, sg_add_rmsnorm_fwd,
     sg_add_rmsnorm_bwd, sg_add_rmsnorm_bwd_work, sg_softmax_ce_work, sg_softmax_ce_status, sg_softmax_ce_fwd,
-    sg_softmax_ce_bwd, sg_timing_start, sg_timing_stop, last_error, status_string, KIND_NAMES,
+    sg_softmax_ce_bwd, sg_pack8, sg_unpack8, sg_block_norm_fwd, sg_block_norm_bwd, sg_block_norm_bwd_work,
+    sg_linear8_work, sg_linear8_status, sg_linear8_fwd, sg_linear8_bwd, sg_timing_start, sg_timing_stop, last_error, status_string, KIND_NAMES,
 )

@@ -400,7 +400,8 @@ sg_status sg_device_status(int32_t *code)
             return SG_OK;
         }
     }
-    return sg_softmax_ce_status(code, 0);
+    const sg_status rc = sg_softmax_ce_status(code, 0);
+    return rc != SG_OK || *code != SG_OK ? rc : sg_linear8_status(code, 0);
 }
 
 // ---------------------------------------------------------------- positives

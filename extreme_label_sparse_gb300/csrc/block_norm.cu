@@ -1,0 +1,699 @@
+// The norms before and after a block, fused with its gate and the residual's
+// scale (definitions in include/sg.h):
+//   v = x rx post,  u = alpha residual + gate v,  y = u ru pre
+// and the gradient through both.  Bound by memory: a row lies in the registers
+// of one CTA (forward) or in shared memory (backward) between its two sums and
+// their uses, so each input is read once and each output written once.
+#include <cmath>
+
+#include "norm.cuh"
+#include "quant8.cuh"
+
+namespace {
+
+constexpr int64_t kMaxBlockCols = 16384;
+
+struct BlockFwd {
+    const void *x, *res, *post, *gate, *pre;
+    void *u, *y;
+    int8_t *y8, *x8, *u8;
+    float *rx, *ru, *y8_scale, *x8_scale, *u8_scale;
+    int64_t ldx, ldr, ldu, ldy, ldy8, ldx8, ldu8, nrows;
+    int cols;
+    float alpha, eps;
+};
+
+constexpr int block_ctas(int warps) { return norm_ctas(warps, true); }
+
+// A row by WARPS warps (one warp: eight rows to a CTA), NV segments to a warp;
+// row groups step over the rows, with the next S rows on their way to shared
+// memory.
+template <typename T, bool VEC, int WARPS, int NV, int S>
+__global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_block_fwd(const BlockFwd a)
+{
+    __shared__ RowSums sm;
+    extern __shared__ uint4 dyn[];
+    const Ring8<T, 2, NV, S, norm_threads(WARPS)> ring(dyn);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int wr = WARPS == 1 ? 0 : warp;
+    const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
+    const int64_t g = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
+    const T *ax = static_cast<const T *>(a.x), *ar = static_cast<const T *>(a.res);
+    const int ng = (a.cols + kGroup - 1) / kGroup;
+    auto fetch = [&](int64_t r, int slot) {
+        if constexpr (VEC) {
+            if (r < a.nrows) {
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int c = (n * WARPS + wr) * kSeg + lane * 8;
+                    if (c < a.cols) {
+                        ring.copy(slot, 0, n, ax + r * a.ldx + c);
+                        if (ar)
+                            ring.copy(slot, 1, n, ar + r * a.ldr + c);
+                    }
+                }
+            }
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        fetch(g + i * groups, i);
+    Pack8<T> post[NV], gate[NV], pre[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c0 = (n * WARPS + wr) * kSeg;
+        post[n] = load8<T, VEC>(static_cast<const T *>(a.post), c0, lane, a.cols);
+        pre[n] = load8<T, VEC>(static_cast<const T *>(a.pre), c0, lane, a.cols);
+        if (a.gate) {
+            gate[n] = load8<T, VEC>(static_cast<const T *>(a.gate), c0, lane, a.cols);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                gate[n].v[j] = from_f<T>(1.f);
+        }
+    }
+    int turn = 0, slot = 0;
+    for (int64_t r = g; r < a.nrows; r += groups, turn += 2) {
+        Pack8<T> p[NV];  // x, then u
+        float ss = 0.f, none = 0.f;
+        if constexpr (VEC)
+            copies_wait<S - 1>();
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c0 = (n * WARPS + wr) * kSeg;
+            if (c0 >= a.cols)
+                break;  // the whole warp: neither has a later segment columns of it
+            float v[8];
+            if constexpr (VEC) {
+                if (c0 + lane * 8 < a.cols)
+                    p[n] = ring.get(slot, 0, n);
+                else
+                    p[n] = pack8<T>({});
+            } else {
+                p[n] = load8<T, VEC>(ax + r * a.ldx, c0, lane, a.cols);
+            }
+            unpack8(p[n], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss = fmaf(v[j], v[j], ss);
+            if (a.x8)
+                store_groups<VEC>(a.x8 + r * a.ldx8, a.x8_scale + r * ng, c0, lane, a.cols, v);
+        }
+        row_reduce<WARPS, false>(ss, none, sm, turn);
+        const float rx = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+        ss = 0.f;
+        uint32_t most = 0;  // of |u pre|
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c0 = (n * WARPS + wr) * kSeg;
+            if (c0 >= a.cols)
+                break;
+            float v[8], w[8];
+            unpack8(p[n], v);
+            if (ar) {
+                Pack8<T> t;
+                if constexpr (VEC) {
+                    if (c0 + lane * 8 < a.cols)
+                        t = ring.get(slot, 1, n);
+                    else
+                        t = pack8<T>({});
+                } else {
+                    t = load8<T, VEC>(ar + r * a.ldr, c0, lane, a.cols);
+                }
+                unpack8(t, w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = fmaf(v[j] * rx * to_f(post[n].v[j]), to_f(gate[n].v[j]), ar ? a.alpha * w[j] : 0.f);
+            // the second norm is taken of the sum as it is stored, so that the
+            // backward pass sees the same row
+            p[n] = pack8<T>(v);
+            unpack8(p[n], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ss = fmaf(v[j], v[j], ss);
+                most = max(most, mag(v[j] * to_f(pre[n].v[j])));
+            }
+            if (a.u)
+                store8<T, VEC>(static_cast<T *>(a.u) + r * a.ldu, c0, lane, a.cols, p[n]);
+            if (a.u8)
+                store_groups<VEC>(a.u8 + r * a.ldu8, a.u8_scale + r * ng, c0, lane, a.cols, v);
+        }
+        fetch(r + S * groups, slot);
+        slot = slot + 1 == S ? 0 : slot + 1;
+        float top = __uint_as_float(min(most, 0x7f800000u));  // NaN as infinity, which stays the largest
+        row_reduce<WARPS, true>(ss, top, sm, turn + 1);
+        const float ru = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+        if (lane == 0 && wr == 0) {
+            if (a.rx)
+                a.rx[r] = rx;
+            if (a.ru)
+                a.ru[r] = ru;
+        }
+        // max |y| without a third reduction: ru max |u pre|; a row whose sum is
+        // not finite has neither scale nor values
+        const Scale8 s8 = scale8_of(mag(ss < INFINITY ? top * ru : NAN));
+        if (a.y8 && lane == 0 && wr == 0)
+            a.y8_scale[r] = s8.scale;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c0 = (n * WARPS + wr) * kSeg;
+            if (c0 >= a.cols)
+                break;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] = (to_f(p[n].v[j]) * ru) * to_f(pre[n].v[j]);
+            if (a.y)
+                store8<T, VEC>(static_cast<T *>(a.y) + r * a.ldy, c0, lane, a.cols, pack8<T>(y));
+            if (a.y8)
+                store8q<VEC>(a.y8 + r * a.ldy8, c0, lane, a.cols, quant8(y, s8.inv));
+        }
+    }
+}
+
+struct BlockBwd {
+    const void *dy, *u, *x, *du_in, *post, *gate, *pre;
+    const float *u_scale, *x_scale, *rx, *ru;
+    void *dres, *dx;
+    float *part;  // [row groups][2][cols]: sums of dy m and of du h; or NULL
+    int64_t lddy, ldu, ldx, ldi, ldo, lddx, nrows;
+    int cols;
+    float alpha;
+};
+
+// A thread's pieces of the next rows on their way to shared memory, as Ring8:
+// dy and du_in, and x and u, or (HELD) their eight bytes in one unit and their
+// scales in another.
+template <typename T, bool HELD, int NV, int S, int THREADS>
+struct BackRing {
+    static constexpr int P = sizeof(Pack8<T>) / 16;
+    static constexpr int kUnits = HELD ? 2 * P + 2 : 4 * P;
+    static constexpr int kBytes = S * NV * kUnits * THREADS * 16;
+    uint4 *base;
+
+    __device__ __forceinline__ explicit BackRing(void *smem) : base(static_cast<uint4 *>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ uint4 *at(int slot, int n, int unit) const
+    {
+        return base + ((slot * NV + n) * kUnits + unit) * THREADS;
+    }
+    // m: 0 dy, 1 du_in, 2 x, 3 u
+    __device__ __forceinline__ void copy(int slot, int n, int m, const T *src) const
+    {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint32_t dst = tc::smem_u32(at(slot, n, m * P + i));
+            if constexpr (P == 2)
+                tc::cp_async16_l1(dst, reinterpret_cast<const uint4 *>(src) + i);
+            else
+                tc::cp_async16(dst, reinterpret_cast<const uint4 *>(src) + i);
+        }
+    }
+    // m: 0 x, 1 u
+    __device__ __forceinline__ void copy8(int slot, int n, int m, const int8_t *src, const float *scale) const
+    {
+        const uint32_t d = tc::smem_u32(at(slot, n, 2 * P)) + m * 8, s = tc::smem_u32(at(slot, n, 2 * P + 1)) + m * 4;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(scale) : "memory");
+    }
+    __device__ __forceinline__ void get(int slot, int n, int m, float (&v)[8]) const
+    {
+        Pack8<T> p;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            reinterpret_cast<uint4 *>(&p)[i] = *at(slot, n, m * P + i);
+        unpack8(p, v);
+    }
+    __device__ __forceinline__ void get8(int slot, int n, int m, float (&v)[8]) const
+    {
+        unquant8(reinterpret_cast<const uint2 *>(at(slot, n, 2 * P))[m], v);
+        const float s = reinterpret_cast<const float *>(at(slot, n, 2 * P + 1))[m];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] *= s;
+    }
+};
+
+// Row groups of WARPS warps step over the rows; a thread keeps the two sums of
+// its columns in registers until its last row, and the groups' sums are joined
+// by k_block_dw.
+template <typename T, bool VEC, bool HELD, int WARPS, int NV, int S>
+__global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_block_bwd(const BlockBwd a)
+{
+    __shared__ RowSums sm;
+    extern __shared__ uint4 dyn[];
+    const BackRing<T, HELD, NV, S, norm_threads(WARPS)> ring(dyn);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int wr = WARPS == 1 ? 0 : warp;
+    const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
+    const int64_t g = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
+    const int ng = (a.cols + kGroup - 1) / kGroup;
+    tc::grid_go();
+    const T *ady = static_cast<const T *>(a.dy), *ai = static_cast<const T *>(a.du_in);
+    auto fetch = [&](int64_t r, int slot) {
+        if constexpr (VEC) {
+            if (r < a.nrows) {
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int c = (n * WARPS + wr) * kSeg + lane * 8;
+                    if (c < a.cols) {
+                        ring.copy(slot, n, 0, ady + r * a.lddy + c);
+                        if (ai)
+                            ring.copy(slot, n, 1, ai + r * a.ldi + c);
+                        if constexpr (HELD) {
+                            ring.copy8(slot, n, 0, static_cast<const int8_t *>(a.x) + r * a.ldx + c,
+                                       a.x_scale + r * ng + c / kGroup);
+                            ring.copy8(slot, n, 1, static_cast<const int8_t *>(a.u) + r * a.ldu + c,
+                                       a.u_scale + r * ng + c / kGroup);
+                        } else {
+                            ring.copy(slot, n, 2, static_cast<const T *>(a.x) + r * a.ldx + c);
+                            ring.copy(slot, n, 3, static_cast<const T *>(a.u) + r * a.ldu + c);
+                        }
+                    }
+                }
+            }
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        fetch(g + i * groups, i);
+    Pack8<T> post[NV], gate[NV], pre[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c0 = (n * WARPS + wr) * kSeg;
+        post[n] = load8<T, VEC>(static_cast<const T *>(a.post), c0, lane, a.cols);
+        pre[n] = load8<T, VEC>(static_cast<const T *>(a.pre), c0, lane, a.cols);
+        if (a.gate) {
+            gate[n] = load8<T, VEC>(static_cast<const T *>(a.gate), c0, lane, a.cols);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                gate[n].v[j] = from_f<T>(1.f);
+        }
+    }
+    float dpre[NV][8] = {}, dh[NV][8] = {};
+    int turn = 0, slot = 0;
+    float next_u = g < a.nrows ? a.ru[g] : 0.f, next_x = g < a.nrows ? a.rx[g] : 0.f;
+    for (int64_t r = g; r < a.nrows; r += groups, turn += 2) {
+        const float ru = next_u, rx = next_x;
+        if (r + groups < a.nrows) {
+            next_u = a.ru[r + groups];
+            next_x = a.rx[r + groups];
+        }
+        // the row's values of this lane, again for each use (from shared memory,
+        // or, without VEC, from the caches)
+        auto dy_of = [&](int n, int c0, float (&v)[8]) {
+            if constexpr (VEC)
+                ring.get(slot, n, 0, v);
+            else
+                unpack8(load8<T, VEC>(ady + r * a.lddy, c0, lane, a.cols), v);
+        };
+        auto u_of = [&](int n, int c0, float (&v)[8]) {
+            if constexpr (VEC && HELD)
+                ring.get8(slot, n, 1, v);
+            else if constexpr (VEC)
+                ring.get(slot, n, 3, v);
+            else if constexpr (HELD)
+                load_groups<VEC>(static_cast<const int8_t *>(a.u) + r * a.ldu, a.u_scale + r * ng, c0, lane, a.cols, v);
+            else
+                unpack8(load8<T, VEC>(static_cast<const T *>(a.u) + r * a.ldu, c0, lane, a.cols), v);
+        };
+        auto x_of = [&](int n, int c0, float (&v)[8]) {
+            if constexpr (VEC && HELD)
+                ring.get8(slot, n, 0, v);
+            else if constexpr (VEC)
+                ring.get(slot, n, 2, v);
+            else if constexpr (HELD)
+                load_groups<VEC>(static_cast<const int8_t *>(a.x) + r * a.ldx, a.x_scale + r * ng, c0, lane, a.cols, v);
+            else
+                unpack8(load8<T, VEC>(static_cast<const T *>(a.x) + r * a.ldx, c0, lane, a.cols), v);
+        };
+        float dot = 0.f, none = 0.f;
+        if constexpr (VEC)
+            copies_wait<S - 1>();
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c0 = (n * WARPS + wr) * kSeg;
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;  // and neither has a later segment columns of this thread
+            float dy[8], u[8];
+            dy_of(n, c0, dy);
+            u_of(n, c0, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float t = dy[j] * u[j];
+                dpre[n][j] = fmaf(t, ru, dpre[n][j]);
+                dot = fmaf(t, to_f(pre[n].v[j]), dot);
+            }
+        }
+        row_reduce<WARPS, false>(dot, none, sm, turn);
+        // as in the norm's own gradient: neither a square of u nor one of its
+        // factor without the other, so that rows of any scale stay in range
+        const float back_u = dot / (float)a.cols * ru * ru;
+        float du[NV][8];
+        dot = 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c0 = (n * WARPS + wr) * kSeg;
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;
+            float t[8], v[8];
+            if (ai) {
+                if constexpr (VEC)
+                    ring.get(slot, n, 1, v);
+                else
+                    unpack8(load8<T, VEC>(ai + r * a.ldi, c0, lane, a.cols), v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = 0.f;
+            }
+            u_of(n, c0, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = fmaf(-back_u, t[j] * ru, v[j]);
+            dy_of(n, c0, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                du[n][j] = v[j] = fmaf(to_f(pre[n].v[j]) * ru, t[j], v[j]);
+            x_of(n, c0, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = du[n][j] * t[j];
+                dh[n][j] = fmaf(d, rx, dh[n][j]);
+                dot = fmaf(d, to_f(post[n].v[j]) * to_f(gate[n].v[j]), dot);
+                v[j] *= a.alpha;
+            }
+            if (a.dres)
+                store8<T, VEC>(static_cast<T *>(a.dres) + r * a.ldo, c0, lane, a.cols, pack8<T>(v));
+        }
+        row_reduce<WARPS, false>(dot, none, sm, turn + 1);
+        const float back_x = dot / (float)a.cols * rx * rx;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c0 = (n * WARPS + wr) * kSeg;
+            if (VEC && c0 + lane * 8 >= a.cols)
+                break;
+            float v[8];
+            x_of(n, c0, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = fmaf(to_f(post[n].v[j]) * to_f(gate[n].v[j]) * rx, du[n][j], -back_x * (v[j] * rx));
+            store8<T, VEC>(static_cast<T *>(a.dx) + r * a.lddx, c0, lane, a.cols, pack8<T>(v));
+        }
+        fetch(r + S * groups, slot);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    if (a.part) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = col_of<VEC>((n * WARPS + wr) * kSeg, lane, j);
+                if (c < a.cols) {
+                    a.part[g * 2 * (int64_t)a.cols + c] = dpre[n][j];
+                    a.part[(g * 2 + 1) * (int64_t)a.cols + c] = dh[n][j];
+                }
+            }
+    }
+}
+
+// The column sums joined in a fixed order, as k_norm_dw: blockIdx.y 0 for dpre, 1
+// for S = sum of du h, of which dpost = gate S and dgate = post S.
+template <typename T, int NC>
+__global__ void __launch_bounds__(1024)
+    k_block_dw(const float *__restrict__ part, int nparts, int64_t cols, const T *__restrict__ post,
+               const T *__restrict__ gate, float *__restrict__ dpost, float *__restrict__ dgate,
+               float *__restrict__ dpre)
+{
+    __shared__ float sm[32][NC];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t c = (int64_t)blockIdx.x * NC + lane % NC;
+    float s = 0.f;
+    tc::grid_wait();
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = threadIdx.x / NC; i < nparts; i += 1024 / NC)
+            s += part[(2 * i + blockIdx.y) * cols + c];
+    }
+#pragma unroll
+    for (int o = NC; o < 32; o *= 2)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane < NC)
+        sm[warp][lane] = s;
+    __syncthreads();
+    if (threadIdx.x < NC && c < cols) {
+        s = 0.f;
+        for (int i = 0; i < 32; ++i)
+            s += sm[i][lane];
+        if (blockIdx.y == 0) {
+            if (dpre)
+                dpre[c] = s;
+        } else {
+            if (dpost)
+                dpost[c] = s * (gate ? to_f(gate[c]) : 1.f);
+            if (dgate)
+                dgate[c] = s * to_f(post[c]);
+        }
+    }
+}
+
+#define BLOCK_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(32, 2)
+
+template <typename T, bool VEC, int W, int N>
+sg_status run_fwd(const BlockFwd &a, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr int S = VEC ? ring_rows<T, 2, W, N>(block_ctas(W)) : 1;
+    constexpr int smem = VEC ? Ring8<T, 2, N, S, norm_threads(W)>::kBytes : 0;
+    const int64_t need = W == 1 ? ceil_div(a.nrows, 8) : a.nrows, most = kSMs * block_ctas(W);
+    NORM_TRY(allow_smem(k_block_fwd<T, VEC, W, N, S>, smem, done));
+    k_block_fwd<T, VEC, W, N, S><<<(unsigned)(need < most ? need : most), norm_threads(W), smem, st>>>(a);
+    return SG_OK;
+}
+
+template <typename T, bool HELD, int W, int N>
+constexpr int back_rows()
+{
+    const int s = (216 << 10) / block_ctas(W) / BackRing<T, HELD, N, 1, norm_threads(W)>::kBytes;
+    return s > 4 ? 4 : s < 1 ? 1 : s;
+}
+
+template <typename T, bool VEC, bool HELD, int W, int N>
+sg_status run_bwd(const BlockBwd &a, int64_t grid, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr int S = VEC ? back_rows<T, HELD, W, N>() : 1;
+    constexpr int smem = VEC ? BackRing<T, HELD, N, S, norm_threads(W)>::kBytes : 0;
+    if constexpr (smem > 226 << 10) {  // fp32 rows above 8192 columns: not one is held
+        return run_bwd<T, false, HELD, W, N>(a, grid, st);
+    } else {
+        NORM_TRY(allow_smem(k_block_bwd<T, VEC, HELD, W, N, S>, smem, done));
+        k_block_bwd<T, VEC, HELD, W, N, S><<<(unsigned)grid, norm_threads(W), smem, st>>>(a);
+        return SG_OK;
+    }
+}
+
+template <typename T, bool VEC>
+sg_status launch_fwd(const BlockFwd &a, cudaStream_t st)
+{
+#define X(W, N)                             \
+    if (a.cols <= (int64_t)(W) * (N) * kSeg) \
+        return run_fwd<T, VEC, W, N>(a, st);
+    BLOCK_SHAPES(X)
+#undef X
+    return SG_ERR_UNSUPPORTED;  // not reached: cols <= kMaxBlockCols
+}
+
+template <typename T, bool VEC, bool HELD>
+sg_status launch_bwd(const BlockBwd &a, int64_t grid, cudaStream_t st)
+{
+#define X(W, N)                             \
+    if (a.cols <= (int64_t)(W) * (N) * kSeg) \
+        return run_bwd<T, VEC, HELD, W, N>(a, grid, st);
+    BLOCK_SHAPES(X)
+#undef X
+    return SG_ERR_UNSUPPORTED;  // not reached: cols <= kMaxBlockCols
+}
+
+// CTAs of the backward kernel, and the row groups they make
+int64_t bwd_groups(int64_t nrows, int64_t cols, int64_t *grid)
+{
+    int warps = 0;
+#define X(W, N)                                          \
+    if (warps == 0 && cols <= (int64_t)(W) * (N) * kSeg) \
+        warps = (W);
+    BLOCK_SHAPES(X)
+#undef X
+    const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * block_ctas(warps);
+    *grid = need < most ? need : most;
+    return warps == 1 ? *grid * 8 : *grid;
+}
+
+template <typename T>
+sg_status backward(const BlockBwd &a, bool vec, int64_t grid, int64_t groups, float *dpost, float *dgate, float *dpre,
+                   cudaStream_t st)
+{
+    if (a.u_scale)
+        NORM_TRY((vec ? launch_bwd<T, true, true>(a, grid, st) : launch_bwd<T, false, true>(a, grid, st)));
+    else
+        NORM_TRY((vec ? launch_bwd<T, true, false>(a, grid, st) : launch_bwd<T, false, false>(a, grid, st)));
+    SG_TRY_CUDA(cudaGetLastError());
+    if (!a.part)
+        return SG_OK;
+    const bool few = a.cols < 2048;
+    return launch(few ? k_block_dw<T, 8> : k_block_dw<T, 32>, dim3((unsigned)ceil_div(a.cols, few ? 8 : 32), 2), 1024,
+                  0, 1, true, st, (const float *)a.part, (int)groups, (int64_t)a.cols, static_cast<const T *>(a.post),
+                  static_cast<const T *>(a.gate), dpost, dgate, dpre);
+}
+
+sg_status check_block(const char *fn, int64_t nrows, int64_t cols, int32_t dtype, const void *post, const void *gate,
+                      const void *pre, double residual_scale)
+{
+    NORM_TRY(check_rows(fn, nrows, cols, dtype));
+    if (cols > kMaxBlockCols)
+        NORM_FAIL(SG_ERR_UNSUPPORTED, "%s: cols=%lld is above %lld", fn, (long long)cols, (long long)kMaxBlockCols);
+    if (!post || !pre)
+        NORM_FAIL(SG_ERR_INVALID, "%s: a weight is NULL (post_weight, pre_weight)", fn);
+    if (!std::isfinite((float)residual_scale))
+        NORM_FAIL(SG_ERR_INVALID, "%s: residual_scale=%g is not a finite fp32 number", fn, residual_scale);
+    const int64_t es = elem_size(dtype);
+    NORM_TRY(check_mat(fn, "post_weight", post, cols, cols, es));
+    NORM_TRY(check_mat(fn, "gate", gate, cols, cols, es));
+    return check_mat(fn, "pre_weight", pre, cols, cols, es);
+}
+
+}  // namespace
+
+extern "C" {
+
+sg_status sg_block_norm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows, int64_t cols,
+                            int32_t dtype, const void *post_weight, const void *gate, const void *pre_weight,
+                            double residual_scale, double eps, void *u, int64_t ldu, float *rstd_x, float *rstd_u,
+                            void *y, int64_t ldy, int8_t *y8, int64_t ldy8, float *y8_scale, int8_t *x8, int64_t ldx8,
+                            float *x8_scale, int8_t *u8, int64_t ldu8, float *u8_scale, void *stream)
+{
+    const char *fn = "sg_block_norm_fwd";
+    NvtxRange nvtx_(fn);
+    NORM_TRY(check_block(fn, rows, cols, dtype, post_weight, gate, pre_weight, residual_scale));
+    if (rows && (!x || (!y && !y8)))
+        NORM_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL (x, y or y8)", fn);
+    if (rows && ((y8 && !y8_scale) || (x8 && !x8_scale) || (u8 && !u8_scale)))
+        NORM_FAIL(SG_ERR_INVALID, "%s: 8-bit rows need their scales", fn);
+    if (!(eps >= 0.0) || !std::isfinite(eps))
+        NORM_FAIL(SG_ERR_INVALID, "%s: eps=%g is not a finite number >= 0", fn, eps);
+    const int64_t es = elem_size(dtype);
+    NORM_TRY(check_mat(fn, "x", x, ldx, cols, es));
+    NORM_TRY(check_mat(fn, "residual", residual, ldr, cols, es));
+    NORM_TRY(check_mat(fn, "u", u, ldu, cols, es));
+    NORM_TRY(check_mat(fn, "y", y, ldy, cols, es));
+    NORM_TRY(check_mat(fn, "y8", y8, ldy8, cols, 1));
+    NORM_TRY(check_mat(fn, "x8", x8, ldx8, cols, 1));
+    NORM_TRY(check_mat(fn, "u8", u8, ldu8, cols, 1));
+    NORM_TRY(check_vec(fn, "rstd_x", rstd_x));
+    NORM_TRY(check_vec(fn, "rstd_u", rstd_u));
+    NORM_TRY(check_vec(fn, "y8_scale", y8_scale));
+    NORM_TRY(check_vec(fn, "x8_scale", x8_scale));
+    NORM_TRY(check_vec(fn, "u8_scale", u8_scale));
+    if (rows == 0)
+        return SG_OK;
+    BlockFwd a;
+    a.x = x, a.res = residual, a.post = post_weight, a.gate = gate, a.pre = pre_weight, a.u = u, a.y = y;
+    a.y8 = y8, a.x8 = x8, a.u8 = u8, a.rx = rstd_x, a.ru = rstd_u;
+    a.y8_scale = y8_scale, a.x8_scale = x8_scale, a.u8_scale = u8_scale;
+    a.ldx = ldx, a.ldr = ldr, a.ldu = ldu, a.ldy = ldy, a.ldy8 = ldy8, a.ldx8 = ldx8, a.ldu8 = ldu8;
+    a.nrows = rows, a.cols = (int)cols, a.alpha = (float)residual_scale, a.eps = (float)eps;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool vec = cols % 8 == 0 && vec_ok(x, ldx, es) && vec_ok(residual, ldr, es) && vec_ok(post_weight, cols, es) &&
+                     vec_ok(gate, cols, es) && vec_ok(pre_weight, cols, es) && vec_ok(u, ldu, es) &&
+                     vec_ok(y, ldy, es) && vec8_ok(y8, ldy8) && vec8_ok(x8, ldx8) && vec8_ok(u8, ldu8);
+    if (dtype == SG_BF16)
+        NORM_TRY((vec ? launch_fwd<__nv_bfloat16, true>(a, st) : launch_fwd<__nv_bfloat16, false>(a, st)));
+    else if (dtype == SG_F16)
+        NORM_TRY((vec ? launch_fwd<__half, true>(a, st) : launch_fwd<__half, false>(a, st)));
+    else
+        NORM_TRY((vec ? launch_fwd<float, true>(a, st) : launch_fwd<float, false>(a, st)));
+    SG_TRY_CUDA(cudaGetLastError());
+    return SG_OK;
+}
+
+sg_status sg_block_norm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes)
+{
+    const char *fn = "sg_block_norm_bwd_work";
+    if (!bytes)
+        NORM_FAIL(SG_ERR_INVALID, "%s: bytes is NULL", fn);
+    NORM_TRY(check_rows(fn, rows, cols, SG_F32));
+    if (cols > kMaxBlockCols)
+        NORM_FAIL(SG_ERR_UNSUPPORTED, "%s: cols=%lld is above %lld", fn, (long long)cols, (long long)kMaxBlockCols);
+    int64_t grid;
+    *bytes = bwd_groups(rows, cols, &grid) * 2 * cols * 4;
+    return SG_OK;
+}
+
+sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, int64_t ldu, const float *u_scale,
+                            const void *x, int64_t ldx, const float *x_scale, const void *du_in, int64_t lddu_in,
+                            int64_t rows, int64_t cols, int32_t dtype, const void *post_weight, const void *gate,
+                            const void *pre_weight, double residual_scale, const float *rstd_x, const float *rstd_u,
+                            void *dresidual, int64_t lddr, void *dx, int64_t lddx, float *dpost, float *dgate,
+                            float *dpre, void *work, int64_t work_bytes, void *stream)
+{
+    const char *fn = "sg_block_norm_bwd";
+    NvtxRange nvtx_(fn);
+    NORM_TRY(check_block(fn, rows, cols, dtype, post_weight, gate, pre_weight, residual_scale));
+    if (rows && (!dy || !u || !x || !rstd_x || !rstd_u || !dx))
+        NORM_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL (dy, u, x, rstd_x, rstd_u, dx)", fn);
+    if (!u_scale != !x_scale)
+        NORM_FAIL(SG_ERR_INVALID, "%s: x and u are both held in 8 bits, with their scales, or neither", fn);
+    if (dgate && !gate)
+        NORM_FAIL(SG_ERR_INVALID, "%s: dgate without a gate", fn);
+    const int64_t es = elem_size(dtype), hs = u_scale ? 1 : es;
+    NORM_TRY(check_mat(fn, "dy", dy, lddy, cols, es));
+    NORM_TRY(check_mat(fn, "u", u, ldu, cols, hs));
+    NORM_TRY(check_mat(fn, "x", x, ldx, cols, hs));
+    NORM_TRY(check_mat(fn, "du_in", du_in, lddu_in, cols, es));
+    NORM_TRY(check_mat(fn, "dresidual", dresidual, lddr, cols, es));
+    NORM_TRY(check_mat(fn, "dx", dx, lddx, cols, es));
+    NORM_TRY(check_vec(fn, "u_scale", u_scale));
+    NORM_TRY(check_vec(fn, "x_scale", x_scale));
+    NORM_TRY(check_vec(fn, "rstd_x", rstd_x));
+    NORM_TRY(check_vec(fn, "rstd_u", rstd_u));
+    NORM_TRY(check_vec(fn, "dpost", dpost));
+    NORM_TRY(check_vec(fn, "dgate", dgate));
+    NORM_TRY(check_vec(fn, "dpre", dpre));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 0) {
+        for (float *d : {dpost, dgate, dpre})
+            if (d)
+                SG_TRY_CUDA(cudaMemsetAsync(d, 0, (size_t)cols * 4, st));
+        return SG_OK;
+    }
+    int64_t grid;
+    const int64_t groups = bwd_groups(rows, cols, &grid), need = groups * 2 * cols * 4;
+    const bool sums = dpost || dgate || dpre;
+    if (sums && (!work || work_bytes < need || ((uintptr_t)work) % 4 != 0))
+        NORM_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_block_norm_bwd_work), aligned to 4", fn,
+                  (long long)need);
+    BlockBwd a;
+    a.dy = dy, a.u = u, a.x = x, a.du_in = du_in, a.post = post_weight, a.gate = gate, a.pre = pre_weight;
+    a.u_scale = u_scale, a.x_scale = x_scale, a.rx = rstd_x, a.ru = rstd_u, a.dres = dresidual, a.dx = dx;
+    a.part = sums ? static_cast<float *>(work) : nullptr;
+    a.lddy = lddy, a.ldu = ldu, a.ldx = ldx, a.ldi = lddu_in, a.ldo = lddr, a.lddx = lddx;
+    a.nrows = rows, a.cols = (int)cols, a.alpha = (float)residual_scale;
+    const bool held_ok = u_scale ? vec8_ok(u, ldu) && vec8_ok(x, ldx) : vec_ok(u, ldu, es) && vec_ok(x, ldx, es);
+    const bool vec = cols % 8 == 0 && held_ok && vec_ok(dy, lddy, es) && vec_ok(du_in, lddu_in, es) &&
+                     vec_ok(post_weight, cols, es) && vec_ok(gate, cols, es) && vec_ok(pre_weight, cols, es) &&
+                     vec_ok(dresidual, lddr, es) && vec_ok(dx, lddx, es);
+    if (dtype == SG_BF16)
+        return backward<__nv_bfloat16>(a, vec, grid, groups, dpost, dgate, dpre, st);
+    if (dtype == SG_F16)
+        return backward<__half>(a, vec, grid, groups, dpost, dgate, dpre, st);
+    return backward<float>(a, vec, grid, groups, dpost, dgate, dpre, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,938 @@
+// Linear layer on 8-bit integers with a scale for each token and each channel,
+// and its gradients (definitions in include/sg.h):
+//   out[t][n] = xs[t] ws[n] sum_h x8[t][h] W8[n][h],
+//   dx = dout (ws W8),  dW = dout^T (xs x8).
+// The integer rate of this chip's tensor cores is far below their 16-bit rate,
+// and a product of 16-bit operands loses nothing: an int8 is exact in fp16, a
+// product of two is below 2^14, and a sum of 1024 of them at most 2^24, exact in
+// an fp32 accumulator.  So the operands are brought to 16 bits first, and after
+// 1024 terms an accumulator is added to fp32 sums in registers, rounded to
+// nearest (the tensor cores' own sums round toward zero), while the next terms
+// go into the other one.
+//
+// One kernel for the three products: a persistent CTA, or a pair of CTAs on one
+// 256 x 256 tile where there are more than 128 tokens, walks a list of tiles.  A
+// producer warp streams K blocks of 64 through a ring of shared-memory stages
+// (TMA, 128-byte swizzle), one thread issues tcgen05.mma into one of two TMEM
+// accumulators, and eight warps take the sums of the other one.  Products of few
+// tiles are split along K, their parts joined in a fixed order.
+#include <cmath>
+#include <utility>
+
+#include "launch.cuh"
+#include "quant8.cuh"
+#include "tc_tile.cuh"
+
+namespace {
+
+#define LIN_FAIL(code, ...)        \
+    do {                           \
+        sg_set_error(__VA_ARGS__); \
+        return code;               \
+    } while (0)
+#define LIN_TRY(expr)           \
+    do {                        \
+        sg_status rc_ = (expr); \
+        if (rc_ != SG_OK)       \
+            return rc_;         \
+    } while (0)
+
+constexpr int kSMs = 152;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kBN = 256;      // tile columns
+constexpr int kDrain = 16;    // K blocks summed in a TMEM accumulator: 1024 terms
+
+template <int CG>
+struct Cfg {
+    static constexpr int BM = 128 * CG;  // tile rows
+    static constexpr int BRows = kBN / CG;
+    static constexpr uint32_t kA = 2 * kBox;  // bytes of A's and B's part of a stage
+    static constexpr uint32_t kB = (BRows / 64) * kBox;
+    static constexpr uint32_t kStage = kA + kB;
+    static constexpr int NS = CG == 2 ? 6 : 4;
+    static constexpr uint32_t kSmem = NS * kStage + kEpiWarps * kStgWarp + 1024;
+    static constexpr int C = kSMs / CG;  // clusters
+};
+
+// out = A B^T: operands stored with K along their rows, or (mn) with K rows
+struct Prod {
+    int32_t a_mn, b_mn;
+    int32_t M, N;            // of the output
+    int32_t mt, nt, nk;      // tiles, K blocks
+    int32_t split, units;    // parts of K; tiles times parts
+    int32_t f16;             // operands are fp16, not bf16
+    int32_t otype;           // sg_dtype of the output
+    void *out;               // where its rows do not suit TMA, else NULL
+    int64_t ldo;
+    const float *rs, *cs;    // factors of its rows and columns, or NULL
+    const float *inv;        // factor of all, or NULL
+    float *acc;              // parts, [unit][CTA][column / 4][128 rows][4], where split > 1
+};
+
+struct LinCtl {
+    uint64_t full[6], empty[6], tfull[2], tempty[2];
+    uint32_t tmem;
+    int abort_flag;
+};
+
+struct LinArgs {
+    Prod p[2];
+    // units of the first product in turn over the clusters, `each` to each and
+    // one more to the first `hi`, which take only b_hi turns of the second's
+    int32_t each, hi, b_hi, b_lo;
+    int32_t ab, an;  // rows of a box of A by its rows, and boxes
+    int32_t kt;      // rows of a box whose rows are K, where those are the tokens
+    int32_t *status;
+};
+
+// errors of calls that were given no status word
+__device__ int32_t g_linear_status;
+
+__device__ __forceinline__ int32_t *lin_status(int32_t *status) { return status ? status : &g_linear_status; }
+
+struct Unit {
+    int which, m0, n0, k0, nk, id;
+};
+
+// unit i of cluster c
+template <int CG>
+__device__ __forceinline__ bool unit_at(const LinArgs &a, int c, int i, Unit &t)
+{
+    constexpr int C = Cfg<CG>::C, BM = Cfg<CG>::BM;
+    const int mine = a.each + (c < a.hi ? 1 : 0);
+    uint32_t u;
+    t.which = i >= mine;
+    if (i < mine) {
+        u = (uint32_t)i * C + c;
+    } else {
+        const int j = i - mine;
+        if (j < a.b_hi)
+            u = (uint32_t)j * C + c;
+        else if (j < a.b_lo && c >= a.hi)
+            u = (uint32_t)a.b_hi * C + (uint32_t)(j - a.b_hi) * (C - a.hi) + (c - a.hi);
+        else
+            return false;
+    }
+    const Prod &p = a.p[t.which];
+    if (u >= (uint32_t)p.units)
+        return false;
+    // the parts of K run slowest, the row tiles fastest inside bands of 16 of
+    // them: what the clusters read at one time stays in the L2 cache
+    const uint32_t tiles = (uint32_t)p.mt * p.nt, s = u / tiles;
+    uint32_t x = u - s * tiles;
+    const uint32_t per = 16u * p.nt, b = x / per;
+    x -= b * per;
+    const uint32_t mc = min(16u, p.mt - b * 16), n = x / mc;
+    t.m0 = (int)(b * 16 + (x - n * mc)) * BM;
+    t.n0 = (int)n * kBN;
+    t.k0 = (int)((int64_t)s * p.nk / p.split);
+    t.nk = (int)((int64_t)(s + 1) * p.nk / p.split) - t.k0;
+    t.id = (int)u;
+    return true;
+}
+
+// 16 packed words (32 columns of 16 bits, or 16 of 32) of this warp's 32 rows
+// where their rows may start anywhere: through shared memory, so that a warp
+// writes pieces of rows
+template <int SIZE>
+__device__ __forceinline__ void store_rows(const Prod &p, int row0, int x0, uint8_t *stg, int lane,
+                                           const uint32_t (&w)[16])
+{
+    uint32_t *rows = reinterpret_cast<uint32_t *>(stg);
+    if (lane == 0)
+        bulk_wait_read<0>();  // the other product's outputs may go by store_box
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+        rows[lane * 17 + x] = w[x];
+    __syncwarp();
+    if constexpr (SIZE == 2) {
+        for (int r = 0; r < 32 && row0 + r < p.M; ++r)
+            if (x0 + lane < p.N)
+                static_cast<uint16_t *>(p.out)[(row0 + r) * p.ldo + x0 + lane] =
+                    (uint16_t)(rows[r * 17 + lane / 2] >> (16 * (lane & 1)));
+    } else {
+        for (int r = lane / 16; r < 32 && row0 + r < p.M; r += 2)
+            if (x0 + (lane & 15) < p.N)
+                static_cast<uint32_t *>(p.out)[(row0 + r) * p.ldo + x0 + (lane & 15)] = rows[r * 17 + (lane & 15)];
+    }
+}
+
+template <int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear(const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mB0,
+             const __grid_constant__ CUtensorMap mO0, const __grid_constant__ CUtensorMap mA1,
+             const __grid_constant__ CUtensorMap mB1, const __grid_constant__ CUtensorMap mO1,
+             const __grid_constant__ LinArgs a)
+{
+    using K = Cfg<CG>;
+    constexpr int NS = K::NS;
+    __shared__ LinCtl c;
+    extern __shared__ uint8_t dsm[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)cluster_rank() : 0;
+    const int cl = (int)blockIdx.x / CG;
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        c.abort_flag = 0;
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&c.full[s]), 1);
+            mbar_init(smem_u32(&c.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c.tfull[b]), 1);
+            mbar_init(smem_u32(&c.tempty[b]), CG * kEpiWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kEpiWarps + 1) {
+        tmem_alloc_cg<CG>(smem_u32(&c.tmem), 512);
+        tmem_relinquish_cg<CG>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();
+    tc_fence_after();
+    grid_wait();
+    grid_go();
+    const uint32_t tbase = c.tmem;
+    volatile int *abort_flag = &c.abort_flag;
+    int32_t *status = lin_status(a.status);
+    Unit t;
+
+    if (warp == kEpiWarps) {
+        // ---------------------------------------------------------- producer
+        if (lane == 0) {
+            Ring r;
+            bool ok = true;
+            for (int i = 0; ok && unit_at<CG>(a, cl, i, t); ++i) {
+                const Prod &p = a.p[t.which];
+                const CUtensorMap *mA = t.which ? &mA1 : &mA0, *mB = t.which ? &mB1 : &mB0;
+                const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
+                // a pair has more than 128 rows: whole boxes
+                const int ab = CG == 2 ? 64 : a.ab, an = CG == 2 ? 2 : a.an, kt = CG == 2 || !p.a_mn ? 64 : a.kt;
+                const uint32_t bytes = CG * 128 * ((p.a_mn ? 2 * kt : an * ab) + K::BRows / 64 * (p.b_mn ? kt : 64));
+                for (int k = t.k0 * 64, k1 = k + t.nk * 64; k < k1; k += 64, r.next(NS)) {
+                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status);
+                    if (!ok)
+                        break;
+                    uint32_t bar = smem_u32(&c.full[r.i]);
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(bar, bytes);
+                    if constexpr (CG == 2)
+                        bar = mapa(bar, 0);
+                    const uint32_t st = base + (uint32_t)r.i * K::kStage;
+                    if (p.a_mn) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_2d_cg<CG>(st + j * kBox, mA, am + 64 * j, k, bar);
+                    } else {
+                        tma_load_2d_cg<CG>(st, mA, k, am, bar);
+                        if (an == 2)
+                            tma_load_2d_cg<CG>(st + ab * 128, mA, k, am + ab, bar);
+                    }
+#pragma unroll
+                    for (int j = 0; j < K::BRows / 64; ++j)
+                        tma_load_2d_cg<CG>(st + K::kA + j * kBox, mB, p.b_mn ? bn + 64 * j : k, p.b_mn ? k : bn + 64 * j,
+                                           bar);
+                }
+            }
+            if (!ok) {
+                // gave up: copies may still be on their way into this CTA (and
+                // signal the pair's first CTA); they land long before this
+                const uint64_t t0 = global_ns();
+                while (global_ns() - t0 < 1000000u) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kEpiWarps + 1) {
+        // ---------------------------------------------------------- MMA
+        if (rank == 0) {
+            Ring r;
+            int it = 0;
+            bool ok = true;
+            for (int i = 0; ok && unit_at<CG>(a, cl, i, t); ++i) {
+                const Prod &p = a.p[t.which];
+                const uint32_t idesc =
+                    p.f16 ? idesc_f16(K::BM, kBN, p.a_mn, p.b_mn) : idesc_bf16(K::BM, kBN, p.a_mn, p.b_mn);
+                const OpDesc da(base, p.a_mn), db(base + K::kA, p.b_mn);
+                const int kt = CG == 2 || !p.a_mn ? 64 : a.kt;
+                for (int kb = 0; ok && kb < t.nk; ++it) {
+                    const int buf = it & 1, end = min(t.nk, kb + kDrain);
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tempty[buf]),
+                                                                   ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, status));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    for (int k0 = kb; kb < end; ++kb) {
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait_cluster(smem_u32(&c.full[r.i]), r.ph, abort_flag, status));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint32_t st = (uint32_t)r.i * (K::kStage / 16);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) {
+                                if (CG == 1 && ks * 16 >= kt)
+                                    break;
+                                mma_cg<CG, false>(tbase + buf * kBN, da.at(st, ks), db.at(st, ks), idesc,
+                                                  (kb > k0 || ks > 0) ? 1u : 0u);
+                            }
+                            mma_commit_cg<CG>(smem_u32(&c.empty[r.i]));
+                        }
+                        __syncwarp();
+                        r.next(NS);
+                    }
+                    if (ok && lane == 0)
+                        mma_commit_cg<CG>(smem_u32(&c.tfull[buf]));
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue
+        // a warp reads its quarter of the TMEM lanes (tile rows) and one half
+        // of the tile's columns; a thread has one row, whose 128 sums it holds
+        const int q = warp & 3, half = warp >> 2;
+        uint8_t *stg = dsm + (base - smem_u32(dsm)) + NS * K::kStage + warp * kStgWarp;
+        int it = 0, box = 0;
+        bool ok = true;
+        for (int i = 0; ok && unit_at<CG>(a, cl, i, t); ++i) {
+            const Prod &p = a.p[t.which];
+            const int row0 = t.m0 + rank * 128 + q * 32, col0 = t.n0 + half * (kBN / 2);  // the warp's first
+            float v[4][32];
+            for (int kb = 0; kb < t.nk; kb += kDrain, ++it) {
+                const int buf = it & 1;
+                const uint32_t tm = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kBN + half * (kBN / 2));
+                ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&c.tfull[buf]), (uint32_t)(it >> 1) & 1u,
+                                                               abort_flag, status));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (kb == 0) {
+                    tmem_ld_chunk2<32>(tm, tm + 32, v[0], v[1]);
+                    tmem_ld_chunk2<32>(tm + 64, tm + 96, v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float w[16];
+                            tmem_ld_chunk<16>(tm + cc * 32 + h * 16, w);
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                v[cc][16 * h + x] += w[x];
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&c.tempty[buf]);
+                    // the accumulator's values are in registers already
+                    // (wait::ld): nothing in memory has to be visible with this
+                    if constexpr (CG == 2)
+                        mbar_arrive_remote_relaxed(mapa(bar, 0));
+                    else
+                        mbar_arrive(bar);
+                }
+            }
+            if (!ok)
+                break;
+            if (p.split > 1) {
+                float4 *acc = reinterpret_cast<float4 *>(p.acc) + ((int64_t)t.id * CG + rank) * (kBN / 4) * 128 +
+                              half * (kBN / 8) * 128 + q * 32 + lane;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        acc[(cc * 8 + x) * 128] =
+                            make_float4(v[cc][4 * x], v[cc][4 * x + 1], v[cc][4 * x + 2], v[cc][4 * x + 3]);
+                continue;
+            }
+            const CUtensorMap *mO = t.which ? &mO1 : &mO0;
+            float rs = p.inv ? *p.inv : 1.f;
+            if (p.rs)
+                rs = row0 + lane < p.M ? p.rs[row0 + lane] : 0.f;
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                const int x0 = col0 + cc * 32;
+                if (p.cs) {
+                    const float mine = x0 + lane < p.N ? p.cs[x0 + lane] : 0.f;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        v[cc][x] = v[cc][x] * rs * __shfl_sync(0xffffffffu, mine, x);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        v[cc][x] *= rs;
+                }
+                uint32_t w[16];
+                if (p.otype == SG_F32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = __float_as_uint(v[cc][16 * h + x]);
+                        if (p.out)
+                            store_rows<4>(p, row0, x0 + 16 * h, stg, lane, w);
+                        else
+                            store_box(mO, x0 + 16 * h, row0, row0 < p.M && x0 + 16 * h < p.N, stg + (box ^= kStgWarp / 2),
+                                      lane, w);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        w[x] = pack16(v[cc][2 * x], v[cc][2 * x + 1], p.otype == SG_F16);
+                    if (p.out)
+                        store_rows<2>(p, row0, x0, stg, lane, w);
+                    else
+                        store_box(mO, x0, row0, row0 < p.M && x0 < p.N, stg + (box ^= kStgWarp / 2), lane, w);
+                }
+            }
+        }
+        if (lane == 0)
+            bulk_wait<0>();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();
+    if (warp == kEpiWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc_cg<CG>(tbase, 512);
+    }
+}
+
+// ---------------------------------------------------------------- small kernels
+// The parts of a split product, joined in their order: a CTA has 32 rows and 32
+// columns of a tile, a warp four of the columns.
+template <int CG>
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Prod p)
+{
+    __shared__ float rows[32][33];
+    const int lane = threadIdx.x & 31, c4 = threadIdx.x / 32;
+    const uint32_t x = blockIdx.x / (CG * 4), rq = blockIdx.x % (CG * 4);  // tile, 32-row part of it
+    // the tile's place, as in unit_at
+    const uint32_t per = 16u * p.nt, b = x / per, y = x - b * per;
+    const uint32_t mc = min(16u, p.mt - b * 16), n = y / mc;
+    const int row0 = (int)(b * 16 + (y - n * mc)) * Cfg<CG>::BM + rq * 32, col0 = (int)n * kBN + blockIdx.y * 32;
+    grid_wait();
+    if (row0 >= p.M || col0 >= p.N)
+        return;
+    const int64_t step = (int64_t)p.mt * p.nt * CG * (kBN / 4) * 128;
+    const float4 *src = reinterpret_cast<const float4 *>(p.acc) +
+                        (((int64_t)x * CG + rq / 4) * (kBN / 4) + blockIdx.y * 8 + c4) * 128 + (rq & 3) * 32 + lane;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < p.split; ++s) {
+        const float4 o = src[s * step];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+    }
+    rows[lane][c4 * 4] = v.x;
+    rows[lane][c4 * 4 + 1] = v.y;
+    rows[lane][c4 * 4 + 2] = v.z;
+    rows[lane][c4 * 4 + 3] = v.w;
+    __syncthreads();
+    const int col = col0 + lane;
+    if (col >= p.N)
+        return;
+    const float cs = p.cs ? p.cs[col] : p.inv ? *p.inv : 1.f;
+    for (int r = c4; r < 32 && row0 + r < p.M; r += 8) {
+        const float z = rows[r][lane] * (p.rs ? p.rs[row0 + r] : 1.f) * cs;
+        const int64_t at = (row0 + r) * p.ldo + col;
+        if (p.otype == SG_F32)
+            static_cast<float *>(p.out)[at] = z;
+        else if (p.otype == SG_F16)
+            static_cast<__half *>(p.out)[at] = __float2half_rn(z);
+        else
+            static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(z);
+    }
+}
+
+// A power of two that brings the largest of n scales to [256, 512), where the
+// largest value held in 8 bits (127 times it) is still an fp16 number, and its
+// inverse.  CTA 0: the first vector, CTA 1: the second.
+__global__ void __launch_bounds__(1024)
+    k_factor(const float *s0, int64_t n0, float *f0, const float *s1, int64_t n1, float *f1)
+{
+    __shared__ float sm[32];
+    const float *s = blockIdx.x ? s1 : s0;
+    const int64_t n = blockIdx.x ? n1 : n0;
+    float top = 0.f;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        const float v = fabsf(s[i]);
+        if (v < INFINITY)
+            top = fmaxf(top, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0)
+        sm[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 32; ++w)
+            top = fmaxf(top, sm[w]);
+        int e = 0;
+        if (top > 0.f)
+            frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
+        e = top > 0.f ? 9 - e : 0;
+        e = e > 126 ? 126 : e;
+        float *f = blockIdx.x ? f1 : f0;
+        f[0] = ldexpf(1.f, e);
+        f[1] = ldexpf(1.f, -e);
+    }
+}
+
+struct Widen {
+    const int8_t *src;
+    int64_t ld, rows;
+    int32_t cols, group;   // group: columns of a scale, 0: the row's
+    const float *scale;    // NULL: the integers themselves
+    const float *factor;   // of the scales, or NULL
+    uint16_t *dst;
+    int64_t ldd;
+    int32_t f16;
+};
+
+// int8 rows to 16 bits: the integers, or the values they stand for.  A warp
+// takes a row, 16 columns to a lane.
+template <bool VEC>
+__global__ void __launch_bounds__(256) k_widen(const Widen a)
+{
+    const int lane = threadIdx.x & 31;
+    const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
+    grid_wait();
+    grid_go();
+    const float f = a.factor ? *a.factor : 1.f;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows; r += (int64_t)gridDim.x * 8) {
+        const int8_t *src = a.src + r * a.ld;
+        const float *sc = a.scale ? a.scale + r * ng : nullptr;
+        uint16_t *dst = a.dst + r * a.ldd;
+        for (int c = lane * 16; c < a.cols; c += 512) {
+            uint32_t in[4];
+            if (VEC && c + 16 <= a.cols) {
+                *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(src + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    in[i] = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c + 4 * i + j < a.cols)
+                            in[i] |= (uint32_t)(uint8_t)src[c + 4 * i + j] << (8 * j);
+                }
+            }
+            // a group is a whole number of 16 columns
+            const float s = sc ? sc[a.group ? c / a.group : 0] * f : 1.f;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float lo = (float)(int8_t)(in[i / 2] >> (16 * (i & 1)));
+                const float hi = (float)(int8_t)(in[i / 2] >> (16 * (i & 1) + 8));
+                w[i] = pack16(lo * s, hi * s, a.f16);
+            }
+            // ldd is a whole number of eights
+            uint4 *out = reinterpret_cast<uint4 *>(dst + c);
+            out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c + 8 < a.ldd)
+                out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+
+// rows that do not start on 16 bytes, copied to a stride that does
+__global__ void __launch_bounds__(256)
+    k_linear_copy(const uint16_t *__restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t *__restrict__ dst,
+                  int64_t ldd)
+{
+    grid_wait();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int c = threadIdx.x; c < cols; c += 256)
+            dst[r * ldd + c] = src[r * ld + c];
+}
+
+// ---------------------------------------------------------------- host
+template <int CG>
+sg_status launch_linear(const CUtensorMap (&m)[6], const LinArgs &a, cudaStream_t st)
+{
+    // once for each device (one bit of the mask)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    SG_TRY_CUDA(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        SG_TRY_CUDA(cudaFuncSetAttribute(k_linear<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<CG>::kSmem));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    LIN_TRY(launch(k_linear<CG>, dim3(Cfg<CG>::C * CG), kThreads, (int)Cfg<CG>::kSmem, CG, true, st, m[0], m[1], m[2],
+                   m[3], m[4], m[5], a));
+    for (const Prod &p : a.p)
+        if (p.units && p.split > 1)
+            LIN_TRY(launch(k_linear_join<CG>, dim3((unsigned)(p.mt * p.nt * CG * 4), kBN / 32), 256, 0, 1, true, st, p));
+    return SG_OK;
+}
+
+// Time of a unit of nk K blocks, in K blocks: its own, and an end that the
+// other units' work hides in part; a part of a split tile is written, read and
+// joined in fp32.
+double unit_cost(int64_t nk, bool split) { return (double)nk + (split ? 10.0 : 2.0); }
+
+constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 64};
+
+// parts of K of the products (the second may have no tiles) so that the
+// clusters end early
+void choose_splits(Prod &a, Prod &b, int C)
+{
+    const int64_t ta = (int64_t)a.mt * a.nt, tb = (int64_t)b.mt * b.nt;
+    double best = -1;
+    int sa = 1, sb = 1;
+    for (int i : kSplits) {
+        if (i > 1 && (i > a.nk || ta * i > 4 * C))
+            break;
+        for (int j : kSplits) {
+            if (j > 1 && (j > b.nk || tb * j > 4 * C || !tb))
+                break;
+            const double ca = unit_cost(ceil_div(a.nk, i), i > 1), cb = unit_cost(ceil_div(b.nk, j), j > 1);
+            const double na = (double)(ta * i), nb = (double)(tb * j);
+            const double even = (na * ca + nb * cb) / C;
+            // what the longest cluster has of each alone
+            const double la = (double)ceil_div(ta * i, C) * ca, lb = (double)ceil_div(tb * j, C) * cb;
+            double span = even > la ? even : la;
+            if (lb > span)
+                span = lb;
+            span += 0.5 * ((even > la && even > lb) ? (ca > cb ? ca : cb) * 0.3 : 0.0) + (i > 1 ? 2.0 + 0.1 * i : 0) +
+                    (j > 1 ? 2.0 + 0.1 * j : 0);
+            if (best < 0 || span < best) {
+                best = span;
+                sa = i;
+                sb = j;
+            }
+        }
+    }
+    a.split = sa;
+    b.split = sb;
+    a.units = (int32_t)(ta * sa);
+    b.units = (int32_t)(tb * sb);
+}
+
+// turns of the second product's units so that all clusters end at about the
+// same time
+void schedule(LinArgs &a, int C)
+{
+    const int64_t na = a.p[0].units, nb = a.p[1].units, hi = na % C;
+    a.each = (int32_t)(na / C);
+    a.hi = (int32_t)hi;
+    const double ca = unit_cost(ceil_div(a.p[0].nk, a.p[0].split), false);
+    const double cb = nb ? unit_cost(ceil_div(a.p[1].nk, a.p[1].split), false) : 1.0;
+    const int64_t less = (int64_t)ceil(ca / cb);
+    int64_t q = hi ? (nb - less * (C - hi)) / C : 0;
+    if (q < 0)
+        q = 0;
+    a.b_hi = (int32_t)q;
+    const int64_t rest = nb - q * C;
+    a.b_lo = (int32_t)(q + ceil_div(rest > 0 ? rest : 0, C - hi));
+}
+
+constexpr int64_t kPiece = 256ll << 20;  // bytes of W in 16 bits, forward
+
+// One call's tiles and the places of its work memory
+struct Plan {
+    int CG = 1, BM = 128, C = kSMs;
+    int64_t ldh = 0, ldn = 0;  // row strides of the copies
+    int64_t ab = 64, an = 2, kt = 64;
+    int64_t Nc = 0;            // forward: channels of a piece
+    bool copy = false;         // of dout
+    Prod p[2] = {};
+    int64_t o_f = 0, o_x = 0, o_W = 0, o_d = 0, o_acc[2] = {0, 0}, bytes = 0;
+};
+
+void shape(Prod &p, const Plan &pl, int64_t M, int64_t N, int64_t Kd)
+{
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.mt = (int32_t)ceil_div(M, pl.BM);
+    p.nt = (int32_t)ceil_div(N, kBN);
+    p.nk = (int32_t)ceil_div(Kd, 64);
+}
+
+void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, bool backward, bool want_dx,
+               bool want_dW, Plan *p)
+{
+    p->CG = T > 128 ? 2 : 1;
+    p->BM = 128 * p->CG;
+    p->C = kSMs / p->CG;
+    p->ldh = ceil_div(H, 8) * 8;
+    p->ldn = ceil_div(N, 8) * 8;
+    if (T <= 128) {  // boxes of the rows that there are
+        p->an = T <= 64 ? 1 : 2;
+        p->ab = ceil_div(ceil_div(T, p->an), 8) * 8;
+    }
+    if (T < 64)
+        p->kt = ceil_div(T, 16) * 16;
+    auto take = [&](int64_t n) {
+        const int64_t at = p->bytes;
+        p->bytes += ceil_div(n, 256) * 256;
+        return at;
+    };
+    p->o_f = take(16);
+    if (!backward) {
+        int64_t Nc = kPiece / 2 / p->ldh / kBN * kBN;
+        if (Nc < kBN)
+            Nc = kBN;
+        p->Nc = Nc < N ? Nc : N;
+        p->o_x = take(T * p->ldh * 2);
+        p->o_W = take(p->Nc * p->ldh * 2);
+        // the last piece may be split otherwise: room for either
+        int64_t most = 0;
+        for (int64_t n : {p->Nc, N % p->Nc}) {
+            if (n == 0)
+                continue;
+            Prod a = {}, none = {};
+            shape(a, *p, T, n, H);
+            choose_splits(a, none, p->C);
+            const int64_t need = a.split > 1 ? (int64_t)a.units * p->BM * kBN * 4 : 0;
+            most = need > most ? need : most;
+        }
+        p->o_acc[0] = take(most);
+        return;
+    }
+    // dW's units first, as their K is often the longer
+    Prod &w = p->p[0], &x = p->p[1];
+    if (want_dW)
+        shape(w, *p, N, H, T);
+    if (want_dx)
+        shape(x, *p, T, H, N);
+    if (!want_dW)
+        std::swap(w, x);
+    choose_splits(w, x, p->C);
+    p->copy = !tma_ok(dout, ldd, 2);
+    p->o_x = take(want_dW ? T * p->ldh * 2 : 0);
+    p->o_W = take(want_dx ? N * p->ldh * 2 : 0);
+    p->o_d = take(p->copy ? T * p->ldn * 2 : 0);
+    for (int i = 0; i < 2; ++i)
+        p->o_acc[i] = take(p->p[i].split > 1 ? (int64_t)p->p[i].units * p->BM * kBN * 4 : 0);
+}
+
+sg_status widen(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const float *scale, int32_t group,
+                const float *factor, uint8_t *dst, int64_t ldd, bool f16, cudaStream_t st)
+{
+    Widen w = {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16};
+    const bool vec = ((uintptr_t)src & 15) == 0 && ld % 16 == 0;
+    const int64_t need = ceil_div(rows, 8), most = kSMs * 8;
+    return launch(vec ? k_widen<true> : k_widen<false>, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st,
+                  w);
+}
+
+sg_status check_linear(const char *fn, const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
+                       int64_t N)
+{
+    if (T < 0 || H < 1 || N < 1)
+        LIN_FAIL(SG_ERR_INVALID, "%s: need T >= 0, H >= 1 and N >= 1 (T=%lld H=%lld N=%lld)", fn, (long long)T,
+                 (long long)H, (long long)N);
+    // the last: tiles are counted in 31 bits
+    if (T > (1 << 24) || H > (1 << 20) || N > (1 << 24) || ceil_div(T, 128) * ceil_div(N, 256) >= (1ll << 28))
+        LIN_FAIL(SG_ERR_UNSUPPORTED, "%s: T=%lld, H=%lld, N=%lld or T N is above 2^24, 2^20, 2^24 or 2^43", fn,
+                 (long long)T, (long long)H, (long long)N);
+    if (ldx < H || ldw < H)
+        LIN_FAIL(SG_ERR_INVALID, "%s: a row stride (%lld, %lld) is below H=%lld", fn, (long long)ldx, (long long)ldw,
+                 (long long)H);
+    return SG_OK;
+}
+
+// whether vectors of 32-bit elements (any of them may be NULL) are aligned to them
+template <typename... P>
+bool aligned4(const P *...p)
+{
+    return (((uintptr_t)p | ...) & 3) == 0;
+}
+
+// map of an output where TMA can write it (a store ends on a multiple of 16
+// bytes: with other widths it would go past a row's end)
+sg_status out_map(Prod &p, CUtensorMap *m, const CUtensorMap &none, void *out, int64_t ldo, int32_t dtype, const char *name)
+{
+    const int es = dtype == SG_F32 ? 4 : 2;
+    p.otype = dtype;
+    p.ldo = ldo;
+    p.out = out;
+    *m = none;
+    if (p.split > 1 || !tma_ok(out, ldo, es) || (int64_t)p.N * es % 16 != 0)
+        return SG_OK;
+    LIN_TRY(map_of(m, out, p.N, p.M, ldo, es, name, 32, true));
+    p.out = nullptr;
+    return SG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sg_status sg_linear8_status(int32_t *code, int32_t clear)
+{
+    const char *fn = "sg_linear8_status";
+    if (!code)
+        LIN_FAIL(SG_ERR_INVALID, "%s: code is NULL", fn);
+    *code = SG_OK;
+    SG_TRY_CUDA(cudaDeviceSynchronize());
+    SG_TRY_CUDA(cudaMemcpyFromSymbol(code, g_linear_status, sizeof(int32_t)));
+    const int32_t none = SG_OK;
+    if (clear && *code != SG_OK)
+        SG_TRY_CUDA(cudaMemcpyToSymbol(g_linear_status, &none, sizeof(int32_t)));
+    return SG_OK;
+}
+
+sg_status sg_linear8_work(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw, int64_t N,
+                          const void *dout, int64_t lddout, int32_t backward, int64_t *bytes)
+{
+    const char *fn = "sg_linear8_work";
+    if (!bytes)
+        LIN_FAIL(SG_ERR_INVALID, "%s: bytes is NULL", fn);
+    LIN_TRY(check_linear(fn, x8, ldx, T, H, W8, ldw, N));
+    *bytes = 0;
+    if (T == 0)
+        return SG_OK;
+    // backward: either gradient may be left out, which changes the splits
+    for (int i = 0; i < (backward ? 3 : 1); ++i) {
+        Plan p;
+        make_plan(T, H, N, dout, lddout, backward != 0, i != 1, i != 2, &p);
+        *bytes = p.bytes > *bytes ? p.bytes : *bytes;
+    }
+    return SG_OK;
+}
+
+sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, int64_t T, int64_t H, const int8_t *W8,
+                         int64_t ldw, const float *W_scale, int64_t N, void *out, int64_t ldo, int32_t dtype, void *work,
+                         int64_t work_bytes, int32_t *status, void *stream)
+{
+    const char *fn = "sg_linear8_fwd";
+    NvtxRange nvtx_(fn);
+    LIN_TRY(check_linear(fn, x8, ldx, T, H, W8, ldw, N));
+    if (dtype != SG_BF16 && dtype != SG_F16 && dtype != SG_F32)
+        LIN_FAIL(SG_ERR_INVALID, "%s: dtype %d is not SG_BF16, SG_F16 or SG_F32", fn, dtype);
+    if (!W8 || !W_scale || (T && (!x8 || !x_scale || !out)))
+        LIN_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
+    if (!aligned4(x_scale, W_scale, status))
+        LIN_FAIL(SG_ERR_INVALID, "%s: a vector or status is not aligned to its elements", fn);
+    const int64_t es = dtype == SG_F32 ? 4 : 2;
+    if (ldo < N || (uintptr_t)out % es != 0)
+        LIN_FAIL(SG_ERR_INVALID, "%s: out has a row stride below N or is not aligned to its elements", fn);
+    if (T == 0)
+        return SG_OK;
+    Plan pl;
+    make_plan(T, H, N, nullptr, 0, false, false, false, &pl);
+    if (!work || work_bytes < pl.bytes || ((uintptr_t)work & 255) != 0)
+        LIN_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_linear8_work), aligned to 256", fn, (long long)pl.bytes);
+    cudaStream_t st = (cudaStream_t)stream;
+    uint8_t *w8 = static_cast<uint8_t *>(work);
+    LIN_TRY(widen(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true, st));
+    for (int64_t n0 = 0; n0 < N; n0 += pl.Nc) {
+        const int64_t nc = N - n0 < pl.Nc ? N - n0 : pl.Nc;
+        LIN_TRY(widen(W8 + n0 * ldw, ldw, nc, H, nullptr, 0, nullptr, w8 + pl.o_W, pl.ldh, true, st));
+        LinArgs a = {};
+        a.ab = (int32_t)pl.ab, a.an = (int32_t)pl.an, a.kt = (int32_t)pl.kt, a.status = status;
+        Prod &p = a.p[0];
+        shape(p, pl, T, nc, H);
+        choose_splits(p, a.p[1], pl.C);
+        p.f16 = 1;
+        p.rs = x_scale;
+        p.cs = W_scale + n0;
+        p.acc = reinterpret_cast<float *>(w8 + pl.o_acc[0]);
+        CUtensorMap m[6];
+        LIN_TRY(map_of(&m[0], w8 + pl.o_x, H, T, pl.ldh, 2, "x", (uint32_t)pl.ab));
+        LIN_TRY(map_of(&m[1], w8 + pl.o_W, H, nc, pl.ldh, 2, "W"));
+        LIN_TRY(out_map(p, &m[2], m[0], static_cast<uint8_t *>(out) + n0 * es, ldo, dtype, "out"));
+        m[3] = m[4] = m[5] = m[0];
+        schedule(a, pl.C);
+        LIN_TRY(pl.CG == 1 ? launch_linear<1>(m, a, st) : launch_linear<2>(m, a, st));
+    }
+    return SG_OK;
+}
+
+sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, int32_t x_group, int64_t T, int64_t H,
+                         const int8_t *W8, int64_t ldw, const float *W_scale, int64_t N, const void *dout, int64_t lddout,
+                         int32_t dtype, void *dx, int64_t lddx, void *dW, int64_t lddw, void *work, int64_t work_bytes,
+                         int32_t *status, void *stream)
+{
+    const char *fn = "sg_linear8_bwd";
+    NvtxRange nvtx_(fn);
+    LIN_TRY(check_linear(fn, x8, dW ? ldx : H, T, H, W8, dx ? ldw : H, N));
+    if (dtype != SG_BF16 && dtype != SG_F16)
+        LIN_FAIL(SG_ERR_INVALID, "%s: dtype %d is not SG_BF16 or SG_F16", fn, dtype);
+    if (x_group != 0 && x_group != rows::kGroup)
+        LIN_FAIL(SG_ERR_INVALID, "%s: x_group=%d is not 0 (the row) or %d", fn, x_group, rows::kGroup);
+    if (T && (!dout || (!dx && !dW) || (dx && (!W8 || !W_scale)) || (dW && (!x8 || !x_scale))))
+        LIN_FAIL(SG_ERR_INVALID, "%s: a required pointer is NULL", fn);
+    if (!aligned4(x_scale, W_scale, status))
+        LIN_FAIL(SG_ERR_INVALID, "%s: a vector or status is not aligned to its elements", fn);
+    if (T && (lddout < N || (uintptr_t)dout % 2 != 0))
+        LIN_FAIL(SG_ERR_INVALID, "%s: dout has a row stride below N or is not aligned to its elements", fn);
+    if ((dx && (lddx < H || (uintptr_t)dx % 2 != 0)) || (dW && (lddw < H || (uintptr_t)dW % 2 != 0)))
+        LIN_FAIL(SG_ERR_INVALID, "%s: dx or dW has a row stride below H or is not aligned to its elements", fn);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {
+        if (dW)
+            SG_TRY_CUDA(cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)H * 2, (size_t)N, st));
+        return SG_OK;
+    }
+    Plan pl;
+    make_plan(T, H, N, dout, lddout, true, dx != nullptr, dW != nullptr, &pl);
+    if (!work || work_bytes < pl.bytes || ((uintptr_t)work & 255) != 0)
+        LIN_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_linear8_work), aligned to 256", fn, (long long)pl.bytes);
+    uint8_t *w8 = static_cast<uint8_t *>(work);
+    const bool f16 = dtype == SG_F16;
+    // factors of the scales: fp16 has not their range
+    float *fac = f16 ? reinterpret_cast<float *>(w8 + pl.o_f) : nullptr;
+    if (f16) {
+        k_factor<<<2, 1024, 0, st>>>(W_scale, dx ? N : 0, fac, x_scale,
+                                     dW ? T * (x_group ? ceil_div(H, (int64_t)x_group) : 1) : 0, fac + 2);
+        SG_TRY_CUDA(cudaGetLastError());
+    }
+    if (pl.copy) {
+        LIN_TRY(launch(k_linear_copy, dim3((unsigned)(T < kSMs * 8 ? T : kSMs * 8)), 256, 0, 1, true, st,
+                       static_cast<const uint16_t *>(dout), lddout, T, (int)N,
+                       reinterpret_cast<uint16_t *>(w8 + pl.o_d), pl.ldn));
+        dout = w8 + pl.o_d;
+        lddout = pl.ldn;
+    }
+    if (dx)
+        LIN_TRY(widen(W8, ldw, N, H, W_scale, 0, fac, w8 + pl.o_W, pl.ldh, f16, st));
+    if (dW)
+        LIN_TRY(widen(x8, ldx, T, H, x_scale, x_group, fac ? fac + 2 : nullptr, w8 + pl.o_x, pl.ldh, f16, st));
+    LinArgs a = {};
+    a.p[0] = pl.p[0], a.p[1] = pl.p[1];
+    a.ab = (int32_t)pl.ab, a.an = (int32_t)pl.an, a.kt = (int32_t)pl.kt, a.status = status;
+    CUtensorMap m[6];
+    for (int i = 0; i < 2; ++i) {
+        Prod &p = a.p[i];
+        CUtensorMap *mi = m + 3 * i;
+        const bool is_dW = dW && i == 0;
+        if (!p.units) {
+            mi[0] = mi[1] = mi[2] = m[0];
+            continue;
+        }
+        p.f16 = f16;
+        p.acc = reinterpret_cast<float *>(w8 + pl.o_acc[i]);
+        p.a_mn = is_dW;
+        p.b_mn = 1;
+        p.inv = fac ? fac + (is_dW ? 3 : 1) : nullptr;
+        LIN_TRY(map_of(&mi[0], dout, N, T, lddout, 2, "dout", (uint32_t)(is_dW ? pl.kt : pl.ab)));
+        if (is_dW)
+            LIN_TRY(map_of(&mi[1], w8 + pl.o_x, H, T, pl.ldh, 2, "x", (uint32_t)pl.kt));
+        else
+            LIN_TRY(map_of(&mi[1], w8 + pl.o_W, H, N, pl.ldh, 2, "W"));
+        LIN_TRY(out_map(p, &mi[2], mi[0], is_dW ? dW : dx, is_dW ? lddw : lddx, dtype, is_dW ? "dW" : "dx"));
+    }
+    schedule(a, pl.C);
+    return pl.CG == 1 ? launch_linear<1>(m, a, st) : launch_linear<2>(m, a, st);
+}
+
+}  // extern "C"

@@ -96,6 +96,18 @@ def load():
                                   C.c_int),
             "sg_softmax_ce_bwd": ([P, i64, i64, i64, P, i64, i64, i32, P, i32, f64, P, P, P, i64, P, i64, P, i64, P,
                                    P], C.c_int),
+            "sg_pack8": ([P, i64, i64, i64, i32, i32, P, i64, P, P], C.c_int),
+            "sg_unpack8": ([P, i64, P, i64, i64, i32, P, i64, i32, P], C.c_int),
+            "sg_block_norm_fwd": ([P, i64, P, i64, i64, i64, i32, P, P, P, f64, f64, P, i64, P, P, P, i64, P, i64, P,
+                                   P, i64, P, P, i64, P, P], C.c_int),
+            "sg_block_norm_bwd_work": ([i64, i64, C.POINTER(i64)], C.c_int),
+            "sg_block_norm_bwd": ([P, i64, P, i64, P, P, i64, P, P, i64, i64, i64, i32, P, P, P, f64, P, P, P, i64, P,
+                                   i64, P, P, P, P, i64, P], C.c_int),
+            "sg_linear8_work": ([P, i64, i64, i64, P, i64, i64, P, i64, i32, C.POINTER(i64)], C.c_int),
+            "sg_linear8_status": ([C.POINTER(i32), i32], C.c_int),
+            "sg_linear8_fwd": ([P, i64, P, i64, i64, P, i64, P, i64, P, i64, i32, P, i64, P, P], C.c_int),
+            "sg_linear8_bwd": ([P, i64, P, i32, i64, i64, P, i64, P, i64, P, i64, i32, P, i64, P, i64, P, i64, P, P],
+                               C.c_int),
             "sg_timing_start": ([P, i32], C.c_int),
             "sg_timing_stop": ([P, P, P], C.c_int),
             "sg_last_error": ([], C.c_char_p),
@@ -217,8 +229,8 @@ def sg_layout_status(layout: Layout, clear: bool = True) -> int:
 
 def sg_device_status() -> int:
     """First non-zero status word among the live layouts of the current
-    device, else that of sg_softmax_ce_status (0 if none); reads without
-    clearing."""
+    device, else that of sg_softmax_ce_status or sg_linear8_status (0 if none);
+    reads without clearing."""
     code = C.c_int32(0)
     _check(load().sg_device_status(C.byref(code)))
     return int(code.value)
@@ -704,6 +716,180 @@ def sg_softmax_ce_bwd(h: torch.Tensor, W: torch.Tensor, targets, lse, dloss, dh=
           work.numel(), _vec(status, "status", 1, torch.int32, dev))
 
 
+# ---------------------------------------------------------------- blocks on 8-bit integers
+def _scales(t, name: str, rows: int, cols: int, dev: int):
+    """(pointer, group) of the scales of rows x cols 8-bit integers: a vector
+    has one for each row (group 0), a matrix of ceil(cols / 128) columns one for
+    each 128 columns of a row (group 128)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() == 1:
+        return _vec(t, name, rows, torch.float32, dev), 0
+    if t.shape != (rows, (cols + 127) // 128):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows,)} or {(rows, (cols + 127) // 128)}")
+    return _vec(t, name, None, torch.float32, dev), 128
+
+
+def _groups(t, name: str, rows: int, cols: int, dev: int):
+    """Pointer of scales of 128 columns each; NULL for None."""
+    if t is None:
+        return None
+    p, group = _scales(t, name, rows, cols, dev)
+    if not group:
+        raise ValueError(f"{name} must have a scale for each 128 columns: {(rows, (cols + 127) // 128)}")
+    return p
+
+
+def sg_pack8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor):
+    """Rows to 8-bit integers q (int8) with fp32 scales: scale[rows] one for
+    each row, or scale[rows, ceil(cols / 128)] one for each 128 columns (see
+    sg.h)."""
+    rows, cols, dt, dev = _open(x, "x", _FLOATS)
+    xp, ldx = _mat(x, "x", rows, cols, dt, dev)
+    qp, ldq = _mat(q, "q", rows, cols, torch.int8, dev)
+    sp, group = _scales(scale, "scale", rows, cols, dev)
+    _call((_lib or load()).sg_pack8, dev, xp, ldx, rows, cols, _DTYPE[dt], group, qp, ldq, sp)
+
+
+def sg_unpack8(q: torch.Tensor, scale: torch.Tensor, y: torch.Tensor):
+    """y = q times its scales (see sg_pack8), rounded to y's dtype."""
+    rows, cols, dt, dev = _open(y, "y", _FLOATS)
+    qp, ldq = _mat(q, "q", rows, cols, torch.int8, dev)
+    yp, ldy = _mat(y, "y", rows, cols, dt, dev)
+    sp, group = _scales(scale, "scale", rows, cols, dev)
+    _call((_lib or load()).sg_unpack8, dev, qp, ldq, sp, rows, cols, group, yp, ldy, _DTYPE[dt])
+
+
+def sg_block_norm_fwd(x: torch.Tensor, post_weight: torch.Tensor, pre_weight: torch.Tensor, eps: float, residual=None,
+                      gate=None, residual_scale: float = 1.0, u=None, rstd_x=None, rstd_u=None, y=None, y8=None,
+                      y8_scale=None, x8=None, x_scale=None, u8=None, u_scale=None):
+    """u = residual_scale residual + gate norm(x) post_weight, y = norm(u)
+    pre_weight; y8 with y8_scale hold y in 8 bits with a scale for each row, x8
+    and u8 with x_scale and u_scale x and u with one for each 128 columns.
+    Outputs that are None are not written (see sg.h)."""
+    rows, cols, dt, dev = _open(x, "x", _FLOATS)
+    f32, i8 = torch.float32, torch.int8
+    xp, ldx = _mat(x, "x", rows, cols, dt, dev)
+    rp, ldr = _mat(residual, "residual", rows, cols, dt, dev)
+    up, ldu = _mat(u, "u", rows, cols, dt, dev)
+    yp, ldy = _mat(y, "y", rows, cols, dt, dev)
+    y8p, ldy8 = _mat(y8, "y8", rows, cols, i8, dev)
+    x8p, ldx8 = _mat(x8, "x8", rows, cols, i8, dev)
+    u8p, ldu8 = _mat(u8, "u8", rows, cols, i8, dev)
+    _call((_lib or load()).sg_block_norm_fwd, dev, xp, ldx, rp, ldr, rows, cols, _DTYPE[dt],
+          _vec(post_weight, "post_weight", cols, dt, dev), _vec(gate, "gate", cols, dt, dev),
+          _vec(pre_weight, "pre_weight", cols, dt, dev), residual_scale, eps, up, ldu,
+          _vec(rstd_x, "rstd_x", rows, f32, dev), _vec(rstd_u, "rstd_u", rows, f32, dev), yp, ldy, y8p, ldy8,
+          _vec(y8_scale, "y8_scale", rows, f32, dev), x8p, ldx8, _groups(x_scale, "x_scale", rows, cols, dev), u8p, ldu8,
+          _groups(u_scale, "u_scale", rows, cols, dev))
+
+
+@functools.lru_cache(4096)
+def sg_block_norm_bwd_work(rows: int, cols: int) -> int:
+    """Bytes of work memory that sg_block_norm_bwd needs for dpost, dgate and
+    dpre."""
+    n = C.c_int64(0)
+    _check(load().sg_block_norm_bwd_work(rows, cols, C.byref(n)))
+    return n.value
+
+
+def sg_block_norm_bwd(dy: torch.Tensor, u: torch.Tensor, x: torch.Tensor, post_weight: torch.Tensor,
+                      pre_weight: torch.Tensor, rstd_x: torch.Tensor, rstd_u: torch.Tensor, dx: torch.Tensor,
+                      dresidual=None, dpost=None, dpre=None, dgate=None, gate=None, residual_scale: float = 1.0,
+                      du_in=None, u_scale=None, x_scale=None, work=None):
+    """Gradient of sg_block_norm_fwd (see sg.h), from u and x in dy's dtype, or
+    both in 8 bits with u_scale and x_scale.  work: a uint8 tensor of
+    sg_block_norm_bwd_work bytes; one is taken from torch's allocator if it is
+    None."""
+    rows, cols, dt, dev = _open(dy, "dy", _FLOATS)
+    f32 = torch.float32
+    held = dt if u_scale is None and x_scale is None else torch.int8
+    gp, ldg = _mat(dy, "dy", rows, cols, dt, dev)
+    up, ldu = _mat(u, "u", rows, cols, held, dev)
+    xp, ldx = _mat(x, "x", rows, cols, held, dev)
+    ip, ldi = _mat(du_in, "du_in", rows, cols, dt, dev)
+    rp, ldr = _mat(dresidual, "dresidual", rows, cols, dt, dev)
+    op, ldo = _mat(dx, "dx", rows, cols, dt, dev)
+    if work is None and not (dpost is None and dpre is None and dgate is None):
+        work = torch.empty(sg_block_norm_bwd_work(rows, cols), dtype=torch.uint8, device=dy.device)
+    _call((_lib or load()).sg_block_norm_bwd, dev, gp, ldg, up, ldu, _groups(u_scale, "u_scale", rows, cols, dev), xp,
+          ldx, _groups(x_scale, "x_scale", rows, cols, dev), ip, ldi, rows, cols, _DTYPE[dt],
+          _vec(post_weight, "post_weight", cols, dt, dev), _vec(gate, "gate", cols, dt, dev),
+          _vec(pre_weight, "pre_weight", cols, dt, dev), residual_scale, _vec(rstd_x, "rstd_x", rows, f32, dev),
+          _vec(rstd_u, "rstd_u", rows, f32, dev), rp, ldr, op, ldo, _vec(dpost, "dpost", cols, f32, dev),
+          _vec(dgate, "dgate", cols, f32, dev), _vec(dpre, "dpre", cols, f32, dev),
+          _vec(work, "work", None, torch.uint8, dev), 0 if work is None else work.numel())
+
+
+@functools.lru_cache(4096)
+def _linear_bytes(x16, ldx, T, H, W16, ldw, N, d16, ldd, backward) -> int:
+    n = C.c_int64(0)
+    _check(load().sg_linear8_work(x16, ldx, T, H, W16, ldw, N, d16, ldd, backward, C.byref(n)))
+    return n.value
+
+
+def sg_linear8_work(x8: torch.Tensor, W8: torch.Tensor, dout=None) -> int:
+    """Bytes of work memory that sg_linear8_fwd needs for this x8 and W8, or,
+    with dout, sg_linear8_bwd."""
+    T, H, _, dev = _open(x8, "x8", _INT8)
+    N = W8.shape[0] if isinstance(W8, torch.Tensor) and W8.dim() == 2 else -1
+    xp, ldx = _mat(x8, "x8", T, H, torch.int8, dev)
+    wp, ldw = _mat(W8, "W8", N, H, torch.int8, dev)
+    dp, ldd = _mat(dout, "dout", T, N, dout.dtype if dout is not None else None, dev)
+    return _linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, (dp or 0) & 15, ldd, int(dout is not None))
+
+
+def sg_linear8_status(clear: bool = True) -> int:
+    """The status word of the current device's sg_linear8 calls that were given
+    none of their own (0: no error); waits for the device."""
+    code = C.c_int32(0)
+    _check(load().sg_linear8_status(C.byref(code), int(bool(clear))))
+    return int(code.value)
+
+
+def sg_linear8_fwd(x8: torch.Tensor, x_scale: torch.Tensor, W8: torch.Tensor, W_scale: torch.Tensor, out: torch.Tensor,
+                   work=None, status=None):
+    """out[t, n] = x_scale[t] W_scale[n] sum_h x8[t, h] W8[n, h] (see sg.h).
+    work: a uint8 tensor of sg_linear8_work bytes; one is taken from torch's
+    allocator if it is None.  status: an int32 tensor of one element; errors go
+    to the device's word (sg_linear8_status) if it is None."""
+    T, N, dt, dev = _open(out, "out", _FLOATS)
+    H = x8.shape[1] if isinstance(x8, torch.Tensor) and x8.dim() == 2 else -1
+    f32, i8 = torch.float32, torch.int8
+    xp, ldx = _mat(x8, "x8", T, H, i8, dev)
+    wp, ldw = _mat(W8, "W8", N, H, i8, dev)
+    op, ldo = _mat(out, "out", T, N, dt, dev)
+    if work is None:
+        work = torch.empty(_linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, 0, N, 0), dtype=torch.uint8,
+                           device=out.device)
+    _call((_lib or load()).sg_linear8_fwd, dev, xp, ldx, _vec(x_scale, "x_scale", T, f32, dev), T, H, wp, ldw,
+          _vec(W_scale, "W_scale", N, f32, dev), N, op, ldo, _DTYPE[dt], _vec(work, "work", None, torch.uint8, dev),
+          work.numel(), _vec(status, "status", 1, torch.int32, dev))
+
+
+def sg_linear8_bwd(x8: torch.Tensor, x_scale: torch.Tensor, W8: torch.Tensor, W_scale: torch.Tensor, dout: torch.Tensor,
+                   dx=None, dW=None, work=None, status=None):
+    """dx and dW (either may be None) of sg_linear8_fwd from dout (see sg.h).
+    x_scale[T], or x_scale[T, ceil(H / 128)] where x8 was kept with a scale for
+    each 128 columns; work and status as there."""
+    T, N, dt, dev = _open(dout, "dout", _16BIT)
+    H = x8.shape[1] if isinstance(x8, torch.Tensor) and x8.dim() == 2 else -1
+    f32, i8 = torch.float32, torch.int8
+    xp, ldx = _mat(x8, "x8", T, H, i8, dev)
+    wp, ldw = _mat(W8, "W8", N, H, i8, dev)
+    gp, ldg = _mat(dout, "dout", T, N, dt, dev)
+    dxp, lddx = _mat(dx, "dx", T, H, dt, dev)
+    dwp, lddw = _mat(dW, "dW", N, H, dt, dev)
+    sp, group = _scales(x_scale, "x_scale", T, H, dev)
+    if work is None:
+        work = torch.empty(_linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, gp & 15, ldg, 1), dtype=torch.uint8,
+                           device=dout.device)
+    _call((_lib or load()).sg_linear8_bwd, dev, xp, ldx, sp, group, T, H, wp, ldw, _vec(W_scale, "W_scale", N, f32, dev),
+          N, gp, ldg, _DTYPE[dt], dxp, lddx, dwp, lddw, _vec(work, "work", None, torch.uint8, dev), work.numel(),
+          _vec(status, "status", 1, torch.int32, dev))
+
+
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 _16BIT = (torch.bfloat16, torch.float16)
 _8OR16BIT = _16BIT + (_E4M3,)
+_INT8 = (torch.int8,)

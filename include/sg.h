@@ -164,7 +164,8 @@ SG_API sg_status sg_layout_status(sg_layout *layout, int32_t *code, int32_t clea
 /* The device-wide view of the same words: waits for the current device, then
  * sets *code to the first non-zero status word among the live layouts built on
  * that device (in the order they were built), else to that of the softmax cross
- * entropy calls without one of their own (sg_softmax_ce_status), or SG_OK.
+ * entropy calls without one of their own (sg_softmax_ce_status) or of the 8-bit
+ * linear layer's (sg_linear8_status), or SG_OK.
  * Clears nothing: a layout's word is reset with sg_layout_status(..., clear =
  * 1).  Returns
  * SG_ERR_INVALID for a NULL `code` and SG_ERR_CUDA if the device reports an
@@ -512,6 +513,102 @@ SG_API sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_
                                    double smoothing, const float *lse, const float *dloss, void *dh, int64_t lddh,
                                    void *dW, int64_t lddw, void *work, int64_t work_bytes, int32_t *status,
                                    void *stream);
+
+/* ---------------------------------------------------------------- blocks on 8-bit integers
+ * What an encoder's blocks need in front of the output layer when their linear
+ * layers run on 8-bit integers: rows held in 8 bits, the norms around a block,
+ * and the linear layer itself, each with its gradient.  The conventions are
+ * those of the section above.  8-bit rows hold values of -127 to 127 and have
+ * fp32 scales, contiguous: one for each row (group 0), or scale[rows][ceil(cols
+ * / 128)], one for each 128 columns of a row (group 128; the last may be fewer).
+ *
+ * sg_pack8 -- rows to 8 bits, as a training program keeps activations for the
+ * backward pass: for a group with a = max |x|,
+ *   scale = a / 127,   q = rint(x (127 / a)),   x is about q scale
+ * in fp32, ties to even.  Scales are at least 2^-126, and at most what leaves 127
+ * scale an fp32 number; 0 for a group of zeros, and NaN where the group holds an
+ * infinity or NaN (its q are 0).  q must not overlap x.  cols <= 32768 with group
+ * 0.
+ * sg_unpack8 -- y = round(q scale) in dtype; any values of q (-128 too). */
+SG_API sg_status sg_pack8(const void *x, int64_t ldx, int64_t rows, int64_t cols, int32_t dtype, int32_t group,
+                          int8_t *q, int64_t ldq, float *scale, void *stream);
+SG_API sg_status sg_unpack8(const int8_t *q, int64_t ldq, const float *scale, int64_t rows, int64_t cols,
+                            int32_t group, void *y, int64_t ldy, int32_t dtype, void *stream);
+
+/* sg_block_norm_fwd -- the norm of a block's output x, its gate, the residual
+ * with its scale, and the norm before the next block:
+ *   v = x rstd_x post_weight,           rstd_x = 1 / sqrt(mean(x^2) + eps)
+ *   u = round(residual_scale residual + gate v)
+ *   y = u rstd_u pre_weight,            rstd_u = 1 / sqrt(mean(u^2) + eps)
+ * with u rounded to dtype before its norm is taken.  residual NULL: none; gate
+ * NULL: 1.  post_weight, gate and pre_weight have cols elements of dtype.
+ * Outputs, each where its pointer is given: u, rstd_x[rows], rstd_u[rows], y,
+ * y8 with y8_scale[rows] (y in 8 bits, one scale for a row, what sg_linear8_fwd
+ * reads; rounded from fp32 y), and for the backward pass x8 and u8 (x and u in 8
+ * bits, group 128, as sg_pack8 makes them) with x8_scale and u8_scale.  One of y
+ * and y8 is needed.  u may be x or residual, and y any of them; cols <= 16384.
+ * The sums of squares are formed in fp32 as they are, with the range that
+ * sg_add_rmsnorm_fwd states. */
+SG_API sg_status sg_block_norm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows,
+                                   int64_t cols, int32_t dtype, const void *post_weight, const void *gate,
+                                   const void *pre_weight, double residual_scale, double eps, void *u, int64_t ldu,
+                                   float *rstd_x, float *rstd_u, void *y, int64_t ldy, int8_t *y8, int64_t ldy8,
+                                   float *y8_scale, int8_t *x8, int64_t ldx8, float *x8_scale, int8_t *u8,
+                                   int64_t ldu8, float *u8_scale, void *stream);
+
+/* sg_block_norm_bwd -- its gradient.  With m = u rstd_u, h = x rstd_x:
+ *   g = dy pre_weight,            du = rstd_u (g - m mean(g m)) + du_in
+ *   k = du gate post_weight,      dx = rstd_x (k - h mean(k h))
+ *   dresidual = residual_scale du
+ *   dpre[c] = sum over rows of dy m,   with s[c] = sum over rows of du h:
+ *   dpost = gate s,   dgate = post_weight s
+ * u and x have dtype (u_scale and x_scale NULL), or are both held in 8 bits
+ * (int8_t, group 128) with their scales.  du_in (may be NULL) is the gradient
+ * that reaches u by the residual.  dresidual, dpost, dgate and dpre may be NULL;
+ * the last three are fp32, summed in an order that is always the same for the
+ * same sizes, and need work (aligned to 4 bytes).  du is not rounded on its way
+ * to dx.  dresidual may be dy or du_in, or u where that has dtype, and dx any of
+ * them or x. */
+SG_API sg_status sg_block_norm_bwd_work(int64_t rows, int64_t cols, int64_t *bytes);
+SG_API sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, int64_t ldu, const float *u_scale,
+                                   const void *x, int64_t ldx, const float *x_scale, const void *du_in,
+                                   int64_t lddu_in, int64_t rows, int64_t cols, int32_t dtype,
+                                   const void *post_weight, const void *gate, const void *pre_weight,
+                                   double residual_scale, const float *rstd_x, const float *rstd_u, void *dresidual,
+                                   int64_t lddr, void *dx, int64_t lddx, float *dpost, float *dgate, float *dpre,
+                                   void *work, int64_t work_bytes, void *stream);
+
+/* sg_linear8_fwd -- a linear layer on 8-bit integers with a scale for each
+ * token and each output channel:
+ *   out[t][n] = x_scale[t] W_scale[n] sum_h x8[t][h] W8[n][h]
+ * x8[T][H] and W8[N][H], one scale for a row; out[T][N] in dtype (SG_BF16,
+ * SG_F16, SG_F32).  Sums of 1024 products are exact, and those are added in fp32,
+ * rounded to nearest.
+ * sg_linear8_bwd -- the gradients for x and W as if they had not been rounded:
+ *   dx[t][h] = sum_n dout[t][n] W_scale[n] W8[n][h]
+ *   dW[n][h] = sum_t dout[t][n] x_scale[t][.] x8[t][h]
+ * from dout[T][N] in dtype (SG_BF16, SG_F16), the type of dx[T][H] and dW[N][H]
+ * too; either may be NULL (then what it alone needs may be NULL as well).
+ * x8 may have one scale for a row (x_group 0) or for 128 columns (x_group 128):
+ * what sg_pack8 or sg_block_norm_fwd kept.  The values that 8 bits stand for enter
+ * the products rounded to dtype (times a power of two, taken out again, in fp16),
+ * and parts of 1024 terms are added in fp32.
+ * The results are the same bits for the same call.  A token or channel whose
+ * scale is NaN gives NaN.  status and errors found on the device: as
+ * sg_softmax_ce_fwd, with sg_linear8_status for calls without a status word.
+ * T <= 2^24, H <= 2^20, N <= 2^24, T N < 2^43.  work is aligned to 256 bytes;
+ * sg_linear8_work wants the same x8, W8, strides (and dout, where backward is 1)
+ * as the call. */
+SG_API sg_status sg_linear8_work(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
+                                 int64_t N, const void *dout, int64_t lddout, int32_t backward, int64_t *bytes);
+SG_API sg_status sg_linear8_status(int32_t *code, int32_t clear);
+SG_API sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, int64_t T, int64_t H,
+                                const int8_t *W8, int64_t ldw, const float *W_scale, int64_t N, void *out, int64_t ldo,
+                                int32_t dtype, void *work, int64_t work_bytes, int32_t *status, void *stream);
+SG_API sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, int32_t x_group, int64_t T,
+                                int64_t H, const int8_t *W8, int64_t ldw, const float *W_scale, int64_t N,
+                                const void *dout, int64_t lddout, int32_t dtype, void *dx, int64_t lddx, void *dW,
+                                int64_t lddw, void *work, int64_t work_bytes, int32_t *status, void *stream);
 
 /* ---------------------------------------------------------------- timing
  * Per-kernel device timing for benchmarks: while enabled, every kernel the
