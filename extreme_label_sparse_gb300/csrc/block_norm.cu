@@ -25,6 +25,26 @@ struct BlockFwd {
 
 constexpr int block_ctas(int warps) { return norm_ctas(warps, true); }
 
+// gate post_weight and pre_weight of a thread's columns (0 past the last)
+template <typename T, bool VEC, int WARPS, int NV>
+__device__ __forceinline__ void block_weights(const void *post, const void *gate, const void *pre, int wr, int lane,
+                                              int cols, float2 (&gp)[NV][4], float2 (&pw)[NV][4])
+{
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c0 = (n * WARPS + wr) * kSeg;
+        unpack4(load8<T, VEC>(static_cast<const T *>(pre), c0, lane, cols), pw[n]);
+        unpack4(load8<T, VEC>(static_cast<const T *>(post), c0, lane, cols), gp[n]);
+        if (gate) {
+            float2 g[4];
+            unpack4(load8<T, VEC>(static_cast<const T *>(gate), c0, lane, cols), g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                gp[n][i] = mul2(gp[n][i], g[i]);
+        }
+    }
+}
+
 // A row by WARPS warps (one warp: eight rows to a CTA), NV segments to a warp;
 // row groups step over the rows, with the next S rows on their way to shared
 // memory.
@@ -59,32 +79,20 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
 #pragma unroll
     for (int i = 0; i < S; ++i)
         fetch(g + i * groups, i);
-    Pack8<T> post[NV], gate[NV], pre[NV];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int c0 = (n * WARPS + wr) * kSeg;
-        post[n] = load8<T, VEC>(static_cast<const T *>(a.post), c0, lane, a.cols);
-        pre[n] = load8<T, VEC>(static_cast<const T *>(a.pre), c0, lane, a.cols);
-        if (a.gate) {
-            gate[n] = load8<T, VEC>(static_cast<const T *>(a.gate), c0, lane, a.cols);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                gate[n].v[j] = from_f<T>(1.f);
-        }
-    }
+    float2 gp[NV][4], pre[NV][4];  // gate post_weight, pre_weight
+    block_weights<T, VEC, WARPS, NV>(a.post, a.gate, a.pre, wr, lane, a.cols, gp, pre);
+    auto col0 = [&](int n) { return (n * WARPS + wr) * kSeg; };
     int turn = 0, slot = 0;
     for (int64_t r = g; r < a.nrows; r += groups, turn += 2) {
         Pack8<T> p[NV];  // x, then u
-        float ss = 0.f, none = 0.f;
+        float2 ss = make_float2(0.f, 0.f);
+        float none = 0.f;
         if constexpr (VEC)
             copies_wait<S - 1>();
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int c0 = (n * WARPS + wr) * kSeg;
-            if (c0 >= a.cols)
-                break;  // the whole warp: neither has a later segment columns of it
-            float v[8];
+            const int c0 = col0(n);
+            float2 v[4];
             if constexpr (VEC) {
                 if (c0 + lane * 8 < a.cols)
                     p[n] = ring.get(slot, 0, n);
@@ -93,24 +101,24 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
             } else {
                 p[n] = load8<T, VEC>(ax + r * a.ldx, c0, lane, a.cols);
             }
-            unpack8(p[n], v);
+            unpack4(p[n], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                ss = fmaf(v[j], v[j], ss);
-            if (a.x8)
-                store_groups<VEC>(a.x8 + r * a.ldx8, a.x8_scale + r * ng, c0, lane, a.cols, v);
+            for (int i = 0; i < 4; ++i)
+                ss = fma2(v[i], v[i], ss);
         }
-        row_reduce<WARPS, false>(ss, none, sm, turn);
-        const float rx = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
-        ss = 0.f;
+        float sum = ss.x + ss.y;
+        row_reduce<WARPS, false>(sum, none, sm, turn);
+        if (a.x8)
+            store_groups<T, VEC, NV>(
+                p, lane, a.cols, [&](int) { return a.x8 + r * a.ldx8; }, [&](int) { return a.x8_scale + r * ng; }, col0);
+        const float rx = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+        ss = make_float2(0.f, 0.f);
         uint32_t most = 0;  // of |u pre|
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int c0 = (n * WARPS + wr) * kSeg;
-            if (c0 >= a.cols)
-                break;
-            float v[8], w[8];
-            unpack8(p[n], v);
+            const int c0 = col0(n);
+            float2 v[4], w[4];
+            unpack4(p[n], v);
             if (ar) {
                 Pack8<T> t;
                 if constexpr (VEC) {
@@ -121,56 +129,68 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 } else {
                     t = load8<T, VEC>(ar + r * a.ldr, c0, lane, a.cols);
                 }
-                unpack8(t, w);
+                unpack4(t, w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = mul2(w[i], both(a.alpha));
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = 0.f;
+                for (int i = 0; i < 4; ++i)
+                    w[i] = make_float2(0.f, 0.f);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = fmaf(v[j] * rx * to_f(post[n].v[j]), to_f(gate[n].v[j]), ar ? a.alpha * w[j] : 0.f);
+            for (int i = 0; i < 4; ++i)
+                v[i] = fma2(mul2(v[i], both(rx)), gp[n][i], w[i]);
             // the second norm is taken of the sum as it is stored, so that the
             // backward pass sees the same row
-            p[n] = pack8<T>(v);
-            unpack8(p[n], v);
+            p[n] = pack4<T>(v);
+            unpack4(p[n], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ss = fmaf(v[j], v[j], ss);
-                most = max(most, mag(v[j] * to_f(pre[n].v[j])));
+            for (int i = 0; i < 4; ++i)
+                ss = fma2(v[i], v[i], ss);
+            if (a.y8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 t = mul2(v[i], pre[n][i]);
+                    most = max(most, max(mag(t.x), mag(t.y)));
+                }
             }
             if (a.u)
                 store8<T, VEC>(static_cast<T *>(a.u) + r * a.ldu, c0, lane, a.cols, p[n]);
-            if (a.u8)
-                store_groups<VEC>(a.u8 + r * a.ldu8, a.u8_scale + r * ng, c0, lane, a.cols, v);
         }
         fetch(r + S * groups, slot);
         slot = slot + 1 == S ? 0 : slot + 1;
         float top = __uint_as_float(min(most, 0x7f800000u));  // NaN as infinity, which stays the largest
-        row_reduce<WARPS, true>(ss, top, sm, turn + 1);
-        const float ru = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+        sum = ss.x + ss.y;
+        row_reduce<WARPS, true>(sum, top, sm, turn + 1);
+        if (a.u8)
+            store_groups<T, VEC, NV>(
+                p, lane, a.cols, [&](int) { return a.u8 + r * a.ldu8; }, [&](int) { return a.u8_scale + r * ng; }, col0);
+        const float ru = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
         if (lane == 0 && wr == 0) {
             if (a.rx)
                 a.rx[r] = rx;
             if (a.ru)
                 a.ru[r] = ru;
         }
-        // max |y| without a third reduction: ru max |u pre|; a row whose sum is
-        // not finite has neither scale nor values
-        const Scale8 s8 = scale8_of(mag(ss < INFINITY ? top * ru : NAN));
-        if (a.y8 && lane == 0 && wr == 0)
-            a.y8_scale[r] = s8.scale;
+        Scale8 s8 = {};
+        if (a.y8) {
+            // max |y| without a third reduction: ru max |u pre|; a row whose sum
+            // is not finite has neither scale nor values
+            s8 = scale8_of(mag(sum < INFINITY ? top * ru : NAN));
+            if (lane == 0 && wr == 0)
+                a.y8_scale[r] = s8.scale;
+        }
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int c0 = (n * WARPS + wr) * kSeg;
-            if (c0 >= a.cols)
-                break;
-            float y[8];
+            const int c0 = col0(n);
+            float2 y[4];
+            unpack4(p[n], y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[j] = (to_f(p[n].v[j]) * ru) * to_f(pre[n].v[j]);
+            for (int i = 0; i < 4; ++i)
+                y[i] = mul2(mul2(y[i], both(ru)), pre[n][i]);
             if (a.y)
-                store8<T, VEC>(static_cast<T *>(a.y) + r * a.ldy, c0, lane, a.cols, pack8<T>(y));
+                store8<T, VEC>(static_cast<T *>(a.y) + r * a.ldy, c0, lane, a.cols, pack4<T>(y));
             if (a.y8)
                 store8q<VEC>(a.y8 + r * a.ldy8, c0, lane, a.cols, quant8(y, s8.inv));
         }
@@ -221,21 +241,40 @@ struct BackRing {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(scale) : "memory");
     }
-    __device__ __forceinline__ void get(int slot, int n, int m, float (&v)[8]) const
+    __device__ __forceinline__ void get(int slot, int n, int m, float2 (&v)[4]) const
     {
         Pack8<T> p;
 #pragma unroll
         for (int i = 0; i < P; ++i)
             reinterpret_cast<uint4 *>(&p)[i] = *at(slot, n, m * P + i);
-        unpack8(p, v);
+        unpack4(p, v);
     }
-    __device__ __forceinline__ void get8(int slot, int n, int m, float (&v)[8]) const
+    __device__ __forceinline__ uint2 get8(int slot, int n, int m) const
     {
-        unquant8(reinterpret_cast<const uint2 *>(at(slot, n, 2 * P))[m], v);
-        const float s = reinterpret_cast<const float *>(at(slot, n, 2 * P + 1))[m];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] *= s;
+        return reinterpret_cast<const uint2 *>(at(slot, n, 2 * P))[m];
+    }
+    __device__ __forceinline__ float scale(int slot, int n, int m) const
+    {
+        return reinterpret_cast<const float *>(at(slot, n, 2 * P + 1))[m];
+    }
+};
+
+// Eight values v s, s common to elements 0 to 3 (s0) and 4 to 7 (s1).  Rows held
+// in 8 bits have the integers in v: their scales go into factors of the row.
+struct Held {
+    float2 v[4];
+    float s0, s1;
+
+    __device__ __forceinline__ float s(int i) const { return i < 2 ? s0 : s1; }
+    // the sum of t v's elements, each times its s
+    template <bool HELD>
+    __device__ __forceinline__ float sum(const float2 (&t)[4]) const
+    {
+        const float2 a = add2(t[0], t[1]), b = add2(t[2], t[3]);
+        if constexpr (HELD)
+            return s0 * (a.x + a.y) + s1 * (b.x + b.y);
+        const float2 c = add2(a, b);
+        return c.x + c.y;
     }
 };
 
@@ -283,21 +322,9 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
 #pragma unroll
     for (int i = 0; i < S; ++i)
         fetch(g + i * groups, i);
-    Pack8<T> post[NV], gate[NV], pre[NV];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int c0 = (n * WARPS + wr) * kSeg;
-        post[n] = load8<T, VEC>(static_cast<const T *>(a.post), c0, lane, a.cols);
-        pre[n] = load8<T, VEC>(static_cast<const T *>(a.pre), c0, lane, a.cols);
-        if (a.gate) {
-            gate[n] = load8<T, VEC>(static_cast<const T *>(a.gate), c0, lane, a.cols);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                gate[n].v[j] = from_f<T>(1.f);
-        }
-    }
-    float dpre[NV][8] = {}, dh[NV][8] = {};
+    float2 gp[NV][4], pre[NV][4];  // gate post_weight, pre_weight
+    block_weights<T, VEC, WARPS, NV>(a.post, a.gate, a.pre, wr, lane, a.cols, gp, pre);
+    float2 dpre[NV][4] = {}, dh[NV][4] = {};
     int turn = 0, slot = 0;
     float next_u = g < a.nrows ? a.ru[g] : 0.f, next_x = g < a.nrows ? a.rx[g] : 0.f;
     for (int64_t r = g; r < a.nrows; r += groups, turn += 2) {
@@ -308,32 +335,31 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
         }
         // the row's values of this lane, again for each use (from shared memory,
         // or, without VEC, from the caches)
-        auto dy_of = [&](int n, int c0, float (&v)[8]) {
+        auto dy_of = [&](int n, int c0, float2 (&v)[4]) {
             if constexpr (VEC)
                 ring.get(slot, n, 0, v);
             else
-                unpack8(load8<T, VEC>(ady + r * a.lddy, c0, lane, a.cols), v);
+                unpack4(load8<T, VEC>(ady + r * a.lddy, c0, lane, a.cols), v);
         };
-        auto u_of = [&](int n, int c0, float (&v)[8]) {
-            if constexpr (VEC && HELD)
-                ring.get8(slot, n, 1, v);
-            else if constexpr (VEC)
-                ring.get(slot, n, 3, v);
-            else if constexpr (HELD)
-                load_groups<VEC>(static_cast<const int8_t *>(a.u) + r * a.ldu, a.u_scale + r * ng, c0, lane, a.cols, v);
-            else
-                unpack8(load8<T, VEC>(static_cast<const T *>(a.u) + r * a.ldu, c0, lane, a.cols), v);
+        // m: 0 x, 1 u
+        auto held_of = [&](int n, int c0, int m, const void *rows, int64_t ld, const float *scale, Held &h) {
+            h.s0 = h.s1 = 1.f;
+            if constexpr (VEC && HELD) {
+                unquant8(ring.get8(slot, n, m), h.v);
+                h.s0 = h.s1 = ring.scale(slot, n, m);
+            } else if constexpr (VEC) {
+                ring.get(slot, n, 2 + m, h.v);
+            } else if constexpr (HELD) {
+                unquant8(load8q<VEC>(static_cast<const int8_t *>(rows) + r * ld, c0, lane, a.cols), h.v);
+                const float *s = scale + r * ng + c0 / kGroup;
+                h.s0 = c0 < a.cols ? s[0] : 0.f;
+                h.s1 = c0 + kGroup < a.cols ? s[1] : 0.f;
+            } else {
+                unpack4(load8<T, VEC>(static_cast<const T *>(rows) + r * ld, c0, lane, a.cols), h.v);
+            }
         };
-        auto x_of = [&](int n, int c0, float (&v)[8]) {
-            if constexpr (VEC && HELD)
-                ring.get8(slot, n, 0, v);
-            else if constexpr (VEC)
-                ring.get(slot, n, 2, v);
-            else if constexpr (HELD)
-                load_groups<VEC>(static_cast<const int8_t *>(a.x) + r * a.ldx, a.x_scale + r * ng, c0, lane, a.cols, v);
-            else
-                unpack8(load8<T, VEC>(static_cast<const T *>(a.x) + r * a.ldx, c0, lane, a.cols), v);
-        };
+        auto x_of = [&](int n, int c0, Held &h) { held_of(n, c0, 0, a.x, a.ldx, a.x_scale, h); };
+        auto u_of = [&](int n, int c0, Held &h) { held_of(n, c0, 1, a.u, a.ldu, a.u_scale, h); };
         float dot = 0.f, none = 0.f;
         if constexpr (VEC)
             copies_wait<S - 1>();
@@ -342,56 +368,63 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
             const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;  // and neither has a later segment columns of this thread
-            float dy[8], u[8];
-            dy_of(n, c0, dy);
+            float2 t[4];
+            Held u;
+            dy_of(n, c0, t);
             u_of(n, c0, u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float t = dy[j] * u[j];
-                dpre[n][j] = fmaf(t, ru, dpre[n][j]);
-                dot = fmaf(t, to_f(pre[n].v[j]), dot);
+            for (int i = 0; i < 4; ++i) {
+                t[i] = mul2(t[i], u.v[i]);
+                dpre[n][i] = fma2(t[i], both(ru * u.s(i)), dpre[n][i]);
+                t[i] = mul2(t[i], pre[n][i]);
             }
+            dot += u.template sum<HELD>(t);
         }
         row_reduce<WARPS, false>(dot, none, sm, turn);
         // as in the norm's own gradient: neither a square of u nor one of its
         // factor without the other, so that rows of any scale stay in range
         const float back_u = dot / (float)a.cols * ru * ru;
-        float du[NV][8];
+        float2 du[NV][4];
         dot = 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;
-            float t[8], v[8];
+            float2 t[4];
+            Held h;
             if (ai) {
                 if constexpr (VEC)
-                    ring.get(slot, n, 1, v);
+                    ring.get(slot, n, 1, du[n]);
                 else
-                    unpack8(load8<T, VEC>(ai + r * a.ldi, c0, lane, a.cols), v);
+                    unpack4(load8<T, VEC>(ai + r * a.ldi, c0, lane, a.cols), du[n]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = 0.f;
+                for (int i = 0; i < 4; ++i)
+                    du[n][i] = make_float2(0.f, 0.f);
             }
-            u_of(n, c0, t);
+            u_of(n, c0, h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = fmaf(-back_u, t[j] * ru, v[j]);
+            for (int i = 0; i < 4; ++i)
+                du[n][i] = fma2(both(-back_u), mul2(h.v[i], both(ru * h.s(i))), du[n][i]);
             dy_of(n, c0, t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                du[n][j] = v[j] = fmaf(to_f(pre[n].v[j]) * ru, t[j], v[j]);
-            x_of(n, c0, t);
+            for (int i = 0; i < 4; ++i)
+                du[n][i] = fma2(mul2(pre[n][i], both(ru)), t[i], du[n][i]);
+            x_of(n, c0, h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = du[n][j] * t[j];
-                dh[n][j] = fmaf(d, rx, dh[n][j]);
-                dot = fmaf(d, to_f(post[n].v[j]) * to_f(gate[n].v[j]), dot);
-                v[j] *= a.alpha;
+            for (int i = 0; i < 4; ++i) {
+                t[i] = mul2(du[n][i], h.v[i]);
+                dh[n][i] = fma2(t[i], both(rx * h.s(i)), dh[n][i]);
+                t[i] = mul2(t[i], gp[n][i]);
             }
-            if (a.dres)
-                store8<T, VEC>(static_cast<T *>(a.dres) + r * a.ldo, c0, lane, a.cols, pack8<T>(v));
+            dot += h.template sum<HELD>(t);
+            if (a.dres) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    t[i] = mul2(du[n][i], both(a.alpha));
+                store8<T, VEC>(static_cast<T *>(a.dres) + r * a.ldo, c0, lane, a.cols, pack4<T>(t));
+            }
         }
         row_reduce<WARPS, false>(dot, none, sm, turn + 1);
         const float back_x = dot / (float)a.cols * rx * rx;
@@ -400,12 +433,12 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
             const int c0 = (n * WARPS + wr) * kSeg;
             if (VEC && c0 + lane * 8 >= a.cols)
                 break;
-            float v[8];
-            x_of(n, c0, v);
+            Held h;
+            x_of(n, c0, h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = fmaf(to_f(post[n].v[j]) * to_f(gate[n].v[j]) * rx, du[n][j], -back_x * (v[j] * rx));
-            store8<T, VEC>(static_cast<T *>(a.dx) + r * a.lddx, c0, lane, a.cols, pack8<T>(v));
+            for (int i = 0; i < 4; ++i)
+                h.v[i] = fma2(mul2(gp[n][i], both(rx)), du[n][i], mul2(both(-back_x), mul2(h.v[i], both(rx * h.s(i)))));
+            store8<T, VEC>(static_cast<T *>(a.dx) + r * a.lddx, c0, lane, a.cols, pack4<T>(h.v));
         }
         fetch(r + S * groups, slot);
         slot = slot + 1 == S ? 0 : slot + 1;
@@ -417,8 +450,8 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
             for (int j = 0; j < 8; ++j) {
                 const int c = col_of<VEC>((n * WARPS + wr) * kSeg, lane, j);
                 if (c < a.cols) {
-                    a.part[g * 2 * (int64_t)a.cols + c] = dpre[n][j];
-                    a.part[(g * 2 + 1) * (int64_t)a.cols + c] = dh[n][j];
+                    a.part[g * 2 * (int64_t)a.cols + c] = j & 1 ? dpre[n][j / 2].y : dpre[n][j / 2].x;
+                    a.part[(g * 2 + 1) * (int64_t)a.cols + c] = j & 1 ? dh[n][j / 2].y : dh[n][j / 2].x;
                 }
             }
     }

@@ -497,7 +497,7 @@ struct Widen {
     const int8_t *src;
     int64_t ld, rows;
     int32_t cols, group;   // group: columns of a scale, 0: the row's
-    const float *scale;    // NULL: the integers themselves
+    const float *scale;    // NULL: the integers themselves, in fp16
     const float *factor;   // of the scales, or NULL
     uint16_t *dst;
     int64_t ldd;
@@ -535,11 +535,25 @@ __global__ void __launch_bounds__(256) k_widen(const Widen a)
             // a group is a whole number of 16 columns
             const float s = sc ? sc[a.group ? c / a.group : 0] * f : 1.f;
             uint32_t w[8];
+            if (!sc) {
+                // a byte plus 128 as the low bits of 1024 in fp16, less 1152
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float lo = (float)(int8_t)(in[i / 2] >> (16 * (i & 1)));
-                const float hi = (float)(int8_t)(in[i / 2] >> (16 * (i & 1) + 8));
-                w[i] = pack16(lo * s, hi * s, a.f16);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u = in[i / 2] ^ 0x80808080u, h = __byte_perm(u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+                    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half(0x6480)));
+                    w[i] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float2 v[4];
+                    rows::unquant8(make_uint2(in[2 * k], in[2 * k + 1]), v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = rows::mul2(v[i], rows::both(s));
+                        w[4 * k + i] = pack16(v[i].x, v[i].y, a.f16);
+                    }
+                }
             }
             // ldd is a whole number of eights
             uint4 *out = reinterpret_cast<uint4 *>(dst + c);

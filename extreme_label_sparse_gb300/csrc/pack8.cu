@@ -7,7 +7,7 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroupsOut = 4;  // eights of a thread under way together
+constexpr int kOut = 4;  // eights of a thread under way together
 
 // i / n = (i magic) >> (32 + shift) for i < 2^31, with magic = ceil(2^(32 +
 // shift) / n) and 2^shift < n <= 2^(shift + 1): the excess of magic, below n /
@@ -28,34 +28,28 @@ struct Div {
     }
 };
 
-// Segments of 256 columns, numbered through all rows; a warp has kGroupsOut of
-// them, a CTA's warps apart.  n is below 2^31.
+// Segments of 256 columns, numbered through all rows; a warp has kOut of them, a
+// CTA's warps apart.  n is below 2^31 less those of a CTA.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     k_pack_groups(const T *__restrict__ x, int64_t ldx, uint32_t n, const Div segs, int cols, int8_t *__restrict__ q,
                   int64_t ldq, float *__restrict__ scale)
 {
     const int lane = threadIdx.x & 31, ng = (cols + kGroup - 1) / kGroup;
-    const uint32_t i0 = blockIdx.x * (kThreads / 32 * kGroupsOut) + threadIdx.x / 32;
-    Pack8<T> p[kGroupsOut];
+    const uint32_t i0 = blockIdx.x * (kThreads / 32 * kOut) + threadIdx.x / 32;
+    Pack8<T> p[kOut];
+    uint32_t r[kOut];
+    int c0[kOut];
 #pragma unroll
-    for (int k = 0; k < kGroupsOut; ++k) {
+    for (int k = 0; k < kOut; ++k) {
         const uint32_t i = i0 + k * (kThreads / 32);
-        if (i < n) {
-            const uint32_t r = segs.of(i);
-            p[k] = load8<T, VEC>(x + r * ldx, (int)(i - r * segs.n) * kSeg, lane, cols);
-        }
+        r[k] = segs.of(i);
+        c0[k] = i < n ? (int)(i - r[k] * segs.n) * kSeg : cols;  // past the last: nothing of it is read or written
+        p[k] = load8<T, VEC>(x + r[k] * ldx, c0[k], lane, cols);
     }
-#pragma unroll
-    for (int k = 0; k < kGroupsOut; ++k) {
-        const uint32_t i = i0 + k * (kThreads / 32);
-        if (i >= n)
-            return;
-        const uint32_t r = segs.of(i);
-        float v[8];
-        unpack8(p[k], v);
-        store_groups<VEC>(q + r * ldq, scale + (int64_t)r * ng, (int)(i - r * segs.n) * kSeg, lane, cols, v);
-    }
+    store_groups<T, VEC, kOut>(
+        p, lane, cols, [&](int k) { return q + r[k] * ldq; }, [&](int k) { return scale + (int64_t)r[k] * ng; },
+        [&](int k) { return c0[k]; });
 }
 
 // A row by WARPS warps (one warp: eight rows to a CTA), held in registers
@@ -77,11 +71,8 @@ __global__ void __launch_bounds__(norm_threads(WARPS))
         p[n] = load8<T, VEC>(x + r * ldx, (n * WARPS + wr) * kSeg, lane, cols);
     uint32_t top = 0;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            top = max(top, mag(to_f(p[n].v[j])));
-    }
+    for (int n = 0; n < NV; ++n)
+        top = max(top, top8(p[n]));
     top = __reduce_max_sync(0xffffffffu, top);
     if constexpr (WARPS > 1) {
         if (lane == 0)
@@ -94,8 +85,8 @@ __global__ void __launch_bounds__(norm_threads(WARPS))
         scale[r] = s.scale;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        float v[8];
-        unpack8(p[n], v);
+        float2 v[4];
+        unpack4(p[n], v);
         store8q<VEC>(q + r * ldq, (n * WARPS + wr) * kSeg, lane, cols, quant8(v, s.inv));
     }
 }
@@ -107,11 +98,11 @@ __global__ void __launch_bounds__(kThreads)
              int cols, T *__restrict__ y, int64_t ldy)
 {
     const int lane = threadIdx.x & 31, ng = (cols + kGroup - 1) / kGroup;
-    const uint32_t i0 = blockIdx.x * (kThreads / 32 * kGroupsOut) + threadIdx.x / 32;
-    uint2 w[kGroupsOut];
-    float s[kGroupsOut], t[kGroupsOut];
+    const uint32_t i0 = blockIdx.x * (kThreads / 32 * kOut) + threadIdx.x / 32;
+    uint2 w[kOut];
+    float s[kOut], t[kOut];
 #pragma unroll
-    for (int k = 0; k < kGroupsOut; ++k) {
+    for (int k = 0; k < kOut; ++k) {
         const uint32_t i = i0 + k * (kThreads / 32);
         if (i < n) {
             const uint32_t r = segs.of(i);
@@ -128,26 +119,24 @@ __global__ void __launch_bounds__(kThreads)
         }
     }
 #pragma unroll
-    for (int k = 0; k < kGroupsOut; ++k) {
+    for (int k = 0; k < kOut; ++k) {
         const uint32_t i = i0 + k * (kThreads / 32);
         if (i >= n)
             return;
         const uint32_t r = segs.of(i);
-        float v[8];
+        float2 v[4];
         unquant8(w[k], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] *= s[k];
-            v[4 + j] *= t[k];
-        }
-        store8<T, VEC>(y + r * ldy, (int)(i - r * segs.n) * kSeg, lane, cols, pack8<T>(v));
+        for (int j = 0; j < 4; ++j)
+            v[j] = mul2(v[j], both(j < 2 ? s[k] : t[k]));
+        store8<T, VEC>(y + r * ldy, (int)(i - r * segs.n) * kSeg, lane, cols, pack4<T>(v));
     }
 }
 
 // rows of one launch of the kernels over segments
-int64_t slab_of(int64_t segs) { return ((1ll << 31) - 1 - kThreads / 32 * kGroupsOut) / segs; }
+int64_t slab_of(int64_t segs) { return ((1ll << 31) - 1 - kThreads / 32 * kOut) / segs; }
 
-unsigned grid_of(int64_t segments) { return (unsigned)ceil_div(segments, kThreads / 32 * kGroupsOut); }
+unsigned grid_of(int64_t segments) { return (unsigned)ceil_div(segments, kThreads / 32 * kOut); }
 
 template <typename T, bool VEC>
 void run_pack(const void *x, int64_t ldx, int64_t nrows, int64_t cols, int32_t group, int8_t *q, int64_t ldq,

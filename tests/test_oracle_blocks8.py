@@ -20,7 +20,7 @@ def test_values_are_within_half_a_step(cols, group):
     q, s = orc.pack8(x, group)
     assert s.shape == ((7, -(-cols // 128)) if group else (7,))
     step = orc.values8(np.ones_like(q), s)
-    # half a step, and fp32's rounding of x (127 / a) of up to 127
+    # half a step, and fp32's rounding of x (127 (1 / a)) of up to 127
     assert (np.abs(orc.values8(q, s) - x) <= step * (0.5 + 127 * 2.0 ** -22)).all()
     assert np.abs(q).max() == 127
 
