@@ -20,8 +20,8 @@
 #include <utility>
 
 #include "launch.cuh"
+#include "linear8_few.cuh"
 #include "quant8.cuh"
-#include "tc_tile.cuh"
 
 namespace {
 
@@ -37,7 +37,6 @@ namespace {
             return rc_;         \
     } while (0)
 
-constexpr int kSMs = 152;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr int kBN = 256;      // tile columns
@@ -85,11 +84,6 @@ struct LinArgs {
     int32_t kt;      // rows of a box whose rows are K, where those are the tokens
     int32_t *status;
 };
-
-// errors of calls that were given no status word
-__device__ int32_t g_linear_status;
-
-__device__ __forceinline__ int32_t *lin_status(int32_t *status) { return status ? status : &g_linear_status; }
 
 struct Unit {
     int which, m0, n0, k0, nk, id;
@@ -536,13 +530,9 @@ __global__ void __launch_bounds__(256) k_widen(const Widen a)
             const float s = sc ? sc[a.group ? c / a.group : 0] * f : 1.f;
             uint32_t w[8];
             if (!sc) {
-                // a byte plus 128 as the low bits of 1024 in fp16, less 1152
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t u = in[i / 2] ^ 0x80808080u, h = __byte_perm(u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
-                    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half(0x6480)));
-                    w[i] = *reinterpret_cast<const uint32_t *>(&v);
-                }
+                for (int i = 0; i < 8; ++i)
+                    w[i] = bytes_f16(in[i / 2] ^ 0x80808080u, i & 1);
             } else {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -814,6 +804,10 @@ sg_status sg_linear8_work(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, c
     *bytes = 0;
     if (T == 0)
         return SG_OK;
+    if (!backward && is_few(x8, ldx, T, W8, ldw)) {
+        *bytes = few_work(T, H, N);
+        return SG_OK;
+    }
     // backward: either gradient may be left out, which changes the splits
     for (int i = 0; i < (backward ? 3 : 1); ++i) {
         Plan p;
@@ -841,11 +835,17 @@ sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
         LIN_FAIL(SG_ERR_INVALID, "%s: out has a row stride below N or is not aligned to its elements", fn);
     if (T == 0)
         return SG_OK;
+    const bool few = is_few(x8, ldx, T, W8, ldw);
     Plan pl;
-    make_plan(T, H, N, nullptr, 0, false, false, false, &pl);
-    if (!work || work_bytes < pl.bytes || ((uintptr_t)work & 255) != 0)
+    if (few)
+        pl.bytes = few_work(T, H, N);
+    else
+        make_plan(T, H, N, nullptr, 0, false, false, false, &pl);
+    if (pl.bytes && (!work || work_bytes < pl.bytes || ((uintptr_t)work & 255) != 0))
         LIN_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_linear8_work), aligned to 256", fn, (long long)pl.bytes);
     cudaStream_t st = (cudaStream_t)stream;
+    if (few)
+        return few_fwd(x8, ldx, x_scale, T, H, W8, ldw, W_scale, N, out, ldo, dtype, work, status, st);
     uint8_t *w8 = static_cast<uint8_t *>(work);
     LIN_TRY(widen(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true, st));
     for (int64_t n0 = 0; n0 < N; n0 += pl.Nc) {

@@ -1,0 +1,546 @@
+// The 8-bit linear layer's forward pass for at most 128 tokens: bound by reading
+// W8, so its bytes are read once and are brought to fp16 on the chip.
+//
+// Channels are the rows of the product: a tile has 128 of them, and out^T = W x^T
+// has the tokens as columns.  TMA streams blocks of 128 x 128 bytes of W8, and
+// the tokens' bytes of the same K, through a ring of stages.  Two teams of four
+// warps take the blocks in turn: a thread has a channel, turns its 128 bytes into
+// fp16 (a byte permutation and a subtraction for two) and stores them in tensor
+// memory, from where the MMA reads its A operand; the tokens' bytes become fp16
+// rows in shared memory (128-byte swizzle), its B operand.  One thread issues the
+// MMAs into one of two accumulators, epilogue warps add up the other one, of 1024
+// terms, in fp32 registers.
+//
+// The blocks of all tiles are cut into equal ranges for the SMs, so that all of
+// them read to the end.  Tiles that a cut falls into are written as fp32 parts and
+// joined in a fixed order by a small kernel; where whole tiles leave less idle
+// time than that takes, the cuts go between tiles.
+#pragma once
+
+#include "launch.cuh"
+#include "tc_tile.cuh"
+
+namespace {
+
+constexpr int kSMs = 152;
+
+// errors of calls that were given no status word
+__device__ int32_t g_linear_status;
+
+__device__ __forceinline__ int32_t *lin_status(int32_t *status) { return status ? status : &g_linear_status; }
+
+// two of four int8 (bytes 0 and 1, or 2 and 3 of u ^ 0x80808080) as fp16: a byte
+// plus 128 as the low bits of 1024, less 1152
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t u, int half)
+{
+    const uint32_t h = __byte_perm(u, 0x64646464u, half ? 0x4342 : 0x4140);
+    const __half2 v =
+        __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half((unsigned short)0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+constexpr int kBlockK = 128;   // bytes of K in a block
+constexpr int kChunk = 8;      // blocks that are summed in tensor memory: 1024 terms
+constexpr uint32_t kWTile = 128 * kBlockK;
+
+// for up to TMAX tokens: stages, operand buffers, epilogue warps
+template <int TMAX>
+struct Few {
+    static constexpr int NS = TMAX <= 16 ? 10 : TMAX <= 64 ? 6 : 5;
+    static constexpr int NB = TMAX <= 64 ? 4 : 2;
+    static constexpr int EW = TMAX <= 64 ? 4 : 8;
+    static constexpr int kCols = TMAX / (EW / 4);  // tokens of an epilogue thread
+    static constexpr int kThreads = 32 * (8 + EW + 2);
+    static constexpr uint32_t kStage = kWTile + TMAX * kBlockK;
+    static constexpr uint32_t kX = TMAX * kBlockK * 2;  // a buffer of the tokens in fp16
+    static constexpr uint32_t kSmem = NS * kStage + NB * kX + 1024;
+    static constexpr uint32_t kA = 2 * TMAX < 64 ? 64 : 2 * TMAX;  // first column of the A buffers, after D's
+};
+
+struct FewCtl {
+    uint64_t full[10], empty[10], ready[4], freed[4], tfull[2], tempty[2];
+    uint32_t tmem;
+    int abort_flag;
+    float xs[128];
+};
+
+struct FewArgs {
+    int32_t T, N, tn;     // tokens, channels, columns of the product (a multiple of 16)
+    int32_t xb;           // rows of a box of the tokens
+    int32_t kb, tiles;    // blocks of a tile, tiles
+    int32_t whole;        // ranges are whole tiles
+    int32_t ctas, per, more;  // ranges of `per` blocks (whole: tiles), the first `more` of one more
+    int32_t otype;
+    const float *xs, *ws;
+    void *out;
+    int64_t ldo;
+    float *part;          // [slot][tn][128]
+    int32_t *status;
+};
+
+// first block of CTA c's range
+__host__ __device__ __forceinline__ int64_t range_at(const FewArgs &a, int c)
+{
+    return ((int64_t)a.per * c + (c < a.more ? c : a.more)) * (a.whole ? a.kb : 1);
+}
+
+// A CTA's range, tile by tile: segments of blocks [k, k + n) of a tile
+struct Segment {
+    int tile, k, n;
+};
+
+__device__ __forceinline__ bool segment_at(const FewArgs &a, int64_t &b, int64_t end, Segment &s)
+{
+    if (b >= end)
+        return false;
+    s.tile = (int)(b / a.kb);
+    s.k = (int)(b - (int64_t)s.tile * a.kb);
+    s.n = (int)(end - b < a.kb - s.k ? end - b : a.kb - s.k);
+    b += s.n;
+    return true;
+}
+
+__device__ __forceinline__ void put(float *p, float z) { *p = z; }
+__device__ __forceinline__ void put(__half *p, float z) { *p = __float2half_rn(z); }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float z) { *p = __float2bfloat16_rn(z); }
+
+// f with a pointer of the output's type to element `at`
+template <typename F>
+__device__ __forceinline__ void with_out(const FewArgs &a, int64_t at, F f)
+{
+    if (a.otype == SG_F32)
+        f(static_cast<float *>(a.out) + at);
+    else if (a.otype == SG_F16)
+        f(static_cast<__half *>(a.out) + at);
+    else
+        f(static_cast<__nv_bfloat16 *>(a.out) + at);
+}
+
+template <int TMAX>
+__global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
+    k_few(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mx,
+          const __grid_constant__ FewArgs a)
+{
+    using F = Few<TMAX>;
+    constexpr int NS = F::NS, NB = F::NB, EW = F::EW;
+    __shared__ FewCtl c;
+    extern __shared__ uint8_t dsm[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        c.abort_flag = 0;
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&c.full[s]), 1);
+            mbar_init(smem_u32(&c.empty[s]), 4);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(smem_u32(&c.ready[b]), 4);
+            mbar_init(smem_u32(&c.freed[b]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c.tfull[b]), 1);
+            mbar_init(smem_u32(&c.tempty[b]), EW);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 9 + EW) {
+        tmem_alloc(smem_u32(&c.tmem), 512);
+        tmem_relinquish();
+    }
+    grid_wait();
+    grid_go();
+    if (threadIdx.x < 128)
+        c.xs[threadIdx.x] = (int)threadIdx.x < a.T ? a.xs[threadIdx.x] : 0.f;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = c.tmem;
+    volatile int *abort_flag = &c.abort_flag;
+    int32_t *status = lin_status(a.status);
+    const int64_t first = range_at(a, (int)blockIdx.x), end = range_at(a, (int)blockIdx.x + 1);
+    const int nblocks = (int)(end - first);
+
+    if (warp < 8) {
+        // ---------------------------------------------------------- bytes to fp16
+        const int team = warp >> 2, q = warp & 3, row = q * 32 + lane, tid = threadIdx.x & 127;
+        for (int i = team; i < nblocks; i += 2) {
+            const int s = i % NS, b = i % NB;
+            const uint32_t st = base + (uint32_t)s * F::kStage, xf = base + NS * F::kStage + (uint32_t)b * F::kX;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[s]), (uint32_t)(i / NS) & 1u, abort_flag, status)) ||
+                !__all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&c.freed[b]), ((uint32_t)(i / NB) & 1u) ^ 1u, abort_flag, status)))
+                break;
+            tc_fence_after();
+            const uint8_t *src = dsm + (st - smem_u32(dsm));
+            const uint32_t ta = tbase + F::kA + (uint32_t)b * 64 + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + row * 128 + (((4 * h + u) ^ (row & 7)) << 4));
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        r[u * 8 + 2 * j] = bytes_f16(in[j] ^ 0x80808080u, 0);
+                        r[u * 8 + 2 * j + 1] = bytes_f16(in[j] ^ 0x80808080u, 1);
+                    }
+                }
+                tmem_st32(ta + h * 32, r);
+            }
+            // the tokens: 16 bytes to a thread at a time, eight threads to a row
+            uint8_t *dst = dsm + (xf - smem_u32(dsm));
+            for (int e = tid; e < a.tn * 8; e += 128) {
+                const int t = e >> 3, u = e & 7;
+                const uint4 w = *reinterpret_cast<const uint4 *>(src + kWTile + t * 128 + ((u ^ (t & 7)) << 4));
+                uint8_t *at = dst + (u >> 2) * (a.tn * 128) + t * 128;
+                const int v = (u & 3) * 2;
+                uint32_t p[8];
+                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    p[2 * j] = bytes_f16(in[j] ^ 0x80808080u, 0);
+                    p[2 * j + 1] = bytes_f16(in[j] ^ 0x80808080u, 1);
+                }
+                *reinterpret_cast<uint4 *>(at + ((v ^ (t & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                *reinterpret_cast<uint4 *>(at + (((v + 1) ^ (t & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
+            }
+            tmem_st_wait();
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&c.empty[s]));
+                mbar_arrive(smem_u32(&c.ready[b]));
+            }
+        }
+    } else if (warp < 8 + EW) {
+        // ---------------------------------------------------------- epilogue
+        // a thread has a channel and up to kCols tokens
+        const int q = warp & 3, t0 = (warp - 8) / 4 * F::kCols;
+        const int cols = min(F::kCols, a.tn - t0);  // a multiple of 16, or nothing to do
+        int64_t b = first;
+        Segment s;
+        int it = 0;
+        bool ok = true;
+        while (ok && segment_at(a, b, end, s)) {
+            const int n = s.tile * 128 + q * 32 + lane;
+            const float ws = n < a.N ? a.ws[n] : 0.f;
+            float v[F::kCols / 16][16] = {};
+            for (int k = 0; k < s.n; k += kChunk, ++it) {
+                const int buf = it & 1;
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(smem_u32(&c.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, status));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t tm = tbase + (uint32_t)(buf * TMAX + t0) + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+                for (int cc = 0; cc < F::kCols / 16; ++cc) {
+                    if (cc * 16 < cols) {
+                        float w[16];
+                        tmem_ld_chunk<16>(tm + cc * 16, w);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            v[cc][x] += w[x];
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&c.tempty[buf]));
+            }
+            if (!ok)
+                break;
+            if (s.n < a.kb) {
+                // a part: the range's first if it does not begin its tile
+                float *p = a.part + ((int64_t)(2 * blockIdx.x + (s.k == 0 ? 1 : 0)) * a.tn + t0) * 128 + q * 32 + lane;
+#pragma unroll
+                for (int cc = 0; cc < F::kCols / 16; ++cc)
+                    if (cc * 16 < cols) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            p[(cc * 16 + x) * 128] = v[cc][x];
+                    }
+            } else if (n < a.N) {
+                with_out(a, t0 * a.ldo + n, [&](auto *p) {
+#pragma unroll
+                    for (int cc = 0; cc < F::kCols / 16; ++cc) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x, p += a.ldo)
+                            if (t0 + cc * 16 + x < a.T)
+                                put(p, v[cc][x] * c.xs[t0 + cc * 16 + x] * ws);
+                        asm volatile("" ::: "memory");  // or the scales of all tokens are loaded first, and spilled
+                    }
+                });
+            }
+        }
+    } else if (warp == 8 + EW) {
+        // ---------------------------------------------------------- producer
+        if (lane == 0) {
+            int64_t b = first;
+            Segment s;
+            Ring r;
+            bool ok = true;
+            const uint32_t bytes = kWTile + (uint32_t)a.xb * kBlockK;
+            while (ok && segment_at(a, b, end, s))
+                for (int k = s.k; k < s.k + s.n; ++k, r.next(NS)) {
+                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status);
+                    if (!ok)
+                        break;
+                    const uint32_t bar = smem_u32(&c.full[r.i]), st = base + (uint32_t)r.i * F::kStage;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    tma_load_2d(st, &mW, k * kBlockK, s.tile * 128, bar);
+                    tma_load_2d(st + kWTile, &mx, k * kBlockK, 0, bar);
+                }
+            if (!ok) {
+                // gave up: copies on their way land long before this
+                const uint64_t t0 = global_ns();
+                while (global_ns() - t0 < 1000000u) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- MMA
+        const uint32_t idesc = idesc_f16(128, a.tn, 0, 0);
+        int64_t b = first;
+        Segment s;
+        Ring r;
+        int it = 0;
+        bool ok = true;
+        while (ok && segment_at(a, b, end, s)) {
+            for (int k = 0; ok && k < s.n; ++it) {
+                const int buf = it & 1, stop = min(s.n, k + kChunk);
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u,
+                                                       abort_flag, status));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                for (int k0 = k; k < stop; ++k) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.ready[r.i]), r.ph, abort_flag, status));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t xf = base + NS * F::kStage + (uint32_t)r.i * F::kX;
+                        const OpDesc dx(xf, false);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(tbase + buf * TMAX, tbase + F::kA + (uint32_t)r.i * 64 + ks * 8,
+                                   dx.at((uint32_t)(ks >> 2) * (a.tn * 128 / 16), ks & 3), idesc,
+                                   (k > k0 || ks > 0) ? 1u : 0u);
+                        mma_commit(smem_u32(&c.freed[r.i]));
+                    }
+                    __syncwarp();
+                    r.next(NB);
+                }
+                if (ok && lane == 0)
+                    mma_commit(smem_u32(&c.tfull[buf]));
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9 + EW) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// The parts of the tile that the cut before CTA `blockIdx.x + 1` falls into,
+// where it is the tile's first cut: added in the order of K.  A thread has a
+// channel and a token; the loads of its parts are under way together.
+__global__ void __launch_bounds__(256) k_few_join(const __grid_constant__ FewArgs a)
+{
+    const int c0 = (int)blockIdx.x;  // has the tile's first blocks
+    const int64_t cut = range_at(a, c0 + 1), tile = cut / a.kb, stop = (tile + 1) * a.kb;
+    int last = c0 + 1;  // one past the tile's last CTA
+    while (last < a.ctas && range_at(a, last) < stop)
+        ++last;
+    const int lane = threadIdx.x & 127, n = (int)tile * 128 + lane, t = (int)blockIdx.y * 2 + threadIdx.x / 128;
+    grid_wait();
+    if (cut == tile * a.kb || range_at(a, c0) > tile * a.kb || n >= a.N || t >= a.T)
+        return;
+    const int64_t step = (int64_t)2 * a.tn * 128;
+    const float *p = a.part + ((int64_t)(2 * c0 + 1) * a.tn + t) * 128 + lane;
+    float z = *p;
+    p += step - (int64_t)a.tn * 128;
+#pragma unroll 8
+    for (int c = c0 + 1; c < last; ++c, p += step)
+        z += *p;
+    with_out(a, t * a.ldo + n, [&](auto *o) { put(o, z * a.xs[t] * a.ws[n]); });
+}
+
+FewArgs few_args(int64_t T, int64_t H, int64_t N)
+{
+    FewArgs a = {};
+    a.T = (int32_t)T;
+    a.N = (int32_t)N;
+    a.tn = (int32_t)ceil_div(T, 16) * 16;
+    a.xb = (int32_t)ceil_div(T, 8) * 8;
+    a.kb = (int32_t)ceil_div(H, kBlockK);
+    a.tiles = (int32_t)ceil_div(N, 128);
+    // whole tiles where they keep the last SM less than five blocks (about 2 us)
+    // longer than equal ranges would
+    a.whole = ceil_div(a.tiles, kSMs) * a.kb - (int64_t)a.tiles * a.kb / kSMs < 5;
+    // at least one tile, or two blocks, to a range
+    const int64_t n = a.whole ? a.tiles : (int64_t)a.tiles * a.kb, most = a.whole ? n : ceil_div(n, 2);
+    a.ctas = (int32_t)(most < kSMs ? most : kSMs);
+    a.per = (int32_t)(n / a.ctas);
+    a.more = (int32_t)(n % a.ctas);
+    return a;
+}
+
+template <int TMAX>
+sg_status launch_few(const CUtensorMap &mW, const CUtensorMap &mx, const FewArgs &a, cudaStream_t st)
+{
+    // once for each device (one bit of the mask)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    SG_TRY_CUDA(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        SG_TRY_CUDA(cudaFuncSetAttribute(k_few<TMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<TMAX>::kSmem));
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch(k_few<TMAX>, dim3((unsigned)a.ctas), Few<TMAX>::kThreads, (int)Few<TMAX>::kSmem, 1, true, st, mW, mx, a);
+}
+
+// ---------------------------------------------------------------- a few rows by integer dot products
+// One to four tokens: a warp has two channels, a lane every 32nd 16 bytes of
+// their rows, and sums of up to kMostDot products in 32-bit integers are exact.
+constexpr int kDotTokens = 4;
+constexpr int64_t kMostDot = (1 << 17) - 1;
+constexpr int kDotRows = 2, kDotThreads = 256;
+
+// 16 bytes at column c of a row, 0 past the last
+__device__ __forceinline__ uint4 bytes16(const int8_t *row, int c, int H)
+{
+    if (c + 16 <= H)
+        return *reinterpret_cast<const uint4 *>(row + c);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (c + j < H)
+            w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int dot16(uint4 a, uint4 b, int s)
+{
+    s = __dp4a((int)a.x, (int)b.x, s);
+    s = __dp4a((int)a.y, (int)b.y, s);
+    s = __dp4a((int)a.z, (int)b.z, s);
+    return __dp4a((int)a.w, (int)b.w, s);
+}
+
+template <int TT>
+__global__ void __launch_bounds__(kDotThreads)
+    k_dot(const int8_t *__restrict__ x8, int64_t ldx, const int8_t *__restrict__ W8, int64_t ldw, int H,
+          const __grid_constant__ FewArgs a)
+{
+    constexpr int U = 4;  // 16 bytes of a row under way together
+    const int lane = threadIdx.x & 31;
+    const int n0 = (blockIdx.x * (kDotThreads / 32) + threadIdx.x / 32) * kDotRows;
+    grid_wait();
+    grid_go();
+    if (n0 >= a.N)
+        return;
+    const int8_t *w[kDotRows];
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r)
+        w[r] = W8 + (int64_t)min(n0 + r, a.N - 1) * ldw;
+    int sum[kDotRows][TT] = {};
+    int c = lane * 16;
+    for (; c + (U - 1) * 512 + 16 <= H; c += U * 512) {
+        uint4 v[kDotRows][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < kDotRows; ++r)
+                v[r][u] = __ldcs(reinterpret_cast<const uint4 *>(w[r] + c + u * 512));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const uint4 x = t < a.T ? *reinterpret_cast<const uint4 *>(x8 + t * ldx + c + u * 512)
+                                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < kDotRows; ++r)
+                    sum[r][t] = dot16(v[r][u], x, sum[r][t]);
+            }
+    }
+    for (; c < H; c += 512) {
+        uint4 v[kDotRows];
+#pragma unroll
+        for (int r = 0; r < kDotRows; ++r)
+            v[r] = bytes16(w[r], c, H);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const uint4 x = t < a.T ? bytes16(x8 + t * ldx, c, H) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < kDotRows; ++r)
+                sum[r][t] = dot16(v[r], x, sum[r][t]);
+        }
+    }
+    int mine = 0;  // lane r TT + t has token t of channel n0 + r
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const int z = __reduce_add_sync(0xffffffffu, sum[r][t]);
+            mine = lane == r * TT + t ? z : mine;
+        }
+    const int t = lane % TT, n = n0 + lane / TT;
+    if (lane < kDotRows * TT && t < a.T && n < a.N)
+        with_out(a, t * a.ldo + n, [&](auto *p) { put(p, (float)mine * a.xs[t] * a.ws[n]); });
+}
+
+template <int TT>
+sg_status launch_dot(const int8_t *x8, int64_t ldx, const int8_t *W8, int64_t ldw, int64_t H, const FewArgs &a,
+                     cudaStream_t st)
+{
+    const int rows = kDotThreads / 32 * kDotRows;
+    return launch(k_dot<TT>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, true, st, x8, ldx, W8, ldw, (int)H, a);
+}
+
+bool is_few(const int8_t *x8, int64_t ldx, int64_t T, const int8_t *W8, int64_t ldw)
+{
+    return T <= 128 && tma_ok(x8, ldx, 1) && tma_ok(W8, ldw, 1);
+}
+
+bool by_dot(int64_t T, int64_t H) { return T <= kDotTokens && H <= kMostDot; }
+
+int64_t few_work(int64_t T, int64_t H, int64_t N)
+{
+    const FewArgs a = few_args(T, H, N);
+    return by_dot(T, H) || a.whole ? 0 : (int64_t)2 * kSMs * a.tn * 128 * 4;
+}
+
+sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
+                  const float *ws, int64_t N, void *out, int64_t ldo, int32_t dtype, void *work, int32_t *status,
+                  cudaStream_t st)
+{
+    FewArgs a = few_args(T, H, N);
+    a.otype = dtype;
+    a.xs = xs, a.ws = ws, a.out = out, a.ldo = ldo;
+    a.part = static_cast<float *>(work);
+    a.status = status;
+    if (by_dot(T, H))
+        return T == 1   ? launch_dot<1>(x8, ldx, W8, ldw, H, a, st)
+               : T == 2 ? launch_dot<2>(x8, ldx, W8, ldw, H, a, st)
+                        : launch_dot<4>(x8, ldx, W8, ldw, H, a, st);
+    CUtensorMap mW, mx;
+    sg_status rc = map_of(&mW, W8, H, N, ldw, 1, "W8", 128);
+    if (rc == SG_OK)
+        rc = map_of(&mx, x8, H, T, ldx, 1, "x8", (uint32_t)a.xb);
+    if (rc == SG_OK)
+        rc = T <= 16 ? launch_few<16>(mW, mx, a, st) : T <= 64 ? launch_few<64>(mW, mx, a, st) : launch_few<128>(mW, mx, a, st);
+    if (rc != SG_OK || a.whole || a.ctas == 1)
+        return rc;
+    return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T, 2)), 256, 0, 1, true, st, a);
+}
+
+}  // namespace

@@ -89,7 +89,7 @@ def test_linear_refusals_and_work(lib):
         rc = lib.sg_linear8_work(*a, C.byref(n))
         return n.value if rc == 0 else rc
 
-    assert work(P, 64, 100, 64, P, 64, 1000, None, 0, 0) > 0
+    assert work(P, 64, 300, 64, P, 64, 1000, None, 0, 0) > 0
     assert work(P, 64, 0, 64, P, 64, 1000, None, 0, 0) == 0
     back = work(P, 64, 100, 64, P, 64, 1000, P, 1000, 1)
     # dout's rows that do not start on 16 bytes are copied
@@ -128,4 +128,4 @@ def test_forward_work_memory_is_bounded(lib, T, H, N):
     most four turns of the tiles (a tile of fp32 sums is 256 KB for two CTAs)."""
     n = C.c_int64(-1)
     assert lib.sg_linear8_work(P, H, T, H, P, H, N, None, 0, 0, C.byref(n)) == 0
-    assert 0 < n.value <= (256 << 20) + 2 * T * H + 4 * 152 * 131072 + 4096
+    assert 0 <= n.value <= (256 << 20) + 2 * T * H + 4 * 152 * 131072 + 4096
