@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok)
                             break;
                         tc_fence_after();
-                        if (lane == 0) {
+                        if (elect_one()) {
                             const uint32_t st = (uint32_t)r.i * (K::kStage / 16);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks) {
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         r.next(NS);
                     }
-                    if (ok && lane == 0)
+                    if (ok && elect_one())
                         mma_commit_cg<CG>(smem_u32(&c.tfull[buf]));
                     __syncwarp();
                 }

@@ -3,8 +3,8 @@
 //
 // Channels are the rows of the product: a tile has 128 of them, and out^T = W x^T
 // has the tokens as columns.  TMA streams blocks of 128 x 128 bytes of W8, and
-// the tokens' bytes of the same K, through a ring of stages.  Two teams of four
-// warps take the blocks in turn: a thread has a channel, turns its 128 bytes into
+// the tokens' bytes of the same K, through a ring of stages.  Teams of four warps take
+// the blocks in turn: a thread has a channel, turns its 128 bytes into
 // fp16 (a byte permutation and a subtraction for two) and stores them in tensor
 // memory, from where the MMA reads its A operand; the tokens' bytes become fp16
 // rows in shared memory (128-byte swizzle), its B operand.  One thread issues the
@@ -43,14 +43,16 @@ constexpr int kBlockK = 128;   // bytes of K in a block
 constexpr int kChunk = 8;      // blocks that are summed in tensor memory: 1024 terms
 constexpr uint32_t kWTile = 128 * kBlockK;
 
-// for up to TMAX tokens: stages, operand buffers, epilogue warps
+// for up to TMAX tokens: stages, operand buffers, teams, epilogue warps
 template <int TMAX>
 struct Few {
     static constexpr int NS = TMAX <= 16 ? 10 : TMAX <= 64 ? 6 : 5;
     static constexpr int NB = TMAX <= 64 ? 4 : 2;
-    static constexpr int EW = TMAX <= 64 ? 4 : 8;
+    static constexpr int TEAMS = TMAX <= 64 ? 4 : 2;
+    static constexpr int CW = 4 * TEAMS;  // warps that turn bytes into fp16
+    static constexpr int EW = TMAX <= 16 ? 4 : 8;
     static constexpr int kCols = TMAX / (EW / 4);  // tokens of an epilogue thread
-    static constexpr int kThreads = 32 * (8 + EW + 2);
+    static constexpr int kThreads = 32 * (CW + EW + 2);
     static constexpr uint32_t kStage = kWTile + TMAX * kBlockK;
     static constexpr uint32_t kX = TMAX * kBlockK * 2;  // a buffer of the tokens in fp16
     static constexpr uint32_t kSmem = NS * kStage + NB * kX + 1024;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
           const __grid_constant__ FewArgs a)
 {
     using F = Few<TMAX>;
-    constexpr int NS = F::NS, NB = F::NB, EW = F::EW;
+    constexpr int NS = F::NS, NB = F::NB, EW = F::EW, CW = F::CW;
     __shared__ FewCtl c;
     extern __shared__ uint8_t dsm[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         }
         fence_mbar_init();
     }
-    if (warp == 9 + EW) {
+    if (warp == CW + EW + 1) {
         tmem_alloc(smem_u32(&c.tmem), 512);
         tmem_relinquish();
     }
@@ -160,20 +162,26 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
     const int64_t first = range_at(a, (int)blockIdx.x), end = range_at(a, (int)blockIdx.x + 1);
     const int nblocks = (int)(end - first);
 
-    if (warp < 8) {
+    if (warp < CW) {
         // ---------------------------------------------------------- bytes to fp16
         const int team = warp >> 2, q = warp & 3, row = q * 32 + lane, tid = threadIdx.x & 127;
-        for (int i = team; i < nblocks; i += 2) {
+        for (int i = team; i < nblocks; i += F::TEAMS) {
             const int s = i % NS, b = i % NB;
             const uint32_t st = base + (uint32_t)s * F::kStage, xf = base + NS * F::kStage + (uint32_t)b * F::kX;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[s]), (uint32_t)(i / NS) & 1u, abort_flag, status)) ||
-                !__all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(&c.freed[b]), ((uint32_t)(i / NB) & 1u) ^ 1u, abort_flag, status)))
+            // The operand buffer first: it is free when the MMAs of block i - NB are
+            // done, which are issued in order, so the bytes of block i - NS, that
+            // the stage had before, have arrived.  A team that waited for its stage
+            // first could come to it while those were still on their way, and take
+            // the barrier's phase before them for its own.
+            static_assert(NB <= NS, "a stage is taken again after its buffer");
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&c.freed[b]), ((uint32_t)(i / NB) & 1u) ^ 1u, abort_flag, status)) ||
+                !__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[s]), (uint32_t)(i / NS) & 1u, abort_flag, status)))
                 break;
             tc_fence_after();
             const uint8_t *src = dsm + (st - smem_u32(dsm));
             const uint32_t ta = tbase + F::kA + (uint32_t)b * 64 + ((uint32_t)(q * 32) << 16);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
 #pragma unroll
@@ -202,8 +210,12 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                     p[2 * j] = bytes_f16(in[j] ^ 0x80808080u, 0);
                     p[2 * j + 1] = bytes_f16(in[j] ^ 0x80808080u, 1);
                 }
-                *reinterpret_cast<uint4 *>(at + ((v ^ (t & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-                *reinterpret_cast<uint4 *>(at + (((v + 1) ^ (t & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
+                // half of a row's threads begin with their second 16 bytes: the
+                // two halves' rows lie in the same banks
+                const bool odd = u >= 4;
+                const uint4 lo = make_uint4(p[0], p[1], p[2], p[3]), hi = make_uint4(p[4], p[5], p[6], p[7]);
+                *reinterpret_cast<uint4 *>(at + (((v + odd) ^ (t & 7)) << 4)) = odd ? hi : lo;
+                *reinterpret_cast<uint4 *>(at + (((v + !odd) ^ (t & 7)) << 4)) = odd ? lo : hi;
             }
             tmem_st_wait();
             fence_proxy_async();
@@ -214,10 +226,10 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                 mbar_arrive(smem_u32(&c.ready[b]));
             }
         }
-    } else if (warp < 8 + EW) {
+    } else if (warp < CW + EW) {
         // ---------------------------------------------------------- epilogue
         // a thread has a channel and up to kCols tokens
-        const int q = warp & 3, t0 = (warp - 8) / 4 * F::kCols;
+        const int q = warp & 3, t0 = (warp - CW) / 4 * F::kCols;
         const int cols = min(F::kCols, a.tn - t0);  // a multiple of 16, or nothing to do
         int64_t b = first;
         Segment s;
@@ -275,7 +287,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                 });
             }
         }
-    } else if (warp == 8 + EW) {
+    } else if (warp == CW + EW) {
         // ---------------------------------------------------------- producer
         if (lane == 0) {
             int64_t b = first;
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                     if (!ok)
                         break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint32_t xf = base + NS * F::kStage + (uint32_t)r.i * F::kX;
                         const OpDesc dx(xf, false);
 #pragma unroll
@@ -335,7 +347,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                     __syncwarp();
                     r.next(NB);
                 }
-                if (ok && lane == 0)
+                if (ok && elect_one())
                     mma_commit(smem_u32(&c.tfull[buf]));
                 __syncwarp();
             }
@@ -343,7 +355,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9 + EW) {
+    if (warp == CW + EW + 1) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
@@ -351,26 +363,37 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
 
 // The parts of the tile that the cut before CTA `blockIdx.x + 1` falls into,
 // where it is the tile's first cut: added in the order of K.  A thread has a
-// channel and a token; the loads of its parts are under way together.
+// channel and every 2 gridDim.y-th token; the loads of its parts are under way
+// together.  The places are worked out once for a CTA (by every thread, the join
+// of 48 x 2048 x 128000 took 10 us).
 __global__ void __launch_bounds__(256) k_few_join(const __grid_constant__ FewArgs a)
 {
+    __shared__ int sm[2];
     const int c0 = (int)blockIdx.x;  // has the tile's first blocks
-    const int64_t cut = range_at(a, c0 + 1), tile = cut / a.kb, stop = (tile + 1) * a.kb;
-    int last = c0 + 1;  // one past the tile's last CTA
-    while (last < a.ctas && range_at(a, last) < stop)
-        ++last;
-    const int lane = threadIdx.x & 127, n = (int)tile * 128 + lane, t = (int)blockIdx.y * 2 + threadIdx.x / 128;
+    if (threadIdx.x == 0) {
+        const int64_t cut = range_at(a, c0 + 1), tile = cut / a.kb, stop = (tile + 1) * a.kb;
+        int parts = 1;  // after the first
+        while (c0 + 1 + parts < a.ctas && range_at(a, c0 + 1 + parts) < stop)
+            ++parts;
+        sm[0] = (int)tile;
+        sm[1] = cut == tile * a.kb || range_at(a, c0) > tile * a.kb ? 0 : parts;
+    }
+    __syncthreads();
     grid_wait();
-    if (cut == tile * a.kb || range_at(a, c0) > tile * a.kb || n >= a.N || t >= a.T)
+    const int lane = threadIdx.x & 127, n = sm[0] * 128 + lane, parts = sm[1];
+    if (parts == 0 || n >= a.N)
         return;
-    const int64_t step = (int64_t)2 * a.tn * 128;
-    const float *p = a.part + ((int64_t)(2 * c0 + 1) * a.tn + t) * 128 + lane;
-    float z = *p;
-    p += step - (int64_t)a.tn * 128;
-#pragma unroll 8
-    for (int c = c0 + 1; c < last; ++c, p += step)
-        z += *p;
-    with_out(a, t * a.ldo + n, [&](auto *o) { put(o, z * a.xs[t] * a.ws[n]); });
+    const int step = 2 * a.tn * 128;
+    const float ws = a.ws[n], *head = a.part + (int64_t)(2 * c0 + 1) * a.tn * 128 + lane;
+    const float *rest = head + a.tn * 128;
+#pragma unroll 2
+    for (int t = (int)blockIdx.y * 2 + threadIdx.x / 128; t < a.T; t += 2 * gridDim.y) {
+        float z = head[t * 128];
+#pragma unroll 4
+        for (int c = 0; c < parts; ++c)
+            z += rest[(int64_t)c * step + t * 128];
+        with_out(a, t * a.ldo + n, [&](auto *o) { put(o, z * a.xs[t] * ws); });
+    }
 }
 
 FewArgs few_args(int64_t T, int64_t H, int64_t N)
@@ -540,7 +563,7 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
         rc = T <= 16 ? launch_few<16>(mW, mx, a, st) : T <= 64 ? launch_few<64>(mW, mx, a, st) : launch_few<128>(mW, mx, a, st);
     if (rc != SG_OK || a.whole || a.ctas == 1)
         return rc;
-    return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T, 2)), 256, 0, 1, true, st, a);
+    return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T, 8)), 256, 0, 1, true, st, a);
 }
 
 }  // namespace

@@ -700,3 +700,21 @@ def test_binding_refuses_what_the_library_cannot_see():
         sg.sg_block_norm_bwd(x, q, q, w, w, r, r, x.clone(), x_scale=s)
     with pytest.raises(ValueError):  # one scale for a row
         sg.sg_block_norm_bwd(x, q, q, w, w, r, r, x.clone(), x_scale=r, u_scale=r)
+
+
+@pytest.mark.parametrize("T", [16, 33, 48, 64, 100])
+def test_linear_of_many_channels_again_and_again(T):
+    """W from memory rather than the L2 cache, whose loads complete out of
+    order: each launch gives the same result."""
+    H, N = 2048, 90000
+    x8, W8, xs, ws = rand8(T, H, 1), rand8(N, H, 2), scales(T, 3), scales(N, 4)
+    out = torch.empty((T, N), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sg_linear8_fwd(x8, xs, W8, ws, out, status=status)
+    at = torch.randint(0, N, (200,), generator=gen(7), device="cuda")
+    check_forward(x8, xs, W8[at], ws[at], out[:, at], "f32")
+    first = out.clone()
+    for _ in range(60):
+        sg.sg_linear8_fwd(x8, xs, W8, ws, out.zero_(), status=status)
+        assert torch.equal(out, first)
+    assert int(status) == 0
