@@ -208,19 +208,32 @@ struct BlockBwd {
 };
 
 // A thread's pieces of the next rows on their way to shared memory, as Ring8:
-// dy and du_in, and x and u, or (HELD) their eight bytes in one unit and their
-// scales in another.
-template <typename T, bool HELD, int NV, int S, int THREADS>
-struct BackRing {
+// dy and du_in, and x and u, or (HELD) their eight bytes and the scale of its
+// group, which the lanes of a warp copy for each other in pieces of 16 bytes: after
+// the wait for the copies comes a __syncwarp.  (Copies of each lane's own 8 bytes
+// and scale: 155 us for 16384 x 4096.)
+template <typename T, bool HELD, int NV, int THREADS>
+struct BackRows {
     static constexpr int P = sizeof(Pack8<T>) / 16;
-    static constexpr int kUnits = HELD ? 2 * P + 2 : 4 * P;
-    static constexpr int kBytes = S * NV * kUnits * THREADS * 16;
-    uint4 *base;
+    static constexpr int k16 = HELD ? 2 * P : 4 * P;  // pieces of 16 bytes
+    static constexpr int kScales = THREADS / 16;
+    static constexpr int kPart = k16 * THREADS * 16 + (HELD ? 2 * (THREADS * 8 + kScales * 4) : 0);  // a segment's
+    static constexpr int kRow = NV * kPart;
+    uint8_t *base;
 
-    __device__ __forceinline__ explicit BackRing(void *smem) : base(static_cast<uint4 *>(smem) + threadIdx.x) {}
-    __device__ __forceinline__ uint4 *at(int slot, int n, int unit) const
+    __device__ __forceinline__ explicit BackRows(void *smem) : base(static_cast<uint8_t *>(smem)) {}
+    __device__ __forceinline__ uint8_t *part(int slot, int n) const { return base + (slot * NV + n) * kPart; }
+    __device__ __forceinline__ uint4 *at(int slot, int n, int piece) const
     {
-        return base + ((slot * NV + n) * kUnits + unit) * THREADS;
+        return reinterpret_cast<uint4 *>(part(slot, n)) + piece * THREADS + threadIdx.x;
+    }
+    __device__ __forceinline__ uint2 *at8(int slot, int n, int m) const
+    {
+        return reinterpret_cast<uint2 *>(part(slot, n) + k16 * THREADS * 16) + m * THREADS + threadIdx.x;
+    }
+    __device__ __forceinline__ float *scale(int slot, int n, int m) const
+    {
+        return reinterpret_cast<float *>(part(slot, n) + (k16 * 16 + 16) * THREADS) + m * kScales + threadIdx.x / 16;
     }
     // m: 0 dy, 1 du_in, 2 x, 3 u
     __device__ __forceinline__ void copy(int slot, int n, int m, const T *src) const
@@ -234,12 +247,27 @@ struct BackRing {
                 tc::cp_async16(dst, reinterpret_cast<const uint4 *>(src) + i);
         }
     }
-    // m: 0 x, 1 u
-    __device__ __forceinline__ void copy8(int slot, int n, int m, const int8_t *src, const float *scale) const
+    // A warp's segment that starts at column c0 of the rows x and u, and their
+    // scales: half the lanes copy 16 bytes of the one, half of the other.
+    __device__ __forceinline__ void copy8(int slot, int n, const int8_t *x, const float *xs, const int8_t *u,
+                                          const float *us, int c0, int cols) const
     {
-        const uint32_t d = tc::smem_u32(at(slot, n, 2 * P)) + m * 8, s = tc::smem_u32(at(slot, n, 2 * P + 1)) + m * 4;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(scale) : "memory");
+        const int lane = threadIdx.x & 31, m = lane >> 4, c = c0 + (lane & 15) * 16;
+        if (c < cols) {
+            const uint32_t d = tc::smem_u32(part(slot, n) + (k16 * 16 + m * 8) * THREADS) +
+                               (threadIdx.x & ~31u) * 8 + (lane & 15) * 16;
+            const int bytes = min(16, cols - c);  // the rest of the 16 is set to 0
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"((m ? u : x) + c), "r"(bytes)
+                         : "memory");
+        }
+        // lanes 0 and 1: x's two groups, 2 and 3: u's
+        const int at = c0 / kGroup + (lane & 1);
+        if (lane < 4 && at * kGroup < cols)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                             tc::smem_u32(part(slot, n) + (k16 * 16 + 16) * THREADS) +
+                             ((lane >> 1) * kScales + threadIdx.x / 32 * 2 + (lane & 1)) * 4),
+                         "l"((lane >> 1 ? us : xs) + at)
+                         : "memory");
     }
     __device__ __forceinline__ void get(int slot, int n, int m, float2 (&v)[4]) const
     {
@@ -248,14 +276,6 @@ struct BackRing {
         for (int i = 0; i < P; ++i)
             reinterpret_cast<uint4 *>(&p)[i] = *at(slot, n, m * P + i);
         unpack4(p, v);
-    }
-    __device__ __forceinline__ uint2 get8(int slot, int n, int m) const
-    {
-        return reinterpret_cast<const uint2 *>(at(slot, n, 2 * P))[m];
-    }
-    __device__ __forceinline__ float scale(int slot, int n, int m) const
-    {
-        return reinterpret_cast<const float *>(at(slot, n, 2 * P + 1))[m];
     }
 };
 
@@ -278,15 +298,49 @@ struct Held {
     }
 };
 
-// Row groups of WARPS warps step over the rows; a thread keeps the two sums of
-// its columns in registers until its last row, and the groups' sums are joined
-// by k_block_dw.
-template <typename T, bool VEC, bool HELD, int WARPS, int NV, int S>
+// Sums of each of R rows over the WARPS warps of a row group, as row_reduce.
+template <int R>
+struct BatchSums {
+    float v[2][R][32];
+};
+
+template <int WARPS, int R>
+__device__ __forceinline__ void batch_reduce(float (&a)[R], BatchSums<R> &sm, int turn)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            a[k] += __shfl_xor_sync(0xffffffffu, a[k], o);
+    if constexpr (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                sm.v[turn & 1][k][threadIdx.x / 32] = a[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            a[k] = sm.v[turn & 1][k][threadIdx.x % WARPS];
+#pragma unroll
+        for (int o = WARPS / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                a[k] += __shfl_xor_sync(0xffffffffu, a[k], o);
+    }
+}
+
+// Row groups of WARPS warps step over batches of R rows: a row is a chain of two
+// sums and three uses of its values, and R of them side by side hide the waits of
+// each other (16384 x 4096 bf16 from 8 bits, one row at a time: 161 us).  The next
+// batch is on its way to shared memory meanwhile.  A thread keeps the two sums of
+// its columns in registers until its last row, and the groups' sums are joined by
+// k_block_dw.
+template <typename T, bool VEC, bool HELD, int WARPS, int NV, int R>
 __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_block_bwd(const BlockBwd a)
 {
-    __shared__ RowSums sm;
+    __shared__ BatchSums<R> sm;
     extern __shared__ uint4 dyn[];
-    const BackRing<T, HELD, NV, S, norm_threads(WARPS)> ring(dyn);
+    const BackRows<T, HELD, NV, norm_threads(WARPS)> rows(dyn);
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int wr = WARPS == 1 ? 0 : warp;
     const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
@@ -294,154 +348,189 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
     const int ng = (a.cols + kGroup - 1) / kGroup;
     tc::grid_go();
     const T *ady = static_cast<const T *>(a.dy), *ai = static_cast<const T *>(a.du_in);
-    auto fetch = [&](int64_t r, int slot) {
+    // the batch of rows r0, r0 + groups, ... into half `half`
+    auto fetch = [&](int64_t r0, int half) {
         if constexpr (VEC) {
-            if (r < a.nrows) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int64_t r = r0 + k * groups;
+                if (r >= a.nrows)
+                    break;
+                const int slot = half * R + k;
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const int c = (n * WARPS + wr) * kSeg + lane * 8;
                     if (c < a.cols) {
-                        ring.copy(slot, n, 0, ady + r * a.lddy + c);
+                        rows.copy(slot, n, 0, ady + r * a.lddy + c);
                         if (ai)
-                            ring.copy(slot, n, 1, ai + r * a.ldi + c);
-                        if constexpr (HELD) {
-                            ring.copy8(slot, n, 0, static_cast<const int8_t *>(a.x) + r * a.ldx + c,
-                                       a.x_scale + r * ng + c / kGroup);
-                            ring.copy8(slot, n, 1, static_cast<const int8_t *>(a.u) + r * a.ldu + c,
-                                       a.u_scale + r * ng + c / kGroup);
-                        } else {
-                            ring.copy(slot, n, 2, static_cast<const T *>(a.x) + r * a.ldx + c);
-                            ring.copy(slot, n, 3, static_cast<const T *>(a.u) + r * a.ldu + c);
+                            rows.copy(slot, n, 1, ai + r * a.ldi + c);
+                        if constexpr (!HELD) {
+                            rows.copy(slot, n, 2, static_cast<const T *>(a.x) + r * a.ldx + c);
+                            rows.copy(slot, n, 3, static_cast<const T *>(a.u) + r * a.ldu + c);
                         }
                     }
+                    if constexpr (HELD)
+                        rows.copy8(slot, n, static_cast<const int8_t *>(a.x) + r * a.ldx, a.x_scale + r * ng,
+                                   static_cast<const int8_t *>(a.u) + r * a.ldu, a.u_scale + r * ng,
+                                   (n * WARPS + wr) * kSeg, a.cols);
                 }
             }
             copies_commit();
         }
     };
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-        fetch(g + i * groups, i);
+    // rstd of the batch that begins with r0, row k's by lane k
+    auto rstd_of = [&](const float *rstd, int64_t r0) {
+        const int64_t r = r0 + lane * groups;
+        return lane < R && r < a.nrows ? rstd[r] : 0.f;
+    };
+    fetch(g, 0);
+    fetch(g + R * groups, 1);
     float2 gp[NV][4], pre[NV][4];  // gate post_weight, pre_weight
     block_weights<T, VEC, WARPS, NV>(a.post, a.gate, a.pre, wr, lane, a.cols, gp, pre);
     float2 dpre[NV][4] = {}, dh[NV][4] = {};
-    int turn = 0, slot = 0;
-    float next_u = g < a.nrows ? a.ru[g] : 0.f, next_x = g < a.nrows ? a.rx[g] : 0.f;
-    for (int64_t r = g; r < a.nrows; r += groups, turn += 2) {
-        const float ru = next_u, rx = next_x;
-        if (r + groups < a.nrows) {
-            next_u = a.ru[r + groups];
-            next_x = a.rx[r + groups];
-        }
-        // the row's values of this lane, again for each use (from shared memory,
-        // or, without VEC, from the caches)
-        auto dy_of = [&](int n, int c0, float2 (&v)[4]) {
+    int turn = 0, half = 0;
+    float next_u = rstd_of(a.ru, g), next_x = rstd_of(a.rx, g);
+    for (int64_t r0 = g; r0 < a.nrows; r0 += R * groups, turn += 2, half ^= 1) {
+        const float rus = next_u, rxs = next_x;
+        next_u = rstd_of(a.ru, r0 + R * groups);
+        next_x = rstd_of(a.rx, r0 + R * groups);
+        // a row's values of this lane, again for each use (from shared memory, or,
+        // without VEC, from the caches); rows past the last have rstd = 0, and
+        // are left out where something is read or written
+        auto dy_of = [&](int k, int n, int c0, float2 (&v)[4]) {
             if constexpr (VEC)
-                ring.get(slot, n, 0, v);
+                rows.get(half * R + k, n, 0, v);
             else
-                unpack4(load8<T, VEC>(ady + r * a.lddy, c0, lane, a.cols), v);
+                unpack4(load8<T, VEC>(ady + (r0 + k * groups) * a.lddy, c0, lane, a.cols), v);
         };
         // m: 0 x, 1 u
-        auto held_of = [&](int n, int c0, int m, const void *rows, int64_t ld, const float *scale, Held &h) {
+        auto held_of = [&](int k, int n, int c0, int m, const void *mat, int64_t ld, const float *scale, Held &h) {
+            const int64_t r = r0 + k * groups;
             h.s0 = h.s1 = 1.f;
             if constexpr (VEC && HELD) {
-                unquant8(ring.get8(slot, n, m), h.v);
-                h.s0 = h.s1 = ring.scale(slot, n, m);
+                unquant8(*rows.at8(half * R + k, n, m), h.v);
+                h.s0 = h.s1 = *rows.scale(half * R + k, n, m);
             } else if constexpr (VEC) {
-                ring.get(slot, n, 2 + m, h.v);
+                rows.get(half * R + k, n, 2 + m, h.v);
             } else if constexpr (HELD) {
-                unquant8(load8q<VEC>(static_cast<const int8_t *>(rows) + r * ld, c0, lane, a.cols), h.v);
+                unquant8(load8q<VEC>(static_cast<const int8_t *>(mat) + r * ld, c0, lane, a.cols), h.v);
                 const float *s = scale + r * ng + c0 / kGroup;
                 h.s0 = c0 < a.cols ? s[0] : 0.f;
                 h.s1 = c0 + kGroup < a.cols ? s[1] : 0.f;
             } else {
-                unpack4(load8<T, VEC>(static_cast<const T *>(rows) + r * ld, c0, lane, a.cols), h.v);
+                unpack4(load8<T, VEC>(static_cast<const T *>(mat) + r * ld, c0, lane, a.cols), h.v);
             }
         };
-        auto x_of = [&](int n, int c0, Held &h) { held_of(n, c0, 0, a.x, a.ldx, a.x_scale, h); };
-        auto u_of = [&](int n, int c0, Held &h) { held_of(n, c0, 1, a.u, a.ldu, a.u_scale, h); };
-        float dot = 0.f, none = 0.f;
+        auto x_of = [&](int k, int n, int c0, Held &h) { held_of(k, n, c0, 0, a.x, a.ldx, a.x_scale, h); };
+        auto u_of = [&](int k, int n, int c0, Held &h) { held_of(k, n, c0, 1, a.u, a.ldu, a.u_scale, h); };
+        auto there = [&](int k) { return k == 0 || r0 + k * groups < a.nrows; };
+        float dot[R], ru[R], rx[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            dot[k] = 0.f;
+            ru[k] = __shfl_sync(0xffffffffu, rus, k);
+            rx[k] = __shfl_sync(0xffffffffu, rxs, k);
+        }
         if constexpr (VEC)
-            copies_wait<S - 1>();
+            copies_wait<1>();
+        if constexpr (VEC && HELD)
+            __syncwarp();
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c0 = (n * WARPS + wr) * kSeg;
-            if (VEC && c0 + lane * 8 >= a.cols)
-                break;  // and neither has a later segment columns of this thread
-            float2 t[4];
-            Held u;
-            dy_of(n, c0, t);
-            u_of(n, c0, u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                t[i] = mul2(t[i], u.v[i]);
-                dpre[n][i] = fma2(t[i], both(ru * u.s(i)), dpre[n][i]);
-                t[i] = mul2(t[i], pre[n][i]);
-            }
-            dot += u.template sum<HELD>(t);
-        }
-        row_reduce<WARPS, false>(dot, none, sm, turn);
-        // as in the norm's own gradient: neither a square of u nor one of its
-        // factor without the other, so that rows of any scale stay in range
-        const float back_u = dot / (float)a.cols * ru * ru;
-        float2 du[NV][4];
-        dot = 0.f;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c0 = (n * WARPS + wr) * kSeg;
-            if (VEC && c0 + lane * 8 >= a.cols)
+        for (int k = 0; k < R; ++k) {
+            if (!there(k))
                 break;
-            float2 t[4];
-            Held h;
-            if (ai) {
-                if constexpr (VEC)
-                    ring.get(slot, n, 1, du[n]);
-                else
-                    unpack4(load8<T, VEC>(ai + r * a.ldi, c0, lane, a.cols), du[n]);
-            } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int c0 = (n * WARPS + wr) * kSeg;
+                if (VEC && c0 + lane * 8 >= a.cols)
+                    break;  // and neither has a later segment columns of this thread
+                float2 t[4];
+                Held u;
+                dy_of(k, n, c0, t);
+                u_of(k, n, c0, u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    t[i] = mul2(t[i], u.v[i]);
+                    dpre[n][i] = fma2(t[i], both(ru[k] * u.s(i)), dpre[n][i]);
+                    t[i] = mul2(t[i], pre[n][i]);
+                }
+                dot[k] += u.template sum<HELD>(t);
+            }
+        }
+        batch_reduce<WARPS, R>(dot, sm, turn);
+        float2 du[R][NV][4];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (!there(k))
+                break;
+            // as in the norm's own gradient: neither a square of u nor one of its
+            // factor without the other, so that rows of any scale stay in range
+            const float back_u = dot[k] / (float)a.cols * ru[k] * ru[k];
+            dot[k] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int c0 = (n * WARPS + wr) * kSeg;
+                if (VEC && c0 + lane * 8 >= a.cols)
+                    break;
+                float2 t[4];
+                Held h;
+                if (ai) {
+                    if constexpr (VEC)
+                        rows.get(half * R + k, n, 1, du[k][n]);
+                    else
+                        unpack4(load8<T, VEC>(ai + (r0 + k * groups) * a.ldi, c0, lane, a.cols), du[k][n]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        du[k][n][i] = make_float2(0.f, 0.f);
+                }
+                u_of(k, n, c0, h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    du[n][i] = make_float2(0.f, 0.f);
-            }
-            u_of(n, c0, h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                du[n][i] = fma2(both(-back_u), mul2(h.v[i], both(ru * h.s(i))), du[n][i]);
-            dy_of(n, c0, t);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                du[n][i] = fma2(mul2(pre[n][i], both(ru)), t[i], du[n][i]);
-            x_of(n, c0, h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                t[i] = mul2(du[n][i], h.v[i]);
-                dh[n][i] = fma2(t[i], both(rx * h.s(i)), dh[n][i]);
-                t[i] = mul2(t[i], gp[n][i]);
-            }
-            dot += h.template sum<HELD>(t);
-            if (a.dres) {
+                    du[k][n][i] = fma2(both(-back_u), mul2(h.v[i], both(ru[k] * h.s(i))), du[k][n][i]);
+                dy_of(k, n, c0, t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    t[i] = mul2(du[n][i], both(a.alpha));
-                store8<T, VEC>(static_cast<T *>(a.dres) + r * a.ldo, c0, lane, a.cols, pack4<T>(t));
+                    du[k][n][i] = fma2(mul2(pre[n][i], both(ru[k])), t[i], du[k][n][i]);
+                x_of(k, n, c0, h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    t[i] = mul2(du[k][n][i], h.v[i]);
+                    dh[n][i] = fma2(t[i], both(rx[k] * h.s(i)), dh[n][i]);
+                    t[i] = mul2(t[i], gp[n][i]);
+                }
+                dot[k] += h.template sum<HELD>(t);
+                if (a.dres) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        t[i] = mul2(du[k][n][i], both(a.alpha));
+                    store8<T, VEC>(static_cast<T *>(a.dres) + (r0 + k * groups) * a.ldo, c0, lane, a.cols, pack4<T>(t));
+                }
             }
         }
-        row_reduce<WARPS, false>(dot, none, sm, turn + 1);
-        const float back_x = dot / (float)a.cols * rx * rx;
+        batch_reduce<WARPS, R>(dot, sm, turn + 1);
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c0 = (n * WARPS + wr) * kSeg;
-            if (VEC && c0 + lane * 8 >= a.cols)
+        for (int k = 0; k < R; ++k) {
+            if (!there(k))
                 break;
-            Held h;
-            x_of(n, c0, h);
+            const float back_x = dot[k] / (float)a.cols * rx[k] * rx[k];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                h.v[i] = fma2(mul2(gp[n][i], both(rx)), du[n][i], mul2(both(-back_x), mul2(h.v[i], both(rx * h.s(i)))));
-            store8<T, VEC>(static_cast<T *>(a.dx) + r * a.lddx, c0, lane, a.cols, pack4<T>(h.v));
+            for (int n = 0; n < NV; ++n) {
+                const int c0 = (n * WARPS + wr) * kSeg;
+                if (VEC && c0 + lane * 8 >= a.cols)
+                    break;
+                Held h;
+                x_of(k, n, c0, h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h.v[i] = fma2(mul2(gp[n][i], both(rx[k])), du[k][n][i],
+                                  mul2(both(-back_x), mul2(h.v[i], both(rx[k] * h.s(i)))));
+                store8<T, VEC>(static_cast<T *>(a.dx) + (r0 + k * groups) * a.lddx, c0, lane, a.cols, pack4<T>(h.v));
+            }
         }
-        fetch(r + S * groups, slot);
-        slot = slot + 1 == S ? 0 : slot + 1;
+        if constexpr (VEC && HELD)
+            __syncwarp();  // the scales are read by other lanes than copy them
+        fetch(r0 + 2 * R * groups, half);
     }
     if (a.part) {
 #pragma unroll
@@ -498,6 +587,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 #define BLOCK_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(32, 2)
+// of the backward kernel: one segment to a thread leaves registers for batches
+#define BLOCK_SHAPES_BWD(X) X(1, 1) X(2, 1) X(4, 1) X(8, 1) X(16, 1) X(16, 2) X(32, 2)
 
 template <typename T, bool VEC, int W, int N>
 sg_status run_fwd(const BlockFwd &a, cudaStream_t st)
@@ -511,24 +602,26 @@ sg_status run_fwd(const BlockFwd &a, cudaStream_t st)
     return SG_OK;
 }
 
+// rows of a batch: two batches are in shared memory at a time
 template <typename T, bool HELD, int W, int N>
 constexpr int back_rows()
 {
-    const int s = (216 << 10) / block_ctas(W) / BackRing<T, HELD, N, 1, norm_threads(W)>::kBytes;
-    return s > 4 ? 4 : s < 1 ? 1 : s;
+    const int s = (216 << 10) / block_ctas(W) / (2 * BackRows<T, HELD, N, norm_threads(W)>::kRow);
+    const int most = W >= 32 || N > 1 ? 2 : 4;
+    return s > most ? most : s < 1 ? 1 : s;
 }
 
 template <typename T, bool VEC, bool HELD, int W, int N>
 sg_status run_bwd(const BlockBwd &a, int64_t grid, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr int S = VEC ? back_rows<T, HELD, W, N>() : 1;
-    constexpr int smem = VEC ? BackRing<T, HELD, N, S, norm_threads(W)>::kBytes : 0;
-    if constexpr (smem > 226 << 10) {  // fp32 rows above 8192 columns: not one is held
+    constexpr int R = VEC ? back_rows<T, HELD, W, N>() : N > 1 || W > 16 ? 1 : 2;
+    constexpr int smem = VEC ? 2 * R * BackRows<T, HELD, N, norm_threads(W)>::kRow : 0;
+    if constexpr (smem > 224 << 10) {  // rows of which not two are held: fp32 above 4096 columns, 16 bits above 8192
         return run_bwd<T, false, HELD, W, N>(a, grid, st);
     } else {
-        NORM_TRY(allow_smem(k_block_bwd<T, VEC, HELD, W, N, S>, smem, done));
-        k_block_bwd<T, VEC, HELD, W, N, S><<<(unsigned)grid, norm_threads(W), smem, st>>>(a);
+        NORM_TRY(allow_smem(k_block_bwd<T, VEC, HELD, W, N, R>, smem, done));
+        k_block_bwd<T, VEC, HELD, W, N, R><<<(unsigned)grid, norm_threads(W), smem, st>>>(a);
         return SG_OK;
     }
 }
@@ -550,7 +643,7 @@ sg_status launch_bwd(const BlockBwd &a, int64_t grid, cudaStream_t st)
 #define X(W, N)                             \
     if (a.cols <= (int64_t)(W) * (N) * kSeg) \
         return run_bwd<T, VEC, HELD, W, N>(a, grid, st);
-    BLOCK_SHAPES(X)
+    BLOCK_SHAPES_BWD(X)
 #undef X
     return SG_ERR_UNSUPPORTED;  // not reached: cols <= kMaxBlockCols
 }
@@ -562,7 +655,7 @@ int64_t bwd_groups(int64_t nrows, int64_t cols, int64_t *grid)
 #define X(W, N)                                          \
     if (warps == 0 && cols <= (int64_t)(W) * (N) * kSeg) \
         warps = (W);
-    BLOCK_SHAPES(X)
+    BLOCK_SHAPES_BWD(X)
 #undef X
     const int64_t need = warps == 1 ? ceil_div(nrows, 8) : nrows, most = kSMs * block_ctas(warps);
     *grid = need < most ? need : most;
@@ -706,9 +799,14 @@ sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, int64_t
                 SG_TRY_CUDA(cudaMemsetAsync(d, 0, (size_t)cols * 4, st));
         return SG_OK;
     }
+    const bool sums = dpost || dgate || dpre;
+    auto vec16_ok = [](const void *m, int64_t ld) { return ((uintptr_t)m & 15) == 0 && ld % 16 == 0; };
+    const bool held_ok = u_scale ? vec16_ok(u, ldu) && vec16_ok(x, ldx) : vec_ok(u, ldu, es) && vec_ok(x, ldx, es);
+    const bool vec = cols % 8 == 0 && held_ok && vec_ok(dy, lddy, es) && vec_ok(du_in, lddu_in, es) &&
+                     vec_ok(post_weight, cols, es) && vec_ok(gate, cols, es) && vec_ok(pre_weight, cols, es) &&
+                     vec_ok(dresidual, lddr, es) && vec_ok(dx, lddx, es);
     int64_t grid;
     const int64_t groups = bwd_groups(rows, cols, &grid), need = groups * 2 * cols * 4;
-    const bool sums = dpost || dgate || dpre;
     if (sums && (!work || work_bytes < need || ((uintptr_t)work) % 4 != 0))
         NORM_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_block_norm_bwd_work), aligned to 4", fn,
                   (long long)need);
@@ -718,10 +816,6 @@ sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, int64_t
     a.part = sums ? static_cast<float *>(work) : nullptr;
     a.lddy = lddy, a.ldu = ldu, a.ldx = ldx, a.ldi = lddu_in, a.ldo = lddr, a.lddx = lddx;
     a.nrows = rows, a.cols = (int)cols, a.alpha = (float)residual_scale;
-    const bool held_ok = u_scale ? vec8_ok(u, ldu) && vec8_ok(x, ldx) : vec_ok(u, ldu, es) && vec_ok(x, ldx, es);
-    const bool vec = cols % 8 == 0 && held_ok && vec_ok(dy, lddy, es) && vec_ok(du_in, lddu_in, es) &&
-                     vec_ok(post_weight, cols, es) && vec_ok(gate, cols, es) && vec_ok(pre_weight, cols, es) &&
-                     vec_ok(dresidual, lddr, es) && vec_ok(dx, lddx, es);
     if (dtype == SG_BF16)
         return backward<__nv_bfloat16>(a, vec, grid, groups, dpost, dgate, dpre, st);
     if (dtype == SG_F16)

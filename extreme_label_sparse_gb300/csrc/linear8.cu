@@ -141,15 +141,24 @@ __device__ __forceinline__ void store_rows(const Prod &p, int row0, int x0, uint
     for (int x = 0; x < 16; ++x)
         rows[lane * 17 + x] = w[x];
     __syncwarp();
+    // eight pieces under way together
     if constexpr (SIZE == 2) {
-        for (int r = 0; r < 32 && row0 + r < p.M; ++r)
-            if (x0 + lane < p.N)
-                static_cast<uint16_t *>(p.out)[(row0 + r) * p.ldo + x0 + lane] =
-                    (uint16_t)(rows[r * 17 + lane / 2] >> (16 * (lane & 1)));
+        if (x0 + lane < p.N) {
+            uint16_t *at = static_cast<uint16_t *>(p.out) + row0 * p.ldo + x0 + lane;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r, at += p.ldo)
+                if (row0 + r < p.M)
+                    *at = (uint16_t)(rows[r * 17 + lane / 2] >> (16 * (lane & 1)));
+        }
     } else {
-        for (int r = lane / 16; r < 32 && row0 + r < p.M; r += 2)
-            if (x0 + (lane & 15) < p.N)
-                static_cast<uint32_t *>(p.out)[(row0 + r) * p.ldo + x0 + (lane & 15)] = rows[r * 17 + (lane & 15)];
+        const int c = lane & 15;
+        if (x0 + c < p.N) {
+            uint32_t *at = static_cast<uint32_t *>(p.out) + (row0 + lane / 16) * p.ldo + x0 + c;
+#pragma unroll 8
+            for (int r = lane / 16; r < 32; r += 2, at += 2 * p.ldo)
+                if (row0 + r < p.M)
+                    *at = rows[r * 17 + c];
+        }
     }
 }
 
@@ -494,62 +503,62 @@ struct Widen {
     const float *scale;    // NULL: the integers themselves, in fp16
     const float *factor;   // of the scales, or NULL
     uint16_t *dst;
-    int64_t ldd;
-    int32_t f16;
+    int64_t ldd;           // a whole number of 16
+    int32_t f16, vec;      // vec: rows start on 16 bytes
 };
 
-// int8 rows to 16 bits: the integers, or the values they stand for.  A warp
-// takes a row, 16 columns to a lane.
-template <bool VEC>
-__global__ void __launch_bounds__(256) k_widen(const Widen a)
+// int8 rows to 16 bits: the integers, or the values they stand for, of one or two
+// matrices.  A warp takes a row, 16 columns to a lane, whose 32 bytes it writes at
+// once (halves of a sector would each go to L2: 64 MB took 40 us).
+__global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0, const __grid_constant__ Widen m1)
 {
     const int lane = threadIdx.x & 31;
-    const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
     grid_wait();
     grid_go();
-    const float f = a.factor ? *a.factor : 1.f;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows; r += (int64_t)gridDim.x * 8) {
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < m0.rows + m1.rows; i += (int64_t)gridDim.x * 8) {
+        const bool second = i >= m0.rows;
+        const Widen &a = second ? m1 : m0;
+        const int64_t r = second ? i - m0.rows : i;
+        const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
+        const float f = a.factor ? *a.factor : 1.f;
         const int8_t *src = a.src + r * a.ld;
         const float *sc = a.scale ? a.scale + r * ng : nullptr;
         uint16_t *dst = a.dst + r * a.ldd;
+#pragma unroll 4
         for (int c = lane * 16; c < a.cols; c += 512) {
             uint32_t in[4];
-            if (VEC && c + 16 <= a.cols) {
+            if (a.vec && c + 16 <= a.cols) {
                 *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(src + c);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    in[i] = 0;
+                for (int j = 0; j < 4; ++j) {
+                    in[j] = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (c + 4 * i + j < a.cols)
-                            in[i] |= (uint32_t)(uint8_t)src[c + 4 * i + j] << (8 * j);
+                    for (int k = 0; k < 4; ++k)
+                        if (c + 4 * j + k < a.cols)
+                            in[j] |= (uint32_t)(uint8_t)src[c + 4 * j + k] << (8 * k);
                 }
             }
-            // a group is a whole number of 16 columns
-            const float s = sc ? sc[a.group ? c / a.group : 0] * f : 1.f;
             uint32_t w[8];
             if (!sc) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = bytes_f16(in[i / 2] ^ 0x80808080u, i & 1);
+                for (int j = 0; j < 8; ++j)
+                    w[j] = bytes_f16(in[j / 2] ^ 0x80808080u, j & 1);
             } else {
+                // a group is a whole number of 16 columns
+                const float s = sc[a.group ? c / a.group : 0] * f;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float2 v[4];
                     rows::unquant8(make_uint2(in[2 * k], in[2 * k + 1]), v);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = rows::mul2(v[i], rows::both(s));
-                        w[4 * k + i] = pack16(v[i].x, v[i].y, a.f16);
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = rows::mul2(v[j], rows::both(s));
+                        w[4 * k + j] = pack16(v[j].x, v[j].y, a.f16);
                     }
                 }
             }
-            // ldd is a whole number of eights
-            uint4 *out = reinterpret_cast<uint4 *>(dst + c);
-            out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (c + 8 < a.ldd)
-                out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            st_global32(dst + c, w);
         }
     }
 }
@@ -594,8 +603,8 @@ double unit_cost(int64_t nk, bool split) { return (double)nk + (split ? 10.0 : 2
 constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 64};
 
 // parts of K of the products (the second may have no tiles) so that the
-// clusters end early
-void choose_splits(Prod &a, Prod &b, int C)
+// clusters end early; the time that they take, in K blocks
+double choose_splits(Prod &a, Prod &b, int C)
 {
     const int64_t ta = (int64_t)a.mt * a.nt, tb = (int64_t)b.mt * b.nt;
     double best = -1;
@@ -627,6 +636,7 @@ void choose_splits(Prod &a, Prod &b, int C)
     b.split = sb;
     a.units = (int32_t)(ta * sa);
     b.units = (int32_t)(tb * sb);
+    return best;
 }
 
 // turns of the second product's units so that all clusters end at about the
@@ -669,13 +679,40 @@ void shape(Prod &p, const Plan &pl, int64_t M, int64_t N, int64_t Kd)
     p.nk = (int32_t)ceil_div(Kd, 64);
 }
 
+// CTAs or pairs of them, and the products' tiles and splits: pairs read less from
+// the L2 cache for a tile, CTAs alone have finer turns (777 x 1001 x 5003: 140
+// tiles in one turn, where 80 of pairs take two).  N: channels, of a piece where
+// the forward pass takes several.
+void choose_tiles(int64_t T, int64_t H, int64_t N, bool backward, bool want_dx, bool want_dW, Plan *p)
+{
+    double best = 0;
+    for (int cg = 1; cg <= (T > 128 ? 2 : 1); ++cg) {
+        Plan q = *p;
+        q.CG = cg;
+        q.BM = 128 * cg;
+        q.C = kSMs / cg;
+        q.p[0] = q.p[1] = Prod{};
+        if (!backward) {
+            shape(q.p[0], q, T, N, H);
+        } else {
+            // dW's units first, as their K is often the longer
+            if (want_dW)
+                shape(q.p[0], q, N, H, T);
+            if (want_dx)
+                shape(q.p[want_dW ? 1 : 0], q, T, H, N);
+        }
+        const double span = choose_splits(q.p[0], q.p[1], q.C) * (cg == 1 ? 1.1 : 1.0);
+        if (cg == 1 || span < best) {
+            best = span;
+            *p = q;
+        }
+    }
+}
+
 void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, bool backward, bool want_dx,
                bool want_dW, Plan *p)
 {
-    p->CG = T > 128 ? 2 : 1;
-    p->BM = 128 * p->CG;
-    p->C = kSMs / p->CG;
-    p->ldh = ceil_div(H, 8) * 8;
+    p->ldh = ceil_div(H, 16) * 16;
     p->ldn = ceil_div(N, 8) * 8;
     if (T <= 128) {  // boxes of the rows that there are
         p->an = T <= 64 ? 1 : 2;
@@ -696,6 +733,7 @@ void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, b
         p->Nc = Nc < N ? Nc : N;
         p->o_x = take(T * p->ldh * 2);
         p->o_W = take(p->Nc * p->ldh * 2);
+        choose_tiles(T, H, p->Nc, false, false, false, p);
         // the last piece may be split otherwise: room for either
         int64_t most = 0;
         for (int64_t n : {p->Nc, N % p->Nc}) {
@@ -710,15 +748,7 @@ void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, b
         p->o_acc[0] = take(most);
         return;
     }
-    // dW's units first, as their K is often the longer
-    Prod &w = p->p[0], &x = p->p[1];
-    if (want_dW)
-        shape(w, *p, N, H, T);
-    if (want_dx)
-        shape(x, *p, T, H, N);
-    if (!want_dW)
-        std::swap(w, x);
-    choose_splits(w, x, p->C);
+    choose_tiles(T, H, N, true, want_dx, want_dW, p);
     p->copy = !tma_ok(dout, ldd, 2);
     p->o_x = take(want_dW ? T * p->ldh * 2 : 0);
     p->o_W = take(want_dx ? N * p->ldh * 2 : 0);
@@ -727,14 +757,17 @@ void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, b
         p->o_acc[i] = take(p->p[i].split > 1 ? (int64_t)p->p[i].units * p->BM * kBN * 4 : 0);
 }
 
-sg_status widen(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const float *scale, int32_t group,
-                const float *factor, uint8_t *dst, int64_t ldd, bool f16, cudaStream_t st)
+Widen widen_of(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const float *scale, int32_t group,
+               const float *factor, uint8_t *dst, int64_t ldd, bool f16)
 {
-    Widen w = {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16};
     const bool vec = ((uintptr_t)src & 15) == 0 && ld % 16 == 0;
-    const int64_t need = ceil_div(rows, 8), most = kSMs * 8;
-    return launch(vec ? k_widen<true> : k_widen<false>, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st,
-                  w);
+    return {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16, vec};
+}
+
+sg_status widen(const Widen &a, const Widen &b, cudaStream_t st)
+{
+    const int64_t need = ceil_div(a.rows + b.rows, 8), most = kSMs * 8;
+    return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, a, b);
 }
 
 sg_status check_linear(const char *fn, const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
@@ -847,10 +880,11 @@ sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     if (few)
         return few_fwd(x8, ldx, x_scale, T, H, W8, ldw, W_scale, N, out, ldo, dtype, work, status, st);
     uint8_t *w8 = static_cast<uint8_t *>(work);
-    LIN_TRY(widen(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true, st));
+    const Widen none = {};
     for (int64_t n0 = 0; n0 < N; n0 += pl.Nc) {
         const int64_t nc = N - n0 < pl.Nc ? N - n0 : pl.Nc;
-        LIN_TRY(widen(W8 + n0 * ldw, ldw, nc, H, nullptr, 0, nullptr, w8 + pl.o_W, pl.ldh, true, st));
+        LIN_TRY(widen(widen_of(W8 + n0 * ldw, ldw, nc, H, nullptr, 0, nullptr, w8 + pl.o_W, pl.ldh, true),
+                      n0 ? none : widen_of(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true), st));
         LinArgs a = {};
         a.ab = (int32_t)pl.ab, a.an = (int32_t)pl.an, a.kt = (int32_t)pl.kt, a.status = status;
         Prod &p = a.p[0];
@@ -917,10 +951,12 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
         dout = w8 + pl.o_d;
         lddout = pl.ldn;
     }
+    Widen wide[2] = {};
     if (dx)
-        LIN_TRY(widen(W8, ldw, N, H, W_scale, 0, fac, w8 + pl.o_W, pl.ldh, f16, st));
+        wide[0] = widen_of(W8, ldw, N, H, W_scale, 0, fac, w8 + pl.o_W, pl.ldh, f16);
     if (dW)
-        LIN_TRY(widen(x8, ldx, T, H, x_scale, x_group, fac ? fac + 2 : nullptr, w8 + pl.o_x, pl.ldh, f16, st));
+        wide[1] = widen_of(x8, ldx, T, H, x_scale, x_group, fac ? fac + 2 : nullptr, w8 + pl.o_x, pl.ldh, f16);
+    LIN_TRY(widen(wide[0], wide[1], st));
     LinArgs a = {};
     a.p[0] = pl.p[0], a.p[1] = pl.p[1];
     a.ab = (int32_t)pl.ab, a.an = (int32_t)pl.an, a.kt = (int32_t)pl.kt, a.status = status;

@@ -103,7 +103,7 @@ def test_linear_refusals_and_work(lib):
     assert work(P, 64, 1 << 24, 64, P, 64, 1 << 24, None, 0, 0) == UNSUPPORTED
     assert lib.sg_linear8_work(P, 64, 1, 64, P, 64, 1, None, 0, 0, None) == INVALID
     big = 1 << 40
-    refused(lib.sg_linear8_fwd, [P, 64, P, 4, 64, P, 64, P, 1000, P, 1000, BF, P, big, P, None],
+    refused(lib.sg_linear8_fwd, [P, 64, P, 300, 64, P, 64, P, 1000, P, 1000, BF, P, big, P, None],
             ((0, None, INVALID), (2, None, INVALID), (5, None, INVALID), (7, None, INVALID), (9, None, INVALID),
              (12, None, INVALID), (13, 16, INVALID), (12, C.c_void_p(16), INVALID), (10, 999, INVALID),
              (11, E4M3, INVALID), (9, OFF1, INVALID), (2, OFF2, INVALID), (7, OFF2, INVALID), (14, OFF2, INVALID)))
