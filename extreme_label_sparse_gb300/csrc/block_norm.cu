@@ -286,15 +286,19 @@ struct Held {
     float s0, s1;
 
     __device__ __forceinline__ float s(int i) const { return i < 2 ? s0 : s1; }
-    // the sum of t v's elements, each times its s
-    template <bool HELD>
-    __device__ __forceinline__ float sum(const float2 (&t)[4]) const
+    // the sum of a b's elements, each times its s; ONE: there is one s
+    template <bool ONE>
+    __device__ __forceinline__ float dot(const float2 (&a)[4], const float2 (&b)[4]) const
     {
-        const float2 a = add2(t[0], t[1]), b = add2(t[2], t[3]);
-        if constexpr (HELD)
-            return s0 * (a.x + a.y) + s1 * (b.x + b.y);
-        const float2 c = add2(a, b);
-        return c.x + c.y;
+        float2 p = mul2(a[0], b[0]), q = mul2(a[2], b[2]);
+        p = fma2(a[1], b[1], p);
+        q = fma2(a[3], b[3], q);
+        if constexpr (ONE) {
+            p = add2(p, q);
+            return s0 * (p.x + p.y);
+        } else {
+            return s0 * (p.x + p.y) + s1 * (q.x + q.y);
+        }
     }
 };
 
@@ -307,13 +311,45 @@ struct BatchSums {
 template <int WARPS, int R>
 __device__ __forceinline__ void batch_reduce(float (&a)[R], BatchSums<R> &sm, int turn)
 {
+    const int lane = threadIdx.x & 31;
+    if constexpr (R == 4) {
+        // the lanes take turns: after two steps a lane has one row, lane / 8's
+        const bool hi = lane & 16, odd = lane & 8;
+        float x = hi ? a[2] : a[0], y = hi ? a[3] : a[1];
+        x += __shfl_xor_sync(0xffffffffu, hi ? a[0] : a[2], 16);
+        y += __shfl_xor_sync(0xffffffffu, hi ? a[1] : a[3], 16);
+        float z = odd ? y : x;
+        z += __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+        if constexpr (WARPS > 1) {
+            if ((lane & 7) == 0)
+                sm.v[turn & 1][lane / 8][threadIdx.x / 32] = z;
+            __syncthreads();
+            const float *row = sm.v[turn & 1][lane / 8];
+            z = (lane & 7) < WARPS ? row[lane & 7] : 0.f;
+            if constexpr (WARPS > 8) {
+#pragma unroll
+                for (int w = 8; w < WARPS; w += 8)
+                    z += row[w + (lane & 7)];
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1)
+                z += __shfl_xor_sync(0xffffffffu, z, o);
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            a[k] = __shfl_sync(0xffffffffu, z, 8 * k);
+        return;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < R; ++k)
             a[k] += __shfl_xor_sync(0xffffffffu, a[k], o);
     if constexpr (WARPS > 1) {
-        if ((threadIdx.x & 31) == 0)
+        if (lane == 0)
 #pragma unroll
             for (int k = 0; k < R; ++k)
                 sm.v[turn & 1][k][threadIdx.x / 32] = a[k];
@@ -452,9 +488,8 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 for (int i = 0; i < 4; ++i) {
                     t[i] = mul2(t[i], u.v[i]);
                     dpre[n][i] = fma2(t[i], both(ru[k] * u.s(i)), dpre[n][i]);
-                    t[i] = mul2(t[i], pre[n][i]);
                 }
-                dot[k] += u.template sum<HELD>(t);
+                dot[k] += u.template dot<VEC || !HELD>(t, pre[n]);
             }
         }
         batch_reduce<WARPS, R>(dot, sm, turn);
@@ -486,8 +521,13 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 }
                 u_of(k, n, c0, h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    du[k][n][i] = fma2(both(-back_u), mul2(h.v[i], both(ru[k] * h.s(i))), du[k][n][i]);
+                for (int i = 0; i < 4; ++i) {
+                    // integers times (rstd s), which is about 1, in one factor
+                    if constexpr (HELD)
+                        du[k][n][i] = fma2(h.v[i], both(-back_u * (ru[k] * h.s(i))), du[k][n][i]);
+                    else
+                        du[k][n][i] = fma2(both(-back_u), mul2(h.v[i], both(ru[k])), du[k][n][i]);
+                }
                 dy_of(k, n, c0, t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -497,9 +537,8 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 for (int i = 0; i < 4; ++i) {
                     t[i] = mul2(du[k][n][i], h.v[i]);
                     dh[n][i] = fma2(t[i], both(rx[k] * h.s(i)), dh[n][i]);
-                    t[i] = mul2(t[i], gp[n][i]);
                 }
-                dot[k] += h.template sum<HELD>(t);
+                dot[k] += h.template dot<VEC || !HELD>(t, gp[n]);
                 if (a.dres) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -522,9 +561,13 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 Held h;
                 x_of(k, n, c0, h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    h.v[i] = fma2(mul2(gp[n][i], both(rx[k])), du[k][n][i],
-                                  mul2(both(-back_x), mul2(h.v[i], both(rx[k] * h.s(i)))));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 w = mul2(gp[n][i], both(rx[k]));
+                    if constexpr (HELD)
+                        h.v[i] = fma2(w, du[k][n][i], mul2(h.v[i], both(-back_x * (rx[k] * h.s(i)))));
+                    else
+                        h.v[i] = fma2(w, du[k][n][i], mul2(both(-back_x), mul2(h.v[i], both(rx[k]))));
+                }
                 store8<T, VEC>(static_cast<T *>(a.dx) + (r0 + k * groups) * a.lddx, c0, lane, a.cols, pack4<T>(h.v));
             }
         }
