@@ -541,6 +541,13 @@ def _mat(t, name: str, rows: int, cols: int, dtype, dev: int):
     (NULL, cols) for None."""
     if t is None:
         return None, cols
+    try:  # as almost all are
+        if t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == dev:
+            rs, cs = t.stride()
+            if cs == 1 and rs >= cols:
+                return t.data_ptr(), rs
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -564,6 +571,11 @@ def _vec(t, name: str, n, dtype, dev: int):
     for None."""
     if t is None:
         return None
+    try:  # as almost all are
+        if t.dtype is dtype and t.get_device() == dev and t.shape == (n,) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -730,6 +742,18 @@ def _scales(t, name: str, rows: int, cols: int, dev: int):
     return _vec(t, name, None, torch.float32, dev), 128
 
 
+def _work(work, bytes_of, device, dev: int):
+    """(tensor, pointer, size) of work memory: the caller's, or one from torch's
+    allocator of bytes_of() bytes.  The tensor is held until the call is made."""
+    if work is None:
+        n = bytes_of()
+        if n == 0:
+            return None, None, 0
+        work = torch.empty(n, dtype=torch.uint8, device=device)
+        return work, work.data_ptr(), n
+    return work, _vec(work, "work", None, torch.uint8, dev), work.numel()
+
+
 def _groups(t, name: str, rows: int, cols: int, dev: int):
     """Pointer of scales of 128 columns each; NULL for None."""
     if t is None:
@@ -810,15 +834,14 @@ def sg_block_norm_bwd(dy: torch.Tensor, u: torch.Tensor, x: torch.Tensor, post_w
     ip, ldi = _mat(du_in, "du_in", rows, cols, dt, dev)
     rp, ldr = _mat(dresidual, "dresidual", rows, cols, dt, dev)
     op, ldo = _mat(dx, "dx", rows, cols, dt, dev)
-    if work is None and not (dpost is None and dpre is None and dgate is None):
-        work = torch.empty(sg_block_norm_bwd_work(rows, cols), dtype=torch.uint8, device=dy.device)
+    sums = not (dpost is None and dpre is None and dgate is None)
+    work, kp, kn = _work(work, lambda: sg_block_norm_bwd_work(rows, cols) if sums else 0, dy.device, dev)
     _call((_lib or load()).sg_block_norm_bwd, dev, gp, ldg, up, ldu, _groups(u_scale, "u_scale", rows, cols, dev), xp,
           ldx, _groups(x_scale, "x_scale", rows, cols, dev), ip, ldi, rows, cols, _DTYPE[dt],
           _vec(post_weight, "post_weight", cols, dt, dev), _vec(gate, "gate", cols, dt, dev),
           _vec(pre_weight, "pre_weight", cols, dt, dev), residual_scale, _vec(rstd_x, "rstd_x", rows, f32, dev),
           _vec(rstd_u, "rstd_u", rows, f32, dev), rp, ldr, op, ldo, _vec(dpost, "dpost", cols, f32, dev),
-          _vec(dgate, "dgate", cols, f32, dev), _vec(dpre, "dpre", cols, f32, dev),
-          _vec(work, "work", None, torch.uint8, dev), 0 if work is None else work.numel())
+          _vec(dgate, "dgate", cols, f32, dev), _vec(dpre, "dpre", cols, f32, dev), kp, kn)
 
 
 @functools.lru_cache(4096)
@@ -859,12 +882,10 @@ def sg_linear8_fwd(x8: torch.Tensor, x_scale: torch.Tensor, W8: torch.Tensor, W_
     xp, ldx = _mat(x8, "x8", T, H, i8, dev)
     wp, ldw = _mat(W8, "W8", N, H, i8, dev)
     op, ldo = _mat(out, "out", T, N, dt, dev)
-    if work is None:
-        work = torch.empty(_linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, 0, N, 0), dtype=torch.uint8,
-                           device=out.device)
+    work, kp, kn = _work(work, lambda: _linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, 0, N, 0), out.device, dev)
     _call((_lib or load()).sg_linear8_fwd, dev, xp, ldx, _vec(x_scale, "x_scale", T, f32, dev), T, H, wp, ldw,
-          _vec(W_scale, "W_scale", N, f32, dev), N, op, ldo, _DTYPE[dt], _vec(work, "work", None, torch.uint8, dev),
-          work.numel(), _vec(status, "status", 1, torch.int32, dev))
+          _vec(W_scale, "W_scale", N, f32, dev), N, op, ldo, _DTYPE[dt], kp, kn,
+          _vec(status, "status", 1, torch.int32, dev))
 
 
 def sg_linear8_bwd(x8: torch.Tensor, x_scale: torch.Tensor, W8: torch.Tensor, W_scale: torch.Tensor, dout: torch.Tensor,
@@ -881,12 +902,10 @@ def sg_linear8_bwd(x8: torch.Tensor, x_scale: torch.Tensor, W8: torch.Tensor, W_
     dxp, lddx = _mat(dx, "dx", T, H, dt, dev)
     dwp, lddw = _mat(dW, "dW", N, H, dt, dev)
     sp, group = _scales(x_scale, "x_scale", T, H, dev)
-    if work is None:
-        work = torch.empty(_linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, gp & 15, ldg, 1), dtype=torch.uint8,
-                           device=dout.device)
+    work, kp, kn = _work(work, lambda: _linear_bytes(xp & 15, ldx, T, H, wp & 15, ldw, N, gp & 15, ldg, 1), dout.device,
+                         dev)
     _call((_lib or load()).sg_linear8_bwd, dev, xp, ldx, sp, group, T, H, wp, ldw, _vec(W_scale, "W_scale", N, f32, dev),
-          N, gp, ldg, _DTYPE[dt], dxp, lddx, dwp, lddw, _vec(work, "work", None, torch.uint8, dev), work.numel(),
-          _vec(status, "status", 1, torch.int32, dev))
+          N, gp, ldg, _DTYPE[dt], dxp, lddx, dwp, lddw, kp, kn, _vec(status, "status", 1, torch.int32, dev))
 
 
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
