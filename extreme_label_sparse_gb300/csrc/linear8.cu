@@ -80,7 +80,7 @@ struct LinArgs {
     // units of the first product in turn over the clusters, `each` to each and
     // one more to the first `hi`, which take only b_hi turns of the second's
     int32_t each, hi, b_hi, b_lo;
-    int32_t ab, an;  // rows of a box of A by its rows, and boxes
+    int32_t ab;      // rows of a box of A by its rows
     int32_t kt;      // rows of a box whose rows are K, where those are the tokens
     int32_t *status;
 };
@@ -207,47 +207,52 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kEpiWarps) {
         // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            Ring r;
-            bool ok = true;
-            for (int i = 0; ok && unit_at<CG>(a, cl, i, t); ++i) {
-                const Prod &p = a.p[t.which];
-                const CUtensorMap *mA = t.which ? &mA1 : &mA0, *mB = t.which ? &mB1 : &mB0;
-                const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
-                // a pair has more than 128 rows: whole boxes
-                const int ab = CG == 2 ? 64 : a.ab, an = CG == 2 ? 2 : a.an, kt = CG == 2 || !p.a_mn ? 64 : a.kt;
-                const uint32_t bytes = CG * 128 * ((p.a_mn ? 2 * kt : an * ab) + K::BRows / 64 * (p.b_mn ? kt : 64));
-                for (int k = t.k0 * 64, k1 = k + t.nk * 64; k < k1; k += 64, r.next(NS)) {
-                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status);
-                    if (!ok)
-                        break;
+        // the whole warp walks the list, an elected thread copies (see elect_one:
+        // by `lane == 0` the copies of a K block took longer than its MMAs)
+        Ring r;
+        bool ok = true;
+        for (int i = 0; ok && unit_at<CG>(a, cl, i, t); ++i) {
+            const Prod &p = a.p[t.which];
+            const CUtensorMap *mA = t.which ? &mA1 : &mA0, *mB = t.which ? &mB1 : &mB0;
+            const int am = t.m0 + rank * 128, bn = t.n0 + rank * 128;
+            // a pair has more than 128 rows: whole boxes
+            const int ab = CG == 2 ? 128 : a.ab, kt = CG == 2 || !p.a_mn ? 64 : a.kt;
+            const uint32_t bytes = CG * 128 * ((p.a_mn ? 2 * kt : ab) + (p.b_mn ? K::BRows / 64 * kt : K::BRows));
+            const bool a_mn = p.a_mn, b_mn = p.b_mn;
+            for (int k = t.k0 * 64, k1 = k + t.nk * 64; k < k1; k += 64, r.next(NS)) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status));
+                if (!ok)
+                    break;
+                if (elect_one()) {
                     uint32_t bar = smem_u32(&c.full[r.i]);
                     if (rank == 0)
                         mbar_arrive_expect_tx(bar, bytes);
                     if constexpr (CG == 2)
                         bar = mapa(bar, 0);
                     const uint32_t st = base + (uint32_t)r.i * K::kStage;
-                    if (p.a_mn) {
+                    if (a_mn) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             tma_load_2d_cg<CG>(st + j * kBox, mA, am + 64 * j, k, bar);
                     } else {
                         tma_load_2d_cg<CG>(st, mA, k, am, bar);
-                        if (an == 2)
-                            tma_load_2d_cg<CG>(st + ab * 128, mA, k, am + ab, bar);
                     }
+                    if (b_mn) {
 #pragma unroll
-                    for (int j = 0; j < K::BRows / 64; ++j)
-                        tma_load_2d_cg<CG>(st + K::kA + j * kBox, mB, p.b_mn ? bn + 64 * j : k, p.b_mn ? k : bn + 64 * j,
-                                           bar);
+                        for (int j = 0; j < K::BRows / 64; ++j)
+                            tma_load_2d_cg<CG>(st + K::kA + j * kBox, mB, bn + 64 * j, k, bar);
+                    } else {
+                        tma_load_2d_cg<CG>(st + K::kA, mB, k, bn, bar);
+                    }
                 }
+                __syncwarp();
             }
-            if (!ok) {
-                // gave up: copies may still be on their way into this CTA (and
-                // signal the pair's first CTA); they land long before this
-                const uint64_t t0 = global_ns();
-                while (global_ns() - t0 < 1000000u) {
-                }
+        }
+        if (!ok && lane == 0) {
+            // gave up: copies may still be on their way into this CTA (and signal
+            // the pair's first CTA); they land long before this
+            const uint64_t t0 = global_ns();
+            while (global_ns() - t0 < 1000000u) {
             }
         }
         __syncwarp();
@@ -663,7 +668,7 @@ constexpr int64_t kPiece = 256ll << 20;  // bytes of W in 16 bits, forward
 struct Plan {
     int CG = 1, BM = 128, C = kSMs;
     int64_t ldh = 0, ldn = 0;  // row strides of the copies
-    int64_t ab = 64, an = 2, kt = 64;
+    int64_t ab = 128, kt = 64;
     int64_t Nc = 0;            // forward: channels of a piece
     bool copy = false;         // of dout
     Prod p[2] = {};
@@ -714,10 +719,8 @@ void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, b
 {
     p->ldh = ceil_div(H, 16) * 16;
     p->ldn = ceil_div(N, 8) * 8;
-    if (T <= 128) {  // boxes of the rows that there are
-        p->an = T <= 64 ? 1 : 2;
-        p->ab = ceil_div(ceil_div(T, p->an), 8) * 8;
-    }
+    if (T <= 128)  // boxes of the rows that there are
+        p->ab = ceil_div(T, 8) * 8;
     if (T < 64)
         p->kt = ceil_div(T, 16) * 16;
     auto take = [&](int64_t n) {
@@ -886,7 +889,7 @@ sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
         LIN_TRY(widen(widen_of(W8 + n0 * ldw, ldw, nc, H, nullptr, 0, nullptr, w8 + pl.o_W, pl.ldh, true),
                       n0 ? none : widen_of(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true), st));
         LinArgs a = {};
-        a.ab = (int32_t)pl.ab, a.an = (int32_t)pl.an, a.kt = (int32_t)pl.kt, a.status = status;
+        a.ab = (int32_t)pl.ab, a.kt = (int32_t)pl.kt, a.status = status;
         Prod &p = a.p[0];
         shape(p, pl, T, nc, H);
         choose_splits(p, a.p[1], pl.C);
@@ -896,7 +899,7 @@ sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
         p.acc = reinterpret_cast<float *>(w8 + pl.o_acc[0]);
         CUtensorMap m[6];
         LIN_TRY(map_of(&m[0], w8 + pl.o_x, H, T, pl.ldh, 2, "x", (uint32_t)pl.ab));
-        LIN_TRY(map_of(&m[1], w8 + pl.o_W, H, nc, pl.ldh, 2, "W"));
+        LIN_TRY(map_of(&m[1], w8 + pl.o_W, H, nc, pl.ldh, 2, "W", (uint32_t)(kBN / pl.CG)));
         LIN_TRY(out_map(p, &m[2], m[0], static_cast<uint8_t *>(out) + n0 * es, ldo, dtype, "out"));
         m[3] = m[4] = m[5] = m[0];
         schedule(a, pl.C);
@@ -959,7 +962,7 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     LIN_TRY(widen(wide[0], wide[1], st));
     LinArgs a = {};
     a.p[0] = pl.p[0], a.p[1] = pl.p[1];
-    a.ab = (int32_t)pl.ab, a.an = (int32_t)pl.an, a.kt = (int32_t)pl.kt, a.status = status;
+    a.ab = (int32_t)pl.ab, a.kt = (int32_t)pl.kt, a.status = status;
     CUtensorMap m[6];
     for (int i = 0; i < 2; ++i) {
         Prod &p = a.p[i];

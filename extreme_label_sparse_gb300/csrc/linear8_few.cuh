@@ -289,27 +289,28 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         }
     } else if (warp == CW + EW) {
         // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            int64_t b = first;
-            Segment s;
-            Ring r;
-            bool ok = true;
-            const uint32_t bytes = kWTile + (uint32_t)a.xb * kBlockK;
-            while (ok && segment_at(a, b, end, s))
-                for (int k = s.k; k < s.k + s.n; ++k, r.next(NS)) {
-                    ok = mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status);
-                    if (!ok)
-                        break;
+        int64_t b = first;
+        Segment s;
+        Ring r;
+        bool ok = true;
+        const uint32_t bytes = kWTile + (uint32_t)a.xb * kBlockK;
+        while (ok && segment_at(a, b, end, s))
+            for (int k = s.k; k < s.k + s.n; ++k, r.next(NS)) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status));
+                if (!ok)
+                    break;
+                if (elect_one()) {
                     const uint32_t bar = smem_u32(&c.full[r.i]), st = base + (uint32_t)r.i * F::kStage;
                     mbar_arrive_expect_tx(bar, bytes);
                     tma_load_2d(st, &mW, k * kBlockK, s.tile * 128, bar);
                     tma_load_2d(st + kWTile, &mx, k * kBlockK, 0, bar);
                 }
-            if (!ok) {
-                // gave up: copies on their way land long before this
-                const uint64_t t0 = global_ns();
-                while (global_ns() - t0 < 1000000u) {
-                }
+                __syncwarp();
+            }
+        if (!ok && lane == 0) {
+            // gave up: copies on their way land long before this
+            const uint64_t t0 = global_ns();
+            while (global_ns() - t0 < 1000000u) {
             }
         }
         __syncwarp();
