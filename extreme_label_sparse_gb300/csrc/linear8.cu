@@ -19,23 +19,9 @@
 #include <cmath>
 #include <utility>
 
-#include "launch.cuh"
 #include "linear8_few.cuh"
-#include "quant8.cuh"
 
 namespace {
-
-#define LIN_FAIL(code, ...)        \
-    do {                           \
-        sg_set_error(__VA_ARGS__); \
-        return code;               \
-    } while (0)
-#define LIN_TRY(expr)           \
-    do {                        \
-        sg_status rc_ = (expr); \
-        if (rc_ != SG_OK)       \
-            return rc_;         \
-    } while (0)
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
@@ -501,73 +487,6 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-struct Widen {
-    const int8_t *src;
-    int64_t ld, rows;
-    int32_t cols, group;   // group: columns of a scale, 0: the row's
-    const float *scale;    // NULL: the integers themselves, in fp16
-    const float *factor;   // of the scales, or NULL
-    uint16_t *dst;
-    int64_t ldd;           // a whole number of 16
-    int32_t f16, vec;      // vec: rows start on 16 bytes
-};
-
-// int8 rows to 16 bits: the integers, or the values they stand for, of one or two
-// matrices.  A warp takes a row, 16 columns to a lane, whose 32 bytes it writes at
-// once (halves of a sector would each go to L2: 64 MB took 40 us).
-__global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0, const __grid_constant__ Widen m1)
-{
-    const int lane = threadIdx.x & 31;
-    grid_wait();
-    grid_go();
-    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < m0.rows + m1.rows; i += (int64_t)gridDim.x * 8) {
-        const bool second = i >= m0.rows;
-        const Widen &a = second ? m1 : m0;
-        const int64_t r = second ? i - m0.rows : i;
-        const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
-        const float f = a.factor ? *a.factor : 1.f;
-        const int8_t *src = a.src + r * a.ld;
-        const float *sc = a.scale ? a.scale + r * ng : nullptr;
-        uint16_t *dst = a.dst + r * a.ldd;
-#pragma unroll 4
-        for (int c = lane * 16; c < a.cols; c += 512) {
-            uint32_t in[4];
-            if (a.vec && c + 16 <= a.cols) {
-                *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(src + c);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    in[j] = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c + 4 * j + k < a.cols)
-                            in[j] |= (uint32_t)(uint8_t)src[c + 4 * j + k] << (8 * k);
-                }
-            }
-            uint32_t w[8];
-            if (!sc) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = bytes_f16(in[j / 2] ^ 0x80808080u, j & 1);
-            } else {
-                // a group is a whole number of 16 columns
-                const float s = sc[a.group ? c / a.group : 0] * f;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float2 v[4];
-                    rows::unquant8(make_uint2(in[2 * k], in[2 * k + 1]), v);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[j] = rows::mul2(v[j], rows::both(s));
-                        w[4 * k + j] = pack16(v[j].x, v[j].y, a.f16);
-                    }
-                }
-            }
-            st_global32(dst + c, w);
-        }
-    }
-}
-
 // rows that do not start on 16 bytes, copied to a stride that does
 __global__ void __launch_bounds__(256)
     k_linear_copy(const uint16_t *__restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t *__restrict__ dst,
@@ -758,19 +677,6 @@ void make_plan(int64_t T, int64_t H, int64_t N, const void *dout, int64_t ldd, b
     p->o_d = take(p->copy ? T * p->ldn * 2 : 0);
     for (int i = 0; i < 2; ++i)
         p->o_acc[i] = take(p->p[i].split > 1 ? (int64_t)p->p[i].units * p->BM * kBN * 4 : 0);
-}
-
-Widen widen_of(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const float *scale, int32_t group,
-               const float *factor, uint8_t *dst, int64_t ldd, bool f16)
-{
-    const bool vec = ((uintptr_t)src & 15) == 0 && ld % 16 == 0;
-    return {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16, vec};
-}
-
-sg_status widen(const Widen &a, const Widen &b, cudaStream_t st)
-{
-    const int64_t need = ceil_div(a.rows + b.rows, 8), most = kSMs * 8;
-    return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, a, b);
 }
 
 sg_status check_linear(const char *fn, const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,

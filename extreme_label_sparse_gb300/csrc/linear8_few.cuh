@@ -17,27 +17,9 @@
 // time than that takes, the cuts go between tiles.
 #pragma once
 
-#include "launch.cuh"
-#include "tc_tile.cuh"
+#include "linear8_widen.cuh"
 
 namespace {
-
-constexpr int kSMs = 152;
-
-// errors of calls that were given no status word
-__device__ int32_t g_linear_status;
-
-__device__ __forceinline__ int32_t *lin_status(int32_t *status) { return status ? status : &g_linear_status; }
-
-// two of four int8 (bytes 0 and 1, or 2 and 3 of u ^ 0x80808080) as fp16: a byte
-// plus 128 as the low bits of 1024, less 1152
-__device__ __forceinline__ uint32_t bytes_f16(uint32_t u, int half)
-{
-    const uint32_t h = __byte_perm(u, 0x64646464u, half ? 0x4342 : 0x4140);
-    const __half2 v =
-        __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half((unsigned short)0x6480)));
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
 
 constexpr int kBlockK = 128;   // bytes of K in a block
 constexpr int kChunk = 8;      // blocks that are summed in tensor memory: 1024 terms
@@ -46,16 +28,20 @@ constexpr uint32_t kWTile = 128 * kBlockK;
 // for up to TMAX tokens: stages, operand buffers, teams, epilogue warps
 template <int TMAX>
 struct Few {
-    static constexpr int NS = TMAX <= 16 ? 10 : TMAX <= 64 ? 6 : 5;
-    static constexpr int NB = TMAX <= 64 ? 4 : 2;
+    // The tokens are brought to fp16 by a launch before, and copied as they are:
+    // with more than 64 of them turning their bytes into fp16 for each tile takes
+    // longer than the tile's own (128 x 2048 x 128000: 101 us).
+    static constexpr bool kWide = TMAX > 64;
+    static constexpr int NS = TMAX <= 16 ? 10 : TMAX <= 64 ? 6 : 4;
+    static constexpr int NB = 4;
     static constexpr int TEAMS = TMAX <= 64 ? 4 : 2;
     static constexpr int CW = 4 * TEAMS;  // warps that turn bytes into fp16
     static constexpr int EW = TMAX <= 16 ? 4 : 8;
     static constexpr int kCols = TMAX / (EW / 4);  // tokens of an epilogue thread
     static constexpr int kThreads = 32 * (CW + EW + 2);
-    static constexpr uint32_t kStage = kWTile + TMAX * kBlockK;
     static constexpr uint32_t kX = TMAX * kBlockK * 2;  // a buffer of the tokens in fp16
-    static constexpr uint32_t kSmem = NS * kStage + NB * kX + 1024;
+    static constexpr uint32_t kStage = kWTile + (kWide ? kX : TMAX * kBlockK);
+    static constexpr uint32_t kSmem = NS * kStage + (kWide ? 0 : NB * kX) + 1024;
     static constexpr uint32_t kA = 2 * TMAX < 64 ? 64 : 2 * TMAX;  // first column of the A buffers, after D's
 };
 
@@ -133,7 +119,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         c.abort_flag = 0;
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&c.full[s]), 1);
-            mbar_init(smem_u32(&c.empty[s]), 4);
+            mbar_init(smem_u32(&c.empty[s]), F::kWide ? 1 : 4);
         }
         for (int b = 0; b < NB; ++b) {
             mbar_init(smem_u32(&c.ready[b]), 4);
@@ -196,33 +182,36 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                 }
                 tmem_st32(ta + h * 32, r);
             }
-            // the tokens: 16 bytes to a thread at a time, eight threads to a row
-            uint8_t *dst = dsm + (xf - smem_u32(dsm));
-            for (int e = tid; e < a.tn * 8; e += 128) {
-                const int t = e >> 3, u = e & 7;
-                const uint4 w = *reinterpret_cast<const uint4 *>(src + kWTile + t * 128 + ((u ^ (t & 7)) << 4));
-                uint8_t *at = dst + (u >> 2) * (a.tn * 128) + t * 128;
-                const int v = (u & 3) * 2;
-                uint32_t p[8];
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[2 * j] = bytes_f16(in[j] ^ 0x80808080u, 0);
-                    p[2 * j + 1] = bytes_f16(in[j] ^ 0x80808080u, 1);
+            if constexpr (!F::kWide) {
+                // the tokens: 16 bytes to a thread at a time, eight threads to a row
+                uint8_t *dst = dsm + (xf - smem_u32(dsm));
+                for (int e = tid; e < a.tn * 8; e += 128) {
+                    const int t = e >> 3, u = e & 7;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + kWTile + t * 128 + ((u ^ (t & 7)) << 4));
+                    uint8_t *at = dst + (u >> 2) * (a.tn * 128) + t * 128;
+                    const int v = (u & 3) * 2;
+                    uint32_t p[8];
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    #pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        p[2 * j] = bytes_f16(in[j] ^ 0x80808080u, 0);
+                        p[2 * j + 1] = bytes_f16(in[j] ^ 0x80808080u, 1);
+                    }
+                    // half of a row's threads begin with their second 16 bytes: the
+                    // two halves' rows lie in the same banks
+                    const bool odd = u >= 4;
+                    const uint4 lo = make_uint4(p[0], p[1], p[2], p[3]), hi = make_uint4(p[4], p[5], p[6], p[7]);
+                    *reinterpret_cast<uint4 *>(at + (((v + odd) ^ (t & 7)) << 4)) = odd ? hi : lo;
+                    *reinterpret_cast<uint4 *>(at + (((v + !odd) ^ (t & 7)) << 4)) = odd ? lo : hi;
                 }
-                // half of a row's threads begin with their second 16 bytes: the
-                // two halves' rows lie in the same banks
-                const bool odd = u >= 4;
-                const uint4 lo = make_uint4(p[0], p[1], p[2], p[3]), hi = make_uint4(p[4], p[5], p[6], p[7]);
-                *reinterpret_cast<uint4 *>(at + (((v + odd) ^ (t & 7)) << 4)) = odd ? hi : lo;
-                *reinterpret_cast<uint4 *>(at + (((v + !odd) ^ (t & 7)) << 4)) = odd ? lo : hi;
             }
             tmem_st_wait();
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(&c.empty[s]));
+                if constexpr (!F::kWide)
+                    mbar_arrive(smem_u32(&c.empty[s]));
                 mbar_arrive(smem_u32(&c.ready[b]));
             }
         }
@@ -293,7 +282,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         Segment s;
         Ring r;
         bool ok = true;
-        const uint32_t bytes = kWTile + (uint32_t)a.xb * kBlockK;
+        const uint32_t bytes = kWTile + (uint32_t)a.xb * kBlockK * (F::kWide ? 2 : 1);
         while (ok && segment_at(a, b, end, s))
             for (int k = s.k; k < s.k + s.n; ++k, r.next(NS)) {
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status));
@@ -304,6 +293,8 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                     mbar_arrive_expect_tx(bar, bytes);
                     tma_load_2d(st, &mW, k * kBlockK, s.tile * 128, bar);
                     tma_load_2d(st + kWTile, &mx, k * kBlockK, 0, bar);
+                    if constexpr (F::kWide)
+                        tma_load_2d(st + kWTile + TMAX * 128, &mx, k * kBlockK + 64, 0, bar);
                 }
                 __syncwarp();
             }
@@ -319,7 +310,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         const uint32_t idesc = idesc_f16(128, a.tn, 0, 0);
         int64_t b = first;
         Segment s;
-        Ring r;
+        Ring r, rs;  // of the operand buffers, and of the stages
         int it = 0;
         bool ok = true;
         while (ok && segment_at(a, b, end, s)) {
@@ -335,18 +326,28 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                     if (!ok)
                         break;
                     tc_fence_after();
+                    if constexpr (F::kWide) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[rs.i]), rs.ph, abort_flag, status));
+                        if (!ok)
+                            break;
+                    }
                     if (elect_one()) {
-                        const uint32_t xf = base + NS * F::kStage + (uint32_t)r.i * F::kX;
+                        const uint32_t xf = F::kWide ? base + (uint32_t)rs.i * F::kStage + kWTile
+                                                     : base + NS * F::kStage + (uint32_t)r.i * F::kX;
+                        const uint32_t atom = F::kWide ? TMAX * 128 : a.tn * 128;  // 64 of K
                         const OpDesc dx(xf, false);
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
                             mma_ts(tbase + buf * TMAX, tbase + F::kA + (uint32_t)r.i * 64 + ks * 8,
-                                   dx.at((uint32_t)(ks >> 2) * (a.tn * 128 / 16), ks & 3), idesc,
+                                   dx.at((uint32_t)(ks >> 2) * (atom / 16), ks & 3), idesc,
                                    (k > k0 || ks > 0) ? 1u : 0u);
                         mma_commit(smem_u32(&c.freed[r.i]));
+                        if constexpr (F::kWide)
+                            mma_commit(smem_u32(&c.empty[rs.i]));
                     }
                     __syncwarp();
                     r.next(NB);
+                    rs.next(NS);
                 }
                 if (ok && elect_one())
                     mma_commit(smem_u32(&c.tfull[buf]));
@@ -537,10 +538,12 @@ bool is_few(const int8_t *x8, int64_t ldx, int64_t T, const int8_t *W8, int64_t 
 
 bool by_dot(int64_t T, int64_t H) { return T <= kDotTokens && H <= kMostDot; }
 
+// bytes of the parts, which come first in the work memory, and of the tokens in fp16
+int64_t few_parts(const FewArgs &a) { return a.whole ? 0 : (int64_t)2 * kSMs * a.tn * 128 * 4; }
+
 int64_t few_work(int64_t T, int64_t H, int64_t N)
 {
-    const FewArgs a = few_args(T, H, N);
-    return by_dot(T, H) || a.whole ? 0 : (int64_t)2 * kSMs * a.tn * 128 * 4;
+    return by_dot(T, H) ? 0 : few_parts(few_args(T, H, N)) + (T > 64 ? T * ceil_div(H, 16) * 32 : 0);
 }
 
 sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
@@ -558,10 +561,21 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
                         : launch_dot<4>(x8, ldx, W8, ldw, H, a, st);
     CUtensorMap mW, mx;
     sg_status rc = map_of(&mW, W8, H, N, ldw, 1, "W8", 128);
-    if (rc == SG_OK)
+    if (rc != SG_OK)
+        return rc;
+    if (T > 64) {
+        uint8_t *wide = static_cast<uint8_t *>(work) + few_parts(a);
+        const int64_t ldh = ceil_div(H, 16) * 16;
+        rc = widen(widen_of(x8, ldx, T, H, nullptr, 0, nullptr, wide, ldh, true), Widen{}, st);
+        if (rc == SG_OK)
+            rc = map_of(&mx, wide, H, T, ldh, 2, "x", (uint32_t)a.xb);
+        if (rc == SG_OK)
+            rc = launch_few<128>(mW, mx, a, st);
+    } else {
         rc = map_of(&mx, x8, H, T, ldx, 1, "x8", (uint32_t)a.xb);
-    if (rc == SG_OK)
-        rc = T <= 16 ? launch_few<16>(mW, mx, a, st) : T <= 64 ? launch_few<64>(mW, mx, a, st) : launch_few<128>(mW, mx, a, st);
+        if (rc == SG_OK)
+            rc = T <= 16 ? launch_few<16>(mW, mx, a, st) : launch_few<64>(mW, mx, a, st);
+    }
     if (rc != SG_OK || a.whole || a.ctas == 1)
         return rc;
     return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T, 8)), 256, 0, 1, true, st, a);

@@ -1,0 +1,132 @@
+// What the 8-bit linear layer's kernels share: its status word, and int8 rows in 16
+// bits.
+#pragma once
+
+#include "launch.cuh"
+#include "quant8.cuh"
+#include "tc_tile.cuh"
+
+namespace {
+
+#define LIN_FAIL(code, ...)        \
+    do {                           \
+        sg_set_error(__VA_ARGS__); \
+        return code;               \
+    } while (0)
+#define LIN_TRY(expr)           \
+    do {                        \
+        sg_status rc_ = (expr); \
+        if (rc_ != SG_OK)       \
+            return rc_;         \
+    } while (0)
+
+constexpr int kSMs = 152;
+
+// errors of calls that were given no status word
+__device__ int32_t g_linear_status;
+
+__device__ __forceinline__ int32_t *lin_status(int32_t *status) { return status ? status : &g_linear_status; }
+
+// two of four int8 (bytes 0 and 1, or 2 and 3 of u ^ 0x80808080) as fp16: a byte
+// plus 128 as the low bits of 1024, less 1152
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t u, int half)
+{
+    const uint32_t h = __byte_perm(u, 0x64646464u, half ? 0x4342 : 0x4140);
+    const __half2 v =
+        __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half((unsigned short)0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+struct Widen {
+    const int8_t *src;
+    int64_t ld, rows;
+    int32_t cols, group;   // group: columns of a scale, 0: the row's
+    const float *scale;    // NULL: the integers themselves, in fp16
+    const float *factor;   // of the scales, or NULL
+    uint16_t *dst;
+    int64_t ldd;           // a whole number of 16
+    int32_t f16, vec;      // vec: rows start on 16 bytes
+};
+
+// int8 rows to 16 bits: the integers, or the values they stand for, of one or two
+// matrices.  A warp takes a row, 16 columns to a lane, whose 32 bytes it writes at
+// once (halves of a sector would each go to L2: 64 MB took 40 us).
+__global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0, const __grid_constant__ Widen m1)
+{
+    const int lane = threadIdx.x & 31;
+    grid_wait();
+    grid_go();
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < m0.rows + m1.rows; i += (int64_t)gridDim.x * 8) {
+        const bool second = i >= m0.rows;
+        const Widen &a = second ? m1 : m0;
+        const int64_t r = second ? i - m0.rows : i;
+        const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
+        const float f = a.factor ? *a.factor : 1.f;
+        const int8_t *src = a.src + r * a.ld;
+        const float *sc = a.scale ? a.scale + r * ng : nullptr;
+        uint16_t *dst = a.dst + r * a.ldd;
+#pragma unroll 4
+        for (int c = lane * 16; c < a.cols; c += 512) {
+            uint32_t in[4];
+            if (a.vec && c + 16 <= a.cols) {
+                *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(src + c);
+            } else if (c + 16 <= a.cols) {
+                // rows that start anywhere: the words that the bytes lie in
+                const int off = (int)((uintptr_t)(src + c) & 3);
+                const uint32_t *at = reinterpret_cast<const uint32_t *>(src + c - off);
+                const uint32_t end = off ? at[4] : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    in[j] = at[j];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    in[j] = __funnelshift_r(in[j], j < 3 ? in[j + 1] : end, 8 * off);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    in[j] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c + 4 * j + k < a.cols)
+                            in[j] |= (uint32_t)(uint8_t)src[c + 4 * j + k] << (8 * k);
+                }
+            }
+            uint32_t w[8];
+            if (!sc) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = bytes_f16(in[j / 2] ^ 0x80808080u, j & 1);
+            } else {
+                // a group is a whole number of 16 columns
+                const float s = sc[a.group ? c / a.group : 0] * f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float2 v[4];
+                    rows::unquant8(make_uint2(in[2 * k], in[2 * k + 1]), v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = rows::mul2(v[j], rows::both(s));
+                        w[4 * k + j] = pack16(v[j].x, v[j].y, a.f16);
+                    }
+                }
+            }
+            st_global32(dst + c, w);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+Widen widen_of(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const float *scale, int32_t group,
+               const float *factor, uint8_t *dst, int64_t ldd, bool f16)
+{
+    const bool vec = ((uintptr_t)src & 15) == 0 && ld % 16 == 0;
+    return {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16, vec};
+}
+
+sg_status widen(const Widen &a, const Widen &b, cudaStream_t st)
+{
+    const int64_t need = ceil_div(a.rows + b.rows, 8), most = kSMs * 8;
+    return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, a, b);
+}
+
+}  // namespace
