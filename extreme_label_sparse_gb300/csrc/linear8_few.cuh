@@ -32,21 +32,22 @@ struct Few {
     // with more than 64 of them turning their bytes into fp16 for each tile takes
     // longer than the tile's own (128 x 2048 x 128000: 101 us).
     static constexpr bool kWide = TMAX > 64;
-    static constexpr int NS = TMAX <= 16 ? 10 : TMAX <= 64 ? 6 : 4;
+    static constexpr int NS = TMAX <= 16 ? 10 : 6;
+    static constexpr int NX = 3;  // stages of the wide tokens, which wait for their MMAs: apart from W's
     static constexpr int NB = 4;
     static constexpr int TEAMS = TMAX <= 64 ? 4 : 2;
     static constexpr int CW = 4 * TEAMS;  // warps that turn bytes into fp16
     static constexpr int EW = TMAX <= 16 ? 4 : 8;
     static constexpr int kCols = TMAX / (EW / 4);  // tokens of an epilogue thread
-    static constexpr int kThreads = 32 * (CW + EW + 2);
+    static constexpr int kThreads = 32 * (CW + EW + 2 + kWide);
     static constexpr uint32_t kX = TMAX * kBlockK * 2;  // a buffer of the tokens in fp16
-    static constexpr uint32_t kStage = kWTile + (kWide ? kX : TMAX * kBlockK);
-    static constexpr uint32_t kSmem = NS * kStage + (kWide ? 0 : NB * kX) + 1024;
+    static constexpr uint32_t kStage = kWTile + (kWide ? 0 : TMAX * kBlockK);
+    static constexpr uint32_t kSmem = NS * kStage + (kWide ? NX : NB) * kX + 1024;
     static constexpr uint32_t kA = 2 * TMAX < 64 ? 64 : 2 * TMAX;  // first column of the A buffers, after D's
 };
 
 struct FewCtl {
-    uint64_t full[10], empty[10], ready[4], freed[4], tfull[2], tempty[2];
+    uint64_t full[10], empty[10], xfull[3], xempty[3], ready[4], freed[4], tfull[2], tempty[2];
     uint32_t tmem;
     int abort_flag;
     float xs[128];
@@ -119,7 +120,11 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         c.abort_flag = 0;
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&c.full[s]), 1);
-            mbar_init(smem_u32(&c.empty[s]), F::kWide ? 1 : 4);
+            mbar_init(smem_u32(&c.empty[s]), 4);
+        }
+        for (int s = 0; s < F::NX; ++s) {
+            mbar_init(smem_u32(&c.xfull[s]), 1);
+            mbar_init(smem_u32(&c.xempty[s]), 1);
         }
         for (int b = 0; b < NB; ++b) {
             mbar_init(smem_u32(&c.ready[b]), 4);
@@ -210,8 +215,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (!F::kWide)
-                    mbar_arrive(smem_u32(&c.empty[s]));
+                mbar_arrive(smem_u32(&c.empty[s]));
                 mbar_arrive(smem_u32(&c.ready[b]));
             }
         }
@@ -276,25 +280,35 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                 });
             }
         }
-    } else if (warp == CW + EW) {
-        // ---------------------------------------------------------- producer
+    } else if (warp == CW + EW || warp == CW + EW + 2) {
+        // ---------------------------------------------------------- producers
+        // of W and the tokens' bytes, or (the second) of the wide tokens
+        const bool xs = warp != CW + EW;
+        const int ns = xs ? F::NX : NS;
         int64_t b = first;
         Segment s;
         Ring r;
         bool ok = true;
-        const uint32_t bytes = kWTile + (uint32_t)a.xb * kBlockK * (F::kWide ? 2 : 1);
+        const uint32_t bytes = xs ? (uint32_t)a.xb * kBlockK * 2 : kWTile + (F::kWide ? 0 : (uint32_t)a.xb * kBlockK);
         while (ok && segment_at(a, b, end, s))
-            for (int k = s.k; k < s.k + s.n; ++k, r.next(NS)) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.empty[r.i]), r.ph ^ 1u, abort_flag, status));
+            for (int k = s.k; k < s.k + s.n; ++k, r.next(ns)) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(xs ? &c.xempty[r.i] : &c.empty[r.i]), r.ph ^ 1u,
+                                                       abort_flag, status));
                 if (!ok)
                     break;
                 if (elect_one()) {
-                    const uint32_t bar = smem_u32(&c.full[r.i]), st = base + (uint32_t)r.i * F::kStage;
+                    const uint32_t bar = smem_u32(xs ? &c.xfull[r.i] : &c.full[r.i]);
                     mbar_arrive_expect_tx(bar, bytes);
-                    tma_load_2d(st, &mW, k * kBlockK, s.tile * 128, bar);
-                    tma_load_2d(st + kWTile, &mx, k * kBlockK, 0, bar);
-                    if constexpr (F::kWide)
-                        tma_load_2d(st + kWTile + TMAX * 128, &mx, k * kBlockK + 64, 0, bar);
+                    if (xs) {
+                        const uint32_t st = base + NS * F::kStage + (uint32_t)r.i * F::kX;
+                        tma_load_2d(st, &mx, k * kBlockK, 0, bar);
+                        tma_load_2d(st + TMAX * 128, &mx, k * kBlockK + 64, 0, bar);
+                    } else {
+                        const uint32_t st = base + (uint32_t)r.i * F::kStage;
+                        tma_load_2d(st, &mW, k * kBlockK, s.tile * 128, bar);
+                        if constexpr (!F::kWide)
+                            tma_load_2d(st + kWTile, &mx, k * kBlockK, 0, bar);
+                    }
                 }
                 __syncwarp();
             }
@@ -310,7 +324,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         const uint32_t idesc = idesc_f16(128, a.tn, 0, 0);
         int64_t b = first;
         Segment s;
-        Ring r, rs;  // of the operand buffers, and of the stages
+        Ring r, rs;  // of the operand buffers, and of the wide tokens' stages
         int it = 0;
         bool ok = true;
         while (ok && segment_at(a, b, end, s)) {
@@ -327,13 +341,12 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                         break;
                     tc_fence_after();
                     if constexpr (F::kWide) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[rs.i]), rs.ph, abort_flag, status));
+                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.xfull[rs.i]), rs.ph, abort_flag, status));
                         if (!ok)
                             break;
                     }
                     if (elect_one()) {
-                        const uint32_t xf = F::kWide ? base + (uint32_t)rs.i * F::kStage + kWTile
-                                                     : base + NS * F::kStage + (uint32_t)r.i * F::kX;
+                        const uint32_t xf = base + NS * F::kStage + (uint32_t)(F::kWide ? rs.i : r.i) * F::kX;
                         const uint32_t atom = F::kWide ? TMAX * 128 : a.tn * 128;  // 64 of K
                         const OpDesc dx(xf, false);
 #pragma unroll
@@ -343,11 +356,11 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                                    (k > k0 || ks > 0) ? 1u : 0u);
                         mma_commit(smem_u32(&c.freed[r.i]));
                         if constexpr (F::kWide)
-                            mma_commit(smem_u32(&c.empty[rs.i]));
+                            mma_commit(smem_u32(&c.xempty[rs.i]));
                     }
                     __syncwarp();
                     r.next(NB);
-                    rs.next(NS);
+                    rs.next(F::NX);
                 }
                 if (ok && elect_one())
                     mma_commit(smem_u32(&c.tfull[buf]));
