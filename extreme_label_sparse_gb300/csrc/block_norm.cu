@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-#define BLOCK_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(4, 2) X(8, 2) X(16, 2) X(32, 2)
+#define BLOCK_SHAPES(X) X(1, 1) X(1, 2) X(2, 2) X(4, 2) X(8, 2) X(16, 2) X(32, 2)
 // of the backward kernel: one segment to a thread leaves registers for batches
 #define BLOCK_SHAPES_BWD(X) X(1, 1) X(2, 1) X(4, 1) X(8, 1) X(16, 1) X(16, 2) X(32, 2)
 

@@ -420,9 +420,9 @@ FewArgs few_args(int64_t T, int64_t H, int64_t N)
     a.xb = (int32_t)ceil_div(T, 8) * 8;
     a.kb = (int32_t)ceil_div(H, kBlockK);
     a.tiles = (int32_t)ceil_div(N, 128);
-    // whole tiles where they keep the last SM less than five blocks (about 2 us)
+    // whole tiles where they keep the last SM less than nine blocks (about 4 us)
     // longer than equal ranges would
-    a.whole = ceil_div(a.tiles, kSMs) * a.kb - (int64_t)a.tiles * a.kb / kSMs < 5;
+    a.whole = ceil_div(a.tiles, kSMs) * a.kb - (int64_t)a.tiles * a.kb / kSMs < 9;
     // at least one tile, or two blocks, to a range
     const int64_t n = a.whole ? a.tiles : (int64_t)a.tiles * a.kb, most = a.whole ? n : ceil_div(n, 2);
     a.ctas = (int32_t)(most < kSMs ? most : kSMs);

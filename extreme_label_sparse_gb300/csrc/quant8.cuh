@@ -1,6 +1,6 @@
 // Rows held in 8-bit integers: a group of columns (128, or the whole row) has a
-// scale s = max |x| / 127 and holds q = rint(x (127 (1 / max |x|))); x is about
-// q s.  Scales are at least 2^-126 (1 / s stays finite) and at most kMostScale, 0
+// scale s = max |x| (1 / 127) and holds q = rint(x (127 (1 / max |x|))), each step
+// in fp32; x is about q s.  Scales are at least 2^-126 (1 / s stays finite) and at most kMostScale, 0
 // for a group of zeros, and NaN for a group that holds an infinity or NaN (its q
 // are 0), so that such values are not lost silently.
 #pragma once
@@ -50,7 +50,7 @@ __device__ __forceinline__ Scale8 scale8_of(uint32_t top)
         return {0.f, __uint_as_float(0x7fc00000u)};
     if (a < 127.0f * 0x1p-126f)
         return {0x1p126f, top ? 0x1p-126f : 0.f};
-    return {__fmul_rn(__frcp_rn(a), 127.0f), fminf(__fdiv_rn(a, 127.0f), kMostScale)};
+    return {__fmul_rn(__frcp_rn(a), 127.0f), fminf(__fmul_rn(a, 1.0f / 127.0f), kMostScale)};
 }
 
 // Eight values as int8.  Adding 1.5 2^23 rounds to whole numbers, ties to even,

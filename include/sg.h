@@ -524,7 +524,7 @@ SG_API sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_
  *
  * sg_pack8 -- rows to 8 bits, as a training program keeps activations for the
  * backward pass: for a group with a = max |x|,
- *   scale = a / 127,   q = rint(x (127 (1 / a))),   x is about q scale
+ *   scale = a (1 / 127),   q = rint(x (127 (1 / a))),   x is about q scale
  * each step in fp32, ties to even.  Scales are at least 2^-126, and at most what leaves 127
  * scale an fp32 number; 0 for a group of zeros, and NaN where the group holds an
  * infinity or NaN (its q are 0).  q must not overlap x.  cols <= 32768 with group

@@ -30,7 +30,7 @@ def pack8(x, group: int):
             if a < f(127) * least:
                 inv, scale[r, g] = f(2.0 ** 126), least if a > 0 else f(0)
             else:
-                inv, scale[r, g] = f(1) / a * f(127), min(a / f(127), MOST)
+                inv, scale[r, g] = f(1) / a * f(127), min(a * (f(1) / f(127)), MOST)
             q[r, g * w:(g + 1) * w] = np.rint(v * inv)
     return q, scale if group else scale[:, 0]
 
