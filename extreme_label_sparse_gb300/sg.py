@@ -518,11 +518,19 @@ def sg_rewire(layout: Layout, h, dZ, W, n_drop: int, idx_out, W_out):
 _DTYPE = {torch.bfloat16: SG_BF16, torch.float16: SG_F16, torch.float32: SG_F32, torch.float8_e4m3fn: SG_E4M3}
 _E4M3 = torch.float8_e4m3fn
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _open(t, name: str, dtypes):
     """(rows, columns, dtype, device index) of the matrix that the others of a
     call go by."""
+    try:  # as almost all are
+        dtype, dev = t.dtype, t.get_device()
+        if dev >= 0 and dtype in dtypes:
+            rows, cols = t.shape
+            return rows, cols, dtype, dev
+    except (AttributeError, ValueError, RuntimeError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
@@ -593,7 +601,7 @@ def _call(fn, dev: int, *args):
     """One library call on the current stream of device `dev`, which is made
     the current device for it."""
     st = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == (_get_device or torch.cuda.current_device)():
         status = fn(*args, st)
     else:
         with torch.cuda.device(dev):

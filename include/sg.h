@@ -594,8 +594,9 @@ SG_API sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, 
  * the products rounded to dtype (times a power of two, taken out again, in fp16),
  * and parts of 1024 terms are added in fp32.
  * The results are the same bits for the same call.  A token or channel whose
- * scale is NaN gives NaN.  status and errors found on the device: as
- * sg_softmax_ce_fwd, with sg_linear8_status for calls without a status word.
+ * scale is NaN gives NaN.  Outputs must not overlap inputs.  status and errors
+ * found on the device: as sg_softmax_ce_fwd, with sg_linear8_status for calls
+ * without a status word.
  * T <= 2^24, H <= 2^20, N <= 2^24, T N < 2^43.  work is aligned to 256 bytes;
  * sg_linear8_work wants the same x8, W8, strides (and dout, where backward is 1)
  * as the call. */

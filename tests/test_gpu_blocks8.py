@@ -718,3 +718,48 @@ def test_linear_of_many_channels_again_and_again(T):
         sg.sg_linear8_fwd(x8, xs, W8, ws, out.zero_(), status=status)
         assert torch.equal(out, first)
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("T", [2, 20, 100, 200])
+def test_linear_weights_beyond_2_31_bytes(T):
+    """Offsets pass 32 bits: the last channels of 2.2e9 weights."""
+    H, N = 2048, (1 << 20) + 40001
+    x8, xs = rand8(T, H, 1), scales(T, 3)
+    W8 = torch.zeros((N, H), dtype=torch.int8, device="cuda")
+    at = torch.tensor([0, 5, N // 2, N - 300, N - 2, N - 1], device="cuda")
+    W8[at] = rand8(6, H, 2)
+    ws = scales(N, 4)
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    sg.sg_linear8_fwd(x8, xs, W8, ws, out)
+    check_forward(x8, xs, W8[at], ws[at], out[:, at], "bf16")
+    out[:, at] = 0
+    assert not bool(out.any())
+
+
+def test_linear_output_beyond_2_31_elements():
+    T, H, N = 140, 64, (1 << 24) - 5
+    x8, W8, xs, ws = rand8(T, H, 1), rand8(N, H, 2), scales(T, 3), scales(N, 4)
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    sg.sg_linear8_fwd(x8, xs, W8, ws, out)
+    at = torch.cat([torch.randint(0, N, (300,), generator=gen(7), device="cuda"), torch.arange(N - 3, N, device="cuda")])
+    check_forward(x8, xs, W8[at], ws[at], out[:, at], "bf16")
+
+
+def test_block_norm_beyond_2_31_elements():
+    rows, cols = (1 << 17) + 300, 16384
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rand(3, cols, "bf16", 1)
+    w = weights(cols, "bf16")
+    y, x8 = torch.empty_like(x), torch.empty((rows, cols), dtype=torch.int8, device="cuda")
+    s, rx, ru = torch.empty((rows, 128), device="cuda"), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    u = torch.empty_like(x)
+    sg.sg_block_norm_fwd(x, w[0], w[2], EPS, gate=w[1], u=u, rstd_x=rx, rstd_u=ru, y=y, x8=x8, x_scale=s)
+    want = block(x[-3:].contiguous(), None, *w, 0, 0)
+    assert all(torch.equal(a[-3:], want[k]) for a, k in ((u, "u"), (y, "y"), (x8, "x8"), (s, "x_scale"), (rx, "rstd_x")))
+    assert not bool(y[:-3].any()) and not bool(x8[:-3].any())
+    dx, dres = y, torch.empty_like(x)
+    dpre = torch.empty(cols, device="cuda")
+    sg.sg_block_norm_bwd(x, u, x, w[0], w[2], rx, ru, dx, dresidual=dres, gate=w[1], dpre=dpre)
+    last = [t[-3:].contiguous() for t in (x, u, x)] + [None, None, None, rx[-3:].contiguous(), ru[-3:].contiguous()]
+    check_backward(last, w, "bf16", {"dx": dx[-3:], "dresidual": dres[-3:], "dpre": dpre}, alpha=1.0)
+    assert not bool(dres[:-3].any()) and not bool(dx[:-3].any())
