@@ -24,6 +24,7 @@ namespace {
 constexpr int kBlockK = 128;   // bytes of K in a block
 constexpr int kChunk = 8;      // blocks that are summed in tensor memory: 1024 terms
 constexpr uint32_t kWTile = 128 * kBlockK;
+constexpr int kMaxFew = 512;   // tokens that this way takes
 
 // for up to TMAX tokens: stages, operand buffers, teams, epilogue warps
 template <int TMAX>
@@ -50,12 +51,13 @@ struct FewCtl {
     uint64_t full[10], empty[10], xfull[3], xempty[3], ready[4], freed[4], tfull[2], tempty[2];
     uint32_t tmem;
     int abort_flag;
-    float xs[128];
+    float xs[kMaxFew];
 };
 
 struct FewArgs {
     int32_t T, N, tn;     // tokens, channels, columns of the product (a multiple of 16)
     int32_t xb;           // rows of a box of the tokens
+    int32_t tt;           // tiles of the tokens: above 128, of 128 each, and next to each other in the list
     int32_t kb, tiles;    // blocks of a tile, tiles
     int32_t whole;        // ranges are whole tiles
     int32_t ctas, per, more;  // ranges of `per` blocks (whole: tiles), the first `more` of one more
@@ -142,8 +144,8 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
     }
     grid_wait();
     grid_go();
-    if (threadIdx.x < 128)
-        c.xs[threadIdx.x] = (int)threadIdx.x < a.T ? a.xs[threadIdx.x] : 0.f;
+    for (int i = threadIdx.x; i < a.T; i += F::kThreads)
+        c.xs[i] = a.xs[i];
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
         int it = 0;
         bool ok = true;
         while (ok && segment_at(a, b, end, s)) {
-            const int n = s.tile * 128 + q * 32 + lane;
+            const int n = s.tile / a.tt * 128 + q * 32 + lane, t1 = s.tile % a.tt * 128 + t0;  // the thread's first token
             const float ws = n < a.N ? a.ws[n] : 0.f;
             float v[F::kCols / 16][16] = {};
             for (int k = 0; k < s.n; k += kChunk, ++it) {
@@ -268,13 +270,13 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                             p[(cc * 16 + x) * 128] = v[cc][x];
                     }
             } else if (n < a.N) {
-                with_out(a, t0 * a.ldo + n, [&](auto *p) {
+                with_out(a, t1 * a.ldo + n, [&](auto *p) {
 #pragma unroll
                     for (int cc = 0; cc < F::kCols / 16; ++cc) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x, p += a.ldo)
-                            if (t0 + cc * 16 + x < a.T)
-                                put(p, v[cc][x] * c.xs[t0 + cc * 16 + x] * ws);
+                            if (t1 + cc * 16 + x < a.T)
+                                put(p, v[cc][x] * c.xs[t1 + cc * 16 + x] * ws);
                         asm volatile("" ::: "memory");  // or the scales of all tokens are loaded first, and spilled
                     }
                 });
@@ -301,11 +303,12 @@ __global__ void __launch_bounds__(Few<TMAX>::kThreads, 1)
                     mbar_arrive_expect_tx(bar, bytes);
                     if (xs) {
                         const uint32_t st = base + NS * F::kStage + (uint32_t)r.i * F::kX;
-                        tma_load_2d(st, &mx, k * kBlockK, 0, bar);
-                        tma_load_2d(st + TMAX * 128, &mx, k * kBlockK + 64, 0, bar);
+                        const int t1 = s.tile % a.tt * 128;
+                        tma_load_2d(st, &mx, k * kBlockK, t1, bar);
+                        tma_load_2d(st + TMAX * 128, &mx, k * kBlockK + 64, t1, bar);
                     } else {
                         const uint32_t st = base + (uint32_t)r.i * F::kStage;
-                        tma_load_2d(st, &mW, k * kBlockK, s.tile * 128, bar);
+                        tma_load_2d(st, &mW, k * kBlockK, s.tile / a.tt * 128, bar);
                         if constexpr (!F::kWide)
                             tma_load_2d(st + kWTile, &mx, k * kBlockK, 0, bar);
                     }
@@ -395,19 +398,19 @@ __global__ void __launch_bounds__(256) k_few_join(const __grid_constant__ FewArg
     }
     __syncthreads();
     grid_wait();
-    const int lane = threadIdx.x & 127, n = sm[0] * 128 + lane, parts = sm[1];
+    const int lane = threadIdx.x & 127, n = sm[0] / a.tt * 128 + lane, t1 = sm[0] % a.tt * 128, parts = sm[1];
     if (parts == 0 || n >= a.N)
         return;
     const int step = 2 * a.tn * 128;
     const float ws = a.ws[n], *head = a.part + (int64_t)(2 * c0 + 1) * a.tn * 128 + lane;
     const float *rest = head + a.tn * 128;
 #pragma unroll 2
-    for (int t = (int)blockIdx.y * 2 + threadIdx.x / 128; t < a.T; t += 2 * gridDim.y) {
+    for (int t = (int)blockIdx.y * 2 + threadIdx.x / 128; t < min(a.tn, a.T - t1); t += 2 * gridDim.y) {
         float z = head[t * 128];
 #pragma unroll 4
         for (int c = 0; c < parts; ++c)
             z += rest[(int64_t)c * step + t * 128];
-        with_out(a, t * a.ldo + n, [&](auto *o) { put(o, z * a.xs[t] * ws); });
+        with_out(a, (t1 + t) * a.ldo + n, [&](auto *o) { put(o, z * a.xs[t1 + t] * ws); });
     }
 }
 
@@ -416,10 +419,11 @@ FewArgs few_args(int64_t T, int64_t H, int64_t N)
     FewArgs a = {};
     a.T = (int32_t)T;
     a.N = (int32_t)N;
-    a.tn = (int32_t)ceil_div(T, 16) * 16;
-    a.xb = (int32_t)ceil_div(T, 8) * 8;
+    a.tt = (int32_t)ceil_div(T, 128);
+    a.tn = a.tt > 1 ? 128 : (int32_t)ceil_div(T, 16) * 16;
+    a.xb = a.tt > 1 ? 128 : (int32_t)ceil_div(T, 8) * 8;
     a.kb = (int32_t)ceil_div(H, kBlockK);
-    a.tiles = (int32_t)ceil_div(N, 128);
+    a.tiles = (int32_t)ceil_div(N, 128) * a.tt;
     // whole tiles where they keep the last SM less than nine blocks (about 4 us)
     // longer than equal ranges would
     a.whole = ceil_div(a.tiles, kSMs) * a.kb - (int64_t)a.tiles * a.kb / kSMs < 9;
@@ -544,9 +548,12 @@ sg_status launch_dot(const int8_t *x8, int64_t ldx, const int8_t *W8, int64_t ld
     return launch(k_dot<TT>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, true, st, x8, ldx, W8, ldw, (int)H, a);
 }
 
+// W8 is copied as it is, and so are up to 64 tokens.  Above kMaxFew tokens W8 is
+// better brought to 16 bits once, for the 16-bit products at twice the rate of
+// k_few, which turns it into fp16 for each 128 tokens.
 bool is_few(const int8_t *x8, int64_t ldx, int64_t T, const int8_t *W8, int64_t ldw)
 {
-    return T <= 128 && tma_ok(x8, ldx, 1) && tma_ok(W8, ldw, 1);
+    return T <= kMaxFew && tma_ok(W8, ldw, 1) && (T > 64 || tma_ok(x8, ldx, 1));
 }
 
 bool by_dot(int64_t T, int64_t H) { return T <= kDotTokens && H <= kMostDot; }
@@ -591,7 +598,7 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
     }
     if (rc != SG_OK || a.whole || a.ctas == 1)
         return rc;
-    return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T, 8)), 256, 0, 1, true, st, a);
+    return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T < 128 ? T : 128, 8)), 256, 0, 1, true, st, a);
 }
 
 }  // namespace

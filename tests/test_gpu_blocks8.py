@@ -404,7 +404,7 @@ def test_block_norm_many_rows_are_the_same_bits_each_time():
 LINEAR = [(1, 1, 1), (1, 3, 5), (1, 16, 16), (1, 768, 3000), (2, 64, 128), (3, 100, 7), (7, 1001, 129), (8, 128, 1000),
           (16, 2048, 515), (17, 4096, 260), (31, 130, 96), (33, 64, 1), (48, 1500, 1000), (64, 2064, 256),
           (65, 100, 300), (100, 768, 1000), (127, 5000, 33), (128, 96, 513), (129, 256, 256), (200, 1001, 1003),
-          (256, 8200, 130), (300, 64, 3000), (777, 1000, 500), (1030, 2000, 260), (2100, 520, 72)]
+          (256, 8200, 130), (300, 64, 3000), (385, 4096, 700), (512, 300, 1000), (777, 1000, 500), (1030, 2000, 260), (2100, 520, 72)]
 
 
 def scales(n, seed):
@@ -581,7 +581,7 @@ def test_linear_work_memory_may_hold_anything(T):
 
 def test_linear_channels_in_pieces():
     """More weights than one piece of work memory holds (256 MB in 16 bits)."""
-    T, H, N = 140, 4096, 40000
+    T, H, N = 600, 4096, 40000
     x8, W8, xs, ws = rand8(T, H, 1), rand8(N, H, 2), scales(T, 3), scales(N, 4)
     out = torch.empty((T, N), device="cuda")
     sg.sg_linear8_fwd(x8, xs, W8, ws, out)
@@ -702,7 +702,7 @@ def test_binding_refuses_what_the_library_cannot_see():
         sg.sg_block_norm_bwd(x, q, q, w, w, r, r, x.clone(), x_scale=r, u_scale=r)
 
 
-@pytest.mark.parametrize("T", [16, 33, 48, 64, 100])
+@pytest.mark.parametrize("T", [16, 33, 48, 64, 100, 300])
 def test_linear_of_many_channels_again_and_again(T):
     """W from memory rather than the L2 cache, whose loads complete out of
     order: each launch gives the same result."""
@@ -720,7 +720,7 @@ def test_linear_of_many_channels_again_and_again(T):
     assert int(status) == 0
 
 
-@pytest.mark.parametrize("T", [2, 20, 100, 200])
+@pytest.mark.parametrize("T", [2, 20, 100, 200, 520])
 def test_linear_weights_beyond_2_31_bytes(T):
     """Offsets pass 32 bits: the last channels of 2.2e9 weights."""
     H, N = 2048, (1 << 20) + 40001
