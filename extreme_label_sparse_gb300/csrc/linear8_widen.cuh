@@ -46,27 +46,36 @@ struct Widen {
     uint16_t *dst;
     int64_t ldd;           // a whole number of 16
     int32_t f16, vec;      // vec: rows start on 16 bytes
+    int32_t spans;         // of a row, a warp each
 };
 
 // int8 rows to 16 bits: the integers, or the values they stand for, of one or two
-// matrices.  A warp takes a row, 16 columns to a lane, whose 32 bytes it writes at
-// once (halves of a sector would each go to L2: 64 MB took 40 us).
+// matrices.  A warp takes a row, or a span of one where there are few, 16 columns
+// to a lane, whose 32 bytes it writes at once (halves of a sector would each go to L2: 64 MB took 40 us).
 __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0, const __grid_constant__ Widen m1)
 {
     const int lane = threadIdx.x & 31;
     grid_wait();
     grid_go();
-    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < m0.rows + m1.rows; i += (int64_t)gridDim.x * 8) {
-        const bool second = i >= m0.rows;
+    const int64_t n0 = m0.rows * m0.spans, n = n0 + m1.rows * m1.spans;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < n; i += (int64_t)gridDim.x * 8) {
+        const bool second = i >= n0;
         const Widen &a = second ? m1 : m0;
-        const int64_t r = second ? i - m0.rows : i;
+        int64_t r = second ? i - n0 : i;
+        int first = 0, last = a.cols;
+        if (a.spans > 1) {
+            const int64_t u = r;
+            r = u / a.spans;
+            first = (int)(u - r * a.spans) * 512;
+            last = min(a.cols, first + 512);
+        }
         const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
         const float f = a.factor ? *a.factor : 1.f;
         const int8_t *src = a.src + r * a.ld;
         const float *sc = a.scale ? a.scale + r * ng : nullptr;
         uint16_t *dst = a.dst + r * a.ldd;
 #pragma unroll 4
-        for (int c = lane * 16; c < a.cols; c += 512) {
+        for (int c = first + lane * 16; c < last; c += 512) {
             uint32_t in[4];
             if (a.vec && c + 16 <= a.cols) {
                 *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(src + c);
@@ -120,12 +129,17 @@ Widen widen_of(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const 
                const float *factor, uint8_t *dst, int64_t ldd, bool f16)
 {
     const bool vec = ((uintptr_t)src & 15) == 0 && ld % 16 == 0;
-    return {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16, vec};
+    return {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16, vec, 1};
 }
 
-sg_status widen(const Widen &a, const Widen &b, cudaStream_t st)
+sg_status widen(Widen a, Widen b, cudaStream_t st)
 {
-    const int64_t need = ceil_div(a.rows + b.rows, 8), most = kSMs * 8;
+    const int64_t most = kSMs * 8;
+    // few rows: a warp to 512 columns (128 x 2048: 3 us less)
+    const bool few = a.rows + b.rows < 2 * most;
+    a.spans = few ? (int32_t)ceil_div(a.cols, 512) : 1;
+    b.spans = few ? (int32_t)ceil_div(b.cols, 512) : 1;
+    const int64_t need = ceil_div(a.rows * a.spans + b.rows * b.spans, 8);
     return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, a, b);
 }
 
