@@ -421,8 +421,17 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
     };
     fetch(g, 0);
     fetch(g + R * groups, 1);
-    float2 gp[NV][4], pre[NV][4];  // gate post_weight, pre_weight
-    block_weights<T, VEC, WARPS, NV>(a.post, a.gate, a.pre, wr, lane, a.cols, gp, pre);
+    // gate post_weight and pre_weight, where 1024 threads leave no registers for
+    // them read again for each use (4096 x 16384 bf16: 328 us with them spilled)
+    constexpr bool kKeep = WARPS * NV < 64;
+    float2 gp[kKeep ? NV : 1][4], pre[kKeep ? NV : 1][4];
+    if constexpr (kKeep)
+        block_weights<T, VEC, WARPS, NV>(a.post, a.gate, a.pre, wr, lane, a.cols, gp, pre);
+    auto weights = [&](int n) {
+        if constexpr (!kKeep)
+            block_weights<T, VEC, 1, 1>(a.post, a.gate, a.pre, n * WARPS + wr, lane, a.cols, gp, pre);
+        return kKeep ? n : 0;
+    };
     float2 dpre[NV][4] = {}, dh[NV][4] = {};
     int turn = 0, half = 0;
     float next_u = rstd_of(a.ru, g), next_x = rstd_of(a.rx, g);
@@ -480,6 +489,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 const int c0 = (n * WARPS + wr) * kSeg;
                 if (VEC && c0 + lane * 8 >= a.cols)
                     break;  // and neither has a later segment columns of this thread
+                const int m = weights(n);
                 float2 t[4];
                 Held u;
                 dy_of(k, n, c0, t);
@@ -489,7 +499,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                     t[i] = mul2(t[i], u.v[i]);
                     dpre[n][i] = fma2(t[i], both(ru[k] * u.s(i)), dpre[n][i]);
                 }
-                dot[k] += u.template dot<VEC || !HELD>(t, pre[n]);
+                dot[k] += u.template dot<VEC || !HELD>(t, pre[m]);
             }
         }
         batch_reduce<WARPS, R>(dot, sm, turn);
@@ -507,6 +517,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 const int c0 = (n * WARPS + wr) * kSeg;
                 if (VEC && c0 + lane * 8 >= a.cols)
                     break;
+                const int m = weights(n);
                 float2 t[4];
                 Held h;
                 if (ai) {
@@ -531,14 +542,14 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 dy_of(k, n, c0, t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    du[k][n][i] = fma2(mul2(pre[n][i], both(ru[k])), t[i], du[k][n][i]);
+                    du[k][n][i] = fma2(mul2(pre[m][i], both(ru[k])), t[i], du[k][n][i]);
                 x_of(k, n, c0, h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     t[i] = mul2(du[k][n][i], h.v[i]);
                     dh[n][i] = fma2(t[i], both(rx[k] * h.s(i)), dh[n][i]);
                 }
-                dot[k] += h.template dot<VEC || !HELD>(t, gp[n]);
+                dot[k] += h.template dot<VEC || !HELD>(t, gp[m]);
                 if (a.dres) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -558,11 +569,12 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
                 const int c0 = (n * WARPS + wr) * kSeg;
                 if (VEC && c0 + lane * 8 >= a.cols)
                     break;
+                const int m = weights(n);
                 Held h;
                 x_of(k, n, c0, h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 w = mul2(gp[n][i], both(rx[k]));
+                    const float2 w = mul2(gp[m][i], both(rx[k]));
                     if constexpr (HELD)
                         h.v[i] = fma2(w, du[k][n][i], mul2(h.v[i], both(-back_x * (rx[k] * h.s(i)))));
                     else
@@ -650,7 +662,7 @@ template <typename T, bool HELD, int W, int N>
 constexpr int back_rows()
 {
     const int s = (216 << 10) / block_ctas(W) / (2 * BackRows<T, HELD, N, norm_threads(W)>::kRow);
-    const int most = W >= 32 || N > 1 ? 2 : 4;
+    const int most = W >= 32 ? 1 : N > 1 ? 2 : 4;
     return s > most ? most : s < 1 ? 1 : s;
 }
 
