@@ -11,11 +11,16 @@
 // go into the other one.
 //
 // One kernel for the three products: a persistent CTA, or a pair of CTAs on one
-// 256 x 256 tile where there are more than 128 tokens, walks a list of tiles.  A
-// producer warp streams K blocks of 64 through a ring of shared-memory stages
-// (TMA, 128-byte swizzle), one thread issues tcgen05.mma into one of two TMEM
-// accumulators, and eight warps take the sums of the other one.  Products of few
-// tiles are split along K, their parts joined in a fixed order.
+// 256 x 256 tile, walks a list of tiles.  A producer warp streams K blocks of 64
+// through a ring of shared-memory stages (TMA, 128-byte swizzle), one thread issues
+// tcgen05.mma into one of two TMEM accumulators, and eight warps take the sums of
+// the other one.  Products of few tiles are split along K, their parts joined in a
+// fixed order.  Few tokens go another way (linear8_few.cuh).
+//
+// What bounds it: the tensor cores.  4096 x 4096 x 16384: 299 us, of which the
+// product 262 (2.1 PFLOP/s, 89 % of the tensor pipe's cycles: integers in fp16 draw
+// less power than other values, so the clock stays up) and bringing 80 MB of integers
+// to 16 bits 37.  Gradients of 8192 x 4096 x 4096: 318 us.
 #include <cmath>
 #include <utility>
 

@@ -552,6 +552,42 @@ def test_linear_backward_of_many_tokens_of_one_sign():
     assert (np.abs(f64(dW) - want) <= (2 * HALF["f16"] + 2.0 ** -16) * want).all()
 
 
+def test_two_graphs_that_share_work_memory_in_turn():
+    """Its contents need not survive between calls: two captured calls of other
+    sizes and types over the same memory, replayed one after the other."""
+    calls = []
+    for T, H, N, dtype in ((300, 512, 700, "bf16"), (40, 4096, 500, "f16"), (700, 300, 900, "f16")):
+        x8, W8, xs, ws = rand8(T, H, T, (-H) % 16), rand8(N, H, 2, (-H) % 16), scales(T, 3), scales(N, 4)
+        dout = rand(T, N, dtype, 5)
+        outs = [torch.empty(s, dtype=TYPES[dtype], device="cuda") for s in ((T, N), (T, H), (N, H))]
+        calls.append((x8, xs, W8, ws, dout, outs, max(sg.sg_linear8_work(x8, W8), sg.sg_linear8_work(x8, W8, dout))))
+    work = torch.empty(max(c[6] for c in calls), dtype=torch.uint8, device="cuda")
+
+    def run(c):
+        x8, xs, W8, ws, dout, (out, dx, dW), _ = c
+        sg.sg_linear8_fwd(x8, xs, W8, ws, out, work=work)
+        sg.sg_linear8_bwd(x8, xs, W8, ws, dout, dx=dx, dW=dW, work=work)
+
+    ref = []
+    for c in calls:
+        run(c)
+        ref.append([t.clone() for t in c[5]])
+    graphs = []
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            run(c)
+        graphs.append(g)
+    for i in (0, 1, 2, 1, 0, 2, 2, 0, 1):
+        for t in calls[i][5]:
+            t.zero_()
+        work.fill_(255)
+        graphs[i].replay()
+        assert all(torch.equal(a, b) for a, b in zip(calls[i][5], ref[i])), i
+
+
 def test_linear_without_tokens():
     x8, W8 = rand8(0, 64, 1), rand8(30, 64, 2)
     xs, ws = scales(0, 3), scales(30, 4)
@@ -563,7 +599,7 @@ def test_linear_without_tokens():
     untouched(whole, dW)
 
 
-@pytest.mark.parametrize("T", [1, 4, 40, 128, 200])
+@pytest.mark.parametrize("T", [1, 4, 40, 128, 200, 600])
 def test_linear_work_memory_may_hold_anything(T):
     x8, W8, xs, ws = rand8(T, 1000, 1, 8), rand8(900, 1000, 2, 8), scales(T, 3), scales(900, 4)
     dout = rand(T, 900, "bf16", 5, 4)
@@ -642,9 +678,10 @@ def test_a_training_step_from_8_bit_rows_is_near_the_one_in_64_bits(rows, cols, 
         assert rel <= 0.04, (k, rel)
 
 
-def test_a_step_captured_and_replayed_with_other_inputs():
-    args, _ = step_inputs(300, 512, 600)
-    other, _ = step_inputs(300, 512, 600, 50)
+@pytest.mark.parametrize("rows", [1, 20, 100, 300, 600])
+def test_a_step_captured_and_replayed_with_other_inputs(rows):
+    args, _ = step_inputs(rows, 512, 600)
+    other, _ = step_inputs(rows, 512, 600, 50)
     eager = train_step(*other)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -662,7 +699,7 @@ def test_a_step_captured_and_replayed_with_other_inputs():
     assert all(torch.equal(got[k], eager[k]) for k in eager)
 
 
-@pytest.mark.parametrize("rows", [4, 60, 300])
+@pytest.mark.parametrize("rows", [4, 60, 300, 600])
 def test_steps_on_two_streams_at_once(rows):
     sets = [step_inputs(rows, 512, 1500, s)[0] for s in (0, 50)]
     ref = [train_step(*a) for a in sets]
