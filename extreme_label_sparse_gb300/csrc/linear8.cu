@@ -586,7 +586,6 @@ void schedule(LinArgs &a, int C)
     a.b_lo = (int32_t)(q + ceil_div(rest > 0 ? rest : 0, C - hi));
 }
 
-constexpr int64_t kPiece = 256ll << 20;  // bytes of W in 16 bits, forward
 
 // One call's tiles and the places of its work memory
 struct Plan {
@@ -751,8 +750,8 @@ sg_status sg_linear8_work(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, c
     *bytes = 0;
     if (T == 0)
         return SG_OK;
-    if (!backward && is_few(x8, ldx, T, W8, ldw)) {
-        *bytes = few_work(T, H, N);
+    if (!backward && is_few(T)) {
+        *bytes = few_plan(x8, ldx, T, H, W8, ldw, N).bytes;
         return SG_OK;
     }
     // backward: either gradient may be left out, which changes the splits
@@ -782,18 +781,20 @@ sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
         LIN_FAIL(SG_ERR_INVALID, "%s: out has a row stride below N or is not aligned to its elements", fn);
     if (T == 0)
         return SG_OK;
-    const bool few = is_few(x8, ldx, T, W8, ldw);
     Plan pl;
-    if (few)
-        pl.bytes = few_work(T, H, N);
-    else
+    FewPlan few = {};
+    if (is_few(T)) {
+        few = few_plan(x8, ldx, T, H, W8, ldw, N);
+        pl.bytes = few.bytes;
+    } else {
         make_plan(T, H, N, nullptr, 0, false, false, false, &pl);
+    }
     if (pl.bytes && (!work || work_bytes < pl.bytes || ((uintptr_t)work & 255) != 0))
         LIN_FAIL(SG_ERR_INVALID, "%s: work needs %lld bytes (sg_linear8_work), aligned to 256", fn, (long long)pl.bytes);
     cudaStream_t st = (cudaStream_t)stream;
-    if (few)
-        return few_fwd(x8, ldx, x_scale, T, H, W8, ldw, W_scale, N, out, ldo, dtype, work, status, st);
     uint8_t *w8 = static_cast<uint8_t *>(work);
+    if (is_few(T))
+        return few_fwd(x8, ldx, x_scale, T, H, W8, ldw, W_scale, N, out, ldo, dtype, few, w8, status, st);
     const Widen none = {};
     for (int64_t n0 = 0; n0 < N; n0 += pl.Nc) {
         const int64_t nc = N - n0 < pl.Nc ? N - n0 : pl.Nc;

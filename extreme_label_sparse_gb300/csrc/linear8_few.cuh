@@ -477,19 +477,6 @@ constexpr int kDotTokens = 4;
 constexpr int64_t kMostDot = (1 << 17) - 1;
 constexpr int kDotRows = 2, kDotThreads = 256;
 
-// 16 bytes at column c of a row, 0 past the last
-__device__ __forceinline__ uint4 bytes16(const int8_t *row, int c, int H)
-{
-    if (c + 16 <= H)
-        return *reinterpret_cast<const uint4 *>(row + c);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if (c + j < H)
-            w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ int dot16(uint4 a, uint4 b, int s)
 {
     s = __dp4a((int)a.x, (int)b.x, s);
@@ -514,6 +501,11 @@ __global__ void __launch_bounds__(kDotThreads)
 #pragma unroll
     for (int r = 0; r < kDotRows; ++r)
         w[r] = W8 + (int64_t)min(n0 + r, a.N - 1) * ldw;
+    auto chunk = [&](const int8_t *row, int c) {
+        uint32_t in[4];
+        bytes16(row, c, H, true, in);
+        return make_uint4(in[0], in[1], in[2], in[3]);
+    };
     int sum[kDotRows][TT] = {};
     int c = lane * 16;
     for (; c + (U - 1) * 512 + 16 <= H; c += U * 512) {
@@ -538,10 +530,10 @@ __global__ void __launch_bounds__(kDotThreads)
         uint4 v[kDotRows];
 #pragma unroll
         for (int r = 0; r < kDotRows; ++r)
-            v[r] = bytes16(w[r], c, H);
+            v[r] = chunk(w[r], c);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const uint4 x = t < a.T ? bytes16(x8 + t * ldx, c, H) : make_uint4(0, 0, 0, 0);
+            const uint4 x = t < a.T ? chunk(x8 + t * ldx, c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int r = 0; r < kDotRows; ++r)
                 sum[r][t] = dot16(v[r], x, sum[r][t]);
@@ -568,57 +560,101 @@ sg_status launch_dot(const int8_t *x8, int64_t ldx, const int8_t *W8, int64_t ld
     return launch(k_dot<TT>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, true, st, x8, ldx, W8, ldw, (int)H, a);
 }
 
-// W8 is copied as it is, and so are up to 64 tokens.  Above kMaxFew tokens W8 is
-// better brought to 16 bits once, for the 16-bit products at twice the rate of
-// k_few, which turns it into fp16 for each 128 tokens.
-bool is_few(const int8_t *x8, int64_t ldx, int64_t T, const int8_t *W8, int64_t ldw)
-{
-    return T <= kMaxFew && tma_ok(W8, ldw, 1) && (T > 64 || tma_ok(x8, ldx, 1));
-}
+// Above kMaxFew tokens W8 is better brought to 16 bits once, for the 16-bit products
+// at twice the rate of k_few, which turns it into fp16 for each 128 tokens.
+bool is_few(int64_t T) { return T <= kMaxFew; }
 
 bool by_dot(int64_t T, int64_t H) { return T <= kDotTokens && H <= kMostDot; }
 
-// bytes of the parts, which come first in the work memory, and of the tokens in fp16
-int64_t few_parts(const FewArgs &a) { return a.whole ? 0 : (int64_t)2 * kSMs * a.tn * 128 * 4; }
+// A call's work memory: fp32 parts, tokens (above 64 in fp16; else copies of rows
+// that do not start on 16 bytes), and W8's rows that do not, in pieces of channels
+struct FewPlan {
+    int64_t Nc;              // channels of a piece
+    int64_t ld;              // row stride of copies
+    bool copy_x, copy_W;
+    int64_t o_x, o_W, bytes;
+};
 
-int64_t few_work(int64_t T, int64_t H, int64_t N)
+constexpr int64_t kPiece = 256ll << 20;  // bytes of W8 in the work memory
+
+int64_t few_parts(int64_t T, int64_t H, int64_t N)
 {
-    return by_dot(T, H) ? 0 : few_parts(few_args(T, H, N)) + (T > 64 ? T * ceil_div(H, 16) * 32 : 0);
+    if (by_dot(T, H))
+        return 0;
+    const FewArgs a = few_args(T, H, N);
+    return a.whole ? 0 : (int64_t)2 * kSMs * a.tn * 128 * 4;
+}
+
+FewPlan few_plan(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw, int64_t N)
+{
+    FewPlan p = {};
+    p.ld = ceil_div(H, 16) * 16;
+    p.copy_x = T <= 64 && !tma_ok(x8, ldx, 1);
+    p.copy_W = !tma_ok(W8, ldw, 1);
+    p.Nc = N;
+    if (p.copy_W && N * p.ld > kPiece) {
+        p.Nc = kPiece / p.ld / 128 * 128;
+        p.Nc = p.Nc < 128 ? 128 : p.Nc;
+        p.Nc = p.Nc < N ? p.Nc : N;
+    }
+    auto take = [&](int64_t n) {
+        const int64_t at = p.bytes;
+        p.bytes += ceil_div(n, 256) * 256;
+        return at;
+    };
+    const int64_t one = few_parts(T, H, p.Nc), rest = N % p.Nc ? few_parts(T, H, N % p.Nc) : 0;
+    take(one > rest ? one : rest);
+    p.o_x = take(T > 64 ? T * p.ld * 2 : p.copy_x ? T * p.ld : 0);
+    p.o_W = take(p.copy_W ? p.Nc * p.ld : 0);
+    return p;
 }
 
 sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
-                  const float *ws, int64_t N, void *out, int64_t ldo, int32_t dtype, void *work, int32_t *status,
-                  cudaStream_t st)
+                  const float *ws, int64_t N, void *out, int64_t ldo, int32_t dtype, const FewPlan &p, uint8_t *work,
+                  int32_t *status, cudaStream_t st)
 {
-    FewArgs a = few_args(T, H, N);
-    a.otype = dtype;
-    a.xs = xs, a.ws = ws, a.out = out, a.ldo = ldo;
-    a.part = static_cast<float *>(work);
-    a.status = status;
-    if (by_dot(T, H))
-        return T == 1   ? launch_dot<1>(x8, ldx, W8, ldw, H, a, st)
-               : T == 2 ? launch_dot<2>(x8, ldx, W8, ldw, H, a, st)
-                        : launch_dot<4>(x8, ldx, W8, ldw, H, a, st);
-    CUtensorMap mW, mx;
-    sg_status rc = map_of(&mW, W8, H, N, ldw, 1, "W8", 128);
-    if (rc != SG_OK)
-        return rc;
     if (T > 64) {
-        uint8_t *wide = static_cast<uint8_t *>(work) + few_parts(a);
-        const int64_t ldh = ceil_div(H, 16) * 16;
-        rc = widen(widen_of(x8, ldx, T, H, nullptr, 0, nullptr, wide, ldh, true), Widen{}, st);
-        if (rc == SG_OK)
-            rc = map_of(&mx, wide, H, T, ldh, 2, "x", (uint32_t)a.xb);
-        if (rc == SG_OK)
-            rc = launch_few<128>(mW, mx, a, st);
-    } else {
-        rc = map_of(&mx, x8, H, T, ldx, 1, "x8", (uint32_t)a.xb);
-        if (rc == SG_OK)
-            rc = T <= 16 ? launch_few<16>(mW, mx, a, st) : launch_few<64>(mW, mx, a, st);
+        LIN_TRY(widen(widen_of(x8, ldx, T, H, nullptr, 0, nullptr, work + p.o_x, p.ld, true), Widen{}, st));
+    } else if (p.copy_x) {
+        LIN_TRY(realign(x8, ldx, T, H, work + p.o_x, p.ld, st));
+        x8 = reinterpret_cast<const int8_t *>(work + p.o_x);
+        ldx = p.ld;
     }
-    if (rc != SG_OK || a.whole || a.ctas == 1)
-        return rc;
-    return launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T < 128 ? T : 128, 8)), 256, 0, 1, true, st, a);
+    for (int64_t n0 = 0; n0 < N; n0 += p.Nc) {
+        const int64_t nc = N - n0 < p.Nc ? N - n0 : p.Nc;
+        const int8_t *W = W8 + n0 * ldw;
+        int64_t ld = ldw;
+        if (p.copy_W) {
+            LIN_TRY(realign(W, ldw, nc, H, work + p.o_W, p.ld, st));
+            W = reinterpret_cast<const int8_t *>(work + p.o_W);
+            ld = p.ld;
+        }
+        FewArgs a = few_args(T, H, nc);
+        a.otype = dtype;
+        a.xs = xs, a.ws = ws + n0, a.ldo = ldo;
+        a.out = static_cast<uint8_t *>(out) + n0 * (dtype == SG_F32 ? 4 : 2);
+        a.part = reinterpret_cast<float *>(work);
+        a.status = status;
+        if (by_dot(T, H)) {
+            LIN_TRY((T == 1   ? launch_dot<1>(x8, ldx, W, ld, H, a, st)
+                     : T == 2 ? launch_dot<2>(x8, ldx, W, ld, H, a, st)
+                              : launch_dot<4>(x8, ldx, W, ld, H, a, st)));
+            continue;
+        }
+        CUtensorMap mW, mx;
+        LIN_TRY(map_of(&mW, W, H, nc, ld, 1, "W8", 128));
+        if (T > 64) {
+            LIN_TRY(map_of(&mx, work + p.o_x, H, T, p.ld, 2, "x", (uint32_t)a.xb));
+            LIN_TRY(launch_few<128>(mW, mx, a, st));
+        } else {
+            LIN_TRY(map_of(&mx, x8, H, T, ldx, 1, "x8", (uint32_t)a.xb));
+            LIN_TRY(T <= 16 ? launch_few<16>(mW, mx, a, st) : launch_few<64>(mW, mx, a, st));
+        }
+        if (!a.whole && a.ctas > 1)
+            LIN_TRY(launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T < 128 ? T : 128, 8)), 256, 0, 1,
+                           true, st, a));
+    }
+    return SG_OK;
 }
 
 }  // namespace

@@ -37,6 +37,58 @@ __device__ __forceinline__ uint32_t bytes_f16(uint32_t u, int half)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// 16 bytes at column c (a whole number of 16) of a row of `cols`, 0 past the last;
+// vec: the row starts on 16 bytes
+__device__ __forceinline__ void bytes16(const int8_t *row, int c, int cols, bool vec, uint32_t (&in)[4])
+{
+    if (vec && c + 16 <= cols) {
+        *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(row + c);
+    } else if (c + 16 <= cols) {
+        // rows that start anywhere: the words that the bytes lie in
+        const int off = (int)((uintptr_t)(row + c) & 3);
+        const uint32_t *at = reinterpret_cast<const uint32_t *>(row + c - off);
+        const uint32_t end = off ? at[4] : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            in[j] = at[j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            in[j] = __funnelshift_r(in[j], j < 3 ? in[j + 1] : end, 8 * off);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            in[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + 4 * j + k < cols)
+                    in[j] |= (uint32_t)(uint8_t)row[c + 4 * j + k] << (8 * k);
+        }
+    }
+}
+
+// int8 rows that do not start on 16 bytes, copied to rows that do, of a whole
+// number of 16 (0 past the last column): 48 bytes of traffic for 16, where bringing
+// them to 16 bits takes 80.  A warp takes a row, or 512 columns of one where there
+// are few rows.
+__global__ void __launch_bounds__(256)
+    k_realign(const int8_t *__restrict__ src, int64_t ld, int64_t rows, int cols, int spans, int8_t *__restrict__ dst,
+              int64_t ldd)
+{
+    const int lane = threadIdx.x & 31;
+    grid_wait();
+    grid_go();
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < rows * spans; i += (int64_t)gridDim.x * 8) {
+        const int64_t r = spans > 1 ? i / spans : i;
+        const int first = spans > 1 ? (int)(i - r * spans) * 512 : 0, last = spans > 1 ? min(cols, first + 512) : cols;
+#pragma unroll 4
+        for (int c = first + lane * 16; c < last; c += 512) {
+            uint32_t in[4];
+            bytes16(src + r * ld, c, cols, false, in);
+            *reinterpret_cast<uint4 *>(dst + r * ldd + c) = make_uint4(in[0], in[1], in[2], in[3]);
+        }
+    }
+}
+
 struct Widen {
     const int8_t *src;
     int64_t ld, rows;
@@ -77,29 +129,7 @@ __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0,
 #pragma unroll 4
         for (int c = first + lane * 16; c < last; c += 512) {
             uint32_t in[4];
-            if (a.vec && c + 16 <= a.cols) {
-                *reinterpret_cast<uint4 *>(in) = *reinterpret_cast<const uint4 *>(src + c);
-            } else if (c + 16 <= a.cols) {
-                // rows that start anywhere: the words that the bytes lie in
-                const int off = (int)((uintptr_t)(src + c) & 3);
-                const uint32_t *at = reinterpret_cast<const uint32_t *>(src + c - off);
-                const uint32_t end = off ? at[4] : 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    in[j] = at[j];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    in[j] = __funnelshift_r(in[j], j < 3 ? in[j + 1] : end, 8 * off);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    in[j] = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c + 4 * j + k < a.cols)
-                            in[j] |= (uint32_t)(uint8_t)src[c + 4 * j + k] << (8 * k);
-                }
-            }
+            bytes16(src, c, a.cols, a.vec, in);
             uint32_t w[8];
             if (!sc) {
 #pragma unroll
@@ -141,6 +171,13 @@ sg_status widen(Widen a, Widen b, cudaStream_t st)
     b.spans = few ? (int32_t)ceil_div(b.cols, 512) : 1;
     const int64_t need = ceil_div(a.rows * a.spans + b.rows * b.spans, 8);
     return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, a, b);
+}
+
+sg_status realign(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, uint8_t *dst, int64_t ldd, cudaStream_t st)
+{
+    const int64_t most = kSMs * 8, spans = rows < 2 * most ? ceil_div(cols, 512) : 1, need = ceil_div(rows * spans, 8);
+    return launch(k_realign, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, src, ld, rows, (int)cols,
+                  (int)spans, reinterpret_cast<int8_t *>(dst), ldd);
 }
 
 }  // namespace

@@ -615,13 +615,15 @@ def test_linear_work_memory_may_hold_anything(T):
     assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
-def test_linear_channels_in_pieces():
-    """More weights than one piece of work memory holds (256 MB in 16 bits)."""
-    T, H, N = 600, 4096, 40000
+@pytest.mark.parametrize("T,H,N", [(600, 4096, 40000), (2, 4099, 70000), (7, 4099, 70000), (100, 4099, 70000)])
+def test_linear_channels_in_pieces(T, H, N):
+    """More weights than one piece of work memory holds: 256 MB in 16 bits, or of
+    rows that do not start on 16 bytes in 8."""
     x8, W8, xs, ws = rand8(T, H, 1), rand8(N, H, 2), scales(T, 3), scales(N, 4)
     out = torch.empty((T, N), device="cuda")
     sg.sg_linear8_fwd(x8, xs, W8, ws, out)
-    at = torch.cat([torch.arange(0, 40), torch.arange(32700, 32800), torch.arange(N - 40, N)]).cuda()
+    at = torch.cat([torch.arange(0, 40), torch.arange(32700, 32800), torch.arange(65200, 65400) % N,
+                    torch.arange(N - 40, N)]).cuda()
     check_forward(x8, xs, W8[at], ws[at], out[:, at], "f32")
 
 
