@@ -472,7 +472,7 @@ sg_status launch_few(const CUtensorMap &mW, const CUtensorMap &mx, const FewArgs
 // One to four tokens: a warp has two channels, a lane every 32nd 16 bytes of
 // their rows, and sums of up to kMostDot products in 32-bit integers are exact.
 // Bound by reading W8: 1 x 2048 x 128000 takes 40.6 us (6.5 TB/s), 4 tokens 50 us
-// (the integer products), 1 x 4096 x 4096 4.6 us.
+// (the integer products), 1 x 4096 x 4096 3 us.
 constexpr int kDotTokens = 4;
 constexpr int64_t kMostDot = (1 << 17) - 1;
 constexpr int kDotRows = 2, kDotThreads = 256;
@@ -485,7 +485,43 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int s)
     return __dp4a((int)a.w, (int)b.w, s);
 }
 
-template <int TT>
+// 16 bytes at column c < H of a row that starts anywhere: from the two aligned 16
+// that they lie in, of which each that is read has a byte of the row.  Bytes past the
+// last column may be anything.
+template <bool STREAM>
+__device__ __forceinline__ uint4 any16(const int8_t *row, int c, int H)
+{
+    const int off = (int)((uintptr_t)row & 15);  // the same for the warp
+    const uint4 *at = reinterpret_cast<const uint4 *>(row + c - off);
+    if (off == 0)
+        return STREAM ? __ldcs(at) : *at;
+    const uint4 a = at[0], b = c + 16 - off < H ? at[1] : make_uint4(0, 0, 0, 0);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8) {
+#pragma unroll
+        for (int j = 0; j < 6; ++j)
+            w[j] = w[j + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+            w[j] = w[j + 1];
+    }
+    const int s = 8 * (off & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
+// the first n bytes of 16, and 0
+__device__ __forceinline__ uint4 first_bytes(uint4 v, int n)
+{
+    auto keep = [&](uint32_t w, int j) { return n >= 4 * j + 4 ? w : n <= 4 * j ? 0u : w & ((1u << (8 * (n - 4 * j))) - 1u); };
+    return make_uint4(keep(v.x, 0), keep(v.y, 1), keep(v.z, 2), keep(v.w, 3));
+}
+
+// ANY: rows start anywhere (1 x 1001 x 32000: 14 us, copied to aligned rows first 21;
+// 1 x 1024 x 32000, aligned: 6).
+template <int TT, bool ANY>
 __global__ void __launch_bounds__(kDotThreads)
     k_dot(const int8_t *__restrict__ x8, int64_t ldx, const int8_t *__restrict__ W8, int64_t ldw, int H,
           const __grid_constant__ FewArgs a)
@@ -501,10 +537,17 @@ __global__ void __launch_bounds__(kDotThreads)
 #pragma unroll
     for (int r = 0; r < kDotRows; ++r)
         w[r] = W8 + (int64_t)min(n0 + r, a.N - 1) * ldw;
-    auto chunk = [&](const int8_t *row, int c) {
-        uint32_t in[4];
-        bytes16(row, c, H, true, in);
-        return make_uint4(in[0], in[1], in[2], in[3]);
+    auto load_w = [&](int r, int c) {
+        if constexpr (ANY)
+            return any16<true>(w[r], c, H);
+        else
+            return __ldcs(reinterpret_cast<const uint4 *>(w[r] + c));
+    };
+    auto load_x = [&](int t, int c) {
+        if constexpr (ANY)
+            return any16<false>(x8 + t * ldx, c, H);
+        else
+            return *reinterpret_cast<const uint4 *>(x8 + t * ldx + c);
     };
     int sum[kDotRows][TT] = {};
     int c = lane * 16;
@@ -514,31 +557,44 @@ __global__ void __launch_bounds__(kDotThreads)
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < kDotRows; ++r)
-                v[r][u] = __ldcs(reinterpret_cast<const uint4 *>(w[r] + c + u * 512));
+                v[r][u] = load_w(r, c + u * 512);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const uint4 x = t < a.T ? *reinterpret_cast<const uint4 *>(x8 + t * ldx + c + u * 512)
-                                        : make_uint4(0, 0, 0, 0);
+                const uint4 x = t < a.T ? load_x(t, c + u * 512) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int r = 0; r < kDotRows; ++r)
                     sum[r][t] = dot16(v[r][u], x, sum[r][t]);
             }
     }
-    for (; c < H; c += 512) {
-        uint4 v[kDotRows];
+    // the rest, whose last 16 may go past the row's end (not past its stride's 16):
+    // what W has there meets zeros
+    if (c < H) {
+        uint4 v[kDotRows][U];
 #pragma unroll
-        for (int r = 0; r < kDotRows; ++r)
-            v[r] = chunk(w[r], c);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const uint4 x = t < a.T ? chunk(x8 + t * ldx, c) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < kDotRows; ++r)
-                sum[r][t] = dot16(v[r], x, sum[r][t]);
+                if (c + u * 512 < H)
+                    v[r][u] = load_w(r, c + u * 512);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = c + u * 512;
+            if (at < H) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    uint4 x = t < a.T ? load_x(t, at) : make_uint4(0, 0, 0, 0);
+                    if (at + 16 > H)
+                        x = first_bytes(x, H - at);
+#pragma unroll
+                    for (int r = 0; r < kDotRows; ++r)
+                        sum[r][t] = dot16(v[r][u], x, sum[r][t]);
+                }
+            }
         }
     }
+    __syncwarp();
     int mine = 0;  // lane r TT + t has token t of channel n0 + r
 #pragma unroll
     for (int r = 0; r < kDotRows; ++r)
@@ -552,12 +608,12 @@ __global__ void __launch_bounds__(kDotThreads)
         with_out(a, t * a.ldo + n, [&](auto *p) { put(p, (float)mine * a.xs[t] * a.ws[n]); });
 }
 
-template <int TT>
+template <int TT, bool ANY>
 sg_status launch_dot(const int8_t *x8, int64_t ldx, const int8_t *W8, int64_t ldw, int64_t H, const FewArgs &a,
                      cudaStream_t st)
 {
     const int rows = kDotThreads / 32 * kDotRows;
-    return launch(k_dot<TT>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, true, st, x8, ldx, W8, ldw, (int)H, a);
+    return launch(k_dot<TT, ANY>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, true, st, x8, ldx, W8, ldw, (int)H, a);
 }
 
 // Above kMaxFew tokens W8 is better brought to 16 bits once, for the 16-bit products
@@ -589,8 +645,9 @@ FewPlan few_plan(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8
 {
     FewPlan p = {};
     p.ld = ceil_div(H, 16) * 16;
-    p.copy_x = T <= 64 && !tma_ok(x8, ldx, 1);
-    p.copy_W = !tma_ok(W8, ldw, 1);
+    const bool any = by_dot(T, H) && T <= 2;  // k_dot takes such rows itself
+    p.copy_x = !any && T <= 64 && !tma_ok(x8, ldx, 1);
+    p.copy_W = !any && !tma_ok(W8, ldw, 1);
     p.Nc = N;
     if (p.copy_W && N * p.ld > kPiece) {
         p.Nc = kPiece / p.ld / 128 * 128;
@@ -636,9 +693,10 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
         a.part = reinterpret_cast<float *>(work);
         a.status = status;
         if (by_dot(T, H)) {
-            LIN_TRY((T == 1   ? launch_dot<1>(x8, ldx, W, ld, H, a, st)
-                     : T == 2 ? launch_dot<2>(x8, ldx, W, ld, H, a, st)
-                              : launch_dot<4>(x8, ldx, W, ld, H, a, st)));
+            const bool any = !tma_ok(x8, ldx, 1) || !tma_ok(W, ld, 1);
+            LIN_TRY((T > 2    ? launch_dot<4, false>(x8, ldx, W, ld, H, a, st)
+                     : T == 2 ? (any ? launch_dot<2, true> : launch_dot<2, false>)(x8, ldx, W, ld, H, a, st)
+                              : (any ? launch_dot<1, true> : launch_dot<1, false>)(x8, ldx, W, ld, H, a, st)));
             continue;
         }
         CUtensorMap mW, mx;

@@ -519,10 +519,10 @@ SG_API sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_
  * layers run on 8-bit integers: rows held in 8 bits, the norms around a block,
  * and the linear layer itself, each with its gradient.  The conventions are
  * those of the section above; 8-bit rows are fastest where they start on 16 bytes
- * (a linear layer of up to 512 tokens needs that of W8 to read it once, and of up
- * to 64 tokens of x8 too).  8-bit rows hold values of -127 to 127 and have
- * fp32 scales, contiguous: one for each row (group 0), or scale[rows][ceil(cols
- * / 128)], one for each 128 columns of a row (group 128; the last may be fewer).
+ * (a linear layer copies W8's rows that do not, but for one or two tokens).  8-bit
+ * rows hold values of -127 to 127 and have fp32 scales, contiguous: one for each row
+ * (group 0), or scale[rows][ceil(cols / 128)], one for each 128 columns of a row
+ * (group 128; the last may be fewer).
  *
  * sg_pack8 -- rows to 8 bits, as a training program keeps activations for the
  * backward pass: for a group with a = max |x|,
