@@ -457,39 +457,14 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Pro
     }
 }
 
-// A power of two that brings the largest of n scales to [256, 512), where the
-// largest value held in 8 bits (127 times it) is still an fp16 number, and its
-// inverse.  CTA 0: the first vector, CTA 1: the second.
+// factor_of the largest scales of two vectors, by a CTA each
 __global__ void __launch_bounds__(1024)
     k_factor(const float *s0, int64_t n0, float *f0, const float *s1, int64_t n1, float *f1)
 {
     __shared__ float sm[32];
-    const float *s = blockIdx.x ? s1 : s0;
-    const int64_t n = blockIdx.x ? n1 : n0;
-    float top = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) {
-        const float v = fabsf(s[i]);
-        if (v < INFINITY)
-            top = fmaxf(top, v);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0)
-        sm[threadIdx.x / 32] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 32; ++w)
-            top = fmaxf(top, sm[w]);
-        int e = 0;
-        if (top > 0.f)
-            frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
-        e = top > 0.f ? 9 - e : 0;
-        e = e > 126 ? 126 : e;
-        float *f = blockIdx.x ? f1 : f0;
-        f[0] = ldexpf(1.f, e);
-        f[1] = ldexpf(1.f, -e);
-    }
+    const float2 f = factor_of<1024>(blockIdx.x ? s1 : s0, blockIdx.x ? n1 : n0, sm);
+    if (threadIdx.x == 0)
+        *reinterpret_cast<float2 *>(blockIdx.x ? f1 : f0) = f;
 }
 
 // rows that do not start on 16 bytes, copied to a stride that does
@@ -854,9 +829,12 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     const bool f16 = dtype == SG_F16;
     // factors of the scales: fp16 has not their range
     float *fac = f16 ? reinterpret_cast<float *>(w8 + pl.o_f) : nullptr;
-    if (f16) {
-        k_factor<<<2, 1024, 0, st>>>(W_scale, dx ? N : 0, fac, x_scale,
-                                     dW ? T * (x_group ? ceil_div(H, (int64_t)x_group) : 1) : 0, fac + 2);
+    const int64_t nW = dx ? N : 0, nx = dW ? T * (x_group ? ceil_div(H, (int64_t)x_group) : 1) : 0;
+    // by the kernel that widens, where each of its threads has at most 64 of them
+    // to look at (a launch less: 128 x 768 x 5003)
+    const bool with = f16 && nW + nx <= 64 * 256;
+    if (f16 && !with) {
+        k_factor<<<2, 1024, 0, st>>>(W_scale, nW, fac, x_scale, nx, fac + 2);
         SG_TRY_CUDA(cudaGetLastError());
     }
     if (pl.copy) {
@@ -868,9 +846,10 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     }
     Widen wide[2] = {};
     if (dx)
-        wide[0] = widen_of(W8, ldw, N, H, W_scale, 0, fac, w8 + pl.o_W, pl.ldh, f16);
+        wide[0] = widen_of(W8, ldw, N, H, W_scale, 0, fac, w8 + pl.o_W, pl.ldh, f16, with ? nW : 0);
     if (dW)
-        wide[1] = widen_of(x8, ldx, T, H, x_scale, x_group, fac ? fac + 2 : nullptr, w8 + pl.o_x, pl.ldh, f16);
+        wide[1] = widen_of(x8, ldx, T, H, x_scale, x_group, fac ? fac + 2 : nullptr, w8 + pl.o_x, pl.ldh, f16,
+                           with ? nx : 0);
     LIN_TRY(widen(wide[0], wide[1], st));
     LinArgs a = {};
     a.p[0] = pl.p[0], a.p[1] = pl.p[1];

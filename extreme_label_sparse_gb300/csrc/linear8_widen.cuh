@@ -89,12 +89,42 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// A power of two that brings the largest of n scales to [256, 512), where the
+// largest value held in 8 bits (127 times it) is still an fp16 number, and its
+// inverse: for all THREADS of a CTA.
+template <int THREADS>
+__device__ __forceinline__ float2 factor_of(const float *s, int64_t n, float *sm)
+{
+    float top = 0.f;
+    for (int64_t i = threadIdx.x; i < n; i += THREADS) {
+        const float v = fabsf(s[i]);
+        if (v < INFINITY)
+            top = fmaxf(top, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        sm[threadIdx.x / 32] = top;
+    __syncthreads();
+    for (int i = 0; i < THREADS / 32; ++i)
+        top = fmaxf(top, sm[i]);
+    int e = 0;
+    if (top > 0.f)
+        frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
+    e = top > 0.f ? 9 - e : 0;
+    e = e > 126 ? 126 : e;
+    return make_float2(ldexpf(1.f, e), ldexpf(1.f, -e));
+}
+
 struct Widen {
     const int8_t *src;
     int64_t ld, rows;
     int32_t cols, group;   // group: columns of a scale, 0: the row's
     const float *scale;    // NULL: the integers themselves, in fp16
-    const float *factor;   // of the scales, or NULL
+    float *factor;         // of the scales, and its inverse, or NULL
+    int32_t scales;        // if not 0: the factor is not there yet, and goes by so many
     uint16_t *dst;
     int64_t ldd;           // a whole number of 16
     int32_t f16, vec;      // vec: rows start on 16 bytes
@@ -109,6 +139,23 @@ __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0,
     const int lane = threadIdx.x & 31;
     grid_wait();
     grid_go();
+    // few scales: each CTA works the factors out, one keeps them for later launches
+    __shared__ float sm[8];
+    float2 f0 = make_float2(1.f, 1.f), f1 = f0;
+    if (m0.scales)
+        f0 = factor_of<256>(m0.scale, m0.scales, sm);
+    else if (m0.factor)
+        f0.x = *m0.factor;
+    if (m1.scales)
+        f1 = factor_of<256>(m1.scale, m1.scales, sm);
+    else if (m1.factor)
+        f1.x = *m1.factor;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (m0.scales)
+            *reinterpret_cast<float2 *>(m0.factor) = f0;
+        if (m1.scales)
+            *reinterpret_cast<float2 *>(m1.factor) = f1;
+    }
     const int64_t n0 = m0.rows * m0.spans, n = n0 + m1.rows * m1.spans;
     for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < n; i += (int64_t)gridDim.x * 8) {
         const bool second = i >= n0;
@@ -122,7 +169,7 @@ __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0,
             last = min(a.cols, first + 512);
         }
         const int ng = a.group ? (a.cols + a.group - 1) / a.group : 1;
-        const float f = a.factor ? *a.factor : 1.f;
+        const float f = second ? f1.x : f0.x;
         const int8_t *src = a.src + r * a.ld;
         const float *sc = a.scale ? a.scale + r * ng : nullptr;
         uint16_t *dst = a.dst + r * a.ldd;
@@ -156,10 +203,11 @@ __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0,
 
 // ---------------------------------------------------------------- host
 Widen widen_of(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const float *scale, int32_t group,
-               const float *factor, uint8_t *dst, int64_t ldd, bool f16)
+               float *factor, uint8_t *dst, int64_t ldd, bool f16, int64_t scales = 0)
 {
     const bool vec = ((uintptr_t)src & 15) == 0 && ld % 16 == 0;
-    return {src, ld, rows, (int32_t)cols, group, scale, factor, reinterpret_cast<uint16_t *>(dst), ldd, f16, vec, 1};
+    return {src,    ld,  rows, (int32_t)cols, group, scale, factor, (int32_t)scales, reinterpret_cast<uint16_t *>(dst),
+            ldd, f16, vec,  1};
 }
 
 sg_status widen(Widen a, Widen b, cudaStream_t st)
