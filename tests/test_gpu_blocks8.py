@@ -524,6 +524,27 @@ def test_linear_backward_of_one_gradient(T, H, N):
     check_gradients(x8, xs, W8, ws, dout, dx, dW, "bf16")
 
 
+@pytest.mark.parametrize("T,H,N", [
+    (200, 1500, 3000),   # dx in parts, first
+    (64, 2048, 4096),    # dW first, of which each cluster has some
+    (600, 2048, 2200),   # pairs of CTAs, dx first
+    (1100, 1000, 1200),
+    (128, 1024, 4864),   # 152 tiles of dW, as many as clusters
+    (3000, 300, 700),    # dW in parts
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_linear_backward_units_of_both_products(T, H, N, dtype):
+    """Every tile of either product is computed, by the cluster whose turn it is;
+    outputs that held NaN before."""
+    x8, W8, xs, ws = rand8(T, H, 1, (-H) % 16), rand8(N, H, 2, (-H) % 16), scales(T, 3), scales(N, 4)
+    dout = rand(T, N, dtype, 5, (-N) % 8)
+    dx, dW = (torch.full(s, float("nan"), dtype=TYPES[dtype], device="cuda") for s in ((T, H), (N, H)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sg.sg_linear8_bwd(x8, xs, W8, ws, dout, dx=dx, dW=dW, status=status)
+    check_gradients(x8, xs, W8, ws, dout, dx, dW, dtype)
+    assert int(status) == 0
+
+
 @pytest.mark.parametrize("T", [50, 300])
 def test_linear_backward_f16_of_small_and_uneven_scales(T):
     """fp16's range is that of the scales' ratios, not of the scales."""
