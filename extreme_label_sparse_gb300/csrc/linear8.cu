@@ -862,9 +862,11 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     // factors of the scales: fp16 has not their range
     float *fac = f16 ? reinterpret_cast<float *>(w8 + pl.o_f) : nullptr;
     const int64_t nW = dx ? N : 0, nx = dW ? T * (x_group ? ceil_div(H, (int64_t)x_group) : 1) : 0;
-    // by the kernel that widens, where each of its threads has at most 64 of them
-    // to look at (a launch less: 128 x 768 x 5003)
-    const bool with = f16 && nW + nx <= 64 * 256;
+    // by the kernel that widens, where each of its threads has at most 24 scales to
+    // look at: a launch less (whole calls of 128 x 768 x 3000, 5003 and 5800: 26, 29
+    // and 27 us for 32, 33 and 32).  Each CTA reads them all, so that the kernels alone
+    // win up to 3000 (18.2 us for 19.0), lose 1.4 us at 5800, and 6 at 11000.
+    const bool with = f16 && nW + nx <= 24 * 256;
     if (f16 && !with) {
         k_factor<<<2, 1024, 0, st>>>(W_scale, nW, fac, x_scale, nx, fac + 2);
         SG_TRY_CUDA(cudaGetLastError());

@@ -96,10 +96,15 @@ template <int THREADS>
 __device__ __forceinline__ float2 factor_of(const float *s, int64_t n, float *sm)
 {
     float top = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += THREADS) {
-        const float v = fabsf(s[i]);
-        if (v < INFINITY)
-            top = fmaxf(top, v);
+    // eight under way together; those past the end read the last again
+    for (int64_t i = threadIdx.x; i < n; i += 8 * THREADS) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = fabsf(s[min(i + j * THREADS, n - 1)]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            top = fmaxf(top, v[j] < INFINITY ? v[j] : 0.f);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
