@@ -89,9 +89,10 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// A power of two that brings the largest of n scales to [256, 512), where the
-// largest value held in 8 bits (127 times it) is still an fp16 number, and its
-// inverse: for all THREADS of a CTA.
+// A power of two that brings the largest of n scales to about [256, 512), where the
+// largest magnitude held in 8 bits (128 times it) is still an fp16 number, and its
+// inverse: for all THREADS of a CTA.  fp16 rounds 65520 to infinity, so a scale
+// that would come to 511.875 or more is brought to half of that.
 template <int THREADS>
 __device__ __forceinline__ float2 factor_of(const float *s, int64_t n, float *sm)
 {
@@ -116,9 +117,10 @@ __device__ __forceinline__ float2 factor_of(const float *s, int64_t n, float *sm
     for (int i = 0; i < THREADS / 32; ++i)
         top = fmaxf(top, sm[i]);
     int e = 0;
-    if (top > 0.f)
-        frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
-    e = top > 0.f ? 9 - e : 0;
+    if (top > 0.f) {
+        const float f = frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
+        e = (f < 511.875f / 512.0f ? 9 : 8) - e;
+    }
     e = e > 126 ? 126 : e;
     return make_float2(ldexpf(1.f, e), ldexpf(1.f, -e));
 }

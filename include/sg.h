@@ -583,8 +583,8 @@ SG_API sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, 
 /* sg_linear8_fwd -- a linear layer on 8-bit integers with a scale for each
  * token and each output channel:
  *   out[t][n] = x_scale[t] W_scale[n] sum_h x8[t][h] W8[n][h]
- * x8[T][H] and W8[N][H], one scale for a row; out[T][N] in dtype (SG_BF16,
- * SG_F16, SG_F32).  Sums of 1024 products are exact, and those are added in fp32,
+ * x8[T][H] and W8[N][H] (any values, -128 too), one scale for a row; out[T][N] in
+ * dtype (SG_BF16, SG_F16, SG_F32).  Sums of 1024 products are exact, and those are added in fp32,
  * rounded to nearest.
  * sg_linear8_bwd -- the gradients for x and W as if they had not been rounded:
  *   dx[t][h] = sum_n dout[t][n] W_scale[n] W8[n][h]
