@@ -5,7 +5,11 @@
 #include "sg_internal.cuh"
 
 // `after`: the kernel before it in the stream is one of this call's, which this
-// one may overlap
+// one may overlap.  It waits for that one's end (grid_wait) before it uses anything
+// that the call writes, and before it ends, so that the next kernel's wait reaches
+// all of them.  A call's first kernel is launched without: nothing says that a
+// kernel of the program's before it waited in its turn, and the wait does not reach
+// past that one.
 template <typename... P, typename... A>
 sg_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, bool after, cudaStream_t st,
                  A... args)

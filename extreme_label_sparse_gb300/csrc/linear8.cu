@@ -806,7 +806,7 @@ sg_status sg_linear8_fwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     for (int64_t n0 = 0; n0 < N; n0 += pl.Nc) {
         const int64_t nc = N - n0 < pl.Nc ? N - n0 : pl.Nc;
         LIN_TRY(widen(widen_of(W8 + n0 * ldw, ldw, nc, H, nullptr, 0, nullptr, w8 + pl.o_W, pl.ldh, true),
-                      n0 ? none : widen_of(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true), st));
+                      n0 ? none : widen_of(x8, ldx, T, H, nullptr, 0, nullptr, w8 + pl.o_x, pl.ldh, true), n0 > 0, st));
         LinArgs a = {};
         a.ab = (int32_t)pl.ab, a.kt = (int32_t)pl.kt, a.status = status;
         Prod &p = a.p[0];
@@ -867,16 +867,19 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     // and 27 us for 32, 33 and 32).  Each CTA reads them all, so that the kernels alone
     // win up to 3000 (18.2 us for 19.0), lose 1.4 us at 5800, and 6 at 11000.
     const bool with = f16 && nW + nx <= 24 * 256;
+    bool after = false;  // this call's kernels have begun
     if (f16 && !with) {
         k_factor<<<2, 1024, 0, st>>>(W_scale, nW, fac, x_scale, nx, fac + 2);
         SG_TRY_CUDA(cudaGetLastError());
+        after = true;
     }
     if (pl.copy) {
-        LIN_TRY(launch(k_linear_copy, dim3((unsigned)(T < kSMs * 8 ? T : kSMs * 8)), 256, 0, 1, true, st,
+        LIN_TRY(launch(k_linear_copy, dim3((unsigned)(T < kSMs * 8 ? T : kSMs * 8)), 256, 0, 1, after, st,
                        static_cast<const uint16_t *>(dout), lddout, T, (int)N,
                        reinterpret_cast<uint16_t *>(w8 + pl.o_d), pl.ldn));
         dout = w8 + pl.o_d;
         lddout = pl.ldn;
+        after = true;
     }
     Widen wide[2] = {};
     if (dx)
@@ -884,7 +887,7 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     if (dW)
         wide[1] = widen_of(x8, ldx, T, H, x_scale, x_group, fac ? fac + 2 : nullptr, w8 + pl.o_x, pl.ldh, f16,
                            with ? nx : 0);
-    LIN_TRY(widen(wide[0], wide[1], st));
+    LIN_TRY(widen(wide[0], wide[1], after, st));
     LinArgs a = {};
     a.p[0] = pl.p[0], a.p[1] = pl.p[1];
     a.ab = (int32_t)pl.ab, a.kt = (int32_t)pl.kt, a.status = status;

@@ -454,7 +454,7 @@ FewArgs few_args(int64_t T, int64_t H, int64_t N)
 }
 
 template <int TMAX>
-sg_status launch_few(const CUtensorMap &mW, const CUtensorMap &mx, const FewArgs &a, cudaStream_t st)
+sg_status launch_few(const CUtensorMap &mW, const CUtensorMap &mx, const FewArgs &a, bool after, cudaStream_t st)
 {
     // once for each device (one bit of the mask)
     static std::atomic<uint64_t> done{0};
@@ -465,7 +465,7 @@ sg_status launch_few(const CUtensorMap &mW, const CUtensorMap &mx, const FewArgs
         SG_TRY_CUDA(cudaFuncSetAttribute(k_few<TMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<TMAX>::kSmem));
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch(k_few<TMAX>, dim3((unsigned)a.ctas), Few<TMAX>::kThreads, (int)Few<TMAX>::kSmem, 1, true, st, mW, mx, a);
+    return launch(k_few<TMAX>, dim3((unsigned)a.ctas), Few<TMAX>::kThreads, (int)Few<TMAX>::kSmem, 1, after, st, mW, mx, a);
 }
 
 // ---------------------------------------------------------------- a few rows by integer dot products
@@ -610,10 +610,10 @@ __global__ void __launch_bounds__(kDotThreads)
 
 template <int TT, bool ANY>
 sg_status launch_dot(const int8_t *x8, int64_t ldx, const int8_t *W8, int64_t ldw, int64_t H, const FewArgs &a,
-                     cudaStream_t st)
+                     bool after, cudaStream_t st)
 {
     const int rows = kDotThreads / 32 * kDotRows;
-    return launch(k_dot<TT, ANY>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, true, st, x8, ldx, W8, ldw, (int)H, a);
+    return launch(k_dot<TT, ANY>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, after, st, x8, ldx, W8, ldw, (int)H, a);
 }
 
 // Above kMaxFew tokens W8 is better brought to 16 bits once, for the 16-bit products
@@ -670,10 +670,13 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
                   const float *ws, int64_t N, void *out, int64_t ldo, int32_t dtype, const FewPlan &p, uint8_t *work,
                   int32_t *status, cudaStream_t st)
 {
+    bool after = false;  // this call's kernels have begun
     if (T > 64) {
-        LIN_TRY(widen(widen_of(x8, ldx, T, H, nullptr, 0, nullptr, work + p.o_x, p.ld, true), Widen{}, st));
+        LIN_TRY(widen(widen_of(x8, ldx, T, H, nullptr, 0, nullptr, work + p.o_x, p.ld, true), Widen{}, after, st));
+        after = true;
     } else if (p.copy_x) {
-        LIN_TRY(realign(x8, ldx, T, H, work + p.o_x, p.ld, st));
+        LIN_TRY(realign(x8, ldx, T, H, work + p.o_x, p.ld, after, st));
+        after = true;
         x8 = reinterpret_cast<const int8_t *>(work + p.o_x);
         ldx = p.ld;
     }
@@ -682,7 +685,8 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
         const int8_t *W = W8 + n0 * ldw;
         int64_t ld = ldw;
         if (p.copy_W) {
-            LIN_TRY(realign(W, ldw, nc, H, work + p.o_W, p.ld, st));
+            LIN_TRY(realign(W, ldw, nc, H, work + p.o_W, p.ld, after, st));
+            after = true;
             W = reinterpret_cast<const int8_t *>(work + p.o_W);
             ld = p.ld;
         }
@@ -694,20 +698,22 @@ sg_status few_fwd(const int8_t *x8, int64_t ldx, const float *xs, int64_t T, int
         a.status = status;
         if (by_dot(T, H)) {
             const bool any = !tma_ok(x8, ldx, 1) || !tma_ok(W, ld, 1);
-            LIN_TRY((T > 2    ? launch_dot<4, false>(x8, ldx, W, ld, H, a, st)
-                     : T == 2 ? (any ? launch_dot<2, true> : launch_dot<2, false>)(x8, ldx, W, ld, H, a, st)
-                              : (any ? launch_dot<1, true> : launch_dot<1, false>)(x8, ldx, W, ld, H, a, st)));
+            LIN_TRY((T > 2    ? launch_dot<4, false>(x8, ldx, W, ld, H, a, after, st)
+                     : T == 2 ? (any ? launch_dot<2, true> : launch_dot<2, false>)(x8, ldx, W, ld, H, a, after, st)
+                              : (any ? launch_dot<1, true> : launch_dot<1, false>)(x8, ldx, W, ld, H, a, after, st)));
+            after = true;
             continue;
         }
         CUtensorMap mW, mx;
         LIN_TRY(map_of(&mW, W, H, nc, ld, 1, "W8", 128));
         if (T > 64) {
             LIN_TRY(map_of(&mx, work + p.o_x, H, T, p.ld, 2, "x", (uint32_t)a.xb));
-            LIN_TRY(launch_few<128>(mW, mx, a, st));
+            LIN_TRY(launch_few<128>(mW, mx, a, after, st));
         } else {
             LIN_TRY(map_of(&mx, x8, H, T, ldx, 1, "x8", (uint32_t)a.xb));
-            LIN_TRY(T <= 16 ? launch_few<16>(mW, mx, a, st) : launch_few<64>(mW, mx, a, st));
+            LIN_TRY(T <= 16 ? launch_few<16>(mW, mx, a, after, st) : launch_few<64>(mW, mx, a, after, st));
         }
+        after = true;
         if (!a.whole && a.ctas > 1)
             LIN_TRY(launch(k_few_join, dim3((unsigned)a.ctas - 1, (unsigned)ceil_div(T < 128 ? T : 128, 8)), 256, 0, 1,
                            true, st, a));

@@ -217,7 +217,8 @@ Widen widen_of(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, const 
             ldd, f16, vec,  1};
 }
 
-sg_status widen(Widen a, Widen b, cudaStream_t st)
+// after: as launch() has it
+sg_status widen(Widen a, Widen b, bool after, cudaStream_t st)
 {
     const int64_t most = kSMs * 8;
     // few rows: a warp to 512 columns (128 x 2048: 3 us less)
@@ -225,13 +226,14 @@ sg_status widen(Widen a, Widen b, cudaStream_t st)
     a.spans = few ? (int32_t)ceil_div(a.cols, 512) : 1;
     b.spans = few ? (int32_t)ceil_div(b.cols, 512) : 1;
     const int64_t need = ceil_div(a.rows * a.spans + b.rows * b.spans, 8);
-    return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, a, b);
+    return launch(k_widen, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, after, st, a, b);
 }
 
-sg_status realign(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, uint8_t *dst, int64_t ldd, cudaStream_t st)
+sg_status realign(const int8_t *src, int64_t ld, int64_t rows, int64_t cols, uint8_t *dst, int64_t ldd, bool after,
+                  cudaStream_t st)
 {
     const int64_t most = kSMs * 8, spans = rows < 2 * most ? ceil_div(cols, 512) : 1, need = ceil_div(rows * spans, 8);
-    return launch(k_realign, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, true, st, src, ld, rows, (int)cols,
+    return launch(k_realign, dim3((unsigned)(need < most ? need : most)), 256, 0, 1, after, st, src, ld, rows, (int)cols,
                   (int)spans, reinterpret_cast<int8_t *>(dst), ldd);
 }
 
