@@ -65,6 +65,9 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
     const int64_t groups = WARPS == 1 ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x;
     const int64_t g = WARPS == 1 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
     const T *ax = static_cast<const T *>(a.x), *ar = static_cast<const T *>(a.res);
+    // 1024 threads lack the registers for both ways to max |y| (4096 x 16384 bf16 to
+    // 16 bits: 105 us, 112 with both, 101 with the third reduction alone)
+    constexpr bool kThird = WARPS == 32;
     const int ng = (a.cols + kGroup - 1) / kGroup;
     auto fetch = [&](int64_t r, int slot) {
         if constexpr (VEC) {
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 ss = fma2(v[i], v[i], ss);
-            if (a.y8) {
+            if (!kThird && a.y8) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 t = mul2(v[i], pre[n][i]);
@@ -181,9 +184,31 @@ __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_bloc
         }
         Scale8 s8 = {};
         if (a.y8) {
-            // max |y| without a third reduction: ru max |u pre|; a row whose sum
-            // is not finite has neither scale nor values
-            s8 = scale8_of(mag(sum < INFINITY ? top * ru : NAN));
+            // max |y|: where that is possible without a third reduction, ru max |u pre|.
+            // Products that fp32 holds in a few bits or as infinity say too little of
+            // y.  Products of 0 are below 2^-150, which leaves integers of 0 with ru
+            // up to 2^22 (a quarter of a step of 2^-126): rows of zeros among them.
+            float last = top * ru;
+            const bool known = mag(top) - 0x00800000u < 0x7f000000u;  // from 2^-126, and finite
+            if (kThird || (!known && !(top == 0.f && ru < 0x1p22f))) {
+                most = 0;
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    float2 y[4];
+                    unpack4(p[n], y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 t = mul2(mul2(y[i], both(ru)), pre[n][i]);
+                        most = max(most, max(mag(t.x), mag(t.y)));
+                    }
+                }
+                last = __uint_as_float(min(most, 0x7f800000u));
+                row_reduce<WARPS, true>(none, last, sm, turn);
+                if constexpr (WARPS > 1)
+                    __syncthreads();  // the next row's first sums use the same buffer
+            }
+            // a row whose sum is not finite has neither scale nor values
+            s8 = scale8_of(mag(sum < INFINITY ? last : NAN));
             if (lane == 0 && wr == 0)
                 a.y8_scale[r] = s8.scale;
         }
