@@ -1,10 +1,11 @@
 """Blocks on 8-bit integers at sizes where a CTA has much to do: several units of
-both products of the linear layer's backward pass.  Everything is compared, with 64-bit results worked out on the GPU."""
+both products of the linear layer's backward pass, and many rows to a row group of
+the norms.  Everything is compared, with 64-bit results worked out on the GPU."""
 import pytest
 import torch
 
 import extreme_label_sparse_gb300 as sg
-from test_gpu_blocks8 import HALF, LEAST, TYPES, rand, rand8, scales
+from test_gpu_blocks8 import ALPHA, E, EPS, HALF, LEAST, TYPES, backward_inputs, rand, rand8, scales, weights
 from test_linear8_turns import PATHS
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,72 @@ def test_linear_backward_of_several_units_to_a_cluster(T, H, N, dtype, group):
         if a.shape[1] >= 64:
             rel = float((out.double() - want).norm() / want.norm())
             assert rel <= 0.82 * HALF[dtype], (what, rel / HALF[dtype])
+
+
+# ---------------------------------------------------------------- norms around a block
+# row groups of the forward and backward kernels on 152 SMs: 2432 of one warp, 1216
+# of two, 608 of four, 304 of eight, 152 of more.  The forward kernel has up to four
+# rows of a group under way, the backward kernel two batches of up to four: the rows
+# below are more than twice that for each group, and a remainder.
+FORWARD = [(21893, 256), (21893, 512), (10951, 768), (5479, 2048), (2743, 4096), (1375, 8192), (1375, 16384)]
+FORWARD_ANY = [(21893, 255), (10951, 1001), (2743, 4001), (1375, 9001)]  # rows that start anywhere
+BACKWARD = [(41349, 256), (20681, 512), (10343, 1024), (5175, 2048), (2591, 4096), (2591, 8192), (1211, 16384)]
+BACKWARD_ANY = [(20001, 255), (10343, 500), (5175, 1001), (2591, 2001), (1300, 4001), (1300, 9001)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,cols,shift", [s + (0,) for s in FORWARD] + [s + (1,) for s in FORWARD_ANY])
+def test_block_norm_forward_of_many_rows_to_a_group(rows, cols, shift, dtype):
+    x, res = rand(rows, cols, dtype, 1, 8 - shift, shift), rand(rows, cols, dtype, 2, 8 - shift, shift, 2.0)
+    post, gate, pre = weights(cols, dtype)
+    n = -(-cols // 128)
+    mats = {k: torch.empty((rows, cols), dtype=t, device="cuda") for k, t in
+            (("u", x.dtype), ("y", x.dtype), ("y8", torch.int8), ("x8", torch.int8), ("u8", torch.int8))}
+    vecs = {k: torch.full((rows,), float("nan"), device="cuda") for k in ("rstd_x", "rstd_u", "y8_scale")}
+    groups = {k: torch.full((rows, n), float("nan"), device="cuda") for k in ("x_scale", "u_scale")}
+    sg.sg_block_norm_fwd(x, post, pre, EPS, residual=res, gate=gate, residual_scale=ALPHA, **mats, **vecs, **groups)
+    rx = (x.double().square().mean(1) + EPS).rsqrt()
+    v = x.double() * rx[:, None] * post.double() * gate.double()
+    near(vecs["rstd_x"][:, None], rx[:, None], "f32", E * rx[:, None], "rstd_x")
+    near(mats["u"], v + ALPHA * res.double(), dtype, E * (v.abs() + (ALPHA * res.double()).abs()), "u")
+    u = mats["u"].double()
+    ru = (u.square().mean(1) + EPS).rsqrt()
+    y = u * ru[:, None] * pre.double()
+    near(vecs["rstd_u"][:, None], ru[:, None], "f32", E * ru[:, None], "rstd_u")
+    near(mats["y"], y, dtype, E * y.abs(), "y")
+    top, s = y.abs().amax(1), vecs["y8_scale"].double()
+    assert bool(((s - top / 127).abs() <= 2 * E * top / 127).all())
+    assert bool(((mats["y8"].double() * s[:, None] - y).abs() <= s[:, None] * (0.5 + 127 * 4 * E)).all())
+    for k, m in (("x", x), ("u", mats["u"])):  # the operator of their own, whose tests are by the definition
+        q, scale = torch.empty_like(mats["y8"]), torch.empty_like(groups["x_scale"])
+        sg.sg_pack8(m, q, scale)
+        assert torch.equal(mats[k + "8"], q) and torch.equal(groups[k + "_scale"], scale), k
+
+
+@pytest.mark.parametrize("held", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,cols,shift", [s + (0,) for s in BACKWARD] + [s + (1,) for s in BACKWARD_ANY])
+def test_block_norm_backward_of_many_rows_to_a_group(rows, cols, shift, dtype, held):
+    dy, u, x, us, xs, di, rx, ru = backward_inputs((rows, cols), dtype, 16 - shift, shift, held)
+    post, gate, pre = weights(cols, dtype)
+    dx, dres = (torch.full((rows, cols), float("nan"), dtype=dy.dtype, device="cuda") for _ in range(2))
+    sums = {k: torch.full((cols,), float("nan"), device="cuda") for k in ("dpost", "dpre", "dgate")}
+    sg.sg_block_norm_bwd(dy, u, x, post, pre, rx, ru, dx, dresidual=dres, gate=gate, residual_scale=ALPHA, du_in=di,
+                         u_scale=us, x_scale=xs, **sums)
+    post, gate, pre, rx, ru = (t.double() for t in (post, gate, pre, rx[:, None], ru[:, None]))
+    m = (values(u, us) if held else u.double()).mul_(ru)
+    h = (values(x, xs) if held else x.double()).mul_(rx)
+    g = dy.double() * pre
+    du = ru * (g - m * (g * m).mean(1, keepdim=True)) + di.double()
+    terms = ru * (g.abs() + m.abs() * (g * m).abs().mean(1, keepdim=True)) + di.double().abs()
+    near(dres, ALPHA * du, dtype, E * ALPHA * terms, "dresidual")
+    # a thread adds its rows one after the other, then the parts are joined
+    chain = (rows + 100) * 2.0 ** -24 + 2 * E
+    near(sums["dpre"][None], (dy.double() * m).sum(0)[None], "f32", chain * (dy.double() * m).abs().sum(0)[None], "dpre")
+    s, t = (du * h).sum(0)[None], (terms * h.abs()).sum(0)[None]
+    near(sums["dpost"][None], gate * s, "f32", chain * gate.abs() * t, "dpost")
+    near(sums["dgate"][None], post * s, "f32", chain * post.abs() * t, "dgate")
+    del m, g
+    k, kt = du * gate * post, terms * (gate * post).abs()
+    near(dx, rx * (k - h * (k * h).mean(1, keepdim=True)), dtype,
+         3 * E * rx * (kt + h.abs() * (kt * h.abs()).mean(1, keepdim=True)), "dx")
