@@ -59,3 +59,20 @@ def test_gradients_and_single_tokens(example):
     for i in (0, 17, rows - 1):
         # the same integers: the sums are exact in either kernel
         assert torch.equal(one.forward(x[i:i + 1], res[i:i + 1])[0], z[i])
+
+
+def test_serving_in_the_first_rows_of_the_same_buffers(example):
+    """A block over fewer rows has the same weights and buffers, and leaves the rows
+    behind its own as they are."""
+    b = example.Block(40, 256, 300)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x, res = (torch.randn((40, 256), generator=g, device="cuda").bfloat16() for _ in range(2))
+    z = b.forward(x, res).clone()
+    one = b.first(1)
+    assert all(getattr(one, k).data_ptr() == getattr(b, k).data_ptr() for k in ("W", "W8", "W_scale", "z", "y8", "status"))
+    for i in (39, 17, 5):
+        assert torch.equal(one.forward(x[i:i + 1], res[i:i + 1])[0], z[i])
+        assert torch.equal(b.z[0], z[i]) and torch.equal(b.z[1:], z[1:])
+    few = b.first(7)
+    assert torch.equal(few.forward(x[20:27], res[20:27]), z[20:27]) and torch.equal(b.z[7:], z[7:])
