@@ -131,3 +131,34 @@ def test_block_norm_backward_of_many_rows_to_a_group(rows, cols, shift, dtype, h
     k, kt = du * gate * post, terms * (gate * post).abs()
     near(dx, rx * (k - h * (k * h).mean(1, keepdim=True)), dtype,
          3 * E * rx * (kt + h.abs() * (kt * h.abs()).mean(1, keepdim=True)), "dx")
+
+
+@pytest.mark.parametrize("rows,cols,shift", [(21893, 256, 0), (10951, 768, 0), (2743, 4096, 0), (611, 16384, 0), (10951, 1001, 1)])
+def test_block_norm_over_its_inputs_with_many_rows_to_a_group(rows, cols, shift):
+    """Rows on their way to the chip are others than those that are written."""
+    x, res = rand(rows, cols, "bf16", 1, 8 - shift, shift), rand(rows, cols, "bf16", 2, 8 - shift, shift)
+    w = weights(cols, "bf16")
+    u, y, rx, ru = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+
+    def fwd(x, res, u, y):
+        sg.sg_block_norm_fwd(x, w[0], w[2], EPS, residual=res, gate=w[1], residual_scale=ALPHA, u=u, y=y, rstd_x=rx, rstd_u=ru)
+
+    fwd(x, res, u, y)
+    for u_at, y_at in ((0, 1), (1, 0)):
+        b = [x.clone(), res.clone()]
+        fwd(b[0], b[1], b[u_at], b[y_at])
+        assert torch.equal(b[u_at], u) and torch.equal(b[y_at], y)
+    dx, dres = torch.empty_like(x), torch.empty_like(x)
+
+    def bwd(b, dx, dres):
+        sums = torch.empty((3, cols), device="cuda")
+        sg.sg_block_norm_bwd(b["dy"], b["u"], b["x"], w[0], w[2], rx, ru, dx, dresidual=dres, gate=w[1], residual_scale=ALPHA,
+                             du_in=b["di"], dpost=sums[0], dpre=sums[1], dgate=sums[2])
+        return sums
+
+    given = {"dy": y, "u": u, "x": x, "di": res}
+    ref = bwd(given, dx, dres)
+    for res_at, dx_at in (("dy", "di"), ("di", "dy"), ("u", "x")):
+        b = {k: v.clone() for k, v in given.items()}
+        assert torch.equal(bwd(b, b[dx_at], b[res_at]), ref)
+        assert torch.equal(b[dx_at], dx) and torch.equal(b[res_at], dres)
