@@ -4,9 +4,10 @@
 // and the gradient through both.  Bound by memory, and by instructions where rows
 // are turned into 8 bits or back: a row lies in the registers of one CTA (forward)
 // or in shared memory (backward) between its two sums and their uses, so each input
-// is read once and each output written once.  16384 x 4096 bf16: forward 83 us (6.5
-// TB/s), with x kept in 8 bits 108; backward 126 us (6.4 TB/s), from 8 bits 132 (5.1
-// TB/s).
+// is read once and each output written once.  16384 x 4096 bf16: forward 84 us (6.4
+// TB/s), with x kept in 8 bits 109, with u in 16 bits and y, x and u in 8, as a
+// training step keeps them, 150 (its bytes take 89); backward 126 us (6.4 TB/s), from
+// 8 bits 132 (5.1 TB/s).
 #include <cmath>
 
 #include "norm.cuh"
@@ -52,7 +53,7 @@ __device__ __forceinline__ void block_weights(const void *post, const void *gate
 // row groups step over the rows, with the next S rows on their way to shared
 // memory.  Two segments to a thread and a row at a time: batches of rows, as the
 // backward kernel has them, took 142 us for 16384 x 4096 bf16 with x kept in 8 bits
-// (now 108), and four warps to a row of up to 1024 columns 146 us for 65536 x 768
+// (now 109), and four warps to a row of up to 1024 columns 146 us for 65536 x 768
 // (two: 99).
 template <typename T, bool VEC, int WARPS, int NV, int S>
 __global__ void __launch_bounds__(norm_threads(WARPS), block_ctas(WARPS)) k_block_fwd(const BlockFwd a)

@@ -653,7 +653,8 @@ sg_status sg_linear8_bwd(const int8_t *x8, int64_t ldx, const float *x_scale, in
     // by the kernel that widens, where each of its threads has at most 24 scales to
     // look at: a launch less (whole calls of 128 x 768 x 3000, 5003 and 5800: 26, 29
     // and 27 us for 32, 33 and 32).  Each CTA reads them all, so that the kernels alone
-    // win up to 3000 (18.2 us for 19.0), lose 1.4 us at 5800, and 6 at 11000.
+    // win up to 3000 (18.2 us for 19.0), lose 1.4 us at 5800, and 6 at 11000: in a
+    // captured graph, where a launch costs the CPU nothing, above 4000 that is lost.
     const bool with = f16 && nW + nx <= 24 * 256;
     bool after = false;  // this call's kernels have begun
     if (f16 && !with) {

@@ -17,9 +17,9 @@
 // time than that takes, the cuts go between tiles.
 //
 // Measured at 2048 x 128000 (262 MB): 16 tokens 49 us (5.3 TB/s; a block takes 750
-// cycles, its bytes 700 at the copy rate), 48 tokens 52 us, 128 tokens 65 us (970
-// cycles: the MMAs take 630 to issue).  4096 x 4096: 16 tokens 9.9 us, 128 tokens
-// 17.7 us, of which the launches, the first loads and the join are the larger part.
+// cycles, its bytes 700 at the copy rate), 48 tokens 53 us, 128 tokens 65 us (970
+// cycles: the MMAs take 630 to issue).  4096 x 4096: 16 tokens 10.5 us, 128 tokens
+// 17.8 us, of which the launches, the first loads and the join are the larger part.
 #pragma once
 
 #include "linear8_widen.cuh"
@@ -29,7 +29,7 @@ namespace {
 constexpr int kBlockK = 128;   // bytes of K in a block
 constexpr int kChunk = 8;      // blocks that are summed in tensor memory: 1024 terms
 constexpr uint32_t kWTile = 128 * kBlockK;
-constexpr int kMaxFew = 512;   // tokens that this way takes
+constexpr int kMaxFew = 512;   // tokens that this way takes: their scales are in shared memory
 
 // for up to TMAX tokens: stages, operand buffers, teams, epilogue warps
 template <int TMAX>
@@ -432,8 +432,10 @@ FewArgs few_args(int64_t T, int64_t H, int64_t N)
     a.xb = a.tt > 1 ? 128 : (int32_t)ceil_div(T, 8) * 8;
     a.kb = (int32_t)ceil_div(H, kBlockK);
     a.tiles = (int32_t)ceil_div(N, 128) * a.tt;
-    // whole tiles where they keep the last SM less than nine blocks (about 4 us)
-    // longer than equal ranges would
+    // Whole tiles where they keep the last SM less than nine blocks (about 4 us)
+    // longer than equal ranges would.  Whole / equal: 6 blocks longer (48 x 1024 x 65536)
+    // 19.8 / 22.4 us, 8 (16 x 1024 x 60000) 16.7 / 17.5; the two meet above the limit
+    // (10 blocks, 48 x 1280 x 40000: 18.1 / 19.1, 11, 16 x 2048 x 65536: 29.1 / 29.9).
     a.whole = ceil_div(a.tiles, kSMs) * a.kb - (int64_t)a.tiles * a.kb / kSMs < 9;
     // Few tiles of many tokens, whose parts are large: each tile cut into as many
     // ranges, where those are at most two blocks longer than equal ones, most of
@@ -616,8 +618,11 @@ sg_status launch_dot(const int8_t *x8, int64_t ldx, const int8_t *W8, int64_t ld
     return launch(k_dot<TT, ANY>, dim3((unsigned)ceil_div(a.N, rows)), kDotThreads, 0, 1, after, st, x8, ldx, W8, ldw, (int)H, a);
 }
 
-// Above kMaxFew tokens W8 is better brought to 16 bits once, for the 16-bit products
-// at twice the rate of k_few, which turns it into fp16 for each 128 tokens.
+// With many tokens W8 is better brought to 16 bits once, for the 16-bit products at
+// twice the rate of k_few, which turns it into fp16 for each 128 tokens.  At 4096 x
+// 4096 the two meet at some 700 tokens (512: 22.5 us this way, 30 the other; 640: 33 and
+// 34; 768: 37 and 35), at 2048 x 65536 at a thousand (640: 141 and 191; 896: 195 and
+// 225; 1024: 220 and 216).  kMaxFew stands below both.
 bool is_few(int64_t T) { return T <= kMaxFew; }
 
 bool by_dot(int64_t T, int64_t H) { return T <= kDotTokens && H <= kMostDot; }

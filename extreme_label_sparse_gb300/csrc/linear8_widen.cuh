@@ -27,8 +27,9 @@ __device__ int32_t g_linear_status;
 
 __device__ __forceinline__ int32_t *lin_status(int32_t *status) { return status ? status : &g_linear_status; }
 
-// two of four int8 (bytes 0 and 1, or 2 and 3 of u ^ 0x80808080) as fp16: a byte
-// plus 128 as the low bits of 1024, less 1152
+// two of four int8 (bytes 0 and 1, or 2 and 3 of u ^ 0x80808080) as fp16, by the
+// usual way of 8-bit weights on 16-bit tensor cores: a byte plus 128 as the low bits
+// of 1024, less 1152
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t u, int half)
 {
     const uint32_t h = __byte_perm(u, 0x64646464u, half ? 0x4342 : 0x4140);
@@ -139,7 +140,10 @@ struct Widen {
 };
 
 // int8 rows to 16 bits: the integers, or the values they stand for, of one or two
-// matrices.  A warp takes a row, or a span of one where there are few, 16 columns
+// matrices.  The gradients' sums run over what the scales belong to, so a scale has to
+// enter a product's operand; the value is rounded to dout's type there, as 16-bit weights
+// would be (two operands for its high and low bits would double the products: dx and
+// dW are off by 2.4e-3 in bf16 so, 1.7e-3 without).  A warp takes a row, or a span of one where there are few, 16 columns
 // to a lane, whose 32 bytes it writes at once (halves of a sector would each go to L2: 64 MB took 40 us).
 __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ Widen m0, const __grid_constant__ Widen m1)
 {

@@ -436,7 +436,9 @@ SG_API sg_status sg_dropout(const void *x, int64_t ldx, int64_t rows, int64_t co
  * pointer is given: u (the next residual, and what the backward pass reads),
  * rstd[rows], y rounded to dtype, and y8[rows][cols] with y8_scale[rows]: y in
  * 8 bits (SG_E4M3), y = y8 * y8_scale with y8_scale = max |y| / 448 of the row
- * (at least 2^-126; 0 for a row of zeros).  One of y and y8 is needed.
+ * (at least 2^-126; 0 for a row of zeros).  It goes by the largest |u weight| of the
+ * row, whose magnitude has to be an fp32 number of all its bits (1e-37 to 3e38) or 0.
+ * One of y and y8 is needed.
  * residual NULL: u = drop(x).  weight[cols] has dtype.  u may be x or residual,
  * and y any of them.  cols <= 32768.
  * The sum of u^2 is formed in fp32 as it is: rows of a root mean square of up
@@ -531,7 +533,8 @@ SG_API sg_status sg_softmax_ce_bwd(const void *h, int64_t ldh, int64_t T, int64_
  * scale an fp32 number; 0 for a group of zeros, and NaN where the group holds an
  * infinity or NaN (its q are 0).  q must not overlap x.  cols <= 32768 with group
  * 0.
- * sg_unpack8 -- y = round(q scale) in dtype; any values of q (-128 too). */
+ * sg_unpack8 -- y = round(q scale) in dtype; any values of q (-128 too).  y must
+ * not overlap q. */
 SG_API sg_status sg_pack8(const void *x, int64_t ldx, int64_t rows, int64_t cols, int32_t dtype, int32_t group,
                           int8_t *q, int64_t ldq, float *scale, void *stream);
 SG_API sg_status sg_unpack8(const int8_t *q, int64_t ldq, const float *scale, int64_t rows, int64_t cols,
@@ -543,10 +546,12 @@ SG_API sg_status sg_unpack8(const int8_t *q, int64_t ldq, const float *scale, in
  *   u = round(residual_scale residual + gate v)
  *   y = u rstd_u pre_weight,            rstd_u = 1 / sqrt(mean(u^2) + eps)
  * with u rounded to dtype before its norm is taken.  residual NULL: none; gate
- * NULL: 1.  post_weight, gate and pre_weight have cols elements of dtype.
+ * NULL: 1.  post_weight, gate and pre_weight have cols elements of dtype, the same
+ * for all rows (a gate of each row or element is no part of this: x's norm would
+ * have to be multiplied by it outside).
  * Outputs, each where its pointer is given: u, rstd_x[rows], rstd_u[rows], y,
  * y8 with y8_scale[rows] (y in 8 bits, one scale for a row, what sg_linear8_fwd
- * reads; rounded from fp32 y), and for the backward pass x8 and u8 (x and u in 8
+ * reads; from fp32 y and its largest magnitude, as sg_pack8 does), and for the backward pass x8 and u8 (x and u in 8
  * bits, group 128, as sg_pack8 makes them) with x8_scale and u8_scale.  One of y
  * and y8 is needed.  u may be x or residual, and y any of them; cols <= 16384.
  * The sums of squares are formed in fp32 as they are, with the range that
@@ -593,15 +598,22 @@ SG_API sg_status sg_block_norm_bwd(const void *dy, int64_t lddy, const void *u, 
  * too; either may be NULL (then what it alone needs may be NULL as well).
  * x8 may have one scale for a row (x_group 0) or for 128 columns (x_group 128):
  * what sg_pack8 or sg_block_norm_fwd kept.  The values that 8 bits stand for enter
- * the products rounded to dtype (times a power of two, taken out again, in fp16),
- * and parts of 1024 terms are added in fp32.
+ * the products rounded to dtype, and parts of 1024 terms are added in fp32: dx and dW
+ * are off by a rounding of their terms and one of their own.  In fp16 the values are
+ * first multiplied by a power of two that suits the largest scale of the call (taken
+ * out again): below 2^-22 of that scale they are held to 2^-32 of it.
  * The results are the same bits for the same call.  A token or channel whose
  * scale is NaN gives NaN.  Outputs must not overlap inputs.  status and errors
  * found on the device: as sg_softmax_ce_fwd, with sg_linear8_status for calls
  * without a status word.
  * T <= 2^24, H <= 2^20, N <= 2^24, T N < 2^43.  work is aligned to 256 bytes;
  * sg_linear8_work wants the same x8, W8, strides (and dout, where backward is 1)
- * as the call. */
+ * as the call.  Forward, it holds at most x8 in 16 bits, 256 MB of W8 at a time (or
+ * 256 channels, where that is more), and at most 80 MB of fp32 parts.  Backward it
+ * holds all of x8 (for dW) and of W8 (for dx) in 16 bits, 2 H (T + N) bytes, where
+ * dout's rows do not start on 16 bytes a copy of it, and at most 80 MB of parts for
+ * each product: a step with 8-bit weights has three times their size in memory while
+ * this call runs. */
 SG_API sg_status sg_linear8_work(const int8_t *x8, int64_t ldx, int64_t T, int64_t H, const int8_t *W8, int64_t ldw,
                                  int64_t N, const void *dout, int64_t lddout, int32_t backward, int64_t *bytes);
 SG_API sg_status sg_linear8_status(int32_t *code, int32_t clear);
